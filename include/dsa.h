@@ -332,6 +332,137 @@ dsa_status dsa_quantize_e4m3_append(const void* x, int32_t B, int32_t n, int32_t
                                     int32_t S_cap, int64_t pos0, const int64_t* positions,
                                     void* ws, size_t ws_bytes, void* stream);
 
+/* Per-head norm and rotary rotation in one pass: what turns a projection's rows into the
+ * operands of the indexer and of attention.  For every head row x of d values (fp32 throughout):
+ *   DSA_NORM_NONE   y = x
+ *   DSA_NORM_RMS    y = x * rsqrt(mean(x^2) + eps) * weight
+ *   DSA_NORM_LAYER  y = (x - mean(x)) * rsqrt(var(x) + eps) * weight + bias   (var: / d)
+ * then, with rope_dim > 0, the values y[rope_off .. rope_off + rope_dim) are rotated by the angles
+ * of the token's position p: the pair (a, c) becomes (a cos - c sin, c cos + a sin), pair j being
+ * values (2j, 2j + 1) (interleaved != 0) or (j, j + rope_dim / 2) of that range, with cos and sin
+ * entries j of table row p.  The result is rounded once, to the output's type.
+ *   x          [B,n,H,d] bf16 (16-byte aligned); strides in elements, 0: dense, else multiples of 8
+ *              with x_stride_h >= d; token i of sequence b, head h at
+ *              x + b*x_stride_b + i*x_stride_t + h*x_stride_h
+ *   weight     [d] fp32 or NULL (1); bias [d] fp32 or NULL (0; layer norm only).  16-byte aligned
+ *   cos, sin   [max_pos, rope_dim / 2] fp32, 16-byte aligned; ignored when rope_dim = 0
+ *   positions  DEVICE int64 [B,n], or NULL: token i of every sequence is at pos0 + i
+ * d: a multiple of 8 in [8, 1024]; rope_off a multiple of 8; rope_dim a multiple of 16 (of 8
+ * interleaved) with rope_off + rope_dim <= d.  A token at position -1 is padding: it is skipped
+ * and its output left as it was.  Any other position that has no table row (or, below, no cache
+ * row) is skipped too and raises DSA_FLAG_BAD_INDEX; with positions NULL the host checks.
+ * n = 0 is allowed and launches nothing. */
+typedef enum { DSA_NORM_NONE = 0, DSA_NORM_RMS = 1, DSA_NORM_LAYER = 2 } dsa_norm;
+typedef struct {
+  int32_t B, n, H, d;
+  const void* x;
+  int64_t x_stride_b, x_stride_t, x_stride_h;
+  dsa_norm norm;
+  float eps;
+  const float* weight;
+  const float* bias;
+  const float* cos;
+  const float* sin;
+  int32_t rope_off, rope_dim, interleaved, max_pos;
+  const int64_t* positions;
+  int64_t pos0;
+} dsa_norm_rope_args;
+
+/* Result as bf16 [B,n,H,d] (16-byte aligned, strides as x's).  out may be x itself with x's
+ * strides; any other overlap of the two is not allowed.  Needs DSA_WS_MIN bytes of workspace. */
+dsa_status dsa_norm_rope(const dsa_norm_rope_args* a, void* out, int64_t out_stride_b, int64_t out_stride_t,
+                         int64_t out_stride_h, void* ws, size_t ws_bytes, void* stream);
+
+/* Result as e4m3 codes with one fp32 scale per token over all its heads -- the FP8 indexer's
+ * operand form, quantised as dsa_quantize_e4m3_append does (scale = amax / 448, or 1; code =
+ * e4m3(y / scale)) but from the fp32 result, without a rounding to bf16 in between.
+ *   codes   [B,S_cap,H*d] (8-byte aligned), scales [B,S_cap] fp32 (4-byte aligned)
+ *   at_position  0: token i of a sequence goes to row i (queries); else to the row of its
+ *                position (the key cache).  Two tokens of one sequence at the same row leave it
+ *                unspecified.
+ * d <= 256 and H * (d / 8 rounded up to 4, 8, 16 or 32) <= 2048.  Needs DSA_WS_MIN bytes. */
+dsa_status dsa_norm_rope_e4m3(const dsa_norm_rope_args* a, uint8_t* codes, float* scales, int32_t S_cap,
+                              int32_t at_position, void* ws, size_t ws_bytes, void* stream);
+
+/* Paged FP8 cache of latent KV rows (512 latent values and 64 rotated ones per token).  A stored
+ * row stands for scale * [codes (512 e4m3) | rope (64 bf16)]: the one scale serves both, so
+ * attention multiplies a whole row's score by it.
+ *   codes   [n_pages, page_size, 512] (16-byte aligned)
+ *   scales  [n_pages, page_size] fp32 (4-byte aligned); positive and finite where rows are used
+ *   rope    [n_pages, page_size, 64] bf16 (16-byte aligned)
+ *   block_table  DEVICE int32 [B, table_ld]: position p of sequence b is row p % page_size of page
+ *                block_table[b * table_ld + p / page_size].  NULL: sequence b is page b
+ *                (n_pages >= B), its rows contiguous.
+ * page_size: any size >= 1.  A sequence holds table_ld * page_size rows (page_size without a
+ * table).  Table entries are read only for positions in use; a used entry outside [0, n_pages)
+ * raises DSA_FLAG_BAD_INDEX and its positions are skipped (attention, append) or read as zeros. */
+typedef struct {
+  int32_t n_pages, page_size, table_ld;
+  uint8_t* codes;
+  float* scales;
+  void* rope;
+  const int32_t* block_table;
+} dsa_latent_cache;
+
+/* Appends latent rows: RMS norm of the 512 latent values, rotation of the 64 rope values,
+ * quantisation and the write through the block table in one pass.
+ *   x       [B,n,576] bf16 (16-byte aligned): [latent | rope] of the projection.  Strides in
+ *           elements, 0: dense, else multiples of 8 with x_stride_t >= 576
+ *   weight  [512] fp32 (16-byte aligned), or NULL: the latent values are taken as they are
+ *   cos, sin [max_pos, 32] fp32 (8-byte aligned), or both NULL: the rope values are not rotated
+ *   positions, pos0, interleaved, padding: as dsa_norm_rope
+ * scale = max(amax / 448, 2^-60) over the 512 normed values (fp32, IEEE division); codes =
+ * e4m3(y / scale); rope = bf16(rotated / scale).  A row with a NaN keeps it (its scale is NaN).
+ * Two tokens that name the same cache row leave it unspecified.  Needs DSA_WS_MIN bytes. */
+typedef struct {
+  int32_t B, n;
+  const void* x;
+  int64_t x_stride_b, x_stride_t;
+  const float* weight;
+  float eps;
+  const float* cos;
+  const float* sin;
+  int32_t interleaved, max_pos;
+  const int64_t* positions;
+  int64_t pos0;
+} dsa_latent_append_args;
+dsa_status dsa_latent_append(const dsa_latent_append_args* a, const dsa_latent_cache* cache, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* Reads rows back: out[b,i] = bf16(scale * [codes | rope]) of position idx[b*n + i], or of pos0 + i
+ * with idx NULL.  out [B,n,576] bf16, dense, 16-byte aligned.  idx: DEVICE int32 [B,n], e.g. a
+ * top-k's rows; -1 gives a row of zeros, any other position outside the sequence's cache zeros and
+ * DSA_FLAG_BAD_INDEX.  n = 0 launches nothing.  Needs DSA_WS_MIN bytes. */
+dsa_status dsa_latent_read(const dsa_latent_cache* cache, int32_t B, int32_t n, const int32_t* idx, int64_t pos0,
+                           void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* Sparse attention over selected rows of the paged FP8 cache: dsa_sparse_attn's latent shape
+ * (576-wide queries, the value is a row's first 512 values) for 1 <= H <= 128 query heads.
+ *   q    [B,T,H,576] bf16 (16-byte aligned); strides in elements, 0: dense, else multiples of 8
+ *        with q_stride_t >= H*576; a query's heads are contiguous
+ *   idx  DEVICE int32 [B,idx_T,k], entries in [-1, S), S <= the rows a sequence of the cache holds;
+ *        idx_T = T, or 1: one index row per sequence read by all its T queries (draft steps).
+ *        -1 is skipped; other entries out of range, and positions without a valid page, are
+ *        skipped and raise DSA_FLAG_BAD_INDEX.  A position listed twice counts twice.
+ *   out  [B,T,H,512] bf16 (16-byte aligned); lse [B,T,H] fp32 (natural log) or NULL
+ * 1 <= k <= 65536.  A row with no valid entry gets out = 0, lse = -inf.  Scores and the softmax's
+ * sums are fp32.  ws: dsa_latent_attn_workspace_size bytes are preferred (DSA_WS_MIN plus room for
+ * the parts of rows split over CTAs when there are few); at least DSA_WS_MIN.  flags: DEVICE word
+ * for DSA_FLAG_* bits, or NULL for the workspace's flag word; with it ws needs no zero fill, so
+ * calls that may overlap can each take scratch of their own and share one flag word. */
+typedef struct {
+  int32_t B, T, S, H;
+  float scale;
+  const void* q;
+  int64_t q_stride_b, q_stride_t;
+  dsa_latent_cache cache;
+  int32_t idx_T;
+  uint32_t* flags;
+} dsa_latent_attn_args;
+dsa_status dsa_latent_attn(const dsa_latent_attn_args* a, const int32_t* idx, int32_t k, void* out, float* lse,
+                           void* ws, size_t ws_bytes, void* stream);
+size_t dsa_latent_attn_workspace_size(const dsa_latent_attn_args* a, int32_t k);
+
 /* Reads the device flag word of a workspace into *flags_out (host) and clears it.
  * Synchronises `stream`. */
 dsa_status dsa_read_device_flags(void* ws, uint32_t* flags_out, void* stream);
@@ -380,12 +511,13 @@ uint64_t dsa_launch_count(void);
  *   recorded.
  * dsa_trace_read(kinds, ms, max_records, dropped): waits for the recorded launches to finish
  *   (host synchronisation on their events), writes up to max_records entries in launch order
- *   -- kinds[i] is DSA_TRACE_INDEXER, _TOPK, _ATTENTION or _OVERLAP, ms[i] the device time in
+ *   -- kinds[i] is DSA_TRACE_INDEXER, _TOPK, _ATTENTION, _OVERLAP or _CACHE (the
+ *   norm, latent append and latent read kernels), ms[i] the device time in
  *   milliseconds (-1 if unavailable) -- returns the number written, stores in *dropped (may
  *   be NULL) the launches the pool could not record, and clears the records.  Host arrays
  *   are owned by the caller; kinds or ms may be NULL.
  * dsa_trace_disable(): stops recording and destroys the pool. */
-enum { DSA_TRACE_INDEXER = 1, DSA_TRACE_TOPK = 2, DSA_TRACE_ATTENTION = 3, DSA_TRACE_OVERLAP = 4 };
+enum { DSA_TRACE_INDEXER = 1, DSA_TRACE_TOPK = 2, DSA_TRACE_ATTENTION = 3, DSA_TRACE_OVERLAP = 4, DSA_TRACE_CACHE = 5 };
 dsa_status dsa_trace_enable(int max_launches);
 int dsa_trace_read(int* kinds, float* ms, int max_records, int* dropped);
 void dsa_trace_disable(void);

@@ -18,6 +18,14 @@ Calls (same names as the C ABI):
   indexshare_schedule_score(M, schedule)  -> float (host only)
   indexshare_schedule_search(M, n_full)   -> (schedule str, score) (host only)
   dsa_quantize_e4m3_append(x, codes, scales, pos0 | positions) -> e4m3 rows + scales in a cache
+  dsa_norm_rope(x, ...)                   -> bf16 [B,n,H,d]: per-head norm + rotation in one pass
+  dsa_norm_rope_e4m3(x, codes, scales, ...) -> the same as e4m3 codes + one scale per token
+  dsa_latent_append(x, cache, ...)        -> norm + rotation + quantisation into a paged FP8 cache
+  dsa_latent_read(cache, idx | n, pos0)   -> bf16 rows [B,n,576] of that cache
+  dsa_latent_attn(at, idx)                -> (out [B,T,H,512] bf16, lse): sparse attention over it
+A latent cache is a dict: codes [pages, page, 512] float8_e4m3fn or uint8, scales [pages, page]
+fp32, rope [pages, page, 64] bf16 and block_table [B, pages per sequence] int32 (None: sequence b
+is page b).
 Operand dicts use the keys produced by ``synth``: an indexer dict holds q, w, k, q_scale,
 k_scale, q_pos0, diag; an attention dict holds q, k, v (None: latent KV), d_v, scale.
 """
@@ -68,6 +76,31 @@ class Layer(_c.Structure):
 class Varlen(_c.Structure):
     _fields_ = [("n_seqs", _c.c_int32), ("cu_q", _c.POINTER(_c.c_int64)), ("cu_k", _c.POINTER(_c.c_int64)),
                 ("q_pos0", _c.POINTER(_c.c_int64))]
+
+
+class NormRopeArgs(_c.Structure):
+    _fields_ = [("B", _c.c_int32), ("n", _c.c_int32), ("H", _c.c_int32), ("d", _c.c_int32), ("x", _P),
+                ("x_stride_b", _c.c_int64), ("x_stride_t", _c.c_int64), ("x_stride_h", _c.c_int64),
+                ("norm", _c.c_int), ("eps", _c.c_float), ("weight", _P), ("bias", _P), ("cos", _P), ("sin", _P),
+                ("rope_off", _c.c_int32), ("rope_dim", _c.c_int32), ("interleaved", _c.c_int32),
+                ("max_pos", _c.c_int32), ("positions", _P), ("pos0", _c.c_int64)]
+
+
+class LatentCache(_c.Structure):
+    _fields_ = [("n_pages", _c.c_int32), ("page_size", _c.c_int32), ("table_ld", _c.c_int32), ("codes", _P),
+                ("scales", _P), ("rope", _P), ("block_table", _P)]
+
+
+class LatentAppendArgs(_c.Structure):
+    _fields_ = [("B", _c.c_int32), ("n", _c.c_int32), ("x", _P), ("x_stride_b", _c.c_int64),
+                ("x_stride_t", _c.c_int64), ("weight", _P), ("eps", _c.c_float), ("cos", _P), ("sin", _P),
+                ("interleaved", _c.c_int32), ("max_pos", _c.c_int32), ("positions", _P), ("pos0", _c.c_int64)]
+
+
+class LatentAttnArgs(_c.Structure):
+    _fields_ = [("B", _c.c_int32), ("T", _c.c_int32), ("S", _c.c_int32), ("H", _c.c_int32), ("scale", _c.c_float),
+                ("q", _P), ("q_stride_b", _c.c_int64), ("q_stride_t", _c.c_int64), ("cache", LatentCache),
+                ("idx_T", _c.c_int32), ("flags", _P)]
 
 
 class DsaError(RuntimeError):
@@ -143,6 +176,22 @@ def load_library(path: str = LIB_PATH):
             lib.dsa_quantize_e4m3_append.restype = S
             lib.dsa_quantize_e4m3_append.argtypes = [_P, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int64, _P, _P,
                                                      _c.c_int32, _c.c_int64, _P, _P, _c.c_size_t, _P]
+            lib.dsa_norm_rope.restype = S
+            lib.dsa_norm_rope.argtypes = [_c.POINTER(NormRopeArgs), _P, _c.c_int64, _c.c_int64, _c.c_int64, _P,
+                                          _c.c_size_t, _P]
+            lib.dsa_norm_rope_e4m3.restype = S
+            lib.dsa_norm_rope_e4m3.argtypes = [_c.POINTER(NormRopeArgs), _P, _P, _c.c_int32, _c.c_int32, _P,
+                                               _c.c_size_t, _P]
+            lib.dsa_latent_append.restype = S
+            lib.dsa_latent_append.argtypes = [_c.POINTER(LatentAppendArgs), _c.POINTER(LatentCache), _P, _c.c_size_t,
+                                              _P]
+            lib.dsa_latent_read.restype = S
+            lib.dsa_latent_read.argtypes = [_c.POINTER(LatentCache), _c.c_int32, _c.c_int32, _P, _c.c_int64, _P, _P,
+                                            _c.c_size_t, _P]
+            lib.dsa_latent_attn.restype = S
+            lib.dsa_latent_attn.argtypes = [_c.POINTER(LatentAttnArgs), _P, _c.c_int32, _P, _P, _P, _c.c_size_t, _P]
+            lib.dsa_latent_attn_workspace_size.restype = _c.c_size_t
+            lib.dsa_latent_attn_workspace_size.argtypes = [_c.POINTER(LatentAttnArgs), _c.c_int32]
             lib.dsa_read_device_flags.restype = S
             lib.dsa_read_device_flags.argtypes = [_P, _c.POINTER(_c.c_uint32), _P]
             lib.dsa_status_string.restype = _c.c_char_p
@@ -198,6 +247,34 @@ def workspace(nbytes: int = WS_MIN, device=None) -> torch.Tensor:
 
 def release_workspace():
     _ws.clear()
+
+
+_flags = {}
+
+
+def _flag_word(dev) -> torch.Tensor:
+    """The device's flag workspace (WS_MIN zeroed bytes): allocated once and kept, so a captured
+    graph may hold its address.  Calls that use it allocate their scratch themselves."""
+    t = _flags.get(dev)
+    if t is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the first call on a device allocates its flag word: make it before a stream capture")
+        with _lock:
+            t = _flags.get(dev)
+            if t is None:
+                t = torch.zeros(WS_MIN, dtype=torch.uint8, device=dev)
+                torch.cuda.current_stream(dev).synchronize()  # other streams may use it at once
+                _flags[dev] = t
+    return t
+
+
+def _launch(dev, fn, *args) -> None:
+    """fn(*args, stream) on `dev`'s current stream, with `dev` current."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
 
 
 # --- struct builders ----------------------------------------------------------------
@@ -488,6 +565,187 @@ def dsa_quantize_e4m3_append(x: torch.Tensor, codes: torch.Tensor, scales: torch
     return codes, scales
 
 
+def _addr(t, dev, dtype, what: str, n: int | None = None):
+    """Device address of an optional dense operand, checked against `dev`, dtype and size."""
+    if t is None:
+        return None
+    assert t.device == dev and t.dtype == dtype and t.is_contiguous(), f"{what}: a dense {dtype} tensor on {dev} is expected"
+    assert n is None or t.numel() == n, f"{what}: {n} values are expected"
+    return t.data_ptr()
+
+
+def _tables(cos, sin, dev):
+    """(cos address, sin address, positions, angles per position) of a pair of rotation tables."""
+    if cos is None and sin is None:
+        return None, None, 0, 0
+    assert cos is not None and sin is not None and cos.shape == sin.shape and cos.dim() == 2, "cos and sin go together, [positions, angles]"
+    return _addr(cos, dev, torch.float32, "cos"), _addr(sin, dev, torch.float32, "sin"), cos.shape[0], cos.shape[1]
+
+
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _head_strides(t):
+    """Strides of a [B,n,H,d] tensor with a dense last axis (0 along an axis of size 1)."""
+    assert t.dim() == 4 and (t.shape[3] == 1 or t.stride(3) == 1), "[B, n, H, d] with dense heads is expected"
+    return _stride(t, 0), _stride(t, 1), _stride(t, 2)
+
+
+def _norm_rope_struct(x, norm, weight, bias, eps, cos, sin, rope_off, interleaved, pos0, positions):
+    dev = x.device
+    assert x.is_cuda and x.dtype == torch.bfloat16, "x: a bf16 CUDA tensor is expected"
+    sb, st, sh = _head_strides(x)
+    B, n, H, d = x.shape
+    c, s, rows, angles = _tables(cos, sin, dev)
+    return NormRopeArgs(B, n, H, d, x.data_ptr(), sb, st, sh, _NORMS[norm], eps,
+                        _addr(weight, dev, torch.float32, "weight", d), _addr(bias, dev, torch.float32, "bias", d), c, s,
+                        rope_off, 2 * angles, interleaved, rows, _addr(positions, dev, torch.int64, "positions", B * n), pos0)
+
+
+def dsa_norm_rope(x: torch.Tensor, *, norm: str = "none", weight: torch.Tensor | None = None,
+                  bias: torch.Tensor | None = None, eps: float = 1e-6, cos: torch.Tensor | None = None,
+                  sin: torch.Tensor | None = None, rope_off: int = 0, interleaved: bool = False, pos0: int = 0,
+                  positions: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Per-head norm ("none", "rms" or "layer") of x [B,n,H,d] bf16, then the rotation of the
+    2 * cos.shape[1] values from rope_off on by row `position` of cos / sin [max_pos, angles] fp32;
+    bf16 out (new, or `out`, strided like x or otherwise; out may be x).  positions: int64 [B,n]
+    (-1: padding, left as it was), or token i at pos0 + i."""
+    a = _norm_rope_struct(x, norm, weight, bias, eps, cos, sin, rope_off, interleaved, pos0, positions)
+    dev = x.device
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+    assert out.shape == x.shape and out.dtype == torch.bfloat16 and out.device == dev
+    if a.n:
+        ws = _flag_word(dev)
+        _launch(dev, load_library().dsa_norm_rope, _c.byref(a), out.data_ptr(), *_head_strides(out), ws.data_ptr(), WS_MIN)
+    return out
+
+
+def dsa_norm_rope_e4m3(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, norm: str = "none",
+                       weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, eps: float = 1e-6,
+                       cos: torch.Tensor | None = None, sin: torch.Tensor | None = None, rope_off: int = 0,
+                       interleaved: bool = False, pos0: int = 0, positions: torch.Tensor | None = None,
+                       at_position: bool = False):
+    """dsa_norm_rope quantised to codes [B,S_cap,H*d] (uint8 or float8_e4m3fn) with one scale per
+    token in scales [B,S_cap]: token i in row i, or with at_position in its position's row."""
+    a = _norm_rope_struct(x, norm, weight, bias, eps, cos, sin, rope_off, interleaved, pos0, positions)
+    dev = x.device
+    assert codes.dtype in (torch.uint8, torch.float8_e4m3fn) and codes.is_contiguous() and codes.device == dev
+    assert codes.shape[0] == a.B and codes.shape[2] == a.H * a.d and scales.shape == codes.shape[:2]
+    sp = _addr(scales, dev, torch.float32, "scales")
+    if a.n:
+        ws = _flag_word(dev)
+        _launch(dev, load_library().dsa_norm_rope_e4m3, _c.byref(a), codes.data_ptr(), sp, codes.shape[1], at_position,
+                ws.data_ptr(), WS_MIN)
+    return codes, scales
+
+
+def latent_cache_struct(cache: dict, B: int | None = None):
+    """(C struct, sequences) of a latent cache dict."""
+    codes, scales, rope, table = cache["codes"], cache["scales"], cache["rope"], cache.get("block_table")
+    dev = codes.device
+    pages, page = scales.shape
+    assert codes.is_cuda and codes.dtype in (torch.float8_e4m3fn, torch.uint8) and codes.is_contiguous()
+    assert codes.shape == (pages, page, 512) and rope.shape == (pages, page, 64)
+    seqs = pages if table is None else table.shape[0]
+    assert B is None or (B <= seqs if table is None else B == seqs), "the cache's sequences and the call's differ"
+    return LatentCache(pages, page, 0 if table is None else table.shape[1], codes.data_ptr(),
+                       _addr(scales, dev, torch.float32, "scales"), _addr(rope, dev, torch.bfloat16, "rope"),
+                       _addr(table, dev, torch.int32, "block_table")), seqs
+
+
+def dsa_latent_append(x: torch.Tensor, cache: dict, *, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                      cos: torch.Tensor | None = None, sin: torch.Tensor | None = None, interleaved: bool = False,
+                      pos0: int = 0, positions: torch.Tensor | None = None) -> dict:
+    """Append x [B,n,576] bf16 to the paged FP8 cache: RMS norm of the 512 latent values (weight
+    [512] fp32; None: taken as they are), rotation of the 64 others (cos / sin [max_pos, 32]; None:
+    not rotated), e4m3 with one scale per row.  positions: int64 [B,n] (-1: padding), or pos0 + i."""
+    dev = x.device
+    assert x.is_cuda and x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[2] == 576 and x.stride(2) == 1
+    B, n = x.shape[:2]
+    lc, _ = latent_cache_struct(cache, B)
+    assert cache["codes"].device == dev
+    c, s, rows, angles = _tables(cos, sin, dev)
+    assert c is None or angles == 32, "cos and sin: 32 angles for the 64 rope values"
+    a = LatentAppendArgs(B, n, x.data_ptr(), _stride(x, 0), _stride(x, 1), _addr(weight, dev, torch.float32, "weight", 512),
+                         eps, c, s, interleaved, rows, _addr(positions, dev, torch.int64, "positions", B * n), pos0)
+    if n:
+        ws = _flag_word(dev)
+        _launch(dev, load_library().dsa_latent_append, _c.byref(a), _c.byref(lc), ws.data_ptr(), WS_MIN)
+    return cache
+
+
+def dsa_latent_read(cache: dict, idx: torch.Tensor | None = None, *, n: int | None = None, pos0: int = 0,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows of the paged FP8 cache as bf16 [B,n,576]: positions idx [B,n] int32 (-1: zeros), or
+    pos0 .. pos0 + n - 1 of every sequence."""
+    dev = cache["codes"].device
+    lc, B = latent_cache_struct(cache)
+    assert (idx is None) != (n is None), "either idx or n"
+    ip = None
+    if idx is not None:
+        assert idx.dim() == 2 and idx.shape[0] <= B and (cache.get("block_table") is None or idx.shape[0] == B)
+        B, n = idx.shape
+        ip = _addr(idx, dev, torch.int32, "idx")
+    if out is None:
+        out = torch.empty((B, n, 576), dtype=torch.bfloat16, device=dev)
+    assert out.shape == (B, n, 576)
+    op = _addr(out, dev, torch.bfloat16, "out")
+    if n:
+        ws = _flag_word(dev)
+        _launch(dev, load_library().dsa_latent_read, _c.byref(lc), B, n, ip, pos0, op, ws.data_ptr(), WS_MIN)
+    return out
+
+
+def latent_attn_struct(at: dict, idx: torch.Tensor) -> LatentAttnArgs:
+    """The C struct of a latent attention operand dict: q [B,T,H,576] bf16 (strided along its batch
+    and token axes), cache, scale and S (the positions idx may name; None: all a sequence holds)."""
+    q, cache = at["q"], at["cache"]
+    B, T, H, d = q.shape
+    dev = q.device
+    assert q.is_cuda and q.dtype == torch.bfloat16 and d == 576 and q.stride(3) == 1
+    assert H == 1 or q.stride(2) == 576, "the heads of one query must be contiguous"
+    lc, _ = latent_cache_struct(cache, B)
+    assert cache["codes"].device == dev
+    assert idx.dim() == 3 and idx.shape[0] == B and idx.shape[1] in (1, T), "idx: [B, T or 1, k]"
+    S = at.get("S")
+    if S is None:
+        S = min((lc.table_ld if lc.block_table else 1) * lc.page_size, 2 ** 31 - 1)
+    return LatentAttnArgs(B, T, int(S), H, at["scale"], q.data_ptr(), _stride(q, 0), _stride(q, 1), lc, idx.shape[1], None)
+
+
+def dsa_latent_attn(at: dict, idx: torch.Tensor, out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = True,
+                    ws: torch.Tensor | None = None):
+    """Sparse attention over the rows idx [B,T,k] (or [B,1,k], shared by a sequence's T queries) of
+    a paged FP8 latent cache: (out [B,T,H,512] bf16, lse [B,T,H] fp32 or None).  `ws`: a workspace
+    to use (uint8, zero-filled once) instead of scratch allocated by the call."""
+    lib = load_library()
+    a = latent_attn_struct(at, idx)
+    dev = at["q"].device
+    ip = _addr(idx, dev, torch.int32, "idx")
+    k = idx.shape[2]
+    if out is None:
+        out = torch.empty((a.B, a.T, a.H, 512), dtype=torch.bfloat16, device=dev)
+    assert out.shape == (a.B, a.T, a.H, 512)
+    op = _addr(out, dev, torch.bfloat16, "out")
+    if lse is True:
+        lse = torch.empty((a.B, a.T, a.H), dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    lp = _addr(lse, dev, torch.float32, "lse", a.B * a.T * a.H)
+    if ws is None:
+        # scratch from the caching allocator, private to this call on its stream (and to its graph,
+        # when one is being captured); the flag word is the device's
+        ws = flags = _flag_word(dev)
+        need = int(lib.dsa_latent_attn_workspace_size(_c.byref(a), k))
+        if need > WS_MIN:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        a.flags = flags.data_ptr()
+    assert ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous()
+    _launch(dev, lib.dsa_latent_attn, _c.byref(a), ip, k, op, lp, ws.data_ptr(), ws.numel())
+    return out, lse
+
+
 def set_wait_limit(cycles: int) -> None:
     """Bound every wait inside the library's kernels launched from now on to `cycles` SM clock
     cycles (0: the default, about one second) -- dsa_set_wait_limit, for testing the timeout
@@ -511,7 +769,7 @@ def launch_count() -> int:
     return int(load_library().dsa_launch_count())
 
 
-TRACE_KINDS = {1: "indexer", 2: "topk", 3: "attention", 4: "overlap"}
+TRACE_KINDS = {1: "indexer", 2: "topk", 3: "attention", 4: "overlap", 5: "cache"}
 
 
 def trace_enable(max_launches: int = 4096) -> None:
@@ -537,18 +795,25 @@ def trace_disable() -> None:
 
 
 def read_device_flags(device=None) -> int:
-    """Flag word of the cached workspace (cleared by the read).  Synchronises."""
+    """Flag words of the cached workspace and of the calls that take none from it (cleared by the
+    read).  Synchronises."""
     lib = load_library()
     ws = workspace(WS_MIN, device)
     v = _c.c_uint32()
     _check(lib.dsa_read_device_flags(_ptr(ws), _c.byref(v), _stream()))
-    return int(v.value)
+    found = int(v.value)
+    if ws.device in _flags:
+        _check(lib.dsa_read_device_flags(_ptr(_flags[ws.device]), _c.byref(v), _stream()))
+        found |= int(v.value)
+    return found
 
 
 __all__ = [
     "indexer_scores", "dsa_topk", "dsa_sparse_attn", "indexshare_group_forward", "topk_overlap",
     "topk_overlap_matrix", "indexshare_schedule_score", "indexshare_schedule_search",
     "dsa_quantize_e4m3_append", "indexshare_group_forward_varlen", "Varlen",
+    "dsa_norm_rope", "dsa_norm_rope_e4m3", "dsa_latent_append", "dsa_latent_read", "dsa_latent_attn",
+    "NormRopeArgs", "LatentCache", "LatentAppendArgs", "LatentAttnArgs",
     "read_device_flags", "workspace", "workspace_size", "topk_workspace_size", "attn_workspace_size",
     "set_wait_limit", "load_library", "DsaError",
     "IndexerArgs", "AttnArgs", "TopkSrc", "Layer",

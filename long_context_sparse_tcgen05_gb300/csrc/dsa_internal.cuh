@@ -23,7 +23,7 @@ long long wait_limit();
 
 // Launch tracing (dsa_trace_enable): when on, a scope brackets one launcher's kernels with
 // CUDA events on its stream; durations are read back by dsa_trace_read.
-enum TraceKind { kTraceIndexer = 1, kTraceTopk = 2, kTraceAttention = 3, kTraceOverlap = 4 };
+enum TraceKind { kTraceIndexer = 1, kTraceTopk = 2, kTraceAttention = 3, kTraceOverlap = 4, kTraceCache = 5 };
 int trace_open(int kind, cudaStream_t st);
 void trace_close(int slot, cudaStream_t st);
 struct TraceScope {
@@ -228,5 +228,87 @@ struct QuantLaunch {
   uint32_t* flags;
 };
 cudaError_t launch_quant_e4m3_rows(const QuantLaunch& p, cudaStream_t st);
+
+int device_sm_count();  // SMs of the current device
+
+// Per-head norm and rotation: x [B, n, H, d] bf16 (strides in elements) to out (same form), or,
+// with out NULL, to codes / scales.  Positions in [0, limit) have a table row and a cache row
+// (limit 0: positions only mark padding).
+struct NormRopeLaunch {
+  int B, n, H, d;
+  const uint16_t* x;
+  int64_t x_sb, x_st, x_sh;
+  int norm;
+  float eps;
+  const float* weight;
+  const float* bias;
+  const float* cos;
+  const float* sin;
+  int rope_off, rope_dim, interleaved;
+  int64_t limit;
+  const int64_t* positions;
+  int64_t pos0;
+  uint16_t* out;
+  int64_t o_sb, o_st, o_sh;
+  uint8_t* codes;
+  float* scales;
+  int S_cap, at_position;
+  uint32_t* flags;
+};
+int norm_rope_group(int d);  // lanes that hold one head
+cudaError_t launch_norm_rope(const NormRopeLaunch& p, cudaStream_t st);
+
+// Paged FP8 latent cache (dsa_latent_cache), checked and with its capacity per sequence.
+constexpr int kLatentDim = 512, kLatentRope = 64;
+struct LatentCacheView {
+  uint8_t* codes;
+  float* scales;
+  uint16_t* rope;
+  const int32_t* table;
+  int table_ld, page_size, n_pages;
+  int64_t cap;  // positions per sequence, at most INT32_MAX
+};
+
+struct LatentAppendLaunch {
+  int B, n;
+  const uint16_t* x;
+  int64_t x_sb, x_st;
+  const float* weight;
+  float eps;
+  const float* cos;
+  const float* sin;
+  int interleaved;
+  int64_t max_pos;
+  const int64_t* positions;
+  int64_t pos0;
+  LatentCacheView cache;
+  uint32_t* flags;
+};
+cudaError_t launch_latent_append(const LatentAppendLaunch& p, cudaStream_t st);
+
+struct LatentReadLaunch {
+  int B, n;
+  const int32_t* idx;
+  int64_t pos0;
+  LatentCacheView cache;
+  uint16_t* out;
+  uint32_t* flags;
+};
+cudaError_t launch_latent_read(const LatentReadLaunch& p, cudaStream_t st);
+
+struct LatentAttnLaunch {
+  int B, T, S, H;
+  float scale;
+  const uint16_t* q;
+  int64_t q_sb, q_st;
+  LatentCacheView cache;
+  const int32_t* idx;   // row (b, t) at idx + b*idx_sb + t*idx_st
+  int64_t idx_sb, idx_st;
+  int kk;
+  uint16_t* out;
+  float* lse;
+  uint32_t* flags;
+};
+cudaError_t launch_latent_attn(const LatentAttnLaunch& p, cudaStream_t st);
 
 }  // namespace dsa
