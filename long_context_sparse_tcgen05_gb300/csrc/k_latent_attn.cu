@@ -1,118 +1,792 @@
-// Sparse attention over selected rows of the paged FP8 latent cache.
+// Sparse attention over selected rows of the paged FP8 latent cache, on tcgen05 tensor cores that
+// read the e4m3 codes as they are stored.
 //
-// One CTA per (query, eight heads): a warp holds a head.  Blocks of 32 selected rows are
-// dequantised into shared memory; each lane forms its head's score with one row, the warp takes
-// the block's maximum and sum (running maximum, fp32), and each thread accumulates two of the 512
-// value columns for the eight heads.
+// A cache row j stands for s_j [c_j | r_j]: 512 e4m3 codes and 64 bf16 rope values under one fp32
+// scale.  For a head with query q, in base-2 units (a = softmax scale * log2 e):
+//   x_j = a s_j (q_c . c_j + q_r . r_j),   O = sum_j 2^x_j s_j c_j / sum_j 2^x_j.
+// Both products take the codes as FP8 operands, so no row is dequantised; the other operand is
+// made of two FP8 terms that together keep bf16's precision:
+//   * q: a power of two 2^k per head brings its largest value to [128, 256); then
+//     q 2^k = hi + lo / 16 with hi = e4m3(q 2^k) and lo = e4m3(16 (q 2^k - hi)).  A bf16 value has 8
+//     significant bits, hi takes 4 and lo the other 4: exact down to 2^-21 of the head's largest.
+//     The rope part stays bf16 (times 2^k, exact).  S has a hi and a lo row per head (M = 128 for
+//     64 heads): hi . c + r . r and lo . c, added by the softmax.
+//   * the weights: y_j = x_j + log2 s_j, p_j = 2^(y_j - M) <= 256 carries the row's scale, and
+//     p_j = hi + lo in e4m3 (each rounded to nearest): relative error 2^-8, and at most 2^-10
+//     absolute where p_j is small, 2^-14 of the largest, since M keeps the largest p in [16, 256].
+//     Both terms accumulate into the same O.  Row sums take p_j / s_j in fp32.
+// FP8 products accumulate exactly enough in fp32 (sums of 2,048 products of mixed size came out
+// equal to the 64-bit sum).
+//
+// Persistent CTAs, one per SM, walk items (query, group of 64 heads, part of the row's blocks of 64
+// keys).  22 warps:
+//   0-3    gather: resolve positions through the block table a block ahead and copy the selected
+//          rows (16-byte cp.async) into three stages of 40 KB, five 128-byte-swizzled atoms each;
+//          leave the rows' scales beside them
+//   4      S (hi and lo rows, 128 x 64) = Q K^T: A is Q in tensor memory, so the product reads only
+//          the codes from shared memory; 16 FP8 steps and 4 bf16 steps for the rope part
+//   5      O^T (512 x 64) += V^T P^T: four chunks of 128 dims, 2 key steps, hi and lo
+//   6-13   softmax: a warp holds 8 heads whole (their hi and lo rows lie in one 16-lane half of a
+//          lane quarter), so maxima and sums never leave a quad of lanes and no barrier joins warps
+//   14-17  rescale O^T when a reference maximum rises (only the heads concerned), and at the end
+//          normalise and store, while the softmax already runs the next item
+//   18-21  convert the next item's queries while the present one runs, and put them into tensor
+//          memory when its last score product is done
+// With fewer items than half the SMs each is split into parts of at least 128 keys; parts are
+// joined by k_latent_combine.  Waits are bounded (DSA_FLAG_TIMEOUT).
 #include <cuda_bf16.h>
 
 #include "dsa_internal.cuh"
 #include "latent_cache.cuh"
+#include "sm100.cuh"
 
 namespace dsa {
 namespace {
+using namespace sm100;
 
-constexpr int kThreads = 256, kHeads = 8, kKeys = 32, kD = kLatentDim + kLatentRope;
-constexpr int kLd = kD + 1;  // row pitch in floats: lanes reading one column of 32 rows hit 32 banks
-constexpr size_t kSmem = (size_t)(kKeys * kLd + kHeads * kD + kHeads * kKeys + 2 * kHeads) * 4;
+constexpr int kHg = 64;                      // heads of an item
+constexpr int kNB = 64;                      // keys of a block
+constexpr int kStages = 3;
+constexpr int kD = kLatentDim + kLatentRope;
+constexpr uint32_t kAtom = kNB * 128;        // 64 rows of 128 bytes
+constexpr uint32_t kStage = 5 * kAtom;       // four atoms of codes, one of rope values
+constexpr uint32_t kPBytes = kHg * 128;      // P: per head 64 hi bytes, then 64 lo bytes
+constexpr int kQVec = 40;                    // 16-byte words of a converted query row (512 + 128 bytes)
+constexpr uint32_t kQBytes = kQVec * 128 * 16;
+constexpr int kGatherWarps = 4, kSWarp = 4, kPvWarp = 5, kSmWarp0 = 6, kSmWarps = 8, kOWarp0 = 14, kQWarp0 = 18;
+constexpr int kThreads = 22 * 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColS = 448;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kTop = 8.f, kAim = 4.f;      // raise M when y exceeds it by 8; the new largest p is 2^4
+constexpr int kInfoReaders = 2 + kSmWarps + 4 + 4;
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+struct Bars {
+  uint64_t q_full, q_empty, qs_full[2];
+  uint64_t kv_full[kStages], kv_empty[kStages], sc_full[kStages];
+  uint64_t s_full, s_empty;
+  uint64_t p_full[2], p_empty[2];
+  uint64_t o_full, o_empty, cmd_full, corr_done;
+  uint64_t l_full[2], l_empty[2];
+  uint64_t info_full[2], info_empty[2];
+  uint64_t drain[2];
+};
+struct Small {
+  alignas(16) float2 sc[kStages][kNB];   // {scale, log2 scale} of a stage's rows; {0, -inf}: skipped
+  alignas(16) float isc[kStages][kNB];   // 1 / scale (0: skipped)
+  alignas(16) int valid[kStages][4];     // by gather warp: some row of the block counts
+  alignas(16) float alpha[2][kHg];       // by block parity: factor of O where `need` is set
+  alignas(16) float lsum[2][kHg];        // reciprocal row sums, by item parity
+  float qs[2][kHg];                      // 2^-k of the item's heads
+  alignas(8) uint8_t need[2][8];         // by block parity and group of 8 heads: O must be rescaled
+  Bars bar;
+  uint32_t tmem;
+  int abort;
+  int nb[2];                             // blocks of the item, by item parity
+  int cmd;                               // to the O warps: rescale before block cmd, or -1: store
+};
+constexpr size_t kSmem = 1024 + kStages * kStage + 2 * kPBytes + kQBytes + sizeof(Small);
+static_assert(kSmem <= 232448, "shared memory of one CTA");
 
-__global__ void __launch_bounds__(kThreads) k_latent_attn(LatentAttnLaunch p) {
-  extern __shared__ float sm[];
-  float* rows = sm;                     // [kKeys][kLd]
-  float* q = rows + kKeys * kLd;        // [kHeads][kD]
-  float* prob = q + kHeads * kD;        // [kHeads][kKeys]
-  float* alpha = prob + kHeads * kKeys; // [kHeads]
-  float* rsum = alpha + kHeads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  const int b = (int)(blockIdx.x / p.T), t = (int)(blockIdx.x % p.T), h0 = blockIdx.y * kHeads;
-  const int32_t* idx = p.idx + b * p.idx_sb + t * p.idx_st;
-  const uint16_t* qg = p.q + b * p.q_sb + t * p.q_st;
-  for (int i = tid; i < kHeads * kD; i += kThreads) q[i] = h0 + i / kD < p.H ? bf(qg[(int64_t)h0 * kD + i]) : 0.f;
-  float m = -INFINITY, l = 0.f;
-  float acc[kHeads][2] = {};
-  for (int j0 = 0; j0 < p.kk; j0 += kKeys) {
-    __syncthreads();
-    uint32_t valid = 0;
-    {
-      const int e = j0 + lane;
-      const int id = e < p.kk ? idx[e] : -1;
-      const int64_t row = id >= 0 && id < p.S ? latent_row(p.cache, b, id) : -1;
-      if (row < 0 && id != -1 && warp == 0) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
-      valid = __ballot_sync(0xffffffffu, row >= 0);
-      for (int r = warp; r < kKeys; r += kThreads / 32) {
-        const int64_t rr = __shfl_sync(0xffffffffu, row, r);
-        float* dst = rows + r * kLd;
-        if (rr < 0) {
-          for (int c = lane; c < kD; c += 32) dst[c] = 0.f;
-          continue;
+__device__ __forceinline__ void mma_fp8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// 16 lanes x 64 columns: thread t receives, for j < 8, lane t/4 at columns 8j + 2(t%4) + {0, 1}
+// (r[4j], r[4j + 1]) and lane t/4 + 8 at the same columns (r[4j + 2], r[4j + 3]).
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// two floats as f16 (a in the low half), f16 pair to e4m3 pair (nearest, saturating) and back
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(h) : "f"(b), "f"(a));
+  return h;
+}
+__device__ __forceinline__ uint16_t e4m3_of_f16x2(uint32_t h) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(c) : "r"(h));
+  return c;
+}
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint16_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"(c));
+  return h;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// An item: head group and part of query row (b, t).
+struct Item {
+  int row, b, t, h0, heads, split;
+};
+__device__ __forceinline__ Item item_of(const LatentAttnLaunch& p, int item) {
+  Item r;
+  const int lrow = item / p.splits;
+  r.split = item - lrow * p.splits;
+  r.row = lrow / p.groups;
+  r.h0 = (lrow - r.row * p.groups) * kHg;
+  r.heads = min(kHg, p.H - r.h0);
+  r.b = r.row / p.T;
+  r.t = r.row - r.b * p.T;
+  return r;
+}
+
+template <bool kPoll>
+__global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* kv_s = base;
+  uint8_t* p_s = kv_s + kStages * kStage;
+  uint8_t* q_s = p_s + 2 * kPBytes;
+  Small* sm = reinterpret_cast<Small*>(q_s + kQBytes);
+  Bars& bar = sm->bar;
+  volatile int* abort_flag = &sm->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int items = p.B * p.T * p.groups * p.splits;
+  const int G = (int)gridDim.x;
+  // a wait that every lane of a warp makes, with one answer for the warp
+  auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait<kPoll>(b, parity, abort_flag, p.wait));
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bar.q_full, 4);
+    mbar_init(&bar.q_empty, 1);
+    mbar_init(&bar.s_full, 1);
+    mbar_init(&bar.s_empty, kSmWarps);
+    mbar_init(&bar.o_full, 1);
+    mbar_init(&bar.o_empty, 4);
+    mbar_init(&bar.cmd_full, 1);
+    mbar_init(&bar.corr_done, 4);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar.kv_full[i], kGatherWarps * 32);
+      mbar_init(&bar.kv_empty[i], 1);
+      mbar_init(&bar.sc_full[i], kGatherWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.qs_full[i], 4);
+      mbar_init(&bar.p_full[i], kSmWarps);
+      mbar_init(&bar.p_empty[i], 1);
+      mbar_init(&bar.l_full[i], kSmWarps);
+      mbar_init(&bar.l_empty[i], 4);
+      mbar_init(&bar.info_full[i], 1);
+      mbar_init(&bar.info_empty[i], kInfoReaders);
+      mbar_init(&bar.drain[i], 1);
+    }
+    sm->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kSWarp) {
+    tmem_alloc(&sm->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
+
+  if (warp < kGatherWarps) {
+    // ================= gather =================
+    int it = 0;
+    uint32_t g = 0;  // blocks so far
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+      const Item I = item_of(p, item);
+      const int32_t* irow = p.idx + I.b * p.idx_sb + I.t * p.idx_st;
+      // blocks of the row = 1 + (last entry other than -1) / 64, searched from the end
+      int last = -1;
+      for (int e0 = p.kk - 1; e0 >= 0 && last < 0; e0 -= 32 * 8) {
+        int v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int e = e0 - u * 32 - lane;
+          v[u] = e >= 0 ? __ldg(irow + e) : -1;
         }
-        const float s = p.cache.scales[rr];
-        for (int c = lane; c < kLatentDim / 2; c += 32) {
-          const float2 f = e4m3x2_to_float2(reinterpret_cast<const uint16_t*>(p.cache.codes + rr * kLatentDim)[c]);
-          dst[2 * c] = f.x * s;
-          dst[2 * c + 1] = f.y * s;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t bal = __ballot_sync(0xffffffffu, v[u] != -1);
+          if (last < 0 && bal) last = e0 - u * 32 - (__ffs(bal) - 1);
         }
-        for (int c = lane; c < kLatentRope; c += 32) dst[kLatentDim + c] = bf(p.cache.rope[rr * kLatentRope + c]) * s;
+      }
+      const int nbr = (last + kNB) / kNB;
+      const int j0 = (int)((int64_t)I.split * nbr / p.splits);
+      const int nb = (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0;
+      if (warp == 0) {
+        ok = wait(&bar.info_empty[it & 1], ((it >> 1) & 1) ^ 1);
+        if (ok && lane == 0) {
+          sm->nb[it & 1] = nb;
+          mbar_arrive(&bar.info_full[it & 1]);
+        }
+      }
+      if (!ok || __any_sync(0xffffffffu, *abort_flag)) break;
+      if (nb == 0) continue;
+      const int rl = warp * 16 + (lane & 15);  // this lane's row of a block (lanes 16-31 repeat)
+      auto load_id = [&](int j) {
+        const int e = (j0 + j) * kNB + rl;
+        return j < nb && e < p.kk ? __ldg(irow + e) : -1;
+      };
+      auto resolve = [&](int id) -> int64_t {
+        if (id == -1) return -1;
+        const int64_t r = id >= 0 && id < p.S ? latent_row(p.cache, I.b, id) : -1;
+        if (r < 0 && lane < 16) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
+        return r;
+      };
+      // ids two blocks ahead, cache rows and scales one ahead
+      int id_n = load_id(1);
+      int64_t row = resolve(load_id(0));
+      float scale = row >= 0 ? __ldg(p.cache.scales + row) : 0.f;
+      for (int j = 0; j < nb; ++j, ++g) {
+        const int st = (int)(g % kStages);
+        const int id_nn = load_id(j + 2);
+        const int64_t row_n = resolve(id_n);
+        if (!(ok = wait(&bar.kv_empty[st], ((g / kStages) & 1) ^ 1))) break;
+        const int cc = lane & 7;
+        uint8_t* stage = kv_s + st * kStage;
+#pragma unroll
+        for (int pass = 0; pass < 4; ++pass) {
+          const int src_lane = pass * 4 + (lane >> 3);
+          const int64_t rr = __shfl_sync(0xffffffffu, row, src_lane);
+          const int r = warp * 16 + src_lane;
+          const uint32_t n = rr >= 0 ? 16 : 0;  // a skipped row is filled with zeros
+          const int64_t rs = rr >= 0 ? rr : 0;
+          const uint8_t* src = p.cache.codes + rs * kLatentDim + cc * 16;
+          const uint8_t* srr = reinterpret_cast<const uint8_t*>(p.cache.rope + rs * kLatentRope) + cc * 16;
+          const uint32_t dst = smem_addr(stage + r * 128 + ((cc ^ (r & 7)) << 4));
+#pragma unroll
+          for (int a = 0; a < 5; ++a)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst + a * kAtom),
+                         "l"(a < 4 ? src + a * 128 : srr), "r"(n)
+                         : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_addr(&bar.kv_full[st])) : "memory");
+        const uint32_t some = __ballot_sync(0xffffffffu, row >= 0);
+        if (lane < 16) {
+          sm->sc[st][rl] = row >= 0 ? make_float2(scale, log2f(scale)) : make_float2(0.f, -INFINITY);
+          sm->isc[st][rl] = row >= 0 ? 1.f / scale : 0.f;
+        }
+        if (lane == 0) sm->valid[st][warp] = some != 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.sc_full[st]);
+        row = row_n;
+        id_n = id_nn;
+        scale = row >= 0 ? __ldg(p.cache.scales + row) : 0.f;
       }
     }
-    __syncthreads();
-    if (valid == 0) continue;  // the same in every warp
-    float s = 0.f;
-    for (int c = 0; c < kD; ++c) s += q[warp * kD + c] * rows[lane * kLd + c];
-    s = (valid >> lane) & 1u ? s * p.scale : -INFINITY;
-    float mx = s;
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+  } else if (warp == kSWarp) {
+    // ================= score product (one thread) =================
+    const uint32_t id8 = idesc_mn(0, 0, 128, kNB), id16 = idesc_mn(1, 1, 128, kNB);
+    const uint64_t kv_desc = desc_sw128(smem_addr(kv_s));
+    if (lane == 0) {
+      int it = 0, oc = 0;
+      uint32_t g = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+        if (!(ok = mbar_wait<kPoll>(&bar.info_full[it & 1], (it >> 1) & 1, abort_flag, p.wait))) break;
+        const int nb = sm->nb[it & 1];
+        mbar_arrive(&bar.info_empty[it & 1]);
+        if (nb == 0) continue;
+        ok = mbar_wait<kPoll>(&bar.q_full, oc & 1, abort_flag, p.wait);
+        for (int j = 0; ok && j < nb; ++j, ++g) {
+          const int st = (int)(g % kStages);
+          ok = mbar_wait<kPoll>(&bar.s_empty, (g & 1) ^ 1, abort_flag, p.wait) &&
+               mbar_wait<kPoll>(&bar.kv_full[st], (g / kStages) & 1, abort_flag, p.wait);
+          if (!ok) break;
+          async_fence();  // the stage was written by cp.async
+          tc_fence_after();
+          const uint64_t kd = kv_desc + (uint64_t)((st * kStage) >> 4);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(m, mx);
-    const float mu = mn == -INFINITY ? 0.f : mn;
-    const float a = __expf(m - mu), pr = (valid >> lane) & 1u ? __expf(s - mu) : 0.f;
-    float sum = pr;
+          for (int k = 0; k < 16; ++k)
+            mma_fp8_ts(tmem + kColS, tmem + kColQ + 8 * k, kd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), id8, k != 0);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = l * a + sum;
-    m = mn;
-    prob[warp * kKeys + lane] = pr;
-    if (lane == 0) alpha[warp] = a;
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      acc[h][0] *= alpha[h];
-      acc[h][1] *= alpha[h];
-    }
-    for (int r = 0; r < kKeys; ++r) {
-      if (!((valid >> r) & 1u)) continue;
-      const float v0 = rows[r * kLd + tid], v1 = rows[r * kLd + tid + 256];
-#pragma unroll
-      for (int h = 0; h < kHeads; ++h) {
-        acc[h][0] += prob[h * kKeys + r] * v0;
-        acc[h][1] += prob[h * kKeys + r] * v1;
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ts(tmem + kColS, tmem + kColQR + 8 * k, kd + (uint64_t)((4 * kAtom + k * 32) >> 4), id16, 1);
+          mma_commit(&bar.s_full);
+        }
+        mma_commit(&bar.q_empty);
+        ++oc;
       }
+      mma_commit(&bar.drain[0]);  // this thread's products end before tensor memory is freed
+      mbar_wait_drain(&bar.drain[0], 0);
+    }
+  } else if (warp == kPvWarp) {
+    // ================= value product (one thread) =================
+    const uint32_t id8 = idesc_mn(0, 0, 128, kHg) | (1u << 15);  // A: 128 dims, MN-major
+    const uint64_t v_desc = desc_sw128(smem_addr(kv_s)), p_desc = desc_sw128(smem_addr(p_s));
+    if (lane == 0) {
+      int it = 0, oc = 0, corr = 0;
+      uint32_t g = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+        if (!(ok = mbar_wait<kPoll>(&bar.info_full[it & 1], (it >> 1) & 1, abort_flag, p.wait))) break;
+        const int nb = sm->nb[it & 1];
+        mbar_arrive(&bar.info_empty[it & 1]);
+        if (nb == 0) continue;
+        ok = mbar_wait<kPoll>(&bar.o_empty, (oc & 1) ^ 1, abort_flag, p.wait);
+        for (int j = 0; ok && j < nb; ++j, ++g) {
+          const int st = (int)(g % kStages), pb = (int)(g & 1);
+          ok = mbar_wait<kPoll>(&bar.p_full[pb], (g >> 1) & 1, abort_flag, p.wait) &&
+               mbar_wait<kPoll>(&bar.kv_full[st], (g / kStages) & 1, abort_flag, p.wait);
+          if (!ok) break;
+          if (j > 0 && *reinterpret_cast<const volatile uint64_t*>(sm->need[pb])) {
+            sm->cmd = (int)(g & 0x3fffffffu);
+            mbar_arrive(&bar.cmd_full);
+            if (!(ok = mbar_wait<kPoll>(&bar.corr_done, corr & 1, abort_flag, p.wait))) break;
+            ++corr;
+          }
+          async_fence();
+          tc_fence_after();
+          const uint64_t vd = v_desc + (uint64_t)((st * kStage) >> 4), pd = p_desc + (uint64_t)((pb * kPBytes) >> 4);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // keys 0-31 and 32-63 by the hi terms, then by the lo terms
+              mma_fp8(tmem + kColO + c * kHg, vd + (uint64_t)((c * kAtom + (k & 1) * 4096) >> 4),
+                      pd + (uint64_t)((k * 32) >> 4), id8, (j | k) != 0);
+          mma_commit(&bar.kv_empty[st]);
+          mma_commit(&bar.p_empty[pb]);
+        }
+        if (!ok) break;
+        mma_commit(&bar.o_full);
+        sm->cmd = -1;
+        mbar_arrive(&bar.cmd_full);
+        ++oc;
+      }
+      mma_commit(&bar.drain[1]);
+      mbar_wait_drain(&bar.drain[1], 0);
+    }
+  } else if (warp < kOWarp0) {
+    // ================= softmax =================
+    const int hgp = 2 * (warp & 3) + ((warp - kSmWarp0) >> 2);  // this warp's 8 heads
+    const int hl = hgp * 8 + (lane >> 2), m = lane & 3;         // this thread's head; keys 8j + 2m + {0, 1}
+    const uint32_t s_addr = tmem + kColS + ((uint32_t)((warp & 3) * 32 + ((warp - kSmWarp0) >> 2) * 16) << 16);
+    int it = 0, oc = 0;
+    uint32_t g = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
+      const int nb = sm->nb[it & 1];
+      float cq = 0.f;
+      if (nb) {
+        if (!(ok = wait(&bar.qs_full[oc & 1], (oc >> 1) & 1))) break;
+        cq = sm->qs[oc & 1][hl] * (p.scale * kLog2e);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+      if (nb == 0) continue;
+      float M = -INFINITY, l = 0.f;
+      int any_valid = 0;
+      for (int j = 0; j < nb; ++j, ++g) {
+        const int st = (int)(g % kStages), pb = (int)(g & 1);
+        if (!(ok = wait(&bar.s_full, g & 1))) break;
+        uint32_t r[32];
+        tc_fence_after();
+        tmem_ld_16x256b_x8(s_addr, r);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.s_empty);
+        if (!(ok = wait(&bar.sc_full[st], (g / kStages) & 1))) break;
+        const int4 vv = *reinterpret_cast<const int4*>(sm->valid[st]);
+        any_valid |= vv.x | vv.y | vv.z | vv.w;
+        float y[16], ymax = -INFINITY;
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+          const float4 s = *reinterpret_cast<const float4*>(&sm->sc[st][8 * jj + 2 * m]);
+          const float t0 = fmaf(__uint_as_float(r[4 * jj + 2]), 0.0625f, __uint_as_float(r[4 * jj]));
+          const float t1 = fmaf(__uint_as_float(r[4 * jj + 3]), 0.0625f, __uint_as_float(r[4 * jj + 1]));
+          y[2 * jj] = fmaf(t0, cq * s.x, s.y);
+          y[2 * jj + 1] = fmaf(t1, cq * s.z, s.w);
+          ymax = fmaxf(ymax, fmaxf(y[2 * jj], y[2 * jj + 1]));
+        }
+        ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 1));
+        ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 2));
+        const bool raise = ymax > M + kTop;
+        const float Mn = raise ? ymax - kAim : M;
+        const float alpha = raise ? ex2(M - Mn) : 1.f;
+        const int any = __any_sync(0xffffffffu, raise);
+        M = Mn;
+        const float Mu = M == -INFINITY ? 0.f : M;
+        l *= alpha;
+        if (!(ok = wait(&bar.p_empty[pb], ((g >> 1) & 1) ^ 1))) break;
+        const uint32_t prow = smem_addr(p_s + pb * kPBytes + hl * 128) + 2 * m;
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+          const float p0 = ex2(y[2 * jj] - Mu), p1 = ex2(y[2 * jj + 1] - Mu);
+          const float2 is = *reinterpret_cast<const float2*>(&sm->isc[st][8 * jj + 2 * m]);
+          l = fmaf(p0, is.x, l);
+          l = fmaf(p1, is.y, l);
+          const uint32_t h = f16x2(p0, p1);
+          const uint16_t hi = e4m3_of_f16x2(h);
+          const uint16_t lo = e4m3_of_f16x2(sub_f16x2(h, f16x2_of_e4m3(hi)));
+          const uint32_t at = prow + (jj & 1) * 8;
+          asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((jj >> 1) ^ (hl & 7)) << 4)), "h"(hi) : "memory");
+          asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((4 + (jj >> 1)) ^ (hl & 7)) << 4)), "h"(lo) : "memory");
+        }
+        if (any && m == 0) sm->alpha[pb][hl] = alpha;
+        if (lane == 0) sm->need[pb][hgp] = (uint8_t)(any != 0);
+        async_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[pb]);
+      }
+      if (!ok) break;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (!any_valid) l = 0.f;
+      if (!(ok = wait(&bar.l_empty[oc & 1], ((oc >> 1) & 1) ^ 1))) break;
+      if (m == 0) {
+        sm->lsum[oc & 1][hl] = l == 0.f ? 0.f : 1.f / l;
+        const Item I = item_of(p, item);
+        const float v = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+        if (p.splits > 1) p.part_lse[(int64_t)item * kHg + hl] = v;
+        else if (p.lse && hl < I.heads) p.lse[(int64_t)I.row * p.H + I.h0 + hl] = v;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.l_full[oc & 1]);
+      ++oc;
+    }
+  } else if (warp < kQWarp0) {
+    // ================= O^T: rescales and the epilogue =================
+    const int q4 = warp & 3, t = threadIdx.x - kOWarp0 * 32;
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    int it = 0, oc = 0;
+    uint32_t cmds = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
+      const int nb = sm->nb[it & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+      const Item I = item_of(p, item);
+      uint16_t* og = p.out + ((int64_t)I.row * p.H + I.h0) * kLatentDim;
+      float* po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
+      if (nb == 0) {  // nothing selected: O = 0, LSE = -inf
+        if (po) {  // the combine reads no part whose weight is 0
+          if (t < kHg) p.part_lse[(int64_t)item * kHg + t] = -INFINITY;
+        } else {
+          for (int i = t; i < I.heads * kLatentDim / 8; i += 128) reinterpret_cast<uint4*>(og)[i] = make_uint4(0, 0, 0, 0);
+          if (p.lse && t < I.heads) p.lse[(int64_t)I.row * p.H + I.h0 + t] = -INFINITY;
+        }
+        continue;
+      }
+      for (;;) {
+        if (!(ok = wait(&bar.cmd_full, cmds & 1))) break;
+        ++cmds;
+        const int cmd = *const_cast<volatile int*>(&sm->cmd);
+        if (cmd < 0) break;
+        // O^T is complete up to the block before: rescale the heads whose maximum rose
+        const uint32_t gp = (uint32_t)cmd - 1;
+        if (!(ok = wait(&bar.p_empty[gp & 1], (gp >> 1) & 1))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int w = 0; w < 8; ++w) {
+          if (!sm->need[cmd & 1][w]) continue;
+          const float4 a0 = *reinterpret_cast<const float4*>(&sm->alpha[cmd & 1][8 * w]);
+          const float4 a1 = *reinterpret_cast<const float4*>(&sm->alpha[cmd & 1][8 * w + 4]);
+          const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+          uint32_t v[4][8];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * a[i]);
+            tmem_st_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
+          }
+        }
+        tmem_wait_stores();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.corr_done);
+      }
+      if (!ok) break;
+      if (!(ok = wait(&bar.l_full[oc & 1], (oc >> 1) & 1))) break;
+      if (!(ok = wait(&bar.o_full, oc & 1))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int n = 0; n < 8; ++n) {  // slice n: dims of chunk n / 2, heads 32 (n % 2) ..
+        const int h0 = (n & 1) * 32, d = (n >> 1) * 128 + q4 * 32 + lane;
+        if (h0 >= I.heads) continue;
+        uint32_t r[32];
+        tmem_ld32(tmem + lane_base + kColO + (n >> 1) * kHg + h0, r);
+        tmem_wait_ld();
+        const float4* ls4 = reinterpret_cast<const float4*>(sm->lsum[oc & 1] + h0);
+#pragma unroll
+        for (int i4 = 0; i4 < 8; ++i4) {
+          const float4 L = ls4[i4];
+          const float lv[4] = {L.x, L.y, L.z, L.w};
+          float o[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) o[u] = lv[u] == 0.f ? 0.f : __uint_as_float(r[4 * i4 + u]) * lv[u];
+          if (po) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (h0 + 4 * i4 + u < I.heads) po[(int64_t)(h0 + 4 * i4 + u) * kLatentDim + d] = o[u];
+          } else {
+            // lane pairs write two neighbouring dims of a head as one word: of heads (i, i + 1)
+            // the even lane writes i, the odd lane i + 1
+            const bool odd = (lane & 1) != 0;
+#pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+              const float other = __shfl_xor_sync(0xffffffffu, odd ? o[u] : o[u + 1], 1);
+              const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(other, o[u + 1]) : __floats2bfloat162_rn(o[u], other);
+              const int h = h0 + 4 * i4 + u + (odd ? 1 : 0);
+              if (h < I.heads) *reinterpret_cast<__nv_bfloat162*>(og + (int64_t)h * kLatentDim + (d & ~1)) = w;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.l_empty[oc & 1]);
+        mbar_arrive(&bar.o_empty);
+      }
+      ++oc;
+    }
+  } else {
+    // ================= queries: hi and lo rows =================
+    // Lane 16 h + i (i < 8) of quarter q holds the hi row of head 16 q + 8 h + i, lane 16 h + 8 + i
+    // its lo row, so that a softmax thread's one load gives it both.
+    const int q4 = warp & 3;
+    const int hl = 16 * q4 + 8 * (lane >> 4) + (lane & 7);
+    const bool lo = (lane & 8) != 0;
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    uint4* mine = reinterpret_cast<uint4*>(q_s) + (warp - kQWarp0) * 32 + lane;  // word w at mine[128 w]
+    int it = 0, oc = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+      const Item I = item_of(p, item);
+      const uint4* q = reinterpret_cast<const uint4*>(p.q + I.b * p.q_sb + I.t * p.q_st + (int64_t)(I.h0 + hl) * kD);
+      const bool live = hl < I.heads;
+      uint32_t top = 0;  // largest magnitude, as bf16 bits (a NaN is above every number)
+#pragma unroll 1
+      for (int c0 = 0; c0 < kD / 8; c0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = live ? __ldg(q + c0 + u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          top = __vmaxu2(top, v[u].x & 0x7fff7fffu);
+          top = __vmaxu2(top, v[u].y & 0x7fff7fffu);
+          top = __vmaxu2(top, v[u].z & 0x7fff7fffu);
+          top = __vmaxu2(top, v[u].w & 0x7fff7fffu);
+        }
+      }
+      top = max(top & 0xffffu, top >> 16);
+      // the largest value's exponent e (not below -100): 2^(7 - e) brings it to [128, 256)
+      const int e = max((int)(top >> 7) - 127, -100);
+      const bool finite = (top >> 7) < 255;
+      const float mul = finite ? __uint_as_float((uint32_t)(7 - e + 127) << 23) : __uint_as_float(0x7fc00000u);
+      const uint32_t sixteen = 0x4c004c00u;  // f16 16.0 twice
+#pragma unroll 1
+      for (int c0 = 0; c0 < kLatentDim / 8; c0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = live ? __ldg(q + c0 + u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < 8; u += 2) {
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const uint4& a = v[u + (x >> 2)];
+            const uint32_t two = (x & 3) == 0 ? a.x : (x & 3) == 1 ? a.y : (x & 3) == 2 ? a.z : a.w;
+            const uint32_t h = f16x2(__uint_as_float(two << 16) * mul, __uint_as_float(two & 0xffff0000u) * mul);
+            const uint16_t hi = e4m3_of_f16x2(h);
+            const uint16_t rest = e4m3_of_f16x2(mul_f16x2(sub_f16x2(h, f16x2_of_e4m3(hi)), sixteen));
+            const uint32_t code = lo ? rest : hi;
+            if (x & 1) w[x >> 1] |= code << 16;
+            else w[x >> 1] = code;
+          }
+          mine[128 * ((c0 + u) >> 1)] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      // the lo row's rope part: 2^-40 of the hi row's, nothing beside it, so that an infinite rope
+      // value of a key gives both rows the same infinity (zeros would make it a NaN)
+      const float mul_r = lo ? mul * 0x1p-40f : mul;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint4 v = live ? __ldg(q + kLatentDim / 8 + c) : make_uint4(0, 0, 0, 0);
+        uint32_t* x = &v.x;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const __nv_bfloat162 b2 =
+              __floats2bfloat162_rn(__uint_as_float(x[u] << 16) * mul_r, __uint_as_float(x[u] & 0xffff0000u) * mul_r);
+          x[u] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
+        mine[128 * (32 + c)] = v;
+      }
+      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
+      const int nb = sm->nb[it & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+      if (nb == 0) continue;
+      if (!(ok = wait(&bar.q_empty, (oc & 1) ^ 1))) break;
+      tc_fence_after();
+      if (!lo) sm->qs[oc & 1][hl] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : 1.f;
+#pragma unroll 1
+      for (int s = 0; s < 5; ++s) {
+        uint32_t r[32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint4 v = mine[128 * (8 * s + u)];
+          r[4 * u] = v.x;
+          r[4 * u + 1] = v.y;
+          r[4 * u + 2] = v.z;
+          r[4 * u + 3] = v.w;
+        }
+        tmem_st_x32(tmem + lane_base + kColQ + 32 * s, r);  // (the rope columns follow the codes')
+      }
+      tmem_wait_stores();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.qs_full[oc & 1]);
+        mbar_arrive(&bar.q_full);
+      }
+      ++oc;
     }
   }
-  if (lane == 0) {
-    rsum[warp] = l == 0.f ? 0.f : 1.f / l;
-    if (p.lse && h0 + warp < p.H) p.lse[(int64_t)blockIdx.x * p.H + h0 + warp] = l == 0.f ? -INFINITY : m + logf(l);
+
+  __syncthreads();
+  if (warp == kSWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.flags, DSA_FLAG_TIMEOUT);
+}
+static_assert(kColQR == kColQ + 128, "the converted query row is stored in one run of columns");
+
+// Joins a split item's parts: O = sum_s w_s O_s with w_s = 2^(lse_s - lse) in proportion.  One CTA
+// per (query, 4 heads): few queries must still fill the GPU.
+constexpr int kCombHeads = 4;
+__global__ void __launch_bounds__(128) k_latent_combine(LatentAttnLaunch p) {
+  __shared__ float wgt[kMaxLatentSplits][kCombHeads];
+  const int row = blockIdx.x, h0 = blockIdx.y * kCombHeads, S = p.splits;
+  const int64_t part0 = ((int64_t)row * p.groups + h0 / kHg) * S;
+  const int hl0 = h0 % kHg;
+  if (threadIdx.x < kCombHeads && h0 + threadIdx.x < p.H) {
+    const float* pl = p.part_lse + part0 * kHg + hl0 + threadIdx.x;
+    float mx = -INFINITY, sum = 0.f;
+    for (int s = 0; s < S; ++s) mx = fmaxf(mx, pl[s * kHg]);
+    for (int s = 0; s < S; ++s) {
+      const float v = pl[s * kHg];
+      const float w = v == -INFINITY ? 0.f : expf(v - mx);  // (a NaN stays)
+      wgt[s][threadIdx.x] = w;
+      sum += w;
+    }
+    for (int s = 0; s < S; ++s) wgt[s][threadIdx.x] = sum == 0.f ? 0.f : wgt[s][threadIdx.x] / sum;
+    if (p.lse) p.lse[(int64_t)row * p.H + h0 + threadIdx.x] = sum == 0.f ? -INFINITY : mx + logf(sum);
   }
   __syncthreads();
-#pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    if (h0 + h >= p.H) break;
-    uint16_t* o = p.out + ((int64_t)blockIdx.x * p.H + h0 + h) * kLatentDim;
-    const float r = rsum[h];
-    o[tid] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[h][0] * r));
-    o[tid + 256] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[h][1] * r));
+  const int hl = threadIdx.x >> 5;
+  if (h0 + hl >= p.H) return;
+  uint2* out = reinterpret_cast<uint2*>(p.out + ((int64_t)row * p.H + h0 + hl) * kLatentDim);
+  for (int i = threadIdx.x & 31; i < kLatentDim / 4; i += 32) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < S; ++s) {
+      const float w = wgt[s][hl];
+      if (w == 0.f) continue;  // an empty part wrote no values
+      const float4 v = reinterpret_cast<const float4*>(p.part_o + ((part0 + s) * kHg + hl0 + hl) * kLatentDim)[i];
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), b = __floats2bfloat162_rn(acc.z, acc.w);
+    out[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
 }
 
 }  // namespace
 
-cudaError_t launch_latent_attn(const LatentAttnLaunch& p, cudaStream_t st) {
+int latent_attn_splits(const LatentAttnLaunch& p) {
+  const int64_t items = (int64_t)p.B * p.T * ((p.H + kHg - 1) / kHg);
+  const int sms = device_sm_count();
+  if (items * 2 > sms) return 1;
+  int s = (int)(sms / items);
+  s = s < (p.kk + 127) / 128 ? s : (p.kk + 127) / 128;  // parts of at least 128 keys
+  return s < 2 ? 1 : s > kMaxLatentSplits ? kMaxLatentSplits : s;
+}
+
+size_t latent_attn_part_bytes(const LatentAttnLaunch& p, int splits) {
+  if (splits <= 1) return 0;
+  return (size_t)p.B * p.T * ((p.H + kHg - 1) / kHg) * splits * kHg * (kLatentDim + 1) * sizeof(float);
+}
+
+// part: room for latent_attn_part_bytes, or NULL: rows are not split.
+cudaError_t launch_latent_attn(LatentAttnLaunch p, float* part, cudaStream_t st) {
   TraceScope trace(kTraceAttention, st);
-  cudaError_t e = cudaFuncSetAttribute(k_latent_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  p.groups = (p.H + kHg - 1) / kHg;
+  p.splits = part ? latent_attn_splits(p) : 1;
+  const int64_t items = (int64_t)p.B * p.T * p.groups * p.splits;
+  if (p.splits > 1) {
+    p.part_o = part;
+    p.part_lse = part + items * kHg * kLatentDim;
+  }
+  p.wait = wait_limit();
+  auto kern = p.wait < kDefaultWaitCycles ? k_latent_attn<true> : k_latent_attn<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  k_latent_attn<<<dim3((unsigned)(p.B * p.T), (unsigned)((p.H + kHeads - 1) / kHeads)), kThreads, kSmem, st>>>(p);
+  const int sms = device_sm_count();
+  kern<<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, st>>>(p);
+  count_launches(1);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.splits <= 1) return e;
+  k_latent_combine<<<dim3((unsigned)(p.B * p.T), (unsigned)((p.H + kCombHeads - 1) / kCombHeads)), 128, 0, st>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }
