@@ -255,7 +255,7 @@ struct NormRopeLaunch {
   int S_cap, at_position;
   uint32_t* flags;
 };
-int norm_rope_group(int d);  // lanes that hold one head
+int norm_rope_units(int d);  // padded 8-value units of one head
 cudaError_t launch_norm_rope(const NormRopeLaunch& p, cudaStream_t st);
 
 // Paged FP8 latent cache (dsa_latent_cache), checked and with its capacity per sequence.

@@ -173,7 +173,7 @@ dsa_status dsa_norm_rope_e4m3(const dsa_norm_rope_args* a, uint8_t* codes, float
   if (s != DSA_OK) return s;
   if (!codes || !scales) return fail(DSA_ERR_INVALID_ARG, "codes and scales must be non-NULL");
   if (S_cap < 1 || (!at_position && S_cap < a->n)) return fail(DSA_ERR_INVALID_ARG, "S_cap = %d rows cannot hold the tokens", S_cap);
-  if (a->d > 256 || (int64_t)a->H * dsa::norm_rope_group(a->d) > 2048)
+  if ((int64_t)a->H * dsa::norm_rope_units(a->d) > 2048)
     return fail(DSA_ERR_UNSUPPORTED, "H = %d heads of d = %d are too wide for one token's scale", a->H, a->d);
   if (!aligned(codes, 8) || !aligned(scales, 4)) return fail(DSA_ERR_MISALIGNED, "codes need 8-byte alignment, scales 4-byte");
   if (at_position) P.limit = P.limit > 0 && P.limit < S_cap ? P.limit : S_cap;

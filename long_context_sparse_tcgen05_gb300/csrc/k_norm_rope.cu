@@ -195,18 +195,18 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bf16(NormRopeLaunch p) {
   }
 }
 
-// e4m3 out, d <= 8 G.  A token belongs to a team: a group of G lanes (one head), a warp (all its
-// heads in one pass) or the CTA (NS passes); the team holds the whole result in registers, takes
-// its largest magnitude and divides.
-template <int G, int NS, int kTeam>
+// e4m3 out.  A token belongs to a team: a group of G lanes (one head), a warp (all its heads in
+// one pass) or the CTA (NP passes over the heads); the team holds the whole result in registers,
+// takes its largest magnitude and divides.
+template <int G, int U, int NP, int kTeam>
 __global__ void __launch_bounds__(kThreads) k_norm_rope_e4m3(NormRopeLaunch p) {
   __shared__ float team_max[kThreads / 32];
   const int lane = threadIdx.x & 31;
   constexpr int kTeams = kThreads / kTeam;  // tokens per CTA
   constexpr int kHeads = kTeam / G;         // heads per pass
   const int t = threadIdx.x % kTeam;
-  const Lane<G, 1> ln{t % G};
-  const int hsub = t / G, at = ln.at(0);
+  const Lane<G, U> ln{t % G};
+  const int hsub = t / G;
   const int64_t toks = (int64_t)p.B * p.n;
   // every thread of a warp runs the same number of steps: the shuffles below take whole warps
   const int64_t step = (int64_t)gridDim.x * kTeams;
@@ -216,27 +216,32 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_e4m3(NormRopeLaunch p) {
     const int b = live ? (int)(tok / p.n) : 0, i = live ? (int)(tok - (int64_t)b * p.n) : 0;
     const int64_t pos = live ? token_pos(p, b, i, t == 0) : -1;
     const uint16_t* x = p.x + b * p.x_sb + i * p.x_st;
-    uint4 raw[NS], par[NS];
+    uint4 raw[NP][U], par[NP][U];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const int h = hsub + s * kHeads;
-      const bool in = pos >= 0 && h < p.H && at < p.d;
-      raw[s] = in ? __ldg(reinterpret_cast<const uint4*>(x + h * p.x_sh + at)) : make_uint4(0, 0, 0, 0);
-      par[s] = in && !p.interleaved && in_rope(p, at)
-                   ? __ldg(reinterpret_cast<const uint4*>(x + h * p.x_sh + partner_at(p, at)))
-                   : make_uint4(0, 0, 0, 0);
-    }
-    Vec8 y[NS];
+    for (int s = 0; s < NP; ++s)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = hsub + s * kHeads, at = ln.at(u);
+        const bool in = pos >= 0 && h < p.H && at < p.d;
+        raw[s][u] = in ? __ldg(reinterpret_cast<const uint4*>(x + h * p.x_sh + at)) : make_uint4(0, 0, 0, 0);
+        par[s][u] = in && !p.interleaved && in_rope(p, at)
+                        ? __ldg(reinterpret_cast<const uint4*>(x + h * p.x_sh + partner_at(p, at)))
+                        : make_uint4(0, 0, 0, 0);
+      }
+    Vec8 y[NP][U];
     uint32_t amax = 0;  // magnitude bits: a NaN is above every number and so is kept
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const uint4 one[1] = {raw[s]};
-      const float2 st = head_stats<G, 1>(p, one, ln);
-      if (pos >= 0 && hsub + s * kHeads < p.H && at < p.d) {
-        y[s] = normed(p, raw[s], st, at);
-        if (in_rope(p, at)) rotate(p, y[s], par[s], st, at, pos);
+    for (int s = 0; s < NP; ++s) {
+      const float2 st = head_stats<G, U>(p, raw[s], ln);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(y[s].v[e]) & 0x7fffffffu);
+      for (int u = 0; u < U; ++u) {
+        const int at = ln.at(u);
+        if (pos >= 0 && hsub + s * kHeads < p.H && at < p.d) {
+          y[s][u] = normed(p, raw[s][u], st, at);
+          if (in_rope(p, at)) rotate(p, y[s][u], par[s][u], st, at, pos);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(y[s][u].v[e]) & 0x7fffffffu);
+        }
       }
     }
     constexpr int kShfl = kTeam < 32 ? kTeam : 32;
@@ -255,29 +260,33 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_e4m3(NormRopeLaunch p) {
     const int64_t dst = (int64_t)b * p.S_cap + (p.at_position ? pos : i);
     uint8_t* codes = p.codes + dst * (int64_t)p.H * p.d;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const int h = hsub + s * kHeads;
-      if (h >= p.H || at >= p.d) continue;
-      const float* v = y[s].v;
-      const uint32_t lo = e4m3x2(v[0] / scale, v[1] / scale) | e4m3x2(v[2] / scale, v[3] / scale) << 16;
-      const uint32_t hi = e4m3x2(v[4] / scale, v[5] / scale) | e4m3x2(v[6] / scale, v[7] / scale) << 16;
-      *reinterpret_cast<uint2*>(codes + (int64_t)h * p.d + at) = make_uint2(lo, hi);
-    }
+    for (int s = 0; s < NP; ++s)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = hsub + s * kHeads, at = ln.at(u);
+        if (h >= p.H || at >= p.d) continue;
+        const float* v = y[s][u].v;
+        const uint32_t lo = e4m3x2(v[0] / scale, v[1] / scale) | e4m3x2(v[2] / scale, v[3] / scale) << 16;
+        const uint32_t hi = e4m3x2(v[4] / scale, v[5] / scale) | e4m3x2(v[6] / scale, v[7] / scale) << 16;
+        *reinterpret_cast<uint2*>(codes + (int64_t)h * p.d + at) = make_uint2(lo, hi);
+      }
     if (t == 0) p.scales[dst] = scale;
   }
 }
 
-template <int G>
+template <int G, int U>
 void launch_e4m3(const NormRopeLaunch& p, int64_t cap, cudaStream_t st) {
   const int64_t toks = (int64_t)p.B * p.n;
   const int lanes = p.H * G;
   auto grid = [&](int64_t per_cta) { return (int)std::min<int64_t>((toks + per_cta - 1) / per_cta, cap); };
-  if (p.H == 1) k_norm_rope_e4m3<G, 1, G><<<grid(kThreads / G), kThreads, 0, st>>>(p);
-  else if (lanes <= 32) k_norm_rope_e4m3<G, 1, 32><<<grid(kThreads / 32), kThreads, 0, st>>>(p);
-  else if (lanes <= 256) k_norm_rope_e4m3<G, 1, 256><<<grid(1), kThreads, 0, st>>>(p);
-  else if (lanes <= 512) k_norm_rope_e4m3<G, 2, 256><<<grid(1), kThreads, 0, st>>>(p);
-  else if (lanes <= 1024) k_norm_rope_e4m3<G, 4, 256><<<grid(1), kThreads, 0, st>>>(p);
-  else k_norm_rope_e4m3<G, 8, 256><<<grid(1), kThreads, 0, st>>>(p);
+  if (p.H == 1) k_norm_rope_e4m3<G, U, 1, G><<<grid(kThreads / G), kThreads, 0, st>>>(p);
+  else if (lanes <= 32) k_norm_rope_e4m3<G, U, 1, 32><<<grid(kThreads / 32), kThreads, 0, st>>>(p);
+  else if (lanes <= 256) k_norm_rope_e4m3<G, U, 1, 256><<<grid(1), kThreads, 0, st>>>(p);
+  else if (lanes <= 512) k_norm_rope_e4m3<G, U, 2, 256><<<grid(1), kThreads, 0, st>>>(p);
+  else if constexpr (U <= 2) {
+    if (lanes <= 1024) k_norm_rope_e4m3<G, U, 4, 256><<<grid(1), kThreads, 0, st>>>(p);
+    else if constexpr (U == 1) k_norm_rope_e4m3<G, U, 8, 256><<<grid(1), kThreads, 0, st>>>(p);
+  }
 }
 
 template <int G, int U, int R>
@@ -290,7 +299,10 @@ void launch_bf16(const NormRopeLaunch& p, int64_t cap, cudaStream_t st) {
 
 }  // namespace
 
-int norm_rope_group(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
+// 8-value units of a head, padded: lanes x units per lane that hold it.
+int norm_rope_units(int d) {
+  return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : d <= 256 ? 32 : d <= 512 ? 64 : 128;
+}
 
 cudaError_t launch_norm_rope(const NormRopeLaunch& p, cudaStream_t st) {
   if (p.B == 0 || p.n == 0) return cudaSuccess;
@@ -304,11 +316,13 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& p, cudaStream_t st) {
     else if (p.d <= 512) launch_bf16<32, 2, 2>(p, cap, st);
     else launch_bf16<32, 4, 1>(p, cap, st);
   } else {
-    switch (norm_rope_group(p.d)) {
-      case 4: launch_e4m3<4>(p, cap, st); break;
-      case 8: launch_e4m3<8>(p, cap, st); break;
-      case 16: launch_e4m3<16>(p, cap, st); break;
-      default: launch_e4m3<32>(p, cap, st); break;
+    switch (norm_rope_units(p.d)) {
+      case 4: launch_e4m3<4, 1>(p, cap, st); break;
+      case 8: launch_e4m3<8, 1>(p, cap, st); break;
+      case 16: launch_e4m3<16, 1>(p, cap, st); break;
+      case 32: launch_e4m3<32, 1>(p, cap, st); break;
+      case 64: launch_e4m3<32, 2>(p, cap, st); break;
+      default: launch_e4m3<32, 4>(p, cap, st); break;
     }
   }
   count_launches(1);

@@ -83,7 +83,7 @@ def test_norm_rope_output_refusals(lib):
     q = lambda a=a, codes=FAKE, scales=FAKE, cap=100, at=1: lib.dsa_norm_rope_e4m3(a, codes, scales, cap, at, FAKE, 256, None)  # noqa: E731
     assert q(codes=None) == INVALID and q(scales=None) == INVALID and q(cap=0) == INVALID and q(cap=2, at=0) == INVALID
     assert q(codes=FAKE + 4) == MISALIGNED and q(scales=FAKE + 2) == MISALIGNED
-    assert q(a=ctypes.byref(_norm(d=512, rope_dim=64))) == UNSUPPORTED
+    assert q(a=ctypes.byref(_norm(H=17, d=1024))) == UNSUPPORTED
     assert q(a=ctypes.byref(_norm(H=257))) == UNSUPPORTED
     assert q(a=ctypes.byref(_norm(positions=None, pos0=40)), cap=42) == INVALID  # past the cache, not the tables
 
