@@ -28,10 +28,15 @@
 //   5      O^T (512 x 64) += V^T P^T: four chunks of 128 dims, 2 key steps, hi and lo
 //   6-13   softmax: a warp holds 8 heads whole (their hi and lo rows lie in one 16-lane half of a
 //          lane quarter), so maxima and sums never leave a quad of lanes and no barrier joins warps
-//   14-17  rescale O^T when a reference maximum rises (only the heads concerned), and at the end
-//          normalise and store, while the softmax already runs the next item
+//   14-17  rescale O^T when a reference maximum rises (only the heads concerned)
 //   18-21  convert the next item's queries while the present one runs, and put them into tensor
 //          memory when its last score product is done
+//   14-21  normalise an item's O, while the softmax already runs the next item: bf16 rows go to the
+//          room of the converted queries (free at that time) and out by bulk copies
+// The issuing warps run as whole warps on warp-uniform values and elect the issuing lane: operand
+// descriptors then stay in uniform registers.  Issued from a lane-0 branch, every product took 60
+// cycles whatever its shape; this way 32 (A in tensor memory) and 48 (A in shared memory: 6 KB of
+// operands at 128 bytes a cycle).
 // With fewer items than half the SMs each is split into parts of at least 128 keys; parts are
 // joined by k_latent_combine.  Waits are bounded (DSA_FLAG_TIMEOUT).
 #include <cuda_bf16.h>
@@ -60,6 +65,9 @@ constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColS = 448;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kTop = 8.f, kAim = 4.f;      // raise M when y exceeds it by 8; the new largest p is 2^4
 constexpr int kInfoReaders = 2 + kSmWarps + 4 + 4;
+constexpr int kEpiThreads = 256;             // O and query warps store an item's O together
+constexpr uint32_t kOPitch = kLatentDim * 2 + 64;  // staged O row: neighbouring heads 16 banks apart
+static_assert(kHg * kOPitch <= kQBytes, "O is staged in the queries' room");
 
 struct Bars {
   uint64_t q_full, q_empty, qs_full[2];
@@ -136,6 +144,27 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+// Named barrier of n threads that ORs a predicate over them: the answer is the same for all, so a
+// decision to leave (a wait ran out in some warp) leaves no warp behind at a later barrier.
+__device__ __forceinline__ bool named_sync_or(int id, int n, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -194,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   Small* sm = reinterpret_cast<Small*>(q_s + kQBytes);
   Bars& bar = sm->bar;
   volatile int* abort_flag = &sm->abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int items = p.B * p.T * p.groups * p.splits;
   const int G = (int)gridDim.x;
   // a wait that every lane of a warp makes, with one answer for the warp
@@ -208,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     mbar_init(&bar.s_full, 1);
     mbar_init(&bar.s_empty, kSmWarps);
     mbar_init(&bar.o_full, 1);
-    mbar_init(&bar.o_empty, 4);
+    mbar_init(&bar.o_empty, 8);
     mbar_init(&bar.cmd_full, 1);
     mbar_init(&bar.corr_done, 4);
     for (int i = 0; i < kStages; ++i) {
@@ -221,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       mbar_init(&bar.p_full[i], kSmWarps);
       mbar_init(&bar.p_empty[i], 1);
       mbar_init(&bar.l_full[i], kSmWarps);
-      mbar_init(&bar.l_empty[i], 4);
+      mbar_init(&bar.l_empty[i], 8);
       mbar_init(&bar.info_full[i], 1);
       mbar_init(&bar.info_empty[i], kInfoReaders);
       mbar_init(&bar.drain[i], 1);
@@ -236,7 +265,77 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm->tmem, 0);
+
+  // An item's O, once its sums and its last value product are there: the O warps store dim chunks 0
+  // and 1, the query warps 2 and 3.  false: a wait ran out in one of them, and all eight leave.
+  // These warps meet at barrier 1 once per item with blocks and once more (meet_last) when they are
+  // done or leave for a wait of their own, so none waits there for one that has left.
+  bool met_failure = false;
+  auto meet_last = [&](bool ok) {
+    if (!met_failure) named_sync_or(1, kEpiThreads, !ok);
+  };
+  auto epilogue = [&](int item, int oc) -> bool {
+    const int q4 = warp & 3, c0 = warp < kQWarp0 ? 0 : 2;
+    const Item I = item_of(p, item);
+    const bool ok = wait(&bar.l_full[oc & 1], (oc >> 1) & 1) && wait(&bar.o_full, oc & 1);
+    // (here the query warps are past the read of their converted queries)
+    if (named_sync_or(1, kEpiThreads, !ok)) {
+      met_failure = true;
+      return false;
+    }
+    tc_fence_after();
+    float* po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
+#pragma unroll 1
+    for (int n = 0; n < 4; ++n) {
+      const int h0 = (n & 1) * 32, c = c0 + (n >> 1), d = c * 128 + q4 * 32 + lane;
+      if (h0 >= I.heads) continue;
+      uint32_t r[32];
+      tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + kColO + c * kHg + h0, r);
+      tmem_wait_ld();
+      const float4* ls4 = reinterpret_cast<const float4*>(sm->lsum[oc & 1] + h0);
+      const uint32_t dst = smem_addr(q_s) + h0 * kOPitch + d * 2;
+#pragma unroll
+      for (int i4 = 0; i4 < 8; ++i4) {
+        const float4 L = ls4[i4];
+        const float lv[4] = {L.x, L.y, L.z, L.w};
+        float o[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[u] = lv[u] == 0.f ? 0.f : __uint_as_float(r[4 * i4 + u]) * lv[u];
+        if (po) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (h0 + 4 * i4 + u < I.heads) po[(int64_t)(h0 + 4 * i4 + u) * kLatentDim + d] = o[u];
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; u += 2) {
+            const __nv_bfloat162 w = __floats2bfloat162_rn(o[u], o[u + 1]);
+            asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + (4 * i4 + u) * kOPitch), "h"(__bfloat16_as_ushort(w.x)) : "memory");
+            asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + (4 * i4 + u + 1) * kOPitch), "h"(__bfloat16_as_ushort(w.y)) : "memory");
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    async_fence();  // the staged rows are read by bulk copies
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&bar.l_empty[oc & 1]);
+      mbar_arrive(&bar.o_empty);
+    }
+    if (po) return true;
+    named_sync(1, kEpiThreads);
+    if (warp >= kQWarp0) {
+      const int h = threadIdx.x - kQWarp0 * 32;
+      if (h < I.heads) {
+        bulk_store(p.out + ((int64_t)I.row * p.H + I.h0 + h) * kLatentDim, smem_addr(q_s) + h * kOPitch, kLatentDim * 2);
+        asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+      }
+      named_sync(2, 128);  // the room may hold converted queries again
+    }
+    return true;
+  };
 
   if (warp < kGatherWarps) {
     // ================= gather =================
@@ -327,26 +426,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
   } else if (warp == kSWarp) {
-    // ================= score product (one thread) =================
+    // ================= score product =================
     const uint32_t id8 = idesc_mn(0, 0, 128, kNB), id16 = idesc_mn(1, 1, 128, kNB);
     const uint64_t kv_desc = desc_sw128(smem_addr(kv_s));
-    if (lane == 0) {
-      int it = 0, oc = 0;
-      uint32_t g = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
-        if (!(ok = mbar_wait<kPoll>(&bar.info_full[it & 1], (it >> 1) & 1, abort_flag, p.wait))) break;
-        const int nb = sm->nb[it & 1];
-        mbar_arrive(&bar.info_empty[it & 1]);
-        if (nb == 0) continue;
-        ok = mbar_wait<kPoll>(&bar.q_full, oc & 1, abort_flag, p.wait);
-        for (int j = 0; ok && j < nb; ++j, ++g) {
-          const int st = (int)(g % kStages);
-          ok = mbar_wait<kPoll>(&bar.s_empty, (g & 1) ^ 1, abort_flag, p.wait) &&
-               mbar_wait<kPoll>(&bar.kv_full[st], (g / kStages) & 1, abort_flag, p.wait);
-          if (!ok) break;
-          async_fence();  // the stage was written by cp.async
-          tc_fence_after();
+    int it = 0, oc = 0;
+    uint32_t g = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
+      const int nb = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
+      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+      if (nb == 0) continue;
+      if (!(ok = wait(&bar.q_full, oc & 1))) break;
+      for (int j = 0; j < nb; ++j, ++g) {
+        const int st = (int)(g % kStages);
+        if (!(ok = wait(&bar.s_empty, (g & 1) ^ 1) && wait(&bar.kv_full[st], (g / kStages) & 1))) break;
+        async_fence();  // the stage was written by cp.async
+        tc_fence_after();
+        if (elect_lane()) {
           const uint64_t kd = kv_desc + (uint64_t)((st * kStage) >> 4);
 #pragma unroll
           for (int k = 0; k < 16; ++k)
@@ -355,40 +452,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           for (int k = 0; k < 4; ++k)
             mma_bf16_ts(tmem + kColS, tmem + kColQR + 8 * k, kd + (uint64_t)((4 * kAtom + k * 32) >> 4), id16, 1);
           mma_commit(&bar.s_full);
+          if (j == nb - 1) mma_commit(&bar.q_empty);
         }
-        mma_commit(&bar.q_empty);
-        ++oc;
+        __syncwarp();
       }
-      mma_commit(&bar.drain[0]);  // this thread's products end before tensor memory is freed
+      ++oc;
+    }
+    if (elect_lane()) {  // the products issued here end before tensor memory is freed
+      mma_commit(&bar.drain[0]);
       mbar_wait_drain(&bar.drain[0], 0);
     }
+    __syncwarp();
   } else if (warp == kPvWarp) {
-    // ================= value product (one thread) =================
+    // ================= value product =================
     const uint32_t id8 = idesc_mn(0, 0, 128, kHg) | (1u << 15);  // A: 128 dims, MN-major
     const uint64_t v_desc = desc_sw128(smem_addr(kv_s)), p_desc = desc_sw128(smem_addr(p_s));
-    if (lane == 0) {
-      int it = 0, oc = 0, corr = 0;
-      uint32_t g = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
-        if (!(ok = mbar_wait<kPoll>(&bar.info_full[it & 1], (it >> 1) & 1, abort_flag, p.wait))) break;
-        const int nb = sm->nb[it & 1];
-        mbar_arrive(&bar.info_empty[it & 1]);
-        if (nb == 0) continue;
-        ok = mbar_wait<kPoll>(&bar.o_empty, (oc & 1) ^ 1, abort_flag, p.wait);
-        for (int j = 0; ok && j < nb; ++j, ++g) {
-          const int st = (int)(g % kStages), pb = (int)(g & 1);
-          ok = mbar_wait<kPoll>(&bar.p_full[pb], (g >> 1) & 1, abort_flag, p.wait) &&
-               mbar_wait<kPoll>(&bar.kv_full[st], (g / kStages) & 1, abort_flag, p.wait);
-          if (!ok) break;
-          if (j > 0 && *reinterpret_cast<const volatile uint64_t*>(sm->need[pb])) {
+    int it = 0, oc = 0, corr = 0;
+    uint32_t g = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
+      const int nb = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
+      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+      if (nb == 0) continue;
+      if (!(ok = wait(&bar.o_empty, (oc & 1) ^ 1))) break;
+      for (int j = 0; j < nb; ++j, ++g) {
+        const int st = (int)(g % kStages), pb = (int)(g & 1);
+        if (!(ok = wait(&bar.p_full[pb], (g >> 1) & 1) && wait(&bar.kv_full[st], (g / kStages) & 1))) break;
+        if (j > 0 && __any_sync(0xffffffffu, *reinterpret_cast<const volatile uint64_t*>(sm->need[pb]) != 0)) {
+          if (lane == 0) {
             sm->cmd = (int)(g & 0x3fffffffu);
             mbar_arrive(&bar.cmd_full);
-            if (!(ok = mbar_wait<kPoll>(&bar.corr_done, corr & 1, abort_flag, p.wait))) break;
-            ++corr;
           }
-          async_fence();
-          tc_fence_after();
+          if (!(ok = wait(&bar.corr_done, corr & 1))) break;
+          ++corr;
+        }
+        async_fence();
+        tc_fence_after();
+        if (elect_lane()) {
           const uint64_t vd = v_desc + (uint64_t)((st * kStage) >> 4), pd = p_desc + (uint64_t)((pb * kPBytes) >> 4);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -398,16 +499,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
                       pd + (uint64_t)((k * 32) >> 4), id8, (j | k) != 0);
           mma_commit(&bar.kv_empty[st]);
           mma_commit(&bar.p_empty[pb]);
+          if (j == nb - 1) mma_commit(&bar.o_full);
         }
-        if (!ok) break;
-        mma_commit(&bar.o_full);
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (lane == 0) {
         sm->cmd = -1;
         mbar_arrive(&bar.cmd_full);
-        ++oc;
       }
+      ++oc;
+    }
+    if (elect_lane()) {
       mma_commit(&bar.drain[1]);
       mbar_wait_drain(&bar.drain[1], 0);
     }
+    __syncwarp();
   } else if (warp < kOWarp0) {
     // ================= softmax =================
     const int hgp = 2 * (warp & 3) + ((warp - kSmWarp0) >> 2);  // this warp's 8 heads
@@ -499,9 +606,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       ++oc;
     }
   } else if (warp < kQWarp0) {
-    // ================= O^T: rescales and the epilogue =================
-    const int q4 = warp & 3, t = threadIdx.x - kOWarp0 * 32;
-    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    // ================= O^T: rescales, half of the epilogue =================
+    const int t = threadIdx.x - kOWarp0 * 32;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     int it = 0, oc = 0;
     uint32_t cmds = 0;
     bool ok = true;
@@ -511,10 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
       const Item I = item_of(p, item);
-      uint16_t* og = p.out + ((int64_t)I.row * p.H + I.h0) * kLatentDim;
-      float* po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
       if (nb == 0) {  // nothing selected: O = 0, LSE = -inf
-        if (po) {  // the combine reads no part whose weight is 0
+        uint16_t* og = p.out + ((int64_t)I.row * p.H + I.h0) * kLatentDim;
+        if (p.splits > 1) {  // the combine reads no part whose weight is 0
           if (t < kHg) p.part_lse[(int64_t)item * kHg + t] = -INFINITY;
         } else {
           for (int i = t; i < I.heads * kLatentDim / 8; i += 128) reinterpret_cast<uint4*>(og)[i] = make_uint4(0, 0, 0, 0);
@@ -553,53 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.corr_done);
       }
-      if (!ok) break;
-      if (!(ok = wait(&bar.l_full[oc & 1], (oc >> 1) & 1))) break;
-      if (!(ok = wait(&bar.o_full, oc & 1))) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int n = 0; n < 8; ++n) {  // slice n: dims of chunk n / 2, heads 32 (n % 2) ..
-        const int h0 = (n & 1) * 32, d = (n >> 1) * 128 + q4 * 32 + lane;
-        if (h0 >= I.heads) continue;
-        uint32_t r[32];
-        tmem_ld32(tmem + lane_base + kColO + (n >> 1) * kHg + h0, r);
-        tmem_wait_ld();
-        const float4* ls4 = reinterpret_cast<const float4*>(sm->lsum[oc & 1] + h0);
-#pragma unroll
-        for (int i4 = 0; i4 < 8; ++i4) {
-          const float4 L = ls4[i4];
-          const float lv[4] = {L.x, L.y, L.z, L.w};
-          float o[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) o[u] = lv[u] == 0.f ? 0.f : __uint_as_float(r[4 * i4 + u]) * lv[u];
-          if (po) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (h0 + 4 * i4 + u < I.heads) po[(int64_t)(h0 + 4 * i4 + u) * kLatentDim + d] = o[u];
-          } else {
-            // lane pairs write two neighbouring dims of a head as one word: of heads (i, i + 1)
-            // the even lane writes i, the odd lane i + 1
-            const bool odd = (lane & 1) != 0;
-#pragma unroll
-            for (int u = 0; u < 4; u += 2) {
-              const float other = __shfl_xor_sync(0xffffffffu, odd ? o[u] : o[u + 1], 1);
-              const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(other, o[u + 1]) : __floats2bfloat162_rn(o[u], other);
-              const int h = h0 + 4 * i4 + u + (odd ? 1 : 0);
-              if (h < I.heads) *reinterpret_cast<__nv_bfloat162*>(og + (int64_t)h * kLatentDim + (d & ~1)) = w;
-            }
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bar.l_empty[oc & 1]);
-        mbar_arrive(&bar.o_empty);
-      }
+      if (!ok || !(ok = epilogue(item, oc))) break;
       ++oc;
     }
+    meet_last(ok);
   } else {
-    // ================= queries: hi and lo rows =================
+    // ================= queries: hi and lo rows; half of the epilogue =================
     // Lane 16 h + i (i < 8) of quarter q holds the hi row of head 16 q + 8 h + i, lane 16 h + 8 + i
     // its lo row, so that a softmax thread's one load gives it both.
     const int q4 = warp & 3;
@@ -608,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     uint4* mine = reinterpret_cast<uint4*>(q_s) + (warp - kQWarp0) * 32 + lane;  // word w at mine[128 w]
     int it = 0, oc = 0;
+    int last = -1;  // the item whose O is still to be stored
     bool ok = true;
     for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
       const Item I = item_of(p, item);
@@ -670,36 +736,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         }
         mine[128 * (32 + c)] = v;
       }
-      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
-      const int nb = sm->nb[it & 1];
+      ok = wait(&bar.info_full[it & 1], (it >> 1) & 1);
+      const int nb = ok ? sm->nb[it & 1] : 0;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
-      if (nb == 0) continue;
-      if (!(ok = wait(&bar.q_empty, (oc & 1) ^ 1))) break;
-      tc_fence_after();
-      if (!lo) sm->qs[oc & 1][hl] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : 1.f;
+      if (ok && lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+      if (ok && nb) {
+        ok = wait(&bar.q_empty, (oc & 1) ^ 1);
+        if (ok) {
+          tc_fence_after();
+          if (!lo) sm->qs[oc & 1][hl] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : 1.f;
 #pragma unroll 1
-      for (int s = 0; s < 5; ++s) {
-        uint32_t r[32];
+          for (int s = 0; s < 5; ++s) {
+            uint32_t r[32];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const uint4 v = mine[128 * (8 * s + u)];
-          r[4 * u] = v.x;
-          r[4 * u + 1] = v.y;
-          r[4 * u + 2] = v.z;
-          r[4 * u + 3] = v.w;
+            for (int u = 0; u < 8; ++u) {
+              const uint4 v = mine[128 * (8 * s + u)];
+              r[4 * u] = v.x;
+              r[4 * u + 1] = v.y;
+              r[4 * u + 2] = v.z;
+              r[4 * u + 3] = v.w;
+            }
+            tmem_st_x32(tmem + lane_base + kColQ + 32 * s, r);  // (the rope columns follow the codes')
+          }
+          tmem_wait_stores();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar.qs_full[oc & 1]);
+            mbar_arrive(&bar.q_full);
+          }
         }
-        tmem_st_x32(tmem + lane_base + kColQ + 32 * s, r);  // (the rope columns follow the codes')
       }
-      tmem_wait_stores();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bar.qs_full[oc & 1]);
-        mbar_arrive(&bar.q_full);
-      }
-      ++oc;
+      // the O warps wait in the last item's epilogue: join them before any wait on a later item
+      // than this one, whose publication they hold up
+      if (ok && last >= 0) ok = epilogue(last, oc - 1);
+      if (!ok) break;
+      if (nb) ++oc;
+      last = nb ? item : -1;
     }
+    if (ok && last >= 0) ok = epilogue(last, oc - 1);
+    meet_last(ok);
+    asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   }
 
   __syncthreads();
