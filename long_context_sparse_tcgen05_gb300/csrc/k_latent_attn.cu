@@ -11,18 +11,20 @@
 //     significant bits, hi takes 4 and lo the other 4: exact down to 2^-21 of the head's largest.
 //     The rope part stays bf16 (times 2^k, exact).  S has a hi and a lo row per head (M = 128 for
 //     64 heads): hi . c + r . r and lo . c, added by the softmax.
-//   * the weights: y_j = x_j + log2 s_j, p_j = 2^(y_j - M) <= 256 carries the row's scale, and
+//   * the weights: y_j = x_j + log2 s_j, p_j = 2^(y_j - M) <= 430 carries the row's scale, and
 //     p_j = hi + lo in e4m3 (each rounded to nearest): relative error 2^-8, and at most 2^-10
-//     absolute where p_j is small, 2^-14 of the largest, since M keeps the largest p in [16, 256].
+//     absolute where p_j is small, 2^-14 of the largest, since M keeps the largest p in [16, 430].
 //     Both terms accumulate into the same O.  Row sums take p_j / s_j in fp32.
 // FP8 products accumulate exactly enough in fp32 (sums of 2,048 products of mixed size came out
 // equal to the 64-bit sum).
 //
 // Persistent CTAs, one per SM, walk items (query, group of 64 heads, part of the row's blocks of 64
-// keys).  22 warps:
-//   0-3    gather: resolve positions through the block table a block ahead and copy the selected
-//          rows (16-byte cp.async) into three stages of 40 KB, five 128-byte-swizzled atoms each;
-//          leave the rows' scales beside them
+// keys).  24 warps:
+//   22-23  take the blocks in turn, up to six ahead: resolve positions through the block table, read
+//          the rows' scales, bring the rows to L2 (the three dependent loads a block took as long
+//          as its copies when the copying warps made them)
+//   0-3    copy the rows (16-byte cp.async) into four stages of 40 KB, five 128-byte-swizzled atoms
+//          each, an atom as soon as the products have released it
 //   4      S (hi and lo rows, 128 x 64) = Q K^T: A is Q in tensor memory, so the product reads only
 //          the codes from shared memory; 16 FP8 steps and 4 bf16 steps for the rope part
 //   5      O^T (512 x 64) += V^T P^T: four chunks of 128 dims, 2 key steps, hi and lo
@@ -51,38 +53,44 @@ using namespace sm100;
 
 constexpr int kHg = 64;                      // heads of an item
 constexpr int kNB = 64;                      // keys of a block
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr int kD = kLatentDim + kLatentRope;
 constexpr uint32_t kAtom = kNB * 128;        // 64 rows of 128 bytes
 constexpr uint32_t kStage = 5 * kAtom;       // four atoms of codes, one of rope values
 constexpr uint32_t kPBytes = kHg * 128;      // P: per head 64 hi bytes, then 64 lo bytes
 constexpr int kQVec = 40;                    // 16-byte words of a converted query row (512 + 128 bytes)
-constexpr uint32_t kQBytes = kQVec * 128 * 16;
+constexpr int kQLocal = 22;                  // of these, kept in local memory (L1 / L2) until they are needed
+constexpr uint32_t kQBytes = (kQVec - kQLocal) * 128 * 16;
 constexpr int kGatherWarps = 4, kSWarp = 4, kPvWarp = 5, kSmWarp0 = 6, kSmWarps = 8, kOWarp0 = 14, kQWarp0 = 18;
-constexpr int kThreads = 22 * 32;
+constexpr int kIxWarp0 = 22, kRing = 6;      // index warps, blocks they may be ahead
+constexpr int kThreads = 24 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColS = 448;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kTop = 8.f, kAim = 4.f;      // raise M when y exceeds it by 8; the new largest p is 2^4
-constexpr int kInfoReaders = 2 + kSmWarps + 4 + 4;
+constexpr float kTop = 8.75f, kAim = 4.f;    // raise M when y exceeds it by 8.75 (p <= 430); then the largest p is 2^4
+constexpr int kInfoReaders = kGatherWarps + 2 + kSmWarps + 4 + 4;
 constexpr int kEpiThreads = 256;             // O and query warps store an item's O together
-constexpr uint32_t kOPitch = kLatentDim * 2 + 64;  // staged O row: neighbouring heads 16 banks apart
-static_assert(kHg * kOPitch <= kQBytes, "O is staged in the queries' room");
+constexpr uint32_t kOPitch = kLatentDim + 64;  // staged half of an O row: neighbouring heads 16 banks apart
+static_assert(kHg * kOPitch <= kQBytes, "halves of O are staged in the queries' room");
 
 struct Bars {
   uint64_t q_full, q_empty, qs_full[2];
-  uint64_t kv_full[kStages], kv_empty[kStages], sc_full[kStages];
+  // kv_empty[st][c]: atom c of stage st may be refilled (0-3 codes, after the value product's dim
+  // chunk c; 4 rope values, after the score product)
+  uint64_t kv_full[kStages], kv_empty[kStages][5];
+  uint64_t ix_full[kRing], ix_empty[kRing];
   uint64_t s_full, s_empty;
   uint64_t p_full[2], p_empty[2];
-  uint64_t o_full, o_empty, cmd_full, corr_done;
+  uint64_t o_full, o_empty, m_full[2], m_empty[2], corr_done;
   uint64_t l_full[2], l_empty[2];
   uint64_t info_full[2], info_empty[2];
   uint64_t drain[2];
 };
 struct Small {
-  alignas(16) float2 sc[kStages][kNB];   // {scale, log2 scale} of a stage's rows; {0, -inf}: skipped
-  alignas(16) float isc[kStages][kNB];   // 1 / scale (0: skipped)
-  alignas(16) int valid[kStages][4];     // by gather warp: some row of the block counts
+  alignas(16) float2 sc[kRing][kNB];     // {scale, log2 scale} of a block's rows; {0, -inf}: skipped
+  alignas(16) float isc[kRing][kNB];     // 1 / scale (0: skipped)
+  alignas(16) int64_t row[kRing][kNB];   // cache row (-1: skipped)
+  int valid[kRing];                      // some row of the block counts
   alignas(16) float alpha[2][kHg];       // by block parity: factor of O where `need` is set
   alignas(16) float lsum[2][kHg];        // reciprocal row sums, by item parity
   float qs[2][kHg];                      // 2^-k of the item's heads
@@ -91,7 +99,6 @@ struct Small {
   uint32_t tmem;
   int abort;
   int nb[2];                             // blocks of the item, by item parity
-  int cmd;                               // to the O warps: rescale before block cmd, or -1: store
 };
 constexpr size_t kSmem = 1024 + kStages * kStage + 2 * kPBytes + kQBytes + sizeof(Small);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -162,6 +169,9 @@ __device__ __forceinline__ bool named_sync_or(int id, int n, bool pred) {
   return r != 0;
 }
 __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* src) {
+  asm volatile("prefetch.global.L2 [%0];\n" ::"l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
@@ -238,17 +248,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     mbar_init(&bar.s_empty, kSmWarps);
     mbar_init(&bar.o_full, 1);
     mbar_init(&bar.o_empty, 8);
-    mbar_init(&bar.cmd_full, 1);
     mbar_init(&bar.corr_done, 4);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.kv_full[i], kGatherWarps * 32);
-      mbar_init(&bar.kv_empty[i], 1);
-      mbar_init(&bar.sc_full[i], kGatherWarps);
+      for (int c = 0; c < 5; ++c) mbar_init(&bar.kv_empty[i][c], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar.ix_full[i], 1);
+      mbar_init(&bar.ix_empty[i], kSmWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.qs_full[i], 4);
       mbar_init(&bar.p_full[i], kSmWarps);
       mbar_init(&bar.p_empty[i], 1);
+      mbar_init(&bar.m_full[i], kSmWarps);
+      mbar_init(&bar.m_empty[i], 4);
       mbar_init(&bar.l_full[i], kSmWarps);
       mbar_init(&bar.l_empty[i], 8);
       mbar_init(&bar.info_full[i], 1);
@@ -267,16 +281,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm->tmem, 0);
 
-  // An item's O, once its sums and its last value product are there: the O warps store dim chunks 0
-  // and 1, the query warps 2 and 3.  false: a wait ran out in one of them, and all eight leave.
-  // These warps meet at barrier 1 once per item with blocks and once more (meet_last) when they are
-  // done or leave for a wait of their own, so none waits there for one that has left.
+  // An item's O, once its sums and its last value product are there: first dim chunks 0 and 1, then
+  // 2 and 3, one of each by the O warps and the other by the query warps.  false: a wait ran out in
+  // one of them, and all eight leave.
+  // These warps meet at barrier 1 in step, and once more (meet_last) when they are done or leave for
+  // a wait of their own, so none waits there for one that has left.
   bool met_failure = false;
   auto meet_last = [&](bool ok) {
     if (!met_failure) named_sync_or(1, kEpiThreads, !ok);
   };
   auto epilogue = [&](int item, int oc) -> bool {
-    const int q4 = warp & 3, c0 = warp < kQWarp0 ? 0 : 2;
+    const int q4 = warp & 3, cw = warp < kQWarp0 ? 0 : 1;
     const Item I = item_of(p, item);
     const bool ok = wait(&bar.l_full[oc & 1], (oc >> 1) & 1) && wait(&bar.o_full, oc & 1);
     // (here the query warps are past the read of their converted queries)
@@ -287,52 +302,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     tc_fence_after();
     float* po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
 #pragma unroll 1
-    for (int n = 0; n < 4; ++n) {
-      const int h0 = (n & 1) * 32, c = c0 + (n >> 1), d = c * 128 + q4 * 32 + lane;
-      if (h0 >= I.heads) continue;
-      uint32_t r[32];
-      tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + kColO + c * kHg + h0, r);
-      tmem_wait_ld();
-      const float4* ls4 = reinterpret_cast<const float4*>(sm->lsum[oc & 1] + h0);
-      const uint32_t dst = smem_addr(q_s) + h0 * kOPitch + d * 2;
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+      for (int h0 = 0; h0 < I.heads; h0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + kColO + (2 * half + cw) * kHg + h0, r);
+        tmem_wait_ld();
+        if (half && h0 == 0 && !po) named_sync(1, kEpiThreads);  // the first half has left the room
+        const float4* ls4 = reinterpret_cast<const float4*>(sm->lsum[oc & 1] + h0);
+        const int d = cw * 128 + q4 * 32 + lane;  // dim within the half
+        const uint32_t dst = smem_addr(q_s) + h0 * kOPitch + d * 2;
 #pragma unroll
-      for (int i4 = 0; i4 < 8; ++i4) {
-        const float4 L = ls4[i4];
-        const float lv[4] = {L.x, L.y, L.z, L.w};
-        float o[4];
+        for (int i4 = 0; i4 < 8; ++i4) {
+          const float4 L = ls4[i4];
+          const float lv[4] = {L.x, L.y, L.z, L.w};
+          float o[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) o[u] = lv[u] == 0.f ? 0.f : __uint_as_float(r[4 * i4 + u]) * lv[u];
-        if (po) {
+          for (int u = 0; u < 4; ++u) o[u] = lv[u] == 0.f ? 0.f : __uint_as_float(r[4 * i4 + u]) * lv[u];
+          if (po) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (h0 + 4 * i4 + u < I.heads) po[(int64_t)(h0 + 4 * i4 + u) * kLatentDim + d] = o[u];
-        } else {
+            for (int u = 0; u < 4; ++u)
+              if (h0 + 4 * i4 + u < I.heads) po[(int64_t)(h0 + 4 * i4 + u) * kLatentDim + half * 256 + d] = o[u];
+          } else {
 #pragma unroll
-          for (int u = 0; u < 4; u += 2) {
-            const __nv_bfloat162 w = __floats2bfloat162_rn(o[u], o[u + 1]);
-            asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + (4 * i4 + u) * kOPitch), "h"(__bfloat16_as_ushort(w.x)) : "memory");
-            asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + (4 * i4 + u + 1) * kOPitch), "h"(__bfloat16_as_ushort(w.y)) : "memory");
+            for (int u = 0; u < 4; u += 2) {
+              const __nv_bfloat162 w = __floats2bfloat162_rn(o[u], o[u + 1]);
+              asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + (4 * i4 + u) * kOPitch), "h"(__bfloat16_as_ushort(w.x)) : "memory");
+              asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + (4 * i4 + u + 1) * kOPitch), "h"(__bfloat16_as_ushort(w.y)) : "memory");
+            }
           }
         }
       }
-    }
-    tc_fence_before();
-    async_fence();  // the staged rows are read by bulk copies
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&bar.l_empty[oc & 1]);
-      mbar_arrive(&bar.o_empty);
-    }
-    if (po) return true;
-    named_sync(1, kEpiThreads);
-    if (warp >= kQWarp0) {
-      const int h = threadIdx.x - kQWarp0 * 32;
-      if (h < I.heads) {
-        bulk_store(p.out + ((int64_t)I.row * p.H + I.h0 + h) * kLatentDim, smem_addr(q_s) + h * kOPitch, kLatentDim * 2);
-        asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
-        asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+      if (half) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.l_empty[oc & 1]);
+          mbar_arrive(&bar.o_empty);
+        }
       }
-      named_sync(2, 128);  // the room may hold converted queries again
+      if (po) continue;
+      async_fence();  // the staged rows are read by bulk copies
+      named_sync(1, kEpiThreads);
+      if (warp >= kQWarp0) {
+        const int h = threadIdx.x - kQWarp0 * 32;
+        if (h < I.heads) {
+          bulk_store(p.out + ((int64_t)I.row * p.H + I.h0 + h) * kLatentDim + half * 256, smem_addr(q_s) + h * kOPitch, kLatentDim);
+          asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+        }
+        if (half) named_sync(2, 128);  // the room may hold converted queries again
+        __syncwarp();
+      }
     }
     return true;
   };
@@ -341,6 +362,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     // ================= gather =================
     int it = 0;
     uint32_t g = 0;  // blocks so far
+    bool ok = true;
+    const uint8_t* const codes = p.cache.codes;
+    const uint8_t* const rope = reinterpret_cast<const uint8_t*>(p.cache.rope);
+    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
+      const int nb = sm->nb[it & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+      for (int j = 0; j < nb; ++j, ++g) {
+        const int st = (int)(g % kStages), ri = (int)(g % kRing);
+        if (!(ok = wait(&bar.ix_full[ri], (g / kRing) & 1))) break;
+        const int cc = lane & 7;
+        uint8_t* stage = kv_s + st * kStage;
+        // atom by atom (the rope atom is free first), 8 lanes per row, 4 rows per pass
+        int64_t row[4];
+        uint32_t dst[4], n[4];
+#pragma unroll
+        for (int pass = 0; pass < 4; ++pass) {
+          const int r = warp * 16 + pass * 4 + (lane >> 3);
+          row[pass] = sm->row[ri][r];
+          n[pass] = row[pass] >= 0 ? 16 : 0;  // a skipped row is filled with zeros
+          if (row[pass] < 0) row[pass] = 0;
+          dst[pass] = smem_addr(stage + r * 128 + ((cc ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          const int a = i == 0 ? 4 : i - 1;
+          ok &= mbar_wait<kPoll>(&bar.kv_empty[st][a], ((g / kStages) & 1) ^ 1, abort_flag, p.wait);
+#pragma unroll
+          for (int pass = 0; pass < 4; ++pass)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst[pass] + a * kAtom),
+                         "l"(a < 4 ? codes + row[pass] * kLatentDim + (a * 128 + cc * 16) : rope + row[pass] * (2 * kLatentRope) + cc * 16),
+                         "r"(n[pass])
+                         : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_addr(&bar.kv_full[st])) : "memory");
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      }
+    }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+  } else if (warp >= kIxWarp0) {
+    // ================= index: positions to cache rows and scales =================
+    int it = 0;
+    uint32_t g = 0;
     bool ok = true;
     for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
       const Item I = item_of(p, item);
@@ -363,68 +428,59 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       const int nbr = (last + kNB) / kNB;
       const int j0 = (int)((int64_t)I.split * nbr / p.splits);
       const int nb = (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0;
-      if (warp == 0) {
-        ok = wait(&bar.info_empty[it & 1], ((it >> 1) & 1) ^ 1);
-        if (ok && lane == 0) {
+      if (warp == kIxWarp0) {
+        if (!(ok = wait(&bar.info_empty[it & 1], ((it >> 1) & 1) ^ 1))) break;
+        if (lane == 0) {
           sm->nb[it & 1] = nb;
           mbar_arrive(&bar.info_full[it & 1]);
         }
       }
-      if (!ok || __any_sync(0xffffffffu, *abort_flag)) break;
-      if (nb == 0) continue;
-      const int rl = warp * 16 + (lane & 15);  // this lane's row of a block (lanes 16-31 repeat)
-      auto load_id = [&](int j) {
-        const int e = (j0 + j) * kNB + rl;
-        return j < nb && e < p.kk ? __ldg(irow + e) : -1;
-      };
-      auto resolve = [&](int id) -> int64_t {
-        if (id == -1) return -1;
-        const int64_t r = id >= 0 && id < p.S ? latent_row(p.cache, I.b, id) : -1;
-        if (r < 0 && lane < 16) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
-        return r;
-      };
-      // ids two blocks ahead, cache rows and scales one ahead
-      int id_n = load_id(1);
-      int64_t row = resolve(load_id(0));
-      float scale = row >= 0 ? __ldg(p.cache.scales + row) : 0.f;
-      for (int j = 0; j < nb; ++j, ++g) {
-        const int st = (int)(g % kStages);
-        const int id_nn = load_id(j + 2);
-        const int64_t row_n = resolve(id_n);
-        if (!(ok = wait(&bar.kv_empty[st], ((g / kStages) & 1) ^ 1))) break;
-        const int cc = lane & 7;
-        uint8_t* stage = kv_s + st * kStage;
+      auto load_ids = [&](int j, int (&id)[2]) {
 #pragma unroll
-        for (int pass = 0; pass < 4; ++pass) {
-          const int src_lane = pass * 4 + (lane >> 3);
-          const int64_t rr = __shfl_sync(0xffffffffu, row, src_lane);
-          const int r = warp * 16 + src_lane;
-          const uint32_t n = rr >= 0 ? 16 : 0;  // a skipped row is filled with zeros
-          const int64_t rs = rr >= 0 ? rr : 0;
-          const uint8_t* src = p.cache.codes + rs * kLatentDim + cc * 16;
-          const uint8_t* srr = reinterpret_cast<const uint8_t*>(p.cache.rope + rs * kLatentRope) + cc * 16;
-          const uint32_t dst = smem_addr(stage + r * 128 + ((cc ^ (r & 7)) << 4));
+        for (int u = 0; u < 2; ++u) {
+          const int e = (j0 + j) * kNB + u * 32 + lane;
+          id[u] = j < nb && e < p.kk ? __ldg(irow + e) : -1;
+        }
+      };
+      int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
+      int id[2];
+      load_ids(j, id);
+      for (; j < nb; j += 2) {
+        const uint32_t gj = g + j;
+        const int ri = (int)(gj % kRing);
+        int64_t row[2];
+        float scale[2];
 #pragma unroll
-          for (int a = 0; a < 5; ++a)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst + a * kAtom),
-                         "l"(a < 4 ? src + a * 128 : srr), "r"(n)
-                         : "memory");
+        for (int u = 0; u < 2; ++u) {
+          row[u] = id[u] >= 0 && id[u] < p.S ? latent_row(p.cache, I.b, id[u]) : -1;
+          if (row[u] < 0 && id[u] != -1) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
         }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_addr(&bar.kv_full[st])) : "memory");
-        const uint32_t some = __ballot_sync(0xffffffffu, row >= 0);
-        if (lane < 16) {
-          sm->sc[st][rl] = row >= 0 ? make_float2(scale, log2f(scale)) : make_float2(0.f, -INFINITY);
-          sm->isc[st][rl] = row >= 0 ? 1.f / scale : 0.f;
+        load_ids(j + 2, id);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          scale[u] = row[u] >= 0 ? __ldg(p.cache.scales + row[u]) : 0.f;
+          if (row[u] >= 0) {
+            const uint8_t* c = p.cache.codes + row[u] * kLatentDim;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) prefetch_l2(c + 128 * x);
+            prefetch_l2(p.cache.rope + row[u] * kLatentRope);
+          }
         }
-        if (lane == 0) sm->valid[st][warp] = some != 0;
+        if (!(ok = wait(&bar.ix_empty[ri], ((gj / kRing) & 1) ^ 1))) break;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = u * 32 + lane;
+          sm->row[ri][r] = row[u];
+          sm->sc[ri][r] = row[u] >= 0 ? make_float2(scale[u], log2f(scale[u])) : make_float2(0.f, -INFINITY);
+          sm->isc[ri][r] = row[u] >= 0 ? 1.f / scale[u] : 0.f;
+        }
+        const bool some = __any_sync(0xffffffffu, row[0] >= 0 || row[1] >= 0);
+        if (lane == 0) sm->valid[ri] = some;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.sc_full[st]);
-        row = row_n;
-        id_n = id_nn;
-        scale = row >= 0 ? __ldg(p.cache.scales + row) : 0.f;
+        if (lane == 0) mbar_arrive(&bar.ix_full[ri]);
       }
+      g += nb;
     }
-    asm volatile("cp.async.wait_all;\n" ::: "memory");
   } else if (warp == kSWarp) {
     // ================= score product =================
     const uint32_t id8 = idesc_mn(0, 0, 128, kNB), id16 = idesc_mn(1, 1, 128, kNB);
@@ -452,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           for (int k = 0; k < 4; ++k)
             mma_bf16_ts(tmem + kColS, tmem + kColQR + 8 * k, kd + (uint64_t)((4 * kAtom + k * 32) >> 4), id16, 1);
           mma_commit(&bar.s_full);
+          mma_commit(&bar.kv_empty[st][4]);
           if (j == nb - 1) mma_commit(&bar.q_empty);
         }
         __syncwarp();
@@ -480,10 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         const int st = (int)(g % kStages), pb = (int)(g & 1);
         if (!(ok = wait(&bar.p_full[pb], (g >> 1) & 1) && wait(&bar.kv_full[st], (g / kStages) & 1))) break;
         if (j > 0 && __any_sync(0xffffffffu, *reinterpret_cast<const volatile uint64_t*>(sm->need[pb]) != 0)) {
-          if (lane == 0) {
-            sm->cmd = (int)(g & 0x3fffffffu);
-            mbar_arrive(&bar.cmd_full);
-          }
+          // the O warps were told when the maxima were known
           if (!(ok = wait(&bar.corr_done, corr & 1))) break;
           ++corr;
         }
@@ -492,22 +546,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         if (elect_lane()) {
           const uint64_t vd = v_desc + (uint64_t)((st * kStage) >> 4), pd = p_desc + (uint64_t)((pb * kPBytes) >> 4);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // keys 0-31 and 32-63 by the hi terms, then by the lo terms
               mma_fp8(tmem + kColO + c * kHg, vd + (uint64_t)((c * kAtom + (k & 1) * 4096) >> 4),
                       pd + (uint64_t)((k * 32) >> 4), id8, (j | k) != 0);
-          mma_commit(&bar.kv_empty[st]);
+            mma_commit(&bar.kv_empty[st][c]);
+          }
           mma_commit(&bar.p_empty[pb]);
           if (j == nb - 1) mma_commit(&bar.o_full);
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (lane == 0) {
-        sm->cmd = -1;
-        mbar_arrive(&bar.cmd_full);
-      }
       ++oc;
     }
     if (elect_lane()) {
@@ -537,8 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       float M = -INFINITY, l = 0.f;
       int any_valid = 0;
       for (int j = 0; j < nb; ++j, ++g) {
-        const int st = (int)(g % kStages), pb = (int)(g & 1);
-        if (!(ok = wait(&bar.s_full, g & 1))) break;
+        const int ri = (int)(g % kRing), pb = (int)(g & 1);
+        // the block's scales are long there, P(g - 2) and its rescales are read: these waits do not
+        // stand between the scores and their softmax
+        if (!(ok = wait(&bar.ix_full[ri], (g / kRing) & 1) && wait(&bar.m_empty[pb], ((g >> 1) & 1) ^ 1) && wait(&bar.p_empty[pb], ((g >> 1) & 1) ^ 1) &&
+                   wait(&bar.s_full, g & 1)))
+          break;
         uint32_t r[32];
         tc_fence_after();
         tmem_ld_16x256b_x8(s_addr, r);
@@ -546,13 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.s_empty);
-        if (!(ok = wait(&bar.sc_full[st], (g / kStages) & 1))) break;
-        const int4 vv = *reinterpret_cast<const int4*>(sm->valid[st]);
-        any_valid |= vv.x | vv.y | vv.z | vv.w;
+        any_valid |= sm->valid[ri];
         float y[16], ymax = -INFINITY;
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
-          const float4 s = *reinterpret_cast<const float4*>(&sm->sc[st][8 * jj + 2 * m]);
+          const float4 s = *reinterpret_cast<const float4*>(&sm->sc[ri][8 * jj + 2 * m]);
           const float t0 = fmaf(__uint_as_float(r[4 * jj + 2]), 0.0625f, __uint_as_float(r[4 * jj]));
           const float t1 = fmaf(__uint_as_float(r[4 * jj + 3]), 0.0625f, __uint_as_float(r[4 * jj + 1]));
           y[2 * jj] = fmaf(t0, cq * s.x, s.y);
@@ -568,12 +621,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         M = Mn;
         const float Mu = M == -INFINITY ? 0.f : M;
         l *= alpha;
-        if (!(ok = wait(&bar.p_empty[pb], ((g >> 1) & 1) ^ 1))) break;
+        if (any && m == 0) sm->alpha[pb][hl] = alpha;
+        if (lane == 0) sm->need[pb][hgp] = (uint8_t)(any != 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.m_full[pb]);
         const uint32_t prow = smem_addr(p_s + pb * kPBytes + hl * 128) + 2 * m;
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
           const float p0 = ex2(y[2 * jj] - Mu), p1 = ex2(y[2 * jj + 1] - Mu);
-          const float2 is = *reinterpret_cast<const float2*>(&sm->isc[st][8 * jj + 2 * m]);
+          const float2 is = *reinterpret_cast<const float2*>(&sm->isc[ri][8 * jj + 2 * m]);
           l = fmaf(p0, is.x, l);
           l = fmaf(p1, is.y, l);
           const uint32_t h = f16x2(p0, p1);
@@ -583,11 +639,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((jj >> 1) ^ (hl & 7)) << 4)), "h"(hi) : "memory");
           asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((4 + (jj >> 1)) ^ (hl & 7)) << 4)), "h"(lo) : "memory");
         }
-        if (any && m == 0) sm->alpha[pb][hl] = alpha;
-        if (lane == 0) sm->need[pb][hgp] = (uint8_t)(any != 0);
         async_fence();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[pb]);
+        if (lane == 0) {
+          mbar_arrive(&bar.p_full[pb]);
+          mbar_arrive(&bar.ix_empty[ri]);
+        }
       }
       if (!ok) break;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
@@ -610,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     const int t = threadIdx.x - kOWarp0 * 32;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     int it = 0, oc = 0;
-    uint32_t cmds = 0;
+    uint32_t g = 0;
     bool ok = true;
     for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
       if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
@@ -628,36 +685,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         }
         continue;
       }
-      for (;;) {
-        if (!(ok = wait(&bar.cmd_full, cmds & 1))) break;
-        ++cmds;
-        const int cmd = *const_cast<volatile int*>(&sm->cmd);
-        if (cmd < 0) break;
-        // O^T is complete up to the block before: rescale the heads whose maximum rose
-        const uint32_t gp = (uint32_t)cmd - 1;
-        if (!(ok = wait(&bar.p_empty[gp & 1], (gp >> 1) & 1))) break;
-        tc_fence_after();
+      for (int j = 0; j < nb; ++j, ++g) {
+        // told at every block, when its maxima are known and its weights are not yet formed
+        if (!(ok = wait(&bar.m_full[g & 1], (g >> 1) & 1))) break;
+        const bool need = j > 0 && __any_sync(0xffffffffu, *reinterpret_cast<const volatile uint64_t*>(sm->need[g & 1]) != 0);
+        if (need) {
+          // O^T complete up to the block before: rescale the heads whose maximum rose
+          if (!(ok = wait(&bar.p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1))) break;
+          tc_fence_after();
 #pragma unroll 1
-        for (int w = 0; w < 8; ++w) {
-          if (!sm->need[cmd & 1][w]) continue;
-          const float4 a0 = *reinterpret_cast<const float4*>(&sm->alpha[cmd & 1][8 * w]);
-          const float4 a1 = *reinterpret_cast<const float4*>(&sm->alpha[cmd & 1][8 * w + 4]);
-          const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-          uint32_t v[4][8];
+          for (int w = 0; w < 8; ++w) {
+            if (!sm->need[g & 1][w]) continue;
+            const float4 a0 = *reinterpret_cast<const float4*>(&sm->alpha[g & 1][8 * w]);
+            const float4 a1 = *reinterpret_cast<const float4*>(&sm->alpha[g & 1][8 * w + 4]);
+            const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            uint32_t v[4][8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
-          tmem_wait_ld();
+            for (int c = 0; c < 4; ++c) tmem_ld_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
+            tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 4; ++c) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * a[i]);
-            tmem_st_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
+              for (int i = 0; i < 8; ++i) v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * a[i]);
+              tmem_st_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
+            }
           }
+          tmem_wait_stores();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.corr_done);
         }
-        tmem_wait_stores();
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.corr_done);
+        if (lane == 0) mbar_arrive(&bar.m_empty[g & 1]);
       }
       if (!ok || !(ok = epilogue(item, oc))) break;
       ++oc;
@@ -671,7 +730,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     const int hl = 16 * q4 + 8 * (lane >> 4) + (lane & 7);
     const bool lo = (lane & 8) != 0;
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-    uint4* mine = reinterpret_cast<uint4*>(q_s) + (warp - kQWarp0) * 32 + lane;  // word w at mine[128 w]
+    // this lane's row, 40 words of 16 bytes: the first in local memory, the others in shared memory
+    uint4* const mine = reinterpret_cast<uint4*>(q_s) + (warp - kQWarp0) * 32 + lane;
+    uint4 stash[kQLocal];
+    auto keep = [&](int w, uint4 v) {
+      if (w < kQLocal) stash[w] = v;
+      else mine[128 * (w - kQLocal)] = v;
+    };
+    // two words of this lane's row from what the two lanes of its head made: each has the hi and lo
+    // codes of one of the words
+    auto swap_keep = [&](int w, uint4 h, uint4 l) {
+      uint4 s = lo ? h : l, r;
+      r.x = __shfl_xor_sync(0xffffffffu, s.x, 8);
+      r.y = __shfl_xor_sync(0xffffffffu, s.y, 8);
+      r.z = __shfl_xor_sync(0xffffffffu, s.z, 8);
+      r.w = __shfl_xor_sync(0xffffffffu, s.w, 8);
+      keep(w, lo ? r : h);
+      keep(w + 1, lo ? l : r);
+    };
     int it = 0, oc = 0;
     int last = -1;  // the item whose O is still to be stored
     bool ok = true;
@@ -679,14 +755,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       const Item I = item_of(p, item);
       const uint4* q = reinterpret_cast<const uint4*>(p.q + I.b * p.q_sb + I.t * p.q_st + (int64_t)(I.h0 + hl) * kD);
       const bool live = hl < I.heads;
+      // the two lanes of a head take 16 values in turn and write both rows' codes
+      const int odd = lo ? 1 : 0;
       uint32_t top = 0;  // largest magnitude, as bf16 bits (a NaN is above every number)
 #pragma unroll 1
-      for (int c0 = 0; c0 < kD / 8; c0 += 8) {
-        uint4 v[8];
+      for (int c0 = 0; c0 < kD / 16; c0 += 12) {
+        uint4 v[12];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = live ? __ldg(q + c0 + u) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < 12; ++u) v[u] = live ? __ldg(q + 2 * (c0 + u) + odd) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 12; ++u) {
           top = __vmaxu2(top, v[u].x & 0x7fff7fffu);
           top = __vmaxu2(top, v[u].y & 0x7fff7fffu);
           top = __vmaxu2(top, v[u].z & 0x7fff7fffu);
@@ -694,69 +772,79 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         }
       }
       top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
       // the largest value's exponent e (not below -100): 2^(7 - e) brings it to [128, 256)
       const int e = max((int)(top >> 7) - 127, -100);
       const bool finite = (top >> 7) < 255;
       const float mul = finite ? __uint_as_float((uint32_t)(7 - e + 127) << 23) : __uint_as_float(0x7fc00000u);
       const uint32_t sixteen = 0x4c004c00u;  // f16 16.0 twice
 #pragma unroll 1
-      for (int c0 = 0; c0 < kLatentDim / 8; c0 += 8) {
+      for (int c0 = 0; c0 < kLatentDim / 16; c0 += 8) {  // words of 16 values; this lane: c0 + odd, + 2, ..
         uint4 v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = live ? __ldg(q + c0 + u) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < 8; ++u) v[u] = live ? __ldg(q + 2 * (c0 + odd + 2 * (u >> 1)) + (u & 1)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int u = 0; u < 8; u += 2) {
-          uint32_t w[4];
+          uint32_t wh[4], wl[4];
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             const uint4& a = v[u + (x >> 2)];
             const uint32_t two = (x & 3) == 0 ? a.x : (x & 3) == 1 ? a.y : (x & 3) == 2 ? a.z : a.w;
             const uint32_t h = f16x2(__uint_as_float(two << 16) * mul, __uint_as_float(two & 0xffff0000u) * mul);
-            const uint16_t hi = e4m3_of_f16x2(h);
-            const uint16_t rest = e4m3_of_f16x2(mul_f16x2(sub_f16x2(h, f16x2_of_e4m3(hi)), sixteen));
-            const uint32_t code = lo ? rest : hi;
-            if (x & 1) w[x >> 1] |= code << 16;
-            else w[x >> 1] = code;
+            const uint32_t hi = e4m3_of_f16x2(h);
+            const uint32_t rest = e4m3_of_f16x2(mul_f16x2(sub_f16x2(h, f16x2_of_e4m3((uint16_t)hi)), sixteen));
+            if (x & 1) {
+              wh[x >> 1] |= hi << 16;
+              wl[x >> 1] |= rest << 16;
+            } else {
+              wh[x >> 1] = hi;
+              wl[x >> 1] = rest;
+            }
           }
-          mine[128 * ((c0 + u) >> 1)] = make_uint4(w[0], w[1], w[2], w[3]);
+          swap_keep(c0 + u, make_uint4(wh[0], wh[1], wh[2], wh[3]), make_uint4(wl[0], wl[1], wl[2], wl[3]));
         }
       }
       // the lo row's rope part: 2^-40 of the hi row's, nothing beside it, so that an infinite rope
       // value of a key gives both rows the same infinity (zeros would make it a NaN)
-      const float mul_r = lo ? mul * 0x1p-40f : mul;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint4 v = live ? __ldg(q + kLatentDim / 8 + c) : make_uint4(0, 0, 0, 0);
-        uint32_t* x = &v.x;
+      for (int c = 0; c < 4; ++c) {
+        const uint4 v = live ? __ldg(q + kLatentDim / 8 + 2 * c + odd) : make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t xh[4], xl[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const __nv_bfloat162 b2 =
-              __floats2bfloat162_rn(__uint_as_float(x[u] << 16) * mul_r, __uint_as_float(x[u] & 0xffff0000u) * mul_r);
-          x[u] = *reinterpret_cast<const uint32_t*>(&b2);
+          const float a = __uint_as_float(x[u] << 16) * mul, b = __uint_as_float(x[u] & 0xffff0000u) * mul;
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b), l2 = __floats2bfloat162_rn(a * 0x1p-40f, b * 0x1p-40f);
+          xh[u] = *reinterpret_cast<const uint32_t*>(&h2);
+          xl[u] = *reinterpret_cast<const uint32_t*>(&l2);
         }
-        mine[128 * (32 + c)] = v;
+        swap_keep(32 + 2 * c, make_uint4(xh[0], xh[1], xh[2], xh[3]), make_uint4(xl[0], xl[1], xl[2], xl[3]));
       }
       ok = wait(&bar.info_full[it & 1], (it >> 1) & 1);
       const int nb = ok ? sm->nb[it & 1] : 0;
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
       if (ok && nb) {
+        uint32_t r[32];
+        auto fetch = [&](int s) {  // words 8 s .. 8 s + 7
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint4 v = 8 * s + u < kQLocal ? stash[8 * s + u] : mine[128 * (8 * s + u - kQLocal)];
+            r[4 * u] = v.x;
+            r[4 * u + 1] = v.y;
+            r[4 * u + 2] = v.z;
+            r[4 * u + 3] = v.w;
+          }
+        };
+        fetch(0);
         ok = wait(&bar.q_empty, (oc & 1) ^ 1);
         if (ok) {
           tc_fence_after();
           if (!lo) sm->qs[oc & 1][hl] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : 1.f;
-#pragma unroll 1
-          for (int s = 0; s < 5; ++s) {
-            uint32_t r[32];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const uint4 v = mine[128 * (8 * s + u)];
-              r[4 * u] = v.x;
-              r[4 * u + 1] = v.y;
-              r[4 * u + 2] = v.z;
-              r[4 * u + 3] = v.w;
-            }
+          for (int s = 0; s < 5; ++s) {
             tmem_st_x32(tmem + lane_base + kColQ + 32 * s, r);  // (the rope columns follow the codes')
+            if (s < 4) fetch(s + 1);
           }
           tmem_wait_stores();
           tc_fence_before();

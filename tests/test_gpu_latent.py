@@ -551,6 +551,31 @@ def test_latent_attn_empty_and_sparse_rows():
     _check_attn(dict(q=_q(2, 240, 64), cache=cache, scale=0.05), big)
 
 
+@pytest.mark.parametrize("T,H,S,k,mul", [(3000, 16, 2000, 700, 2.0), (1500, 64, 4000, 1500, 12.0), (2000, 70, 500, 64, 2.0)])
+def test_latent_attn_many_rows_per_cta(T, H, S, k, mul):
+    """Rows of every length, empty ones among them, one after another in each CTA: sampled rows
+    against 64 bits, the whole against a second run."""
+    cache = _cache(1, S, 64)
+    idx = _idx(1, T, S, k)
+    n = torch.randint(0, k + 1, (T,), generator=_gen(T), device=DEV)
+    n[::9], n[4::9], n[5::9] = 0, k, 1
+    n[100:400] = n[100:400].clamp(max=64)      # long runs of one-block and empty rows
+    n[200:230] = 0
+    idx[0][torch.arange(k, device=DEV) >= n[:, None]] = -1
+    at = dict(q=_q(1, T, H, mul), cache=cache, scale=1 / 24)
+    o, l = dsa.dsa_latent_attn(at, idx)
+    assert dsa.read_device_flags(DEV) == 0
+    for _ in range(3):
+        o2, l2 = dsa.dsa_latent_attn(at, idx)
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+    rows = torch.arange(0, T, T // 60, device=DEV)
+    ref, rl, tol = _attn64(dict(at, q=at["q"][:, rows]), idx[:, rows])
+    assert not bool(((o[:, rows].double() - ref).abs() > tol).any())
+    assert torch.equal(l[:, rows] == -math.inf, rl == -math.inf)
+    assert bool(((l[:, rows].double() - rl)[rl != -math.inf].abs() <= 2.0 ** -14 * (1 + rl[rl != -math.inf].abs())).all())
+    assert bool((o[0, n == 0] == 0).all()) and dsa.read_device_flags(DEV) == 0
+
+
 def test_latent_attn_repeated_positions_count_twice():
     cache = _cache(1, 50, 16)
     idx = torch.tensor([3, 3, 3, 9, 40, 40] * 30, device=DEV, dtype=torch.int32).reshape(1, 1, 180)
