@@ -20,7 +20,7 @@
 //
 // Persistent CTAs, one per SM, walk items (query, group of 64 heads, part of the row's blocks of 64
 // keys).  24 warps:
-//   22-23  take the blocks in turn, up to six ahead: resolve positions through the block table, read
+//   6-7    take the blocks in turn, up to six ahead: resolve positions through the block table, read
 //          the rows' scales, bring the rows to L2 (the three dependent loads a block took as long
 //          as its copies when the copying warps made them)
 //   0-3    copy the rows (16-byte cp.async) into four stages of 40 KB, five 128-byte-swizzled atoms
@@ -28,12 +28,12 @@
 //   4      S (hi and lo rows, 128 x 64) = Q K^T: A is Q in tensor memory, so the product reads only
 //          the codes from shared memory; 16 FP8 steps and 4 bf16 steps for the rope part
 //   5      O^T (512 x 64) += V^T P^T: four chunks of 128 dims, 2 key steps, hi and lo
-//   6-13   softmax: a warp holds 8 heads whole (their hi and lo rows lie in one 16-lane half of a
+//   8-15   softmax: a warp holds 8 heads whole (their hi and lo rows lie in one 16-lane half of a
 //          lane quarter), so maxima and sums never leave a quad of lanes and no barrier joins warps
-//   14-17  rescale O^T when a reference maximum rises (only the heads concerned)
-//   18-21  convert the next item's queries while the present one runs, and put them into tensor
+//   16-19  rescale O^T when a reference maximum rises (only the heads concerned)
+//   20-23  convert the next item's queries while the present one runs, and put them into tensor
 //          memory when its last score product is done
-//   14-21  normalise an item's O, while the softmax already runs the next item: bf16 rows go to the
+//   16-23  normalise an item's O, while the softmax already runs the next item: bf16 rows go to the
 //          room of the converted queries (free at that time) and out by bulk copies
 // The issuing warps run as whole warps on warp-uniform values and elect the issuing lane: operand
 // descriptors then stay in uniform registers.  Issued from a lane-0 branch, every product took 60
@@ -61,16 +61,20 @@ constexpr uint32_t kPBytes = kHg * 128;      // P: per head 64 hi bytes, then 64
 constexpr int kQVec = 40;                    // 16-byte words of a converted query row (512 + 128 bytes)
 constexpr int kQLocal = 22;                  // of these, kept in local memory (L1 / L2) until they are needed
 constexpr uint32_t kQBytes = (kQVec - kQLocal) * 128 * 16;
-constexpr int kGatherWarps = 4, kSWarp = 4, kPvWarp = 5, kSmWarp0 = 6, kSmWarps = 8, kOWarp0 = 14, kQWarp0 = 18;
-constexpr int kIxWarp0 = 22, kRing = 6;      // index warps, blocks they may be ahead
+constexpr int kGatherWarps = 4, kSWarp = 4, kPvWarp = 5, kIxWarp0 = 6, kSmWarp0 = 8, kSmWarps = 8, kOWarp0 = 16, kQWarp0 = 20;
+constexpr int kRing = 6;                     // blocks the index warps may be ahead
 constexpr int kThreads = 24 * 32;
+// Registers by warpgroup (warps 0-3, 4-7, ..), moved at the start from the kernel's own kRegs each;
+// the softmax warps spilled in their block loop at kRegs.
+constexpr int kRegs = 80, kRegsGather = 56, kRegsIssue = 64, kRegsSm = 112, kRegsO = 64, kRegsQ = 72;
+static_assert(kRegsGather + kRegsIssue + 2 * kRegsSm + kRegsO + kRegsQ <= 6 * kRegs, "registers the block is launched with");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColS = 448;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kTop = 8.75f, kAim = 4.f;    // raise M when y exceeds it by 8.75 (p <= 430); then the largest p is 2^4
 constexpr int kInfoReaders = kGatherWarps + 2 + kSmWarps + 4 + 4;
 constexpr int kEpiThreads = 256;             // O and query warps store an item's O together
-constexpr uint32_t kOPitch = kLatentDim + 64;  // staged half of an O row: neighbouring heads 16 banks apart
+constexpr uint32_t kOPitch = kLatentDim + 16;  // staged half of an O row: 8 heads' 16-byte pieces in 32 banks
 static_assert(kHg * kOPitch <= kQBytes, "halves of O are staged in the queries' room");
 
 struct Bars {
@@ -175,6 +179,14 @@ __device__ __forceinline__ void prefetch_l2(const void* src) {
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -238,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   const int G = (int)gridDim.x;
   // a wait that every lane of a warp makes, with one answer for the warp
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait<kPoll>(b, parity, abort_flag, p.wait));
+    return __all_sync(0xffffffffu, mbar_wait<kPoll, true>(b, parity, abort_flag, p.wait));
   };
 
   if (threadIdx.x == 0) {
@@ -301,36 +313,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
     tc_fence_after();
     float* po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
+    // a head without weights (sum 0): zeros, whatever the product left (rare, so one test for all)
+    const bool zeros = __any_sync(0xffffffffu, sm->lsum[oc & 1][lane] == 0.f || sm->lsum[oc & 1][lane + 32] == 0.f);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
+      const uint32_t o_addr = tmem + ((uint32_t)(q4 * 32) << 16) + kColO + (2 * half + cw) * kHg;
+      if (po) {  // fp32 rows of a part, straight out: lane = dim
 #pragma unroll 1
-      for (int h0 = 0; h0 < I.heads; h0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + kColO + (2 * half + cw) * kHg + h0, r);
-        tmem_wait_ld();
-        if (half && h0 == 0 && !po) named_sync(1, kEpiThreads);  // the first half has left the room
-        const float4* ls4 = reinterpret_cast<const float4*>(sm->lsum[oc & 1] + h0);
-        const int d = cw * 128 + q4 * 32 + lane;  // dim within the half
-        const uint32_t dst = smem_addr(q_s) + h0 * kOPitch + d * 2;
+        for (int h0 = 0; h0 < I.heads; h0 += 32) {
+          uint32_t r[32];
+          tmem_ld32(o_addr + h0, r);
+          tmem_wait_ld();
+          float* out = po + (int64_t)h0 * kLatentDim + half * 256 + cw * 128 + q4 * 32 + lane;
 #pragma unroll
-        for (int i4 = 0; i4 < 8; ++i4) {
-          const float4 L = ls4[i4];
-          const float lv[4] = {L.x, L.y, L.z, L.w};
-          float o[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) o[u] = lv[u] == 0.f ? 0.f : __uint_as_float(r[4 * i4 + u]) * lv[u];
-          if (po) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (h0 + 4 * i4 + u < I.heads) po[(int64_t)(h0 + 4 * i4 + u) * kLatentDim + half * 256 + d] = o[u];
-          } else {
-#pragma unroll
-            for (int u = 0; u < 4; u += 2) {
-              const __nv_bfloat162 w = __floats2bfloat162_rn(o[u], o[u + 1]);
-              asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + (4 * i4 + u) * kOPitch), "h"(__bfloat16_as_ushort(w.x)) : "memory");
-              asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + (4 * i4 + u + 1) * kOPitch), "h"(__bfloat16_as_ushort(w.y)) : "memory");
-            }
+          for (int i = 0; i < 32; ++i) {
+            const float L = sm->lsum[oc & 1][h0 + i];
+            if (h0 + i < I.heads) out[(int64_t)i * kLatentDim] = L == 0.f ? 0.f : __uint_as_float(r[i]) * L;
           }
+        }
+      } else {
+        // 16 dims x 64 heads at a time, as 8 x 8 tiles (rows: dims) that stmatrix stores transposed
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          uint32_t r[32];
+          tmem_ld_16x256b_x8(o_addr + ((uint32_t)(16 * x) << 16), r);
+          tmem_wait_ld();
+          if (half && x == 0) named_sync(1, kEpiThreads);  // the first half has left the room
+          const float* ls = sm->lsum[oc & 1] + 2 * (lane & 3);
+          const uint32_t dst = smem_addr(q_s) + (8 * (lane >> 4) + (lane & 7)) * kOPitch +
+                               2 * (cw * 128 + q4 * 32 + 16 * x + 8 * ((lane >> 3) & 1));
+          uint32_t w[16];
+#pragma unroll
+          for (int jj = 0; jj < 8; ++jj) {
+            const float2 L = *reinterpret_cast<const float2*>(ls + 8 * jj);
+            float o[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float f = u & 1 ? L.y : L.x;
+              o[u] = __uint_as_float(r[4 * jj + u]) * f;
+              if (zeros) o[u] = f == 0.f ? 0.f : o[u];
+            }
+            const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
+            w[2 * jj] = *reinterpret_cast<const uint32_t*>(&a);
+            w[2 * jj + 1] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+#pragma unroll
+          for (int jj = 0; jj < 8; jj += 2)
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + 8 * jj * kOPitch),
+                         "r"(w[2 * jj]), "r"(w[2 * jj + 1]), "r"(w[2 * jj + 2]), "r"(w[2 * jj + 3])
+                         : "memory");
         }
       }
       if (half) {
@@ -359,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   };
 
   if (warp < kGatherWarps) {
+    reg_dec<kRegsGather>();
     // ================= gather =================
     int it = 0;
     uint32_t g = 0;  // blocks so far
@@ -389,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
           const int a = i == 0 ? 4 : i - 1;
-          ok &= mbar_wait<kPoll>(&bar.kv_empty[st][a], ((g / kStages) & 1) ^ 1, abort_flag, p.wait);
+          ok &= mbar_wait<kPoll, true>(&bar.kv_empty[st][a], ((g / kStages) & 1) ^ 1, abort_flag, p.wait);
 #pragma unroll
           for (int pass = 0; pass < 4; ++pass)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst[pass] + a * kAtom),
@@ -402,171 +434,175 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       }
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
-  } else if (warp >= kIxWarp0) {
-    // ================= index: positions to cache rows and scales =================
-    int it = 0;
-    uint32_t g = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
-      const Item I = item_of(p, item);
-      const int32_t* irow = p.idx + I.b * p.idx_sb + I.t * p.idx_st;
-      // blocks of the row = 1 + (last entry other than -1) / 64, searched from the end
-      int last = -1;
-      for (int e0 = p.kk - 1; e0 >= 0 && last < 0; e0 -= 32 * 8) {
-        int v[8];
+  } else if (warp < kSmWarp0) {
+    reg_dec<kRegsIssue>();
+    if (warp == kSWarp) {
+      // ================= score product =================
+      const uint32_t id8 = idesc_mn(0, 0, 128, kNB), id16 = idesc_mn(1, 1, 128, kNB);
+      const uint64_t kv_desc = desc_sw128(smem_addr(kv_s));
+      int it = 0, oc = 0;
+      uint32_t g = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+        if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
+        const int nb = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
+        if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+        if (nb == 0) continue;
+        if (!(ok = wait(&bar.q_full, oc & 1))) break;
+        for (int j = 0; j < nb; ++j, ++g) {
+          const int st = (int)(g % kStages);
+          if (!(ok = wait(&bar.s_empty, (g & 1) ^ 1) && wait(&bar.kv_full[st], (g / kStages) & 1))) break;
+          async_fence();  // the stage was written by cp.async
+          tc_fence_after();
+          if (elect_lane()) {
+            const uint64_t kd = kv_desc + (uint64_t)((st * kStage) >> 4);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int e = e0 - u * 32 - lane;
-          v[u] = e >= 0 ? __ldg(irow + e) : -1;
-        }
+            for (int k = 0; k < 16; ++k)
+              mma_fp8_ts(tmem + kColS, tmem + kColQ + 8 * k, kd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), id8, k != 0);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const uint32_t bal = __ballot_sync(0xffffffffu, v[u] != -1);
-          if (last < 0 && bal) last = e0 - u * 32 - (__ffs(bal) - 1);
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_ts(tmem + kColS, tmem + kColQR + 8 * k, kd + (uint64_t)((4 * kAtom + k * 32) >> 4), id16, 1);
+            mma_commit(&bar.s_full);
+            mma_commit(&bar.kv_empty[st][4]);
+            if (j == nb - 1) mma_commit(&bar.q_empty);
+          }
+          __syncwarp();
         }
+        ++oc;
       }
-      const int nbr = (last + kNB) / kNB;
-      const int j0 = (int)((int64_t)I.split * nbr / p.splits);
-      const int nb = (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0;
-      if (warp == kIxWarp0) {
-        if (!(ok = wait(&bar.info_empty[it & 1], ((it >> 1) & 1) ^ 1))) break;
-        if (lane == 0) {
-          sm->nb[it & 1] = nb;
-          mbar_arrive(&bar.info_full[it & 1]);
-        }
+      if (elect_lane()) {  // the products issued here end before tensor memory is freed
+        mma_commit(&bar.drain[0]);
+        mbar_wait_drain(&bar.drain[0], 0);
       }
-      auto load_ids = [&](int j, int (&id)[2]) {
+      __syncwarp();
+    } else if (warp == kPvWarp) {
+      // ================= value product =================
+      const uint32_t id8 = idesc_mn(0, 0, 128, kHg) | (1u << 15);  // A: 128 dims, MN-major
+      const uint64_t v_desc = desc_sw128(smem_addr(kv_s)), p_desc = desc_sw128(smem_addr(p_s));
+      int it = 0, oc = 0, corr = 0;
+      uint32_t g = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+        if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
+        const int nb = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
+        if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+        if (nb == 0) continue;
+        if (!(ok = wait(&bar.o_empty, (oc & 1) ^ 1))) break;
+        for (int j = 0; j < nb; ++j, ++g) {
+          const int st = (int)(g % kStages), pb = (int)(g & 1);
+          if (!(ok = wait(&bar.p_full[pb], (g >> 1) & 1) && wait(&bar.kv_full[st], (g / kStages) & 1))) break;
+          if (j > 0 && __any_sync(0xffffffffu, *reinterpret_cast<const volatile uint64_t*>(sm->need[pb]) != 0)) {
+            // the O warps were told when the maxima were known
+            if (!(ok = wait(&bar.corr_done, corr & 1))) break;
+            ++corr;
+          }
+          async_fence();
+          tc_fence_after();
+          if (elect_lane()) {
+            const uint64_t vd = v_desc + (uint64_t)((st * kStage) >> 4), pd = p_desc + (uint64_t)((pb * kPBytes) >> 4);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int e = (j0 + j) * kNB + u * 32 + lane;
-          id[u] = j < nb && e < p.kk ? __ldg(irow + e) : -1;
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)  // keys 0-31 and 32-63 by the hi terms, then by the lo terms
+                mma_fp8(tmem + kColO + c * kHg, vd + (uint64_t)((c * kAtom + (k & 1) * 4096) >> 4),
+                        pd + (uint64_t)((k * 32) >> 4), id8, (j | k) != 0);
+              mma_commit(&bar.kv_empty[st][c]);
+            }
+            mma_commit(&bar.p_empty[pb]);
+            if (j == nb - 1) mma_commit(&bar.o_full);
+          }
+          __syncwarp();
         }
-      };
-      int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
-      int id[2];
-      load_ids(j, id);
-      for (; j < nb; j += 2) {
-        const uint32_t gj = g + j;
-        const int ri = (int)(gj % kRing);
-        int64_t row[2];
-        float scale[2];
+        if (!ok) break;
+        ++oc;
+      }
+      if (elect_lane()) {
+        mma_commit(&bar.drain[1]);
+        mbar_wait_drain(&bar.drain[1], 0);
+      }
+      __syncwarp();
+    } else {
+      // ================= index: positions to cache rows and scales =================
+      int it = 0;
+      uint32_t g = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+        const Item I = item_of(p, item);
+        const int32_t* irow = p.idx + I.b * p.idx_sb + I.t * p.idx_st;
+        // blocks of the row = 1 + (last entry other than -1) / 64, searched from the end
+        int last = -1;
+        for (int e0 = p.kk - 1; e0 >= 0 && last < 0; e0 -= 32 * 8) {
+          int v[8];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          row[u] = id[u] >= 0 && id[u] < p.S ? latent_row(p.cache, I.b, id[u]) : -1;
-          if (row[u] < 0 && id[u] != -1) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
-        }
-        load_ids(j + 2, id);
+          for (int u = 0; u < 8; ++u) {
+            const int e = e0 - u * 32 - lane;
+            v[u] = e >= 0 ? __ldg(irow + e) : -1;
+          }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          scale[u] = row[u] >= 0 ? __ldg(p.cache.scales + row[u]) : 0.f;
-          if (row[u] >= 0) {
-            const uint8_t* c = p.cache.codes + row[u] * kLatentDim;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) prefetch_l2(c + 128 * x);
-            prefetch_l2(p.cache.rope + row[u] * kLatentRope);
+          for (int u = 0; u < 8; ++u) {
+            const uint32_t bal = __ballot_sync(0xffffffffu, v[u] != -1);
+            if (last < 0 && bal) last = e0 - u * 32 - (__ffs(bal) - 1);
           }
         }
-        if (!(ok = wait(&bar.ix_empty[ri], ((gj / kRing) & 1) ^ 1))) break;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int r = u * 32 + lane;
-          sm->row[ri][r] = row[u];
-          sm->sc[ri][r] = row[u] >= 0 ? make_float2(scale[u], log2f(scale[u])) : make_float2(0.f, -INFINITY);
-          sm->isc[ri][r] = row[u] >= 0 ? 1.f / scale[u] : 0.f;
-        }
-        const bool some = __any_sync(0xffffffffu, row[0] >= 0 || row[1] >= 0);
-        if (lane == 0) sm->valid[ri] = some;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.ix_full[ri]);
-      }
-      g += nb;
-    }
-  } else if (warp == kSWarp) {
-    // ================= score product =================
-    const uint32_t id8 = idesc_mn(0, 0, 128, kNB), id16 = idesc_mn(1, 1, 128, kNB);
-    const uint64_t kv_desc = desc_sw128(smem_addr(kv_s));
-    int it = 0, oc = 0;
-    uint32_t g = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
-      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
-      const int nb = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
-      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
-      if (nb == 0) continue;
-      if (!(ok = wait(&bar.q_full, oc & 1))) break;
-      for (int j = 0; j < nb; ++j, ++g) {
-        const int st = (int)(g % kStages);
-        if (!(ok = wait(&bar.s_empty, (g & 1) ^ 1) && wait(&bar.kv_full[st], (g / kStages) & 1))) break;
-        async_fence();  // the stage was written by cp.async
-        tc_fence_after();
-        if (elect_lane()) {
-          const uint64_t kd = kv_desc + (uint64_t)((st * kStage) >> 4);
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            mma_fp8_ts(tmem + kColS, tmem + kColQ + 8 * k, kd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), id8, k != 0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16_ts(tmem + kColS, tmem + kColQR + 8 * k, kd + (uint64_t)((4 * kAtom + k * 32) >> 4), id16, 1);
-          mma_commit(&bar.s_full);
-          mma_commit(&bar.kv_empty[st][4]);
-          if (j == nb - 1) mma_commit(&bar.q_empty);
-        }
-        __syncwarp();
-      }
-      ++oc;
-    }
-    if (elect_lane()) {  // the products issued here end before tensor memory is freed
-      mma_commit(&bar.drain[0]);
-      mbar_wait_drain(&bar.drain[0], 0);
-    }
-    __syncwarp();
-  } else if (warp == kPvWarp) {
-    // ================= value product =================
-    const uint32_t id8 = idesc_mn(0, 0, 128, kHg) | (1u << 15);  // A: 128 dims, MN-major
-    const uint64_t v_desc = desc_sw128(smem_addr(kv_s)), p_desc = desc_sw128(smem_addr(p_s));
-    int it = 0, oc = 0, corr = 0;
-    uint32_t g = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
-      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
-      const int nb = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
-      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
-      if (nb == 0) continue;
-      if (!(ok = wait(&bar.o_empty, (oc & 1) ^ 1))) break;
-      for (int j = 0; j < nb; ++j, ++g) {
-        const int st = (int)(g % kStages), pb = (int)(g & 1);
-        if (!(ok = wait(&bar.p_full[pb], (g >> 1) & 1) && wait(&bar.kv_full[st], (g / kStages) & 1))) break;
-        if (j > 0 && __any_sync(0xffffffffu, *reinterpret_cast<const volatile uint64_t*>(sm->need[pb]) != 0)) {
-          // the O warps were told when the maxima were known
-          if (!(ok = wait(&bar.corr_done, corr & 1))) break;
-          ++corr;
-        }
-        async_fence();
-        tc_fence_after();
-        if (elect_lane()) {
-          const uint64_t vd = v_desc + (uint64_t)((st * kStage) >> 4), pd = p_desc + (uint64_t)((pb * kPBytes) >> 4);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // keys 0-31 and 32-63 by the hi terms, then by the lo terms
-              mma_fp8(tmem + kColO + c * kHg, vd + (uint64_t)((c * kAtom + (k & 1) * 4096) >> 4),
-                      pd + (uint64_t)((k * 32) >> 4), id8, (j | k) != 0);
-            mma_commit(&bar.kv_empty[st][c]);
+        const int nbr = (last + kNB) / kNB;
+        const int j0 = (int)((int64_t)I.split * nbr / p.splits);
+        const int nb = (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0;
+        if (warp == kIxWarp0) {
+          if (!(ok = wait(&bar.info_empty[it & 1], ((it >> 1) & 1) ^ 1))) break;
+          if (lane == 0) {
+            sm->nb[it & 1] = nb;
+            mbar_arrive(&bar.info_full[it & 1]);
           }
-          mma_commit(&bar.p_empty[pb]);
-          if (j == nb - 1) mma_commit(&bar.o_full);
         }
-        __syncwarp();
+        auto load_ids = [&](int j, int (&id)[2]) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int e = (j0 + j) * kNB + u * 32 + lane;
+            id[u] = j < nb && e < p.kk ? __ldg(irow + e) : -1;
+          }
+        };
+        int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
+        int id[2];
+        load_ids(j, id);
+        for (; j < nb; j += 2) {
+          const uint32_t gj = g + j;
+          const int ri = (int)(gj % kRing);
+          int64_t row[2];
+          float scale[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            row[u] = id[u] >= 0 && id[u] < p.S ? latent_row(p.cache, I.b, id[u]) : -1;
+            if (row[u] < 0 && id[u] != -1) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
+          }
+          load_ids(j + 2, id);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            scale[u] = row[u] >= 0 ? __ldg(p.cache.scales + row[u]) : 0.f;
+            if (row[u] >= 0) {
+              const uint8_t* c = p.cache.codes + row[u] * kLatentDim;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) prefetch_l2(c + 128 * x);
+              prefetch_l2(p.cache.rope + row[u] * kLatentRope);
+            }
+          }
+          if (!(ok = wait(&bar.ix_empty[ri], ((gj / kRing) & 1) ^ 1))) break;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int r = u * 32 + lane;
+            sm->row[ri][r] = row[u];
+            sm->sc[ri][r] = row[u] >= 0 ? make_float2(scale[u], log2f(scale[u])) : make_float2(0.f, -INFINITY);
+            sm->isc[ri][r] = row[u] >= 0 ? 1.f / scale[u] : 0.f;
+          }
+          const bool some = __any_sync(0xffffffffu, row[0] >= 0 || row[1] >= 0);
+          if (lane == 0) sm->valid[ri] = some;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.ix_full[ri]);
+        }
+        g += nb;
       }
-      if (!ok) break;
-      ++oc;
     }
-    if (elect_lane()) {
-      mma_commit(&bar.drain[1]);
-      mbar_wait_drain(&bar.drain[1], 0);
-    }
-    __syncwarp();
   } else if (warp < kOWarp0) {
+    reg_inc<kRegsSm>();
     // ================= softmax =================
     const int hgp = 2 * (warp & 3) + ((warp - kSmWarp0) >> 2);  // this warp's 8 heads
     const int hl = hgp * 8 + (lane >> 2), m = lane & 3;         // this thread's head; keys 8j + 2m + {0, 1}
@@ -663,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       ++oc;
     }
   } else if (warp < kQWarp0) {
+    reg_dec<kRegsO>();
     // ================= O^T: rescales, half of the epilogue =================
     const int t = threadIdx.x - kOWarp0 * 32;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -723,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
     meet_last(ok);
   } else {
+    reg_dec<kRegsQ>();
     // ================= queries: hi and lo rows; half of the epilogue =================
     // Lane 16 h + i (i < 8) of quarter q holds the hi row of head 16 q + 8 h + i, lane 16 h + 8 + i
     // its lo row, so that a softmax thread's one load gives it both.
@@ -945,8 +983,12 @@ cudaError_t launch_latent_attn(LatentAttnLaunch p, float* part, cudaStream_t st)
   }
   p.wait = wait_limit();
   auto kern = p.wait < kDefaultWaitCycles ? k_latent_attn<true> : k_latent_attn<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  // the register moves count on the registers that the block is launched with
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
+  if (fa.numRegs != kRegs) return cudaErrorInvalidKernelImage;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)) != cudaSuccess) return e;
   const int sms = device_sm_count();
   kern<<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, st>>>(p);
   count_launches(1);
