@@ -380,7 +380,7 @@ dsa_status dsa_norm_rope(const dsa_norm_rope_args* a, void* out, int64_t out_str
  *   at_position  0: token i of a sequence goes to row i (queries); else to the row of its
  *                position (the key cache).  Two tokens of one sequence at the same row leave it
  *                unspecified.
- * H * (d rounded up to 32, 64, 128, 256, 512 or 1024) <= 16384.  Needs DSA_WS_MIN bytes. */
+ * H * (d rounded up to 64, 128, 256 or 1024) <= 16384.  Needs DSA_WS_MIN bytes. */
 dsa_status dsa_norm_rope_e4m3(const dsa_norm_rope_args* a, uint8_t* codes, float* scales, int32_t S_cap,
                               int32_t at_position, void* ws, size_t ws_bytes, void* stream);
 

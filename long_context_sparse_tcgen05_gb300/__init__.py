@@ -271,7 +271,9 @@ def _flag_word(dev) -> torch.Tensor:
 def _launch(dev, fn, *args) -> None:
     """fn(*args, stream) on `dev`'s current stream, with `dev` current."""
     if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        if status:
+            _check(status)
     else:
         with torch.cuda.device(dev):
             _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))

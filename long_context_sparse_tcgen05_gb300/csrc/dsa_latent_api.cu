@@ -34,6 +34,12 @@ dsa_status done(cudaError_t e, const char* what) {
   return e == cudaSuccess ? DSA_OK : fail(DSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Kernels count a call's rows in 32 bits.
+dsa_status check_count(int64_t rows, int64_t per) {
+  if (rows > INT_MAX / per) return fail(DSA_ERR_UNSUPPORTED, "%lld tokens are too many for one call", (long long)rows);
+  return DSA_OK;
+}
+
 // Positions that the host knows: rows [pos0, pos0 + n) of `limit`.
 dsa_status check_range(int64_t pos0, int64_t n, int64_t limit, const char* what) {
   if (pos0 < 0 || (limit > 0 && pos0 > limit - n))
@@ -74,6 +80,9 @@ dsa_status norm_rope_launch(const dsa_norm_rope_args* a, dsa::NormRopeLaunch& P)
   if (!aligned(a->weight, 16) || !aligned(a->bias, 16))
     return fail(DSA_ERR_MISALIGNED, "weight and bias must be 16-byte aligned");
   if (!aligned(a->positions, 8)) return fail(DSA_ERR_MISALIGNED, "positions must be 8-byte aligned");
+  // (a warp of the kernel takes at least four heads of a token)
+  const dsa_status s = check_count((int64_t)a->B * a->n, a->H / 4 + 1);
+  if (s != DSA_OK) return s;
   P.B = a->B; P.n = a->n; P.H = a->H; P.d = a->d;
   P.x = static_cast<const uint16_t*>(a->x);
   P.x_sh = a->x_stride_h ? a->x_stride_h : a->d;
@@ -188,6 +197,7 @@ dsa_status dsa_latent_append(const dsa_latent_append_args* a, const dsa_latent_c
                              void* stream) {
   if (!a) return fail(DSA_ERR_INVALID_ARG, "append args are NULL");
   if (a->B < 1 || a->n < 0) return fail(DSA_ERR_INVALID_ARG, "B >= 1 and n >= 0 are required");
+  if (dsa_status c = check_count((int64_t)a->B * a->n, 1)) return c;
   if (!a->x) return fail(DSA_ERR_INVALID_ARG, "x is NULL");
   if (!a->cos != !a->sin) return fail(DSA_ERR_INVALID_ARG, "cos and sin go together");
   if (a->cos && a->max_pos < 1) return fail(DSA_ERR_INVALID_ARG, "max_pos must be >= 1");
@@ -219,8 +229,8 @@ dsa_status dsa_latent_read(const dsa_latent_cache* cache, int32_t B, int32_t n, 
                            void* ws, size_t ws_bytes, void* stream) {
   if (B < 1 || n < 0) return fail(DSA_ERR_INVALID_ARG, "B >= 1 and n >= 0 are required");
   dsa::LatentReadLaunch P{};
-  dsa_status s = cache_view(cache, B, P.cache);
-  if (s != DSA_OK) return s;
+  dsa_status s = check_count((int64_t)B * n, 1);
+  if (s != DSA_OK || (s = cache_view(cache, B, P.cache)) != DSA_OK) return s;
   if (!out) return fail(DSA_ERR_INVALID_ARG, "out is NULL");
   if (!aligned(out, 16) || !aligned(idx, 4)) return fail(DSA_ERR_MISALIGNED, "out must be 16-byte aligned, idx 4-byte");
   if (!idx && (s = check_range(pos0, n, P.cache.cap, "the cache")) != DSA_OK) return s;

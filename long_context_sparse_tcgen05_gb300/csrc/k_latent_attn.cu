@@ -43,6 +43,8 @@
 // joined by k_latent_combine.  Waits are bounded (DSA_FLAG_TIMEOUT).
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "dsa_internal.cuh"
 #include "latent_cache.cuh"
 #include "sm100.cuh"
@@ -971,6 +973,22 @@ size_t latent_attn_part_bytes(const LatentAttnLaunch& p, int splits) {
   return (size_t)p.B * p.T * ((p.H + kHg - 1) / kHg) * splits * kHg * (kLatentDim + 1) * sizeof(float);
 }
 
+// Once per device and instantiation: shared memory, and that the block is launched with the registers
+// that its warpgroups' moves count on.
+static cudaError_t prepare_kernel(void (*kern)(LatentAttnLaunch), int which) {
+  static std::atomic<bool> ready[64][2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && ready[dev][which].load(std::memory_order_acquire)) return cudaSuccess;
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+  if (fa.numRegs != kRegs) return cudaErrorInvalidKernelImage;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)) != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64) ready[dev][which].store(true, std::memory_order_release);
+  return cudaSuccess;
+}
+
 // part: room for latent_attn_part_bytes, or NULL: rows are not split.
 cudaError_t launch_latent_attn(LatentAttnLaunch p, float* part, cudaStream_t st) {
   TraceScope trace(kTraceAttention, st);
@@ -983,12 +1001,8 @@ cudaError_t launch_latent_attn(LatentAttnLaunch p, float* part, cudaStream_t st)
   }
   p.wait = wait_limit();
   auto kern = p.wait < kDefaultWaitCycles ? k_latent_attn<true> : k_latent_attn<false>;
-  // the register moves count on the registers that the block is launched with
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  cudaError_t e = prepare_kernel(kern, kern == k_latent_attn<true> ? 0 : 1);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != kRegs) return cudaErrorInvalidKernelImage;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)) != cudaSuccess) return e;
   const int sms = device_sm_count();
   kern<<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, st>>>(p);
   count_launches(1);

@@ -3,11 +3,10 @@
 // lane (two 16-byte loads) and one rotated pair, so the sum of squares and the largest magnitude
 // are warp shuffles.  HBM-bound: 1,152 bytes in and 644 out per appended token (the other way
 // round to read), plus a 256-byte table row.
-#include <cuda_bf16.h>
-
 #include <algorithm>
 
 #include "dsa_internal.cuh"
+#include "fp8_rows.cuh"
 #include "latent_cache.cuh"
 
 namespace dsa {
@@ -16,34 +15,16 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kMinScale = 0x1p-60f;  // rope / scale stays finite in bf16 for any sane rope value
 
-__device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&t);
-}
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
 __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p) {
   const int lane = threadIdx.x & 31;
-  float w[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = p.weight ? __ldg(p.weight + (e < 8 ? 0 : 256) + lane * 8 + (e & 7)) : 1.f;
-  const int64_t toks = (int64_t)p.B * p.n;
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t tok = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); tok < toks; tok += step) {
-    const int b = (int)(tok / p.n), i = (int)(tok - (int64_t)b * p.n);
-    const int64_t pos = p.positions ? p.positions[tok] : p.pos0 + i;
-    if (pos == -1) continue;
-    const int64_t row = pos >= 0 && (!p.cos || pos < p.max_pos) ? latent_row(p.cache, b, pos) : -1;
-    if (row < 0) {
-      if (lane == 0) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
-      continue;
-    }
+  const uint32_t toks = (uint32_t)p.B * p.n;  // (below 2^31: checked by the caller)
+  const uint32_t step = gridDim.x * (kThreads / 32);
+  uint32_t tok = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  // the next token's position is on its way while a token is worked on
+  int64_t next = p.positions && tok < toks ? __ldg(p.positions + tok) : 0;
+  for (; tok < toks; tok += step) {
+    const int b = (int)(tok / (uint32_t)p.n), i = (int)(tok - (uint32_t)b * (uint32_t)p.n);
+    // the row's values do not wait for its position and its page
     const uint16_t* x = p.x + b * p.x_sb + i * p.x_st;
     const uint4 r0 = __ldg(reinterpret_cast<const uint4*>(x) + lane);
     const uint4 r1 = __ldg(reinterpret_cast<const uint4*>(x) + 32 + lane);
@@ -57,6 +38,14 @@ __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p
     } else {
       a = bf_lo(__ldg(xr + lane));
       c = bf_lo(__ldg(xr + 32 + lane));
+    }
+    const int64_t pos = p.positions ? next : p.pos0 + i;
+    if (p.positions && tok + step < toks) next = __ldg(p.positions + tok + step);
+    if (pos == -1) continue;
+    const int64_t row = pos >= 0 && (!p.cos || pos < p.max_pos) ? latent_row(p.cache, b, pos) : -1;
+    if (row < 0) {
+      if (lane == 0) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
+      continue;
     }
     float cs = 1.f, sn = 0.f;
     if (p.cos) {
@@ -73,29 +62,38 @@ __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float f = rsqrtf(ss * (1.f / kLatentDim) + p.eps);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = y[e] * f * w[e];
+      for (int e4 = 0; e4 < 4; ++e4) {  // (from L1: 16 registers held for them cost a CTA per SM)
+        const float4 w = __ldg(reinterpret_cast<const float4*>(p.weight + (e4 >> 1) * 256 + lane * 8) + (e4 & 1));
+        y[4 * e4] *= f * w.x;
+        y[4 * e4 + 1] *= f * w.y;
+        y[4 * e4 + 2] *= f * w.z;
+        y[4 * e4 + 3] *= f * w.w;
+      }
     }
-    uint32_t amax = 0;  // magnitude bits: a NaN is above every number and so is kept
+    float amax = 0.f;  // (a NaN stays)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) amax = max(amax, __float_as_uint(y[e]) & 0x7fffffffu);
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    const float q = __uint_as_float(amax) / 448.f;
+    for (int e = 0; e < 16; e += 2) amax = max3_abs(amax, y[e], y[e + 1]);
+    // (the bits of a magnitude, NaN on top, order as integers)
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    const float q = amax / 448.f;
     const float scale = q < kMinScale ? kMinScale : q;  // (a NaN stays)
-    uint32_t k[4];
+    with_quotient(scale, [&](auto div) {
+      uint32_t k[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      k[e] = e4m3x2(y[4 * e] / scale, y[4 * e + 1] / scale) | e4m3x2(y[4 * e + 2] / scale, y[4 * e + 3] / scale) << 16;
-    uint8_t* codes = p.cache.codes + row * kLatentDim;
-    *reinterpret_cast<uint2*>(codes + lane * 8) = make_uint2(k[0], k[1]);
-    *reinterpret_cast<uint2*>(codes + 256 + lane * 8) = make_uint2(k[2], k[3]);
-    const float ra = (a * cs - c * sn) / scale, rc = (c * cs + a * sn) / scale;
-    uint16_t* rope = p.cache.rope + row * kLatentRope;
-    if (p.interleaved) {
-      reinterpret_cast<uint32_t*>(rope)[lane] = pack2(ra, rc);
-    } else {
-      rope[lane] = (uint16_t)pack2(ra, 0.f);
-      rope[32 + lane] = (uint16_t)pack2(rc, 0.f);
-    }
+      for (int e = 0; e < 4; ++e)
+        k[e] = pack_e4m3(div(y[4 * e]), div(y[4 * e + 1])) | pack_e4m3(div(y[4 * e + 2]), div(y[4 * e + 3])) << 16;
+      uint8_t* codes = p.cache.codes + row * kLatentDim;
+      *reinterpret_cast<uint2*>(codes + lane * 8) = make_uint2(k[0], k[1]);
+      *reinterpret_cast<uint2*>(codes + 256 + lane * 8) = make_uint2(k[2], k[3]);
+      const float ra = div(a * cs - c * sn), rc = div(c * cs + a * sn);
+      uint16_t* rope = p.cache.rope + row * kLatentRope;
+      if (p.interleaved) {
+        reinterpret_cast<uint32_t*>(rope)[lane] = pack_bf16(ra, rc);
+      } else {
+        rope[lane] = (uint16_t)pack_bf16(ra, 0.f);
+        rope[32 + lane] = (uint16_t)pack_bf16(rc, 0.f);
+      }
+    });
     if (lane == 0) p.cache.scales[row] = scale;
   }
 }
@@ -106,20 +104,20 @@ __device__ __forceinline__ uint4 dequant8(uint2 c, float s) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = e4m3x2_to_float2((uint16_t)((i < 2 ? c.x : c.y) >> ((i & 1) * 16)));
-    o[i] = pack2(f.x * s, f.y * s);
+    o[i] = pack_bf16(f.x * s, f.y * s);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 __global__ void __launch_bounds__(kThreads) k_latent_read(LatentReadLaunch p) {
   const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)p.B * p.n;
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t r = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += step) {
-    const int b = (int)(r / p.n), i = (int)(r - (int64_t)b * p.n);
+  const uint32_t rows = (uint32_t)p.B * p.n;  // (below 2^31: checked by the caller)
+  const uint32_t step = gridDim.x * (kThreads / 32);
+  for (uint32_t r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += step) {
+    const int b = (int)(r / (uint32_t)p.n), i = (int)(r - (uint32_t)b * (uint32_t)p.n);
     const int64_t pos = p.idx ? (int64_t)__ldg(p.idx + r) : p.pos0 + i;
     const int64_t row = pos >= 0 ? latent_row(p.cache, b, pos) : -1;
-    uint4* out = reinterpret_cast<uint4*>(p.out + r * (kLatentDim + kLatentRope));
+    uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)r * (kLatentDim + kLatentRope));
     if (row < 0) {
       if (pos != -1 && lane == 0) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
       out[lane] = out[32 + lane] = make_uint4(0, 0, 0, 0);
@@ -134,8 +132,8 @@ __global__ void __launch_bounds__(kThreads) k_latent_read(LatentReadLaunch p) {
     out[lane] = dequant8(c0, s);
     out[32 + lane] = dequant8(c1, s);
     if (lane < 8)
-      out[64 + lane] = make_uint4(pack2(bf_lo(rp.x) * s, bf_hi(rp.x) * s), pack2(bf_lo(rp.y) * s, bf_hi(rp.y) * s),
-                                  pack2(bf_lo(rp.z) * s, bf_hi(rp.z) * s), pack2(bf_lo(rp.w) * s, bf_hi(rp.w) * s));
+      out[64 + lane] = make_uint4(pack_bf16(bf_lo(rp.x) * s, bf_hi(rp.x) * s), pack_bf16(bf_lo(rp.y) * s, bf_hi(rp.y) * s),
+                                  pack_bf16(bf_lo(rp.z) * s, bf_hi(rp.z) * s), pack_bf16(bf_lo(rp.w) * s, bf_hi(rp.w) * s));
   }
 }
 

@@ -202,7 +202,7 @@ def test_norm_rope_of_constant_zero_and_non_finite_rows():
 E4M3_CASES = NORM_CASES + [
     (2, 9, 8, 576, "layer", 512, 64, False),
     (1, 3, 16, 1024, "rms", 0, 64, True),
-    (1, 3, 32, 512, "none", 0, 64, False),
+    (1, 3, 16, 512, "none", 0, 64, False),
     (3, 4, 1, 320, "rms", 0, 64, False),
     (3, 70, 1, 64, "layer", 0, 64, True),
     (2, 5, 2, 128, "none", 64, 64, False),
