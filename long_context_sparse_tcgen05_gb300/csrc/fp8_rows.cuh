@@ -31,28 +31,78 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+// ---- pairs of fp32 in one 64-bit register: one instruction for two values ---------------------
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float lo_of(f32x2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(f32x2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ f32x2 swapped(f32x2 v) { return pair(hi_of(v), lo_of(v)); }
+__device__ __forceinline__ f32x2 mul_2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add_2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma_2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// the two bf16 of a word
+__device__ __forceinline__ f32x2 unpack_bf16(uint32_t v) { return pair(bf_lo(v), bf_hi(v)); }
+
 // y / s for many y of a row, rounded as IEEE division rounds: with r the rounded reciprocal of s and
 // a = fl(y r), the remainder y - a s is exact in one fma, and fl(a + r (y - a s)) is the rounded
 // quotient (Markstein 1990, "Computation of elementary functions on the IBM RISC System/6000
-// processor", theorem on division) -- three instructions a value.  It needs a quotient and a
-// remainder inside the normal range: scales outside [2^-60, 2^60] (and NaN) divide; a quotient small
-// enough for its remainder to be subnormal is far below the least e4m3 value.
-// (with_quotient picks one of the two for a whole row.)
+// processor", theorem on division) -- three instructions a pair.  It needs a quotient and a remainder
+// inside the normal range: scales outside [2^-60, 2^60] (and NaN) divide; a quotient small enough for
+// its remainder to be subnormal is far below the least e4m3 value.  (with_quotient picks one of the
+// two for a whole row.)
 struct FastQuotient {
-  float s, r;
-  __device__ __forceinline__ float operator()(float y) const {
-    const float a = y * r;
-    return fmaf(fmaf(-a, s, y), r, a);
+  f32x2 minus_s, r;
+  __device__ __forceinline__ explicit FastQuotient(float s) : minus_s(pair(-s, -s)) {
+    const float q = 1.f / s;
+    r = pair(q, q);
+  }
+  __device__ __forceinline__ f32x2 operator()(f32x2 y) const {
+    const f32x2 a = mul_2(y, r);
+    return fma_2(fma_2(a, minus_s, y), r, a);
   }
 };
 struct PlainQuotient {
   float s;
-  __device__ __forceinline__ float operator()(float y) const { return y / s; }
+  __device__ __forceinline__ f32x2 operator()(f32x2 y) const { return pair(lo_of(y) / s, hi_of(y) / s); }
 };
 template <class F>
 __device__ __forceinline__ void with_quotient(float s, F&& f) {
-  if (s >= 0x1p-60f && s <= 0x1p60f) f(FastQuotient{s, 1.f / s});
+  if (s >= 0x1p-60f && s <= 0x1p60f) f(FastQuotient(s));
   else f(PlainQuotient{s});
 }
+// four quotients as e4m3 codes
+template <class Q>
+__device__ __forceinline__ uint32_t codes4(const Q& q, f32x2 a, f32x2 b) {
+  const f32x2 x = q(a), y = q(b);
+  return pack_e4m3(lo_of(x), hi_of(x)) | pack_e4m3(lo_of(y), hi_of(y)) << 16;
+}
+
+// Row r of a grid-stride walk over [B, n] rows as (sequence, row in it), without a division a step.
+struct RowWalk {
+  uint32_t b, i, db, di, n;
+  __device__ __forceinline__ RowWalk(uint32_t r, uint32_t step, uint32_t rows_per_seq)
+      : b(r / rows_per_seq), i(r - b * rows_per_seq), db(step / rows_per_seq), di(step - db * rows_per_seq), n(rows_per_seq) {}
+  __device__ __forceinline__ void next() {
+    b += db;
+    i += di;
+    if (i >= n) i -= n, ++b;
+  }
+};
 
 }  // namespace dsa

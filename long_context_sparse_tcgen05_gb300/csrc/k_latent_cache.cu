@@ -20,10 +20,11 @@ __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p
   const uint32_t toks = (uint32_t)p.B * p.n;  // (below 2^31: checked by the caller)
   const uint32_t step = gridDim.x * (kThreads / 32);
   uint32_t tok = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  RowWalk at_row(tok, step, p.n);
   // the next token's position is on its way while a token is worked on
   int64_t next = p.positions && tok < toks ? __ldg(p.positions + tok) : 0;
-  for (; tok < toks; tok += step) {
-    const int b = (int)(tok / (uint32_t)p.n), i = (int)(tok - (uint32_t)b * (uint32_t)p.n);
+  for (; tok < toks; tok += step, at_row.next()) {
+    const int b = (int)at_row.b, i = (int)at_row.i;
     // the row's values do not wait for its position and its page
     const uint16_t* x = p.x + b * p.x_sb + i * p.x_st;
     const uint4 r0 = __ldg(reinterpret_cast<const uint4*>(x) + lane);
@@ -52,46 +53,43 @@ __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p
       cs = __ldg(p.cos + pos * 32 + lane);
       sn = __ldg(p.sin + pos * 32 + lane);
     }
-    float y[16] = {bf_lo(r0.x), bf_hi(r0.x), bf_lo(r0.y), bf_hi(r0.y), bf_lo(r0.z), bf_hi(r0.z), bf_lo(r0.w), bf_hi(r0.w),
-                   bf_lo(r1.x), bf_hi(r1.x), bf_lo(r1.y), bf_hi(r1.y), bf_lo(r1.z), bf_hi(r1.z), bf_lo(r1.w), bf_hi(r1.w)};
+    f32x2 y[8] = {unpack_bf16(r0.x), unpack_bf16(r0.y), unpack_bf16(r0.z), unpack_bf16(r0.w),
+                  unpack_bf16(r1.x), unpack_bf16(r1.y), unpack_bf16(r1.z), unpack_bf16(r1.w)};
     if (p.weight) {
-      float ss = 0.f;
+      f32x2 s2 = 0;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) ss += y[e] * y[e];
+      for (int e = 0; e < 8; ++e) s2 = fma_2(y[e], y[e], s2);
+      float ss = lo_of(s2) + hi_of(s2);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float f = rsqrtf(ss * (1.f / kLatentDim) + p.eps);
+      const f32x2 f2 = pair(f, f);
 #pragma unroll
       for (int e4 = 0; e4 < 4; ++e4) {  // (from L1: 16 registers held for them cost a CTA per SM)
         const float4 w = __ldg(reinterpret_cast<const float4*>(p.weight + (e4 >> 1) * 256 + lane * 8) + (e4 & 1));
-        y[4 * e4] *= f * w.x;
-        y[4 * e4 + 1] *= f * w.y;
-        y[4 * e4 + 2] *= f * w.z;
-        y[4 * e4 + 3] *= f * w.w;
+        y[2 * e4] = mul_2(mul_2(y[2 * e4], f2), pair(w.x, w.y));
+        y[2 * e4 + 1] = mul_2(mul_2(y[2 * e4 + 1], f2), pair(w.z, w.w));
       }
     }
     float amax = 0.f;  // (a NaN stays)
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) amax = max3_abs(amax, y[e], y[e + 1]);
+    for (int e = 0; e < 8; ++e) amax = max3_abs(amax, lo_of(y[e]), hi_of(y[e]));
     // (the bits of a magnitude, NaN on top, order as integers)
     amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
     const float q = amax / 448.f;
     const float scale = q < kMinScale ? kMinScale : q;  // (a NaN stays)
     with_quotient(scale, [&](auto div) {
-      uint32_t k[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        k[e] = pack_e4m3(div(y[4 * e]), div(y[4 * e + 1])) | pack_e4m3(div(y[4 * e + 2]), div(y[4 * e + 3])) << 16;
       uint8_t* codes = p.cache.codes + row * kLatentDim;
-      *reinterpret_cast<uint2*>(codes + lane * 8) = make_uint2(k[0], k[1]);
-      *reinterpret_cast<uint2*>(codes + 256 + lane * 8) = make_uint2(k[2], k[3]);
-      const float ra = div(a * cs - c * sn), rc = div(c * cs + a * sn);
+      *reinterpret_cast<uint2*>(codes + lane * 8) = make_uint2(codes4(div, y[0], y[1]), codes4(div, y[2], y[3]));
+      *reinterpret_cast<uint2*>(codes + 256 + lane * 8) = make_uint2(codes4(div, y[4], y[5]), codes4(div, y[6], y[7]));
+      const f32x2 r = div(pair(a * cs - c * sn, c * cs + a * sn));
+      const uint32_t rr = pack_bf16(lo_of(r), hi_of(r));
       uint16_t* rope = p.cache.rope + row * kLatentRope;
       if (p.interleaved) {
-        reinterpret_cast<uint32_t*>(rope)[lane] = pack_bf16(ra, rc);
+        reinterpret_cast<uint32_t*>(rope)[lane] = rr;
       } else {
-        rope[lane] = (uint16_t)pack_bf16(ra, 0.f);
-        rope[32 + lane] = (uint16_t)pack_bf16(rc, 0.f);
+        rope[lane] = (uint16_t)rr;
+        rope[32 + lane] = (uint16_t)(rr >> 16);
       }
     });
     if (lane == 0) p.cache.scales[row] = scale;

@@ -18,16 +18,21 @@ namespace {
 constexpr int kThreads = 256;
 static_assert(DSA_NORM_NONE == 0 && DSA_NORM_RMS == 1 && DSA_NORM_LAYER == 2, "kNorm below");
 
+// A unit's 8 values, as pairs.
 struct Vec8 {
-  float v[8];
+  f32x2 p[4];
 };
 
 __device__ __forceinline__ Vec8 unpack8(uint4 r) {
-  return {{bf_lo(r.x), bf_hi(r.x), bf_lo(r.y), bf_hi(r.y), bf_lo(r.z), bf_hi(r.z), bf_lo(r.w), bf_hi(r.w)}};
+  return {{unpack_bf16(r.x), unpack_bf16(r.y), unpack_bf16(r.z), unpack_bf16(r.w)}};
+}
+__device__ __forceinline__ uint4 pack8(const Vec8& y) {
+  return make_uint4(pack_bf16(lo_of(y.p[0]), hi_of(y.p[0])), pack_bf16(lo_of(y.p[1]), hi_of(y.p[1])),
+                    pack_bf16(lo_of(y.p[2]), hi_of(y.p[2])), pack_bf16(lo_of(y.p[3]), hi_of(y.p[3])));
 }
 __device__ __forceinline__ Vec8 load_f8(const float* p) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+  return {{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
 }
 
 // A token's position, or -1 when the token is skipped.  p.limit: rows that a position may name (0:
@@ -54,45 +59,48 @@ template <int kNorm, int G, int U>
 __device__ __forceinline__ float2 head_stats(const NormRopeLaunch& p, const uint4 (&raw)[U], int l) {
   float mean = 0.f;
   if (kNorm == DSA_NORM_LAYER) {
-    float s = 0.f;
+    f32x2 s = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const Vec8 x = unpack8(raw[u]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += x.v[e];
+      for (int e = 0; e < 4; ++e) s = add_2(s, x.p[e]);
     }
-    mean = group_sum<G>(s) / (float)p.d;
+    mean = group_sum<G>(lo_of(s) + hi_of(s)) / (float)p.d;
   }
-  float ss = 0.f;  // squares about the mean: no cancellation between mean^2 and the second moment
+  f32x2 ss = 0;  // squares about the mean: no cancellation between mean^2 and the second moment
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if ((u * G + l) * 8 < p.d) {
       const Vec8 x = unpack8(raw[u]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += (x.v[e] - mean) * (x.v[e] - mean);
+      for (int e = 0; e < 4; ++e) {
+        const f32x2 c = kNorm == DSA_NORM_LAYER ? add_2(x.p[e], pair(-mean, -mean)) : x.p[e];
+        ss = fma_2(c, c, ss);
+      }
     }
   }
-  ss = group_sum<G>(ss);
-  return make_float2(mean, rsqrtf(ss / (float)p.d + p.eps));
+  return make_float2(mean, rsqrtf(group_sum<G>(lo_of(ss) + hi_of(ss)) / (float)p.d + p.eps));
 }
 
-// What a lane needs of a unit whatever its head: the norm's weights, and the cosines and sines of
-// the unit's pairs (interleaved: four of each).
+// What a lane needs of a unit whatever its head: the norm's weights, and the factors of its rotation
+// y <- y c + partner s (half-split: s negative in the first of a pair; interleaved: the partners are
+// the pairs' other values, c = (cos, cos) and s = (-sin, sin)).
 template <int kNorm>
 struct UnitTables {
-  float w[kNorm ? 8 : 1], b[kNorm == DSA_NORM_LAYER ? 8 : 1];
+  f32x2 w[kNorm ? 4 : 1], b[kNorm == DSA_NORM_LAYER ? 4 : 1];
   Vec8 c, s;
   __device__ __forceinline__ void affine(const NormRopeLaunch& p, int at) {
+    const f32x2 one = pair(1.f, 1.f);
     if constexpr (kNorm != DSA_NORM_NONE) {
-      const Vec8 one{{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}};
-      const Vec8 wv = p.weight ? load_f8(p.weight + at) : one;
+      const Vec8 wv = p.weight ? load_f8(p.weight + at) : Vec8{{one, one, one, one}};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = wv.v[e];
+      for (int e = 0; e < 4; ++e) w[e] = wv.p[e];
     }
     if constexpr (kNorm == DSA_NORM_LAYER) {
       const Vec8 bv = p.bias ? load_f8(p.bias + at) : Vec8{};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = bv.v[e];
+      for (int e = 0; e < 4; ++e) b[e] = bv.p[e];
     }
   }
   __device__ __forceinline__ void angles(const NormRopeLaunch& p, int at, int64_t pos) {
@@ -100,16 +108,15 @@ struct UnitTables {
     if (p.interleaved) {
       const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos + pos * half + (j >> 1)));
       const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin + pos * half + (j >> 1)));
-      c.v[0] = cv.x, c.v[1] = cv.y, c.v[2] = cv.z, c.v[3] = cv.w;
-      s.v[0] = sv.x, s.v[1] = sv.y, s.v[2] = sv.z, s.v[3] = sv.w;
+      c = {{pair(cv.x, cv.x), pair(cv.y, cv.y), pair(cv.z, cv.z), pair(cv.w, cv.w)}};
+      s = {{pair(-sv.x, sv.x), pair(-sv.y, sv.y), pair(-sv.z, sv.z), pair(-sv.w, sv.w)}};
     } else {
       const int64_t at_t = pos * half + (j < half ? j : j - half);
       c = load_f8(p.cos + at_t);
       s = load_f8(p.sin + at_t);
-      if (j < half) {  // the first of a pair takes its partner's sine part away
+      const f32x2 sign = j < half ? pair(-1.f, -1.f) : pair(1.f, 1.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s.v[e] = -s.v[e];
-      }
+      for (int e = 0; e < 4; ++e) s.p[e] = mul_2(s.p[e], sign);
     }
   }
 };
@@ -117,12 +124,11 @@ struct UnitTables {
 template <int kNorm>
 __device__ __forceinline__ Vec8 normed(uint4 raw, float2 st, const UnitTables<kNorm>& t) {
   Vec8 y = unpack8(raw);
-  if constexpr (kNorm == DSA_NORM_RMS) {
+  const f32x2 f = pair(st.y, st.y), m = pair(-st.x, -st.x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y.v[e] = y.v[e] * st.y * t.w[e];
-  } else if constexpr (kNorm == DSA_NORM_LAYER) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y.v[e] = (y.v[e] - st.x) * st.y * t.w[e] + t.b[e];
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (kNorm == DSA_NORM_RMS) y.p[e] = mul_2(mul_2(y.p[e], f), t.w[e]);
+    if constexpr (kNorm == DSA_NORM_LAYER) y.p[e] = fma_2(mul_2(add_2(y.p[e], m), f), t.w[e], t.b[e]);
   }
   return y;
 }
@@ -136,45 +142,37 @@ __device__ __forceinline__ int partner_at(const NormRopeLaunch& p, int at) {
   return at - p.rope_off < half ? at + half : at - half;
 }
 
-// Rotates a unit.  o: the (normed) values of its partner unit (half-split only).
-template <int kNorm>
-__device__ __forceinline__ void rotate(const NormRopeLaunch& p, Vec8& y, const Vec8& o, const UnitTables<kNorm>& t) {
-  if (p.interleaved) {
+__device__ __forceinline__ void rotate(Vec8& y, const Vec8& partner, const Vec8& c, const Vec8& s) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float a = y.v[2 * e], b = y.v[2 * e + 1];
-      y.v[2 * e] = a * t.c.v[e] - b * t.s.v[e];
-      y.v[2 * e + 1] = b * t.c.v[e] + a * t.s.v[e];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y.v[e] = y.v[e] * t.c.v[e] + o.v[e] * t.s.v[e];
-  }
+  for (int e = 0; e < 4; ++e) y.p[e] = fma_2(partner.p[e], s.p[e], mul_2(y.p[e], c.p[e]));
+}
+__device__ __forceinline__ Vec8 swapped8(const Vec8& y) {
+  return {{swapped(y.p[0]), swapped(y.p[1]), swapped(y.p[2]), swapped(y.p[3])}};
 }
 
 // The result of one unit of a head whose units are all in registers (U = 1): the partner comes from
-// its lane.  A whole warp calls it; lanes without a unit get what they do not use.
+// lane `src` of the group.  A whole warp calls it; lanes without a unit get what they do not use.
+// turn: the unit is rotated.
 template <int G, int kNorm>
-__device__ __forceinline__ Vec8 unit_result(const NormRopeLaunch& p, uint4 raw, float2 st, int l, const UnitTables<kNorm>& t) {
-  const int at = l * 8;
+__device__ __forceinline__ Vec8 unit_result(const NormRopeLaunch& p, uint4 raw, float2 st, int src, bool turn,
+                                            const UnitTables<kNorm>& t) {
   Vec8 y = normed<kNorm>(raw, st, t), o{};
   if (p.rope_dim > 0) {
-    const bool in = in_rope(p, at);
-    if (!p.interleaved) {
-      const int src = in ? partner_at(p, at) >> 3 : l;
-      if constexpr (kNorm) {
+    if (p.interleaved) {
+      o = swapped8(y);
+    } else if constexpr (kNorm != DSA_NORM_NONE) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = __shfl_sync(0xffffffffu, y.v[e], src, G);
-      } else {  // as the packed values they came in
-        uint4 q;
-        q.x = __shfl_sync(0xffffffffu, raw.x, src, G);
-        q.y = __shfl_sync(0xffffffffu, raw.y, src, G);
-        q.z = __shfl_sync(0xffffffffu, raw.z, src, G);
-        q.w = __shfl_sync(0xffffffffu, raw.w, src, G);
-        o = unpack8(q);
-      }
+      for (int e = 0; e < 4; ++e)
+        o.p[e] = pair(__shfl_sync(0xffffffffu, lo_of(y.p[e]), src, G), __shfl_sync(0xffffffffu, hi_of(y.p[e]), src, G));
+    } else {  // as the packed values they came in
+      uint4 q;
+      q.x = __shfl_sync(0xffffffffu, raw.x, src, G);
+      q.y = __shfl_sync(0xffffffffu, raw.y, src, G);
+      q.z = __shfl_sync(0xffffffffu, raw.z, src, G);
+      q.w = __shfl_sync(0xffffffffu, raw.w, src, G);
+      o = unpack8(q);
     }
-    if (in) rotate<kNorm>(p, y, o, t);
+    if (turn) rotate(y, o, t.c, t.s);
   }
   return y;
 }
@@ -187,13 +185,13 @@ __device__ __forceinline__ Vec8 unit_result_wide(const NormRopeLaunch& p, uint4 
   Vec8 y = normed<kNorm>(raw, st, t);
   if (p.rope_dim > 0 && in_rope(p, at)) {
     t.angles(p, at, pos);
-    Vec8 o{};
+    Vec8 o = swapped8(y);
     if (!p.interleaved) {
       UnitTables<kNorm> pt;
       pt.affine(p, partner_at(p, at));
       o = normed<kNorm>(partner, st, pt);
     }
-    rotate<kNorm>(p, y, o, t);
+    rotate(y, o, t.c, t.s);
   }
   return y;
 }
@@ -208,6 +206,8 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 4 : 2) k_norm_rope_bf16(Nor
   const uint32_t step = gridDim.x * (kThreads / 32);
   UnitTables<kNorm> tab;
   if (U == 1 && l * 8 < p.d) tab.affine(p, l * 8);
+  const bool turn = p.rope_dim > 0 && in_rope(p, l * 8);  // (U = 1: of this lane's unit)
+  const int src = turn ? partner_at(p, l * 8) >> 3 : l;
   for (uint32_t task = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); task < tasks; task += step) {
     const uint32_t tok = task / chunks;
     const int h0 = (int)(task - tok * chunks) * kHeads * R + hsub;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 4 : 2) k_norm_rope_bf16(Nor
       }
     const int64_t pos = checked_pos(p, p.positions ? __ldg(p.positions + tok) : p.pos0 + i, lane == 0 && h0 == 0);
     if (pos < 0) continue;  // uniform over the warp
-    if (U == 1 && p.rope_dim > 0 && in_rope(p, l * 8)) tab.angles(p, l * 8, pos);
+    if (U == 1 && turn) tab.angles(p, l * 8, pos);
     __syncwarp();  // in place: every load of these heads comes before their stores
     uint16_t* out = p.out + b * p.o_sb + i * p.o_st;
 #pragma unroll
@@ -239,11 +239,10 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 4 : 2) k_norm_rope_bf16(Nor
       for (int u = 0; u < U; ++u) {
         const int at = (u * G + l) * 8;
         Vec8 y;
-        if constexpr (U == 1) y = unit_result<G, kNorm>(p, raw[r][u], st, l, tab);
+        if constexpr (U == 1) y = unit_result<G, kNorm>(p, raw[r][u], st, src, turn, tab);
         if (h >= p.H || at >= p.d) continue;
         if constexpr (U > 1) y = unit_result_wide<kNorm>(p, raw[r][u], par[r][u], st, at, pos);
-        *reinterpret_cast<uint4*>(out + h * p.o_sh + at) = make_uint4(pack_bf16(y.v[0], y.v[1]), pack_bf16(y.v[2], y.v[3]),
-                                                                      pack_bf16(y.v[4], y.v[5]), pack_bf16(y.v[6], y.v[7]));
+        *reinterpret_cast<uint4*>(out + h * p.o_sh + at) = pack8(y);
       }
     }
   }
@@ -261,18 +260,22 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
   const uint32_t toks = (uint32_t)p.B * p.n;  // (below 2^31: checked by the caller)
   UnitTables<kNorm> tab;
   if (U == 1 && l * 8 < p.d) tab.affine(p, l * 8);
+  const bool turn = p.rope_dim > 0 && in_rope(p, l * 8);  // (U = 1: of this lane's unit)
+  const int src = turn ? partner_at(p, l * 8) >> 3 : l;
   // every thread of a warp runs the same number of steps: the shuffles below take whole warps
   const uint32_t step = gridDim.x * kTeams;
+  RowWalk at_row(blockIdx.x * kTeams + threadIdx.x / kTeam, step, p.n);
   // the next token's position is on its way while a token is worked on
-  auto position = [&](uint32_t tok) -> int64_t {
+  auto position = [&](uint32_t tok, uint32_t i) -> int64_t {
     if (tok >= toks) return -1;
-    return p.positions ? __ldg(p.positions + tok) : p.pos0 + tok % (uint32_t)p.n;
+    return p.positions ? __ldg(p.positions + tok) : p.pos0 + i;
   };
-  int64_t next = position(blockIdx.x * kTeams + threadIdx.x / kTeam);
+  int64_t next = position(blockIdx.x * kTeams + threadIdx.x / kTeam, at_row.i);
   for (uint32_t base = blockIdx.x * kTeams; base < toks; base += step) {
     const uint32_t tok = base + threadIdx.x / kTeam;
     const bool live = tok < toks;
-    const int b = live ? (int)(tok / (uint32_t)p.n) : 0, i = live ? (int)(tok - (uint32_t)b * (uint32_t)p.n) : 0;
+    const int b = live ? (int)at_row.b : 0, i = live ? (int)at_row.i : 0;
+    at_row.next();
     const uint16_t* x = p.x + b * p.x_sb + i * p.x_st;
     uint4 raw[NP][U];
 #pragma unroll
@@ -284,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
         raw[s][u] = in ? __ldg(reinterpret_cast<const uint4*>(x + h * p.x_sh + at)) : make_uint4(0, 0, 0, 0);
       }
     const int64_t pos = checked_pos(p, next, t == 0);
-    next = position(tok + step);
-    if (U == 1 && pos >= 0 && p.rope_dim > 0 && in_rope(p, l * 8)) tab.angles(p, l * 8, pos);
+    next = position(tok + step, at_row.i);
+    if (U == 1 && pos >= 0 && turn) tab.angles(p, l * 8, pos);
     Vec8 y[NP][U];
     float amax = 0.f;  // (a NaN stays)
 #pragma unroll
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
       for (int u = 0; u < U; ++u) {
         const int at = (u * G + l) * 8;
         const bool in = pos >= 0 && h < p.H && at < p.d;
-        if constexpr (U == 1) y[s][u] = unit_result<G, kNorm>(p, raw[s][u], st, l, tab);
+        if constexpr (U == 1) y[s][u] = unit_result<G, kNorm>(p, raw[s][u], st, src, turn, tab);
         if (!in) continue;
         if constexpr (U > 1) {
           const uint4 par = !p.interleaved && p.rope_dim > 0 && in_rope(p, at)
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
           y[s][u] = unit_result_wide<kNorm>(p, raw[s][u], par, st, at, pos);
         }
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) amax = max3_abs(amax, y[s][u].v[e], y[s][u].v[e + 1]);
+        for (int e = 0; e < 4; ++e) amax = max3_abs(amax, lo_of(y[s][u].p[e]), hi_of(y[s][u].p[e]));
       }
     }
     constexpr int kShfl = kTeam < 32 ? kTeam : 32;
@@ -330,10 +333,8 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
         for (int u = 0; u < U; ++u) {
           const int h = hsub + s * kHeads, at = (u * G + l) * 8;
           if (h >= p.H || at >= p.d) continue;
-          const float* v = y[s][u].v;
-          const uint32_t lo = pack_e4m3(div(v[0]), div(v[1])) | pack_e4m3(div(v[2]), div(v[3])) << 16;
-          const uint32_t hi = pack_e4m3(div(v[4]), div(v[5])) | pack_e4m3(div(v[6]), div(v[7])) << 16;
-          *reinterpret_cast<uint2*>(codes + (int64_t)h * p.d + at) = make_uint2(lo, hi);
+          const f32x2* v = y[s][u].p;
+          *reinterpret_cast<uint2*>(codes + (int64_t)h * p.d + at) = make_uint2(codes4(div, v[0], v[1]), codes4(div, v[2], v[3]));
         }
     });
     if (t == 0) p.scales[dst] = scale;
