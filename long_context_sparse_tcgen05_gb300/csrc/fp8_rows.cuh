@@ -105,4 +105,17 @@ struct RowWalk {
   }
 };
 
+// 16 bytes from global to shared memory behind the thread's back (zeros where !in), groups of them,
+// and the wait for all but the newest N groups.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
 }  // namespace dsa

@@ -15,44 +15,77 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kMinScale = 0x1p-60f;  // rope / scale stays finite in bf16 for any sane rope value
 
+// Everything a token needs is on its way while the one before it is worked on: its 1,152 bytes in
+// the warp's part of shared memory, its angles and block table entry in registers (its position one
+// token earlier still).  Loaded when its turn came, a token took a warp three dependent loads.
 __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p) {
-  const int lane = threadIdx.x & 31;
+  constexpr int kRow = kLatentDim + kLatentRope;
+  __shared__ alignas(16) uint16_t rows[2][kThreads / 32][kRow];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t toks = (uint32_t)p.B * p.n;  // (below 2^31: checked by the caller)
-  const uint32_t step = gridDim.x * (kThreads / 32);
-  uint32_t tok = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  RowWalk at_row(tok, step, p.n);
-  // the next token's position is on its way while a token is worked on
-  int64_t next = p.positions && tok < toks ? __ldg(p.positions + tok) : 0;
-  for (; tok < toks; tok += step, at_row.next()) {
-    const int b = (int)at_row.b, i = (int)at_row.i;
-    // the row's values do not wait for its position and its page
-    const uint16_t* x = p.x + b * p.x_sb + i * p.x_st;
-    const uint4 r0 = __ldg(reinterpret_cast<const uint4*>(x) + lane);
-    const uint4 r1 = __ldg(reinterpret_cast<const uint4*>(x) + 32 + lane);
-    // rope pair `lane`: values (2 lane, 2 lane + 1) or (lane, lane + 32)
-    const uint16_t* xr = x + kLatentDim;
-    float a, c;
-    if (p.interleaved) {
-      const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(xr) + lane);
-      a = bf_lo(v);
-      c = bf_hi(v);
-    } else {
-      a = bf_lo(__ldg(xr + lane));
-      c = bf_lo(__ldg(xr + 32 + lane));
+  const uint32_t step = gridDim.x * (kThreads / 32), first = blockIdx.x * (kThreads / 32) + warp;
+  struct Ahead {
+    int64_t pos;      // -1: skipped, -2: to be flagged
+    int64_t in_page;  // offset in the page (without a table: the cache row)
+    int page;
+    float cs, sn;
+  };
+  auto position = [&](uint32_t tok, uint32_t i) -> int64_t {
+    if (tok >= toks) return -1;
+    return p.positions ? __ldg(p.positions + tok) : p.pos0 + i;
+  };
+  auto fetch = [&](uint32_t tok, const RowWalk& w, int64_t pos, int slot) -> Ahead {
+    Ahead a{pos, 0, 0, 1.f, 0.f};
+    const uint16_t* x = tok < toks ? p.x + w.b * p.x_sb + w.i * p.x_st : p.x;
+    uint16_t* dst = rows[slot][warp];
+    copy16_async(dst + 8 * lane, x + 8 * lane, tok < toks);
+    copy16_async(dst + 256 + 8 * lane, x + 256 + 8 * lane, tok < toks);
+    if (lane < 8) copy16_async(dst + 512 + 8 * lane, x + 512 + 8 * lane, tok < toks);
+    copies_commit();
+    if (pos == -1) return a;
+    if (pos < 0 || pos >= p.cache.cap || (p.cos && pos >= p.max_pos)) {
+      a.pos = -2;
+      return a;
     }
-    const int64_t pos = p.positions ? next : p.pos0 + i;
-    if (p.positions && tok + step < toks) next = __ldg(p.positions + tok + step);
-    if (pos == -1) continue;
-    const int64_t row = pos >= 0 && (!p.cos || pos < p.max_pos) ? latent_row(p.cache, b, pos) : -1;
-    if (row < 0) {
+    if (p.cache.table) {
+      const uint32_t in_seq = (uint32_t)pos / (uint32_t)p.cache.page_size;
+      a.in_page = (uint32_t)pos - in_seq * (uint32_t)p.cache.page_size;
+      a.page = __ldg(p.cache.table + (int64_t)w.b * p.cache.table_ld + in_seq);
+    } else {
+      a.page = (int)w.b;
+      a.in_page = pos;
+    }
+    if (p.cos) {
+      a.cs = __ldg(p.cos + pos * 32 + lane);
+      a.sn = __ldg(p.sin + pos * 32 + lane);
+    }
+    return a;
+  };
+  RowWalk w(first, step, p.n);
+  Ahead nxt = fetch(first, w, position(first, w.i), 0);
+  w.next();
+  int64_t pos_next = position(first + step, w.i);
+  int slot = 0;
+  for (uint32_t tok = first; tok < toks; tok += step, slot ^= 1) {
+    const Ahead now = nxt;
+    nxt = fetch(tok + step, w, pos_next, slot ^ 1);
+    w.next();
+    pos_next = position(tok + 2 * step, w.i);
+    copies_wait<1>();
+    __syncwarp();
+    const uint16_t* x = rows[slot][warp];
+    const uint4 r0 = *reinterpret_cast<const uint4*>(x + 8 * lane), r1 = *reinterpret_cast<const uint4*>(x + 256 + 8 * lane);
+    // rope pair `lane`: values (2 lane, 2 lane + 1) or (lane, lane + 32)
+    const uint16_t* xr = x + kLatentDim + (p.interleaved ? 2 * lane : lane);
+    const float a = bf_lo(xr[0]), c = bf_lo(xr[p.interleaved ? 1 : 32]);
+    __syncwarp();  // the slot may be filled again
+    if (now.pos == -1) continue;
+    if (now.pos < 0 || now.page < 0 || now.page >= p.cache.n_pages) {
       if (lane == 0) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
       continue;
     }
-    float cs = 1.f, sn = 0.f;
-    if (p.cos) {
-      cs = __ldg(p.cos + pos * 32 + lane);
-      sn = __ldg(p.sin + pos * 32 + lane);
-    }
+    const int64_t row = (int64_t)now.page * p.cache.page_size + now.in_page;
+    const float cs = now.cs, sn = now.sn;
     f32x2 y[8] = {unpack_bf16(r0.x), unpack_bf16(r0.y), unpack_bf16(r0.z), unpack_bf16(r0.w),
                   unpack_bf16(r1.x), unpack_bf16(r1.y), unpack_bf16(r1.z), unpack_bf16(r1.w)};
     if (p.weight) {

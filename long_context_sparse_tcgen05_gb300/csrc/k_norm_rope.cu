@@ -254,6 +254,10 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 4 : 2) k_norm_rope_bf16(Nor
 template <int G, int U, int NP, int kTeam, int kNorm>
 __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m3(NormRopeLaunch p) {
   __shared__ float team_max[kThreads / 32];
+  // each thread's units of the next token, copied while a token is worked on (not for the widest
+  // tokens, whose registers hold them off the SM anyway)
+  constexpr bool kAhead = NP * U <= 4;
+  __shared__ uint4 ahead[kAhead ? 2 : 1][kAhead ? NP * U : 1][kThreads];
   constexpr int kTeams = kThreads / kTeam;  // tokens per CTA
   constexpr int kHeads = kTeam / G;         // heads per pass
   const int lane = threadIdx.x & 31, t = threadIdx.x % kTeam, l = t % G, hsub = t / G;
@@ -270,25 +274,57 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
     if (tok >= toks) return -1;
     return p.positions ? __ldg(p.positions + tok) : p.pos0 + i;
   };
-  int64_t next = position(blockIdx.x * kTeams + threadIdx.x / kTeam, at_row.i);
+  const uint32_t first = blockIdx.x * kTeams + threadIdx.x / kTeam;
+  int64_t next = position(first, at_row.i);
+  // unit (s, u) of the token at row w, and whether there is one
+  auto unit_at = [&](uint32_t tok, const RowWalk& w, int s, int u, bool& in) -> const uint16_t* {
+    const int h = hsub + s * kHeads, at = (u * G + l) * 8;
+    in = tok < toks && h < p.H && at < p.d;
+    return in ? p.x + w.b * p.x_sb + w.i * p.x_st + h * p.x_sh + at : p.x;
+  };
+  auto fetch = [&](uint32_t tok, const RowWalk& w, int slot) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int s = 0; s < NP; ++s)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          bool in;
+          const uint16_t* src = unit_at(tok, w, s, u, in);
+          copy16_async(&ahead[slot][s * U + u][threadIdx.x], src, in);
+        }
+      copies_commit();
+    }
+  };
+  fetch(first, at_row, 0);
+  int slot = 0;
   for (uint32_t base = blockIdx.x * kTeams; base < toks; base += step) {
     const uint32_t tok = base + threadIdx.x / kTeam;
     const bool live = tok < toks;
     const int b = live ? (int)at_row.b : 0, i = live ? (int)at_row.i : 0;
-    at_row.next();
-    const uint16_t* x = p.x + b * p.x_sb + i * p.x_st;
     uint4 raw[NP][U];
+    if constexpr (!kAhead) {
 #pragma unroll
-    for (int s = 0; s < NP; ++s)
+      for (int s = 0; s < NP; ++s)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hsub + s * kHeads, at = (u * G + l) * 8;
-        const bool in = live && h < p.H && at < p.d;
-        raw[s][u] = in ? __ldg(reinterpret_cast<const uint4*>(x + h * p.x_sh + at)) : make_uint4(0, 0, 0, 0);
-      }
+        for (int u = 0; u < U; ++u) {
+          bool in;
+          const uint16_t* src = unit_at(tok, at_row, s, u, in);
+          raw[s][u] = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    at_row.next();
     const int64_t pos = checked_pos(p, next, t == 0);
     next = position(tok + step, at_row.i);
     if (U == 1 && pos >= 0 && turn) tab.angles(p, l * 8, pos);
+    if constexpr (kAhead) {
+      fetch(tok + step, at_row, slot ^ 1);
+      copies_wait<1>();
+#pragma unroll
+      for (int s = 0; s < NP; ++s)
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[s][u] = ahead[slot][s * U + u][threadIdx.x];
+      slot ^= 1;
+    }
     Vec8 y[NP][U];
     float amax = 0.f;  // (a NaN stays)
 #pragma unroll
@@ -303,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
         if (!in) continue;
         if constexpr (U > 1) {
           const uint4 par = !p.interleaved && p.rope_dim > 0 && in_rope(p, at)
-                                ? __ldg(reinterpret_cast<const uint4*>(x + h * p.x_sh + partner_at(p, at)))
+                                ? __ldg(reinterpret_cast<const uint4*>(p.x + b * p.x_sb + i * p.x_st + h * p.x_sh + partner_at(p, at)))
                                 : make_uint4(0, 0, 0, 0);
           y[s][u] = unit_result_wide<kNorm>(p, raw[s][u], par, st, at, pos);
         }
