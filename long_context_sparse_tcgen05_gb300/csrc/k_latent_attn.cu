@@ -23,7 +23,7 @@
 //   6-7    take the blocks in turn, up to six ahead: resolve positions through the block table, read
 //          the rows' scales, bring the rows to L2 (the three dependent loads a block took as long
 //          as its copies when the copying warps made them)
-//   0-3    copy the rows (16-byte cp.async) into four stages of 40 KB, five 128-byte-swizzled atoms
+//   0-3    copy the rows (16-byte cp.async) into three stages of 40 KB, five 128-byte-swizzled atoms
 //          each, an atom as soon as the products have released it
 //   4      S (hi and lo rows, 128 x 64) = Q K^T: A is Q in tensor memory, so the product reads only
 //          the codes from shared memory; 16 FP8 steps and 4 bf16 steps for the rope part
@@ -55,14 +55,14 @@ using namespace sm100;
 
 constexpr int kHg = 64;                      // heads of an item
 constexpr int kNB = 64;                      // keys of a block
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kD = kLatentDim + kLatentRope;
 constexpr uint32_t kAtom = kNB * 128;        // 64 rows of 128 bytes
 constexpr uint32_t kStage = 5 * kAtom;       // four atoms of codes, one of rope values
 constexpr uint32_t kPBytes = kHg * 128;      // P: per head 64 hi bytes, then 64 lo bytes
-constexpr int kQVec = 40;                    // 16-byte words of a converted query row (512 + 128 bytes)
-constexpr int kQLocal = 22;                  // of these, kept in local memory (L1 / L2) until they are needed
-constexpr uint32_t kQBytes = (kQVec - kQLocal) * 128 * 16;
+// Converted queries: 128 rows (hi and lo of 64 heads) of 512 codes, then of 64 bf16 rope values, the
+// 16-byte words of a row permuted by the row's low bits (a lane reads its row word by word).
+constexpr uint32_t kQCodes = 128 * kLatentDim, kQBytes = kQCodes + 128 * kLatentRope * 2;
 constexpr int kGatherWarps = 4, kSWarp = 4, kPvWarp = 5, kIxWarp0 = 6, kSmWarp0 = 8, kSmWarps = 8, kOWarp0 = 16, kQWarp0 = 20;
 constexpr int kRing = 6;                     // blocks the index warps may be ahead
 constexpr int kThreads = 24 * 32;
@@ -99,7 +99,7 @@ struct Small {
   int valid[kRing];                      // some row of the block counts
   alignas(16) float alpha[2][kHg];       // by block parity: factor of O where `need` is set
   alignas(16) float lsum[2][kHg];        // reciprocal row sums, by item parity
-  float qs[2][kHg];                      // 2^-k of the item's heads
+  float qs[2][kHg], qnext[kHg];          // 2^-k of the item's heads, and of the converted next one's
   alignas(8) uint8_t need[2][8];         // by block parity and group of 8 heads: O must be rescaled
   Bars bar;
   uint32_t tmem;
@@ -294,6 +294,70 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm->tmem, 0);
+
+  // Heads h0 .. h0 + n - 1 of an item's queries to hi and lo rows in shared memory: a warp takes a head
+  // at a time, 16 latent values and 2 rope values a lane.  Row of head h's hi codes: 32 (h / 16) +
+  // 16 (h / 8 % 2) + h % 8; its lo codes 8 rows on, so that a softmax thread's one load gives it both.
+  auto convert = [&](int item, int h0, int n) {
+    const Item I = item_of(p, item);
+    const uint16_t* q0 = p.q + I.b * p.q_sb + I.t * p.q_st + (int64_t)I.h0 * kD;
+    const uint32_t sixteen = 0x4c004c00u;  // f16 16.0 twice
+#pragma unroll 1
+    for (int hb = h0; hb < h0 + n; hb += 4) {
+      uint4 v[4][2];
+      uint32_t rp[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool live = hb + k < I.heads;
+        const uint4* q = reinterpret_cast<const uint4*>(q0 + (int64_t)(hb + k) * kD);
+        v[k][0] = live ? __ldg(q + lane) : make_uint4(0, 0, 0, 0);
+        v[k][1] = live ? __ldg(q + 32 + lane) : make_uint4(0, 0, 0, 0);
+        rp[k] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + kLatentDim / 8) + lane) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int h = hb + k;
+        // largest magnitude, as bf16 bits (a NaN is above every number)
+        uint32_t top = rp[k] & 0x7fff7fffu;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          top = __vmaxu2(top, __vmaxu2(v[k][u].x & 0x7fff7fffu, v[k][u].y & 0x7fff7fffu));
+          top = __vmaxu2(top, __vmaxu2(v[k][u].z & 0x7fff7fffu, v[k][u].w & 0x7fff7fffu));
+        }
+        top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+        // the largest value's exponent e (not below -100): 2^(7 - e) brings it to [128, 256)
+        const int e = max((int)(top >> 7) - 127, -100);
+        const bool finite = (top >> 7) < 255;
+        const float mul = finite ? __uint_as_float((uint32_t)(7 - e + 127) << 23) : __uint_as_float(0x7fc00000u);
+        if (lane == 0) sm->qnext[h] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : 1.f;
+        const uint32_t row = 32 * (h >> 4) + 16 * ((h >> 3) & 1) + (h & 7);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t w[4] = {v[k][u].x, v[k][u].y, v[k][u].z, v[k][u].w};
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t f = f16x2(__uint_as_float(w[x] << 16) * mul, __uint_as_float(w[x] & 0xffff0000u) * mul);
+            const uint32_t c = e4m3_of_f16x2(f);
+            const uint32_t r = e4m3_of_f16x2(mul_f16x2(sub_f16x2(f, f16x2_of_e4m3((uint16_t)c)), sixteen));
+            if (x & 1) hi[x >> 1] |= c << 16, lo[x >> 1] |= r << 16;
+            else hi[x >> 1] = c, lo[x >> 1] = r;
+          }
+          const uint32_t word = 16 * u + (lane >> 1);  // (row and row + 8 permute alike)
+          uint8_t* dst = q_s + row * kLatentDim + ((word ^ (row & 7)) << 4) + (lane & 1) * 8;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(dst + 8 * kLatentDim) = make_uint2(lo[0], lo[1]);
+        }
+        // the lo row's rope part: 2^-40 of the hi row's, nothing beside it, so that an infinite rope
+        // value of a key gives both rows the same infinity (zeros would make it a NaN)
+        const float a = __uint_as_float(rp[k] << 16) * mul, b = __uint_as_float(rp[k] & 0xffff0000u) * mul;
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b), l2 = __floats2bfloat162_rn(a * 0x1p-40f, b * 0x1p-40f);
+        uint8_t* dst = q_s + kQCodes + row * (2 * kLatentRope) + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(&h2);
+        *reinterpret_cast<uint32_t*>(dst + 8 * 2 * kLatentRope) = *reinterpret_cast<const uint32_t*>(&l2);
+      }
+    }
+  };
 
   // An item's O, once its sums and its last value product are there: first dim chunks 0 and 1, then
   // 2 and 3, one of each by the O warps and the other by the query warps.  false: a wait ran out in
@@ -705,6 +769,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     // ================= O^T: rescales, half of the epilogue =================
     const int t = threadIdx.x - kOWarp0 * 32;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    convert(blockIdx.x, 8 * (warp - kOWarp0), 8);  // half of the first item's queries: nothing else to do yet
+    named_sync(3, kEpiThreads);
     int it = 0, oc = 0;
     uint32_t g = 0;
     bool ok = true;
@@ -764,140 +830,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   } else {
     reg_dec<kRegsQ>();
     // ================= queries: hi and lo rows; half of the epilogue =================
-    // Lane 16 h + i (i < 8) of quarter q holds the hi row of head 16 q + 8 h + i, lane 16 h + 8 + i
-    // its lo row, so that a softmax thread's one load gives it both.
-    const int q4 = warp & 3;
-    const int hl = 16 * q4 + 8 * (lane >> 4) + (lane & 7);
-    const bool lo = (lane & 8) != 0;
-    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-    // this lane's row, 40 words of 16 bytes: the first in local memory, the others in shared memory
-    uint4* const mine = reinterpret_cast<uint4*>(q_s) + (warp - kQWarp0) * 32 + lane;
-    uint4 stash[kQLocal];
-    auto keep = [&](int w, uint4 v) {
-      if (w < kQLocal) stash[w] = v;
-      else mine[128 * (w - kQLocal)] = v;
-    };
-    // two words of this lane's row from what the two lanes of its head made: each has the hi and lo
-    // codes of one of the words
-    auto swap_keep = [&](int w, uint4 h, uint4 l) {
-      uint4 s = lo ? h : l, r;
-      r.x = __shfl_xor_sync(0xffffffffu, s.x, 8);
-      r.y = __shfl_xor_sync(0xffffffffu, s.y, 8);
-      r.z = __shfl_xor_sync(0xffffffffu, s.z, 8);
-      r.w = __shfl_xor_sync(0xffffffffu, s.w, 8);
-      keep(w, lo ? r : h);
-      keep(w + 1, lo ? l : r);
-    };
+    const int qw = warp - kQWarp0, row = 32 * (warp & 3) + lane;  // this lane's row of tensor memory
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     int it = 0, oc = 0;
     int last = -1;  // the item whose O is still to be stored
     bool ok = true;
     for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
-      const Item I = item_of(p, item);
-      const uint4* q = reinterpret_cast<const uint4*>(p.q + I.b * p.q_sb + I.t * p.q_st + (int64_t)(I.h0 + hl) * kD);
-      const bool live = hl < I.heads;
-      // the two lanes of a head take 16 values in turn and write both rows' codes
-      const int odd = lo ? 1 : 0;
-      uint32_t top = 0;  // largest magnitude, as bf16 bits (a NaN is above every number)
-#pragma unroll 1
-      for (int c0 = 0; c0 < kD / 16; c0 += 12) {
-        uint4 v[12];
-#pragma unroll
-        for (int u = 0; u < 12; ++u) v[u] = live ? __ldg(q + 2 * (c0 + u) + odd) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int u = 0; u < 12; ++u) {
-          top = __vmaxu2(top, v[u].x & 0x7fff7fffu);
-          top = __vmaxu2(top, v[u].y & 0x7fff7fffu);
-          top = __vmaxu2(top, v[u].z & 0x7fff7fffu);
-          top = __vmaxu2(top, v[u].w & 0x7fff7fffu);
-        }
-      }
-      top = max(top & 0xffffu, top >> 16);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
-      // the largest value's exponent e (not below -100): 2^(7 - e) brings it to [128, 256)
-      const int e = max((int)(top >> 7) - 127, -100);
-      const bool finite = (top >> 7) < 255;
-      const float mul = finite ? __uint_as_float((uint32_t)(7 - e + 127) << 23) : __uint_as_float(0x7fc00000u);
-      const uint32_t sixteen = 0x4c004c00u;  // f16 16.0 twice
-#pragma unroll 1
-      for (int c0 = 0; c0 < kLatentDim / 16; c0 += 8) {  // words of 16 values; this lane: c0 + odd, + 2, ..
-        uint4 v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = live ? __ldg(q + 2 * (c0 + odd + 2 * (u >> 1)) + (u & 1)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int u = 0; u < 8; u += 2) {
-          uint32_t wh[4], wl[4];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const uint4& a = v[u + (x >> 2)];
-            const uint32_t two = (x & 3) == 0 ? a.x : (x & 3) == 1 ? a.y : (x & 3) == 2 ? a.z : a.w;
-            const uint32_t h = f16x2(__uint_as_float(two << 16) * mul, __uint_as_float(two & 0xffff0000u) * mul);
-            const uint32_t hi = e4m3_of_f16x2(h);
-            const uint32_t rest = e4m3_of_f16x2(mul_f16x2(sub_f16x2(h, f16x2_of_e4m3((uint16_t)hi)), sixteen));
-            if (x & 1) {
-              wh[x >> 1] |= hi << 16;
-              wl[x >> 1] |= rest << 16;
-            } else {
-              wh[x >> 1] = hi;
-              wl[x >> 1] = rest;
-            }
-          }
-          swap_keep(c0 + u, make_uint4(wh[0], wh[1], wh[2], wh[3]), make_uint4(wl[0], wl[1], wl[2], wl[3]));
-        }
-      }
-      // the lo row's rope part: 2^-40 of the hi row's, nothing beside it, so that an infinite rope
-      // value of a key gives both rows the same infinity (zeros would make it a NaN)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint4 v = live ? __ldg(q + kLatentDim / 8 + 2 * c + odd) : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-        uint32_t xh[4], xl[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float a = __uint_as_float(x[u] << 16) * mul, b = __uint_as_float(x[u] & 0xffff0000u) * mul;
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b), l2 = __floats2bfloat162_rn(a * 0x1p-40f, b * 0x1p-40f);
-          xh[u] = *reinterpret_cast<const uint32_t*>(&h2);
-          xl[u] = *reinterpret_cast<const uint32_t*>(&l2);
-        }
-        swap_keep(32 + 2 * c, make_uint4(xh[0], xh[1], xh[2], xh[3]), make_uint4(xl[0], xl[1], xl[2], xl[3]));
+      if (it == 0) {
+        convert(item, 32 + 8 * qw, 8);
+        named_sync(3, kEpiThreads);
+      } else {
+        convert(item, 16 * qw, 16);
       }
       ok = wait(&bar.info_full[it & 1], (it >> 1) & 1);
       const int nb = ok ? sm->nb[it & 1] : 0;
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
-      if (ok && nb) {
-        uint32_t r[32];
-        auto fetch = [&](int s) {  // words 8 s .. 8 s + 7
+      if (ok && nb) ok = wait(&bar.q_empty, (oc & 1) ^ 1);
+      if (named_sync_or(2, 128, !ok)) {  // all rows are there; the four warps go on or leave together
+        ok = false;
+        break;
+      }
+      if (nb) {
+        tc_fence_after();
+        if (lane < 16) sm->qs[oc & 1][16 * qw + lane] = sm->qnext[16 * qw + lane];
+#pragma unroll 1
+        for (int s = 0; s < 5; ++s) {  // eight words at a time: 32 columns (the rope columns follow the codes')
+          uint32_t r[32];
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const uint4 v = 8 * s + u < kQLocal ? stash[8 * s + u] : mine[128 * (8 * s + u - kQLocal)];
+            const uint8_t* src = s < 4 ? q_s + row * kLatentDim + (((8 * s + u) ^ (row & 7)) << 4)
+                                       : q_s + kQCodes + row * (2 * kLatentRope) + ((u ^ (row & 7)) << 4);
+            const uint4 v = *reinterpret_cast<const uint4*>(src);
             r[4 * u] = v.x;
             r[4 * u + 1] = v.y;
             r[4 * u + 2] = v.z;
             r[4 * u + 3] = v.w;
           }
-        };
-        fetch(0);
-        ok = wait(&bar.q_empty, (oc & 1) ^ 1);
-        if (ok) {
-          tc_fence_after();
-          if (!lo) sm->qs[oc & 1][hl] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : 1.f;
-#pragma unroll
-          for (int s = 0; s < 5; ++s) {
-            tmem_st_x32(tmem + lane_base + kColQ + 32 * s, r);  // (the rope columns follow the codes')
-            if (s < 4) fetch(s + 1);
-          }
-          tmem_wait_stores();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bar.qs_full[oc & 1]);
-            mbar_arrive(&bar.q_full);
-          }
+          tmem_st_x32(tmem + lane_base + kColQ + 32 * s, r);
+        }
+        tmem_wait_stores();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.qs_full[oc & 1]);
+          mbar_arrive(&bar.q_full);
         }
       }
+      named_sync(2, 128);  // the room has been read
       // the O warps wait in the last item's epilogue: join them before any wait on a later item
       // than this one, whose publication they hold up
-      if (ok && last >= 0) ok = epilogue(last, oc - 1);
+      if (last >= 0) ok = epilogue(last, oc - 1);
       if (!ok) break;
       if (nb) ++oc;
       last = nb ? item : -1;
