@@ -157,6 +157,23 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+// mbar_wait in few instructions: 24 warps of seven kinds run at a time, and their loops compete for
+// the instruction caches.  The abort word and the bound are read at each wake.
+template <bool kPoll>
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort, long long limit) {
+  if constexpr (kPoll) return mbar_wait<true>(b, parity, abort, limit);
+  if (mbar_try_wait_sleep(b, parity, kSuspendNs)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!mbar_try_wait_sleep(b, parity, kSuspendNs)) {
+    if (*abort) return false;
+    if (clock64() - t0 > limit) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ bool elect_lane() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
@@ -252,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   const int G = (int)gridDim.x;
   // a wait that every lane of a warp makes, with one answer for the warp
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait<kPoll, true>(b, parity, abort_flag, p.wait));
+    return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity, abort_flag, p.wait));
   };
 
   if (threadIdx.x == 0) {
@@ -302,60 +319,59 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     const Item I = item_of(p, item);
     const uint16_t* q0 = p.q + I.b * p.q_sb + I.t * p.q_st + (int64_t)I.h0 * kD;
     const uint32_t sixteen = 0x4c004c00u;  // f16 16.0 twice
+    uint4 nx[2];
+    uint32_t nr;
+    auto load = [&](int h) {
+      const bool live = h < min(I.heads, h0 + n);
+      const uint4* q = reinterpret_cast<const uint4*>(q0 + (int64_t)h * kD);
+      nx[0] = live ? __ldg(q + lane) : make_uint4(0, 0, 0, 0);
+      nx[1] = live ? __ldg(q + 32 + lane) : make_uint4(0, 0, 0, 0);
+      nr = live ? __ldg(reinterpret_cast<const uint32_t*>(q + kLatentDim / 8) + lane) : 0u;
+    };
+    load(h0);
 #pragma unroll 1
-    for (int hb = h0; hb < h0 + n; hb += 4) {
-      uint4 v[4][2];
-      uint32_t rp[4];
+    for (int h = h0; h < h0 + n; ++h) {
+      const uint4 v[2] = {nx[0], nx[1]};
+      const uint32_t rp = nr;
+      load(h + 1);
+      // largest magnitude, as bf16 bits (a NaN is above every number)
+      uint32_t top = rp & 0x7fff7fffu;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool live = hb + k < I.heads;
-        const uint4* q = reinterpret_cast<const uint4*>(q0 + (int64_t)(hb + k) * kD);
-        v[k][0] = live ? __ldg(q + lane) : make_uint4(0, 0, 0, 0);
-        v[k][1] = live ? __ldg(q + 32 + lane) : make_uint4(0, 0, 0, 0);
-        rp[k] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + kLatentDim / 8) + lane) : 0u;
+      for (int u = 0; u < 2; ++u) {
+        top = __vmaxu2(top, __vmaxu2(v[u].x & 0x7fff7fffu, v[u].y & 0x7fff7fffu));
+        top = __vmaxu2(top, __vmaxu2(v[u].z & 0x7fff7fffu, v[u].w & 0x7fff7fffu));
       }
+      top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+      // the largest value's exponent e (not below -100): 2^(7 - e) brings it to [128, 256)
+      const int e = max((int)(top >> 7) - 127, -100);
+      const bool finite = (top >> 7) < 255;
+      const float mul = finite ? __uint_as_float((uint32_t)(7 - e + 127) << 23) : __uint_as_float(0x7fc00000u);
+      if (lane == 0) sm->qnext[h] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : 1.f;
+      const uint32_t row = 32 * (h >> 4) + 16 * ((h >> 3) & 1) + (h & 7);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int h = hb + k;
-        // largest magnitude, as bf16 bits (a NaN is above every number)
-        uint32_t top = rp[k] & 0x7fff7fffu;
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          top = __vmaxu2(top, __vmaxu2(v[k][u].x & 0x7fff7fffu, v[k][u].y & 0x7fff7fffu));
-          top = __vmaxu2(top, __vmaxu2(v[k][u].z & 0x7fff7fffu, v[k][u].w & 0x7fff7fffu));
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t f = f16x2(__uint_as_float(w[x] << 16) * mul, __uint_as_float(w[x] & 0xffff0000u) * mul);
+          const uint32_t c = e4m3_of_f16x2(f);
+          const uint32_t r = e4m3_of_f16x2(mul_f16x2(sub_f16x2(f, f16x2_of_e4m3((uint16_t)c)), sixteen));
+          if (x & 1) hi[x >> 1] |= c << 16, lo[x >> 1] |= r << 16;
+          else hi[x >> 1] = c, lo[x >> 1] = r;
         }
-        top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-        // the largest value's exponent e (not below -100): 2^(7 - e) brings it to [128, 256)
-        const int e = max((int)(top >> 7) - 127, -100);
-        const bool finite = (top >> 7) < 255;
-        const float mul = finite ? __uint_as_float((uint32_t)(7 - e + 127) << 23) : __uint_as_float(0x7fc00000u);
-        if (lane == 0) sm->qnext[h] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : 1.f;
-        const uint32_t row = 32 * (h >> 4) + 16 * ((h >> 3) & 1) + (h & 7);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t w[4] = {v[k][u].x, v[k][u].y, v[k][u].z, v[k][u].w};
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t f = f16x2(__uint_as_float(w[x] << 16) * mul, __uint_as_float(w[x] & 0xffff0000u) * mul);
-            const uint32_t c = e4m3_of_f16x2(f);
-            const uint32_t r = e4m3_of_f16x2(mul_f16x2(sub_f16x2(f, f16x2_of_e4m3((uint16_t)c)), sixteen));
-            if (x & 1) hi[x >> 1] |= c << 16, lo[x >> 1] |= r << 16;
-            else hi[x >> 1] = c, lo[x >> 1] = r;
-          }
-          const uint32_t word = 16 * u + (lane >> 1);  // (row and row + 8 permute alike)
-          uint8_t* dst = q_s + row * kLatentDim + ((word ^ (row & 7)) << 4) + (lane & 1) * 8;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(dst + 8 * kLatentDim) = make_uint2(lo[0], lo[1]);
-        }
-        // the lo row's rope part: 2^-40 of the hi row's, nothing beside it, so that an infinite rope
-        // value of a key gives both rows the same infinity (zeros would make it a NaN)
-        const float a = __uint_as_float(rp[k] << 16) * mul, b = __uint_as_float(rp[k] & 0xffff0000u) * mul;
-        const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b), l2 = __floats2bfloat162_rn(a * 0x1p-40f, b * 0x1p-40f);
-        uint8_t* dst = q_s + kQCodes + row * (2 * kLatentRope) + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(&h2);
-        *reinterpret_cast<uint32_t*>(dst + 8 * 2 * kLatentRope) = *reinterpret_cast<const uint32_t*>(&l2);
+        const uint32_t word = 16 * u + (lane >> 1);  // (row and row + 8 permute alike)
+        uint8_t* dst = q_s + row * kLatentDim + ((word ^ (row & 7)) << 4) + (lane & 1) * 8;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(dst + 8 * kLatentDim) = make_uint2(lo[0], lo[1]);
       }
+      // the lo row's rope part: 2^-40 of the hi row's, nothing beside it, so that an infinite rope
+      // value of a key gives both rows the same infinity (zeros would make it a NaN)
+      const float a = __uint_as_float(rp << 16) * mul, b = __uint_as_float(rp & 0xffff0000u) * mul;
+      const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b), l2 = __floats2bfloat162_rn(a * 0x1p-40f, b * 0x1p-40f);
+      uint8_t* dst = q_s + kQCodes + row * (2 * kLatentRope) + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
+      *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(&h2);
+      *reinterpret_cast<uint32_t*>(dst + 8 * 2 * kLatentRope) = *reinterpret_cast<const uint32_t*>(&l2);
     }
   };
 
@@ -487,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
           const int a = i == 0 ? 4 : i - 1;
-          ok &= mbar_wait<kPoll, true>(&bar.kv_empty[st][a], ((g / kStages) & 1) ^ 1, abort_flag, p.wait);
+          ok &= bar_wait<kPoll>(&bar.kv_empty[st][a], ((g / kStages) & 1) ^ 1, abort_flag, p.wait);
 #pragma unroll
           for (int pass = 0; pass < 4; ++pass)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst[pass] + a * kAtom),
