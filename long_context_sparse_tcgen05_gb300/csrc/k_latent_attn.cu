@@ -155,6 +155,12 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+// 16 lanes x 16 columns, distributed the same way.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 // mbar_wait in few instructions: 24 warps of seven kinds run at a time, and their loops compete for
@@ -319,21 +325,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     const Item I = item_of(p, item);
     const uint16_t* q0 = p.q + I.b * p.q_sb + I.t * p.q_st + (int64_t)I.h0 * kD;
     const uint32_t sixteen = 0x4c004c00u;  // f16 16.0 twice
-    uint4 nx[2];
-    uint32_t nr;
-    auto load = [&](int h) {
-      const bool live = h < min(I.heads, h0 + n);
-      const uint4* q = reinterpret_cast<const uint4*>(q0 + (int64_t)h * kD);
-      nx[0] = live ? __ldg(q + lane) : make_uint4(0, 0, 0, 0);
-      nx[1] = live ? __ldg(q + 32 + lane) : make_uint4(0, 0, 0, 0);
-      nr = live ? __ldg(reinterpret_cast<const uint32_t*>(q + kLatentDim / 8) + lane) : 0u;
+    uint4 nx[2][2];
+    uint32_t nr[2];
+    auto load = [&](int h0_) {  // two heads
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool live = h0_ + k < min(I.heads, h0 + n);
+        const uint4* q = reinterpret_cast<const uint4*>(q0 + (int64_t)(h0_ + k) * kD);
+        nx[k][0] = live ? __ldg(q + lane) : make_uint4(0, 0, 0, 0);
+        nx[k][1] = live ? __ldg(q + 32 + lane) : make_uint4(0, 0, 0, 0);
+        nr[k] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + kLatentDim / 8) + lane) : 0u;
+      }
     };
-    load(h0);
-#pragma unroll 1
-    for (int h = h0; h < h0 + n; ++h) {
-      const uint4 v[2] = {nx[0], nx[1]};
-      const uint32_t rp = nr;
-      load(h + 1);
+    auto one = [&](int h, const uint4 (&v)[2], uint32_t rp) {
       // largest magnitude, as bf16 bits (a NaN is above every number)
       uint32_t top = rp & 0x7fff7fffu;
 #pragma unroll
@@ -372,6 +376,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       uint8_t* dst = q_s + kQCodes + row * (2 * kLatentRope) + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
       *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(&h2);
       *reinterpret_cast<uint32_t*>(dst + 8 * 2 * kLatentRope) = *reinterpret_cast<const uint32_t*>(&l2);
+    };
+    load(h0);
+#pragma unroll 1
+    for (int h = h0; h < h0 + n; h += 2) {
+      const uint4 a[2] = {nx[0][0], nx[0][1]}, b[2] = {nx[1][0], nx[1][1]};
+      const uint32_t ra = nr[0], rb = nr[1];
+      load(h + 2);
+      one(h, a, ra);
+      one(h + 1, b, rb);
     }
   };
 
@@ -395,55 +408,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
     tc_fence_after();
     float* po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
-    // a head without weights (sum 0): zeros, whatever the product left (rare, so one test for all)
-    const bool zeros = __any_sync(0xffffffffu, sm->lsum[oc & 1][lane] == 0.f || sm->lsum[oc & 1][lane + 32] == 0.f);
+    // (a head without weights, sum 0, gives zeros whatever its products left)
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       const uint32_t o_addr = tmem + ((uint32_t)(q4 * 32) << 16) + kColO + (2 * half + cw) * kHg;
-      if (po) {  // fp32 rows of a part, straight out: lane = dim
+      const float* ls = sm->lsum[oc & 1];
+      if (po) {  // a part: fp32 rows, 32 dims a store (a lane's own heads together: a line per lane)
+        float* out = po + half * 256 + cw * 128 + q4 * 32 + lane;
 #pragma unroll 1
-        for (int h0 = 0; h0 < I.heads; h0 += 32) {
-          uint32_t r[32];
-          tmem_ld32(o_addr + h0, r);
+        for (int h0 = 0; h0 < I.heads; h0 += 8) {
+          uint32_t r[8];
+          tmem_ld_x8(o_addr + h0, r);
           tmem_wait_ld();
-          float* out = po + (int64_t)h0 * kLatentDim + half * 256 + cw * 128 + q4 * 32 + lane;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float L = sm->lsum[oc & 1][h0 + i];
-            if (h0 + i < I.heads) out[(int64_t)i * kLatentDim] = L == 0.f ? 0.f : __uint_as_float(r[i]) * L;
+          for (int i = 0; i < 8; ++i) {
+            const float f = ls[h0 + i];
+            out[(h0 + i) * kLatentDim] = f == 0.f ? 0.f : __uint_as_float(r[i]) * f;
           }
         }
       } else {
-        // 16 dims x 64 heads at a time, as 8 x 8 tiles (rows: dims) that stmatrix stores transposed
+        // 16 dims x 16 heads at a time, as 8 x 8 tiles (rows: dims) that stmatrix stores transposed.
+        // (Small loops: unrolled, this code ran at the pace of its instruction fetches.)
+        if (half) named_sync(1, kEpiThreads);  // the first half has left the room
+        const uint32_t dst = smem_addr(q_s) + (8 * (lane >> 4) + (lane & 7)) * kOPitch +
+                             2 * (cw * 128 + q4 * 32 + 8 * ((lane >> 3) & 1));
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          uint32_t r[32];
-          tmem_ld_16x256b_x8(o_addr + ((uint32_t)(16 * x) << 16), r);
+        for (int i = 0; i < 8; ++i) {
+          const int x = 16 * (i >> 2), h0 = 16 * (i & 3);  // dims, heads
+          uint32_t r[8], w[4];
+          tmem_ld_16x256b_x2(o_addr + h0 + ((uint32_t)x << 16), r);
           tmem_wait_ld();
-          if (half && x == 0) named_sync(1, kEpiThreads);  // the first half has left the room
-          const float* ls = sm->lsum[oc & 1] + 2 * (lane & 3);
-          const uint32_t dst = smem_addr(q_s) + (8 * (lane >> 4) + (lane & 7)) * kOPitch +
-                               2 * (cw * 128 + q4 * 32 + 16 * x + 8 * ((lane >> 3) & 1));
-          uint32_t w[16];
 #pragma unroll
-          for (int jj = 0; jj < 8; ++jj) {
-            const float2 L = *reinterpret_cast<const float2*>(ls + 8 * jj);
+          for (int jj = 0; jj < 2; ++jj) {
+            const float2 L = *reinterpret_cast<const float2*>(ls + h0 + 8 * jj + 2 * (lane & 3));
             float o[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const float f = u & 1 ? L.y : L.x;
-              o[u] = __uint_as_float(r[4 * jj + u]) * f;
-              if (zeros) o[u] = f == 0.f ? 0.f : o[u];
+              o[u] = f == 0.f ? 0.f : __uint_as_float(r[4 * jj + u]) * f;
             }
             const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
             w[2 * jj] = *reinterpret_cast<const uint32_t*>(&a);
             w[2 * jj + 1] = *reinterpret_cast<const uint32_t*>(&b);
           }
-#pragma unroll
-          for (int jj = 0; jj < 8; jj += 2)
-            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + 8 * jj * kOPitch),
-                         "r"(w[2 * jj]), "r"(w[2 * jj + 1]), "r"(w[2 * jj + 2]), "r"(w[2 * jj + 3])
-                         : "memory");
+          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + h0 * kOPitch + 2 * x),
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
         }
       }
       if (half) {
@@ -538,9 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           tc_fence_after();
           if (elect_lane()) {
             const uint64_t kd = kv_desc + (uint64_t)((st * kStage) >> 4);
+#pragma unroll 1
+            for (int a = 0; a < 4; ++a)
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              mma_fp8_ts(tmem + kColS, tmem + kColQ + 8 * k, kd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), id8, k != 0);
+              for (int k = 0; k < 4; ++k)
+                mma_fp8_ts(tmem + kColS, tmem + kColQ + 32 * a + 8 * k, kd + (uint64_t)((a * kAtom + k * 32) >> 4), id8, (a | k) != 0);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_bf16_ts(tmem + kColS, tmem + kColQR + 8 * k, kd + (uint64_t)((4 * kAtom + k * 32) >> 4), id16, 1);
@@ -582,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           tc_fence_after();
           if (elect_lane()) {
             const uint64_t vd = v_desc + (uint64_t)((st * kStage) >> 4), pd = p_desc + (uint64_t)((pb * kPBytes) >> 4);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)  // keys 0-31 and 32-63 by the hi terms, then by the lo terms
@@ -915,10 +927,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 }
 static_assert(kColQR == kColQ + 128, "the converted query row is stored in one run of columns");
 
-// Joins a split item's parts: O = sum_s w_s O_s with w_s = 2^(lse_s - lse) in proportion.  One CTA
-// per (query, 4 heads): few queries must still fill the GPU.
+// Joins a split item's parts: O = sum_s w_s O_s with w_s = e^(lse_s - lse).  One CTA per (query, 4
+// heads): few queries must still fill the GPU.
 constexpr int kCombHeads = 4;
-__global__ void __launch_bounds__(128) k_latent_combine(LatentAttnLaunch p) {
+__global__ void __launch_bounds__(kCombHeads * 128) k_latent_combine(LatentAttnLaunch p) {
   __shared__ float wgt[kMaxLatentSplits][kCombHeads];
   const int row = blockIdx.x, h0 = blockIdx.y * kCombHeads, S = p.splits;
   const int64_t part0 = ((int64_t)row * p.groups + h0 / kHg) * S;
@@ -936,24 +948,31 @@ __global__ void __launch_bounds__(128) k_latent_combine(LatentAttnLaunch p) {
     for (int s = 0; s < S; ++s) wgt[s][threadIdx.x] = sum == 0.f ? 0.f : wgt[s][threadIdx.x] / sum;
     if (p.lse) p.lse[(int64_t)row * p.H + h0 + threadIdx.x] = sum == 0.f ? -INFINITY : mx + logf(sum);
   }
+  // the parts' values do not wait for their weights: four dims of a head a thread
+  const int hl = threadIdx.x >> 7, i = threadIdx.x & 127;
+  const float4* src = reinterpret_cast<const float4*>(p.part_o + (part0 * kHg + hl0 + hl) * kLatentDim) + i;
+  const bool live = h0 + hl < p.H;
+  float4 v[8];
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    if (live && s < S) v[s] = src[(int64_t)s * kHg * kLatentDim / 4];
   __syncthreads();
-  const int hl = threadIdx.x >> 5;
-  if (h0 + hl >= p.H) return;
-  uint2* out = reinterpret_cast<uint2*>(p.out + ((int64_t)row * p.H + h0 + hl) * kLatentDim);
-  for (int i = threadIdx.x & 31; i < kLatentDim / 4; i += 32) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < S; ++s) {
-      const float w = wgt[s][hl];
-      if (w == 0.f) continue;  // an empty part wrote no values
-      const float4 v = reinterpret_cast<const float4*>(p.part_o + ((part0 + s) * kHg + hl0 + hl) * kLatentDim)[i];
-      acc.x += w * v.x;
-      acc.y += w * v.y;
-      acc.z += w * v.z;
-      acc.w += w * v.w;
-    }
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), b = __floats2bfloat162_rn(acc.z, acc.w);
-    out[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
+  if (!live) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float4 x, float w) {
+    if (w == 0.f) return;  // an empty part wrote no values
+    acc.x += w * x.x;
+    acc.y += w * x.y;
+    acc.z += w * x.z;
+    acc.w += w * x.w;
+  };
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    if (s < S) add(v[s], wgt[s][hl]);
+  for (int s = 8; s < S; ++s) add(src[(int64_t)s * kHg * kLatentDim / 4], wgt[s][hl]);
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), b = __floats2bfloat162_rn(acc.z, acc.w);
+  reinterpret_cast<uint2*>(p.out + ((int64_t)row * p.H + h0 + hl) * kLatentDim)[i] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 }  // namespace
@@ -1006,7 +1025,7 @@ cudaError_t launch_latent_attn(LatentAttnLaunch p, float* part, cudaStream_t st)
   kern<<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, st>>>(p);
   count_launches(1);
   if ((e = cudaGetLastError()) != cudaSuccess || p.splits <= 1) return e;
-  k_latent_combine<<<dim3((unsigned)(p.B * p.T), (unsigned)((p.H + kCombHeads - 1) / kCombHeads)), 128, 0, st>>>(p);
+  k_latent_combine<<<dim3((unsigned)(p.B * p.T), (unsigned)((p.H + kCombHeads - 1) / kCombHeads)), kCombHeads * 128, 0, st>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }
