@@ -481,6 +481,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     return true;
   };
 
+  // The converted rows' columns 32 s0 .. 32 s1 into tensor memory (the rope columns follow the codes').
+  auto copy_q = [&](int s0, int s1) {
+    const int row = 32 * (warp & 3) + lane;
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s) {  // eight words at a time
+      const uint8_t* src = s < 4 ? q_s + row * kLatentDim + 128 * s : q_s + kQCodes + row * (2 * kLatentRope);
+      uint32_t r[32];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + ((u ^ (row & 7)) << 4));
+        r[4 * u] = v.x;
+        r[4 * u + 1] = v.y;
+        r[4 * u + 2] = v.z;
+        r[4 * u + 3] = v.w;
+      }
+      tmem_st_x32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColQ + 32 * s, r);
+    }
+    tmem_wait_stores();
+    tc_fence_before();
+  };
+  // The first item's queries: sixteen warps that have nothing else to do yet convert four heads each,
+  // eight of them store the rows (a single decode step waits for nothing longer).
+  if (warp >= kSmWarp0) {
+    convert(blockIdx.x, 4 * (warp - kSmWarp0), 4);
+    named_sync(3, 512);
+    if (warp >= kOWarp0) {
+      copy_q(warp < kQWarp0 ? 0 : 3, warp < kQWarp0 ? 3 : 5);
+      named_sync(1, kEpiThreads);
+    }
+  }
+
   if (warp < kGatherWarps) {
     reg_dec<kRegsGather>();
     // ================= gather =================
@@ -797,8 +828,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     // ================= O^T: rescales, half of the epilogue =================
     const int t = threadIdx.x - kOWarp0 * 32;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    convert(blockIdx.x, 8 * (warp - kOWarp0), 8);  // half of the first item's queries: nothing else to do yet
-    named_sync(3, kEpiThreads);
     int it = 0, oc = 0;
     uint32_t g = 0;
     bool ok = true;
@@ -858,62 +887,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   } else {
     reg_dec<kRegsQ>();
     // ================= queries: hi and lo rows; half of the epilogue =================
-    const int qw = warp - kQWarp0, row = 32 * (warp & 3) + lane;  // this lane's row of tensor memory
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int qw = warp - kQWarp0;
     int it = 0, oc = 0;
     int last = -1;  // the item whose O is still to be stored
     bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
-      if (it == 0) {
-        convert(item, 32 + 8 * qw, 8);
-        named_sync(3, kEpiThreads);
-      } else {
-        convert(item, 16 * qw, 16);
-      }
-      ok = wait(&bar.info_full[it & 1], (it >> 1) & 1);
-      const int nb = ok ? sm->nb[it & 1] : 0;
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
-      if (ok && nb) ok = wait(&bar.q_empty, (oc & 1) ^ 1);
-      if (named_sync_or(2, 128, !ok)) {  // all rows are there; the four warps go on or leave together
-        ok = false;
-        break;
-      }
-      if (nb) {
-        tc_fence_after();
-        if (lane < 16) sm->qs[oc & 1][16 * qw + lane] = sm->qnext[16 * qw + lane];
-#pragma unroll 1
-        for (int s = 0; s < 5; ++s) {  // eight words at a time: 32 columns (the rope columns follow the codes')
-          uint32_t r[32];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const uint8_t* src = s < 4 ? q_s + row * kLatentDim + (((8 * s + u) ^ (row & 7)) << 4)
-                                       : q_s + kQCodes + row * (2 * kLatentRope) + ((u ^ (row & 7)) << 4);
-            const uint4 v = *reinterpret_cast<const uint4*>(src);
-            r[4 * u] = v.x;
-            r[4 * u + 1] = v.y;
-            r[4 * u + 2] = v.z;
-            r[4 * u + 3] = v.w;
-          }
-          tmem_st_x32(tmem + lane_base + kColQ + 32 * s, r);
-        }
-        tmem_wait_stores();
-        tc_fence_before();
+    for (int item = blockIdx.x; item < items || last >= 0; item += G, ++it) {
+      int nb = 0;
+      if (item < items) {
+        if (it > 0) convert(item, 16 * qw, 16);
+        ok = wait(&bar.info_full[it & 1], (it >> 1) & 1);
+        nb = ok ? sm->nb[it & 1] : 0;
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar.qs_full[oc & 1]);
-          mbar_arrive(&bar.q_full);
+        if (ok && lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+        if (ok && nb) ok = wait(&bar.q_empty, (oc & 1) ^ 1);
+        if (named_sync_or(2, 128, !ok)) {  // all rows are there; the four warps go on or leave together
+          ok = false;
+          break;
         }
+        if (nb) {
+          if (lane < 16) sm->qs[oc & 1][16 * qw + lane] = sm->qnext[16 * qw + lane];
+          if (it > 0) {
+            tc_fence_after();
+            copy_q(0, 5);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar.qs_full[oc & 1]);
+            mbar_arrive(&bar.q_full);
+          }
+        }
+        named_sync(2, 128);  // the room has been read
       }
-      named_sync(2, 128);  // the room has been read
       // the O warps wait in the last item's epilogue: join them before any wait on a later item
       // than this one, whose publication they hold up
-      if (last >= 0) ok = epilogue(last, oc - 1);
-      if (!ok) break;
+      if (last >= 0 && !(ok = epilogue(last, oc - 1))) break;
       if (nb) ++oc;
       last = nb ? item : -1;
     }
-    if (ok && last >= 0) ok = epilogue(last, oc - 1);
     meet_last(ok);
     asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   }
