@@ -11,16 +11,21 @@
 //     significant bits, hi takes 4 and lo the other 4: exact down to 2^-21 of the head's largest.
 //     The rope part stays bf16 (times 2^k, exact).  S has a hi and a lo row per head (M = 128 for
 //     64 heads): hi . c + r . r and lo . c, added by the softmax.
-//   * the weights: y_j = x_j + log2 s_j, p_j = 2^(y_j - M) <= 430 carries the row's scale, and
-//     p_j = hi + lo in e4m3 (each rounded to nearest): relative error 2^-8, and at most 2^-10
-//     absolute where p_j is small, 2^-14 of the largest, since M keeps the largest p in [16, 430].
-//     Both terms accumulate into the same O.  Row sums take p_j / s_j in fp32.
+//   * the weights: y_j = x_j + log2 s_j carries the row's scale.  A block of 64 keys takes its own
+//     power of two, E = ceil(max y) - 8 per head: p_j = 2^(y_j - E) <= 256, and
+//     p_j = hi + lo / 16 in e4m3 (each rounded to nearest): relative error 2^-8, at most 2^-14
+//     absolute where p_j is small, 2^-21 of the block's largest.  The value product is
+//     block-scaled: its B scales are 2^(E - E0) for the hi and 2^(E - E0 - 4) for the lo terms of a
+//     head, E0 being the head's E at its first block, so blocks of any size add into the same O
+//     without rescaling it (before, each rise of a running maximum had to rescale O between two
+//     products: in ten of a row's 32 blocks, a third of a decode step).  Only when E passes
+//     E0 + 60 is O rescaled and E0 moved.  Row sums take p_j / s_j, times 2^(E - E0), in fp32.
 // FP8 products accumulate exactly enough in fp32 (sums of 2,048 products of mixed size came out
 // equal to the 64-bit sum).
 //
 // Persistent CTAs, one per SM, walk items (query, group of 64 heads, part of the row's blocks of 64
 // keys).  24 warps:
-//   6-7    take the blocks in turn, up to six ahead: resolve positions through the block table, read
+//   6-7    take the blocks in turn, up to four ahead: resolve positions through the block table, read
 //          the rows' scales, bring the rows to L2 (the three dependent loads a block took as long
 //          as its copies when the copying warps made them)
 //   0-3    copy the rows (16-byte cp.async) into three stages of 40 KB, five 128-byte-swizzled atoms
@@ -30,7 +35,8 @@
 //   5      O^T (512 x 64) += V^T P^T: four chunks of 128 dims, 2 key steps, hi and lo
 //   8-15   softmax: a warp holds 8 heads whole (their hi and lo rows lie in one 16-lane half of a
 //          lane quarter), so maxima and sums never leave a quad of lanes and no barrier joins warps
-//   16-19  rescale O^T when a reference maximum rises (only the heads concerned)
+//   16-19  put a block's scales into tensor memory (every lane quarter wants a copy); rescale O^T
+//          when a head's E0 moves
 //   20-23  convert the next item's queries while the present one runs, and put them into tensor
 //          memory when its last score product is done
 //   16-23  normalise an item's O, while the softmax already runs the next item: bf16 rows go to the
@@ -64,16 +70,16 @@ constexpr uint32_t kPBytes = kHg * 128;      // P: per head 64 hi bytes, then 64
 // 16-byte words of a row permuted by the row's low bits (a lane reads its row word by word).
 constexpr uint32_t kQCodes = 128 * kLatentDim, kQBytes = kQCodes + 128 * kLatentRope * 2;
 constexpr int kGatherWarps = 4, kSWarp = 4, kPvWarp = 5, kIxWarp0 = 6, kSmWarp0 = 8, kSmWarps = 8, kOWarp0 = 16, kQWarp0 = 20;
-constexpr int kRing = 6;                     // blocks the index warps may be ahead
+constexpr int kRing = 4;                     // blocks the index warps may be ahead
 constexpr int kThreads = 24 * 32;
 // Registers by warpgroup (warps 0-3, 4-7, ..), moved at the start from the kernel's own kRegs each;
 // the softmax warps spilled in their block loop at kRegs.
 constexpr int kRegs = 80, kRegsGather = 56, kRegsIssue = 64, kRegsSm = 112, kRegsO = 64, kRegsQ = 72;
 static_assert(kRegsGather + kRegsIssue + 2 * kRegsSm + kRegsO + kRegsQ <= 6 * kRegs, "registers the block is launched with");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColS = 448;
+constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColSfA = 416, kColSfB = 424, kColS = 448;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kTop = 8.75f, kAim = 4.f;    // raise M when y exceeds it by 8.75 (p <= 430); then the largest p is 2^4
+constexpr float kMove = 60.f;                // E0 moves when a block's E passes it by this
 constexpr int kInfoReaders = kGatherWarps + 2 + kSmWarps + 4 + 4;
 constexpr int kEpiThreads = 256;             // O and query warps store an item's O together
 constexpr uint32_t kOPitch = kLatentDim + 16;  // staged half of an O row: 8 heads' 16-byte pieces in 32 banks
@@ -87,7 +93,7 @@ struct Bars {
   uint64_t ix_full[kRing], ix_empty[kRing];
   uint64_t s_full, s_empty;
   uint64_t p_full[2], p_empty[2];
-  uint64_t o_full, o_empty, m_full[2], m_empty[2], corr_done;
+  uint64_t o_full, o_empty, m_full[2], m_empty[2], sf_full[2];
   uint64_t l_full[2], l_empty[2];
   uint64_t info_full[2], info_empty[2];
   uint64_t drain[2];
@@ -98,6 +104,7 @@ struct Small {
   alignas(16) int64_t row[kRing][kNB];   // cache row (-1: skipped)
   int valid[kRing];                      // some row of the block counts
   alignas(16) float alpha[2][kHg];       // by block parity: factor of O where `need` is set
+  uint32_t sf[2][kHg];                   // by block parity: the scales of P's four key steps, as exponents + 127
   alignas(16) float lsum[2][kHg];        // reciprocal row sums, by item parity
   float qs[2][kHg], qnext[kHg];          // 2^-k of the item's heads, and of the converted next one's
   alignas(8) uint8_t need[2][8];         // by block parity and group of 8 heads: O must be rescaled
@@ -116,6 +123,21 @@ __device__ __forceinline__ void mma_fp8_ts(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
+// Block-scaled: B's column n and 32 values of K count times 2^(sf[n] - 127), the byte that the
+// instruction descriptor picks of the words at `sfb`; A's rows likewise at `sfa`.
+__device__ __forceinline__ void mma_mxfp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                          uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// Its instruction descriptor: e4m3 operands, A (128 dims) MN-major, N = 64, ue8m0 scales, A's scale
+// byte 0 and B's scale byte `id`.
+__host__ __device__ constexpr uint32_t idesc_mx(uint32_t id) {
+  return (id << 4) | (1u << 15) | ((uint32_t)(64 >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 4) << 24);
+}
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -132,6 +154,9 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st_x2(uint32_t taddr, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};\n" ::"r"(taddr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
@@ -285,7 +310,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     mbar_init(&bar.s_empty, kSmWarps);
     mbar_init(&bar.o_full, 1);
     mbar_init(&bar.o_empty, 8);
-    mbar_init(&bar.corr_done, 4);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.kv_full[i], kGatherWarps * 32);
       for (int c = 0; c < 5; ++c) mbar_init(&bar.kv_empty[i][c], 1);
@@ -300,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       mbar_init(&bar.p_empty[i], 1);
       mbar_init(&bar.m_full[i], kSmWarps);
       mbar_init(&bar.m_empty[i], 4);
+      mbar_init(&bar.sf_full[i], 4);
       mbar_init(&bar.l_full[i], kSmWarps);
       mbar_init(&bar.l_empty[i], 8);
       mbar_init(&bar.info_full[i], 1);
@@ -602,9 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       __syncwarp();
     } else if (warp == kPvWarp) {
       // ================= value product =================
-      const uint32_t id8 = idesc_mn(0, 0, 128, kHg) | (1u << 15);  // A: 128 dims, MN-major
       const uint64_t v_desc = desc_sw128(smem_addr(kv_s)), p_desc = desc_sw128(smem_addr(p_s));
-      int it = 0, oc = 0, corr = 0;
+      int it = 0, oc = 0;
       uint32_t g = 0;
       bool ok = true;
       for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
@@ -615,12 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         if (!(ok = wait(&bar.o_empty, (oc & 1) ^ 1))) break;
         for (int j = 0; j < nb; ++j, ++g) {
           const int st = (int)(g % kStages), pb = (int)(g & 1);
-          if (!(ok = wait(&bar.p_full[pb], (g >> 1) & 1) && wait(&bar.kv_full[st], (g / kStages) & 1))) break;
-          if (j > 0 && __any_sync(0xffffffffu, *reinterpret_cast<const volatile uint64_t*>(sm->need[pb]) != 0)) {
-            // the O warps were told when the maxima were known
-            if (!(ok = wait(&bar.corr_done, corr & 1))) break;
-            ++corr;
-          }
+          if (!(ok = wait(&bar.kv_full[st], (g / kStages) & 1) && wait(&bar.sf_full[pb], (g >> 1) & 1) &&
+                     wait(&bar.p_full[pb], (g >> 1) & 1)))
+            break;
           async_fence();
           tc_fence_after();
           if (elect_lane()) {
@@ -629,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
             for (int c = 0; c < 4; ++c) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)  // keys 0-31 and 32-63 by the hi terms, then by the lo terms
-                mma_fp8(tmem + kColO + c * kHg, vd + (uint64_t)((c * kAtom + (k & 1) * 4096) >> 4),
-                        pd + (uint64_t)((k * 32) >> 4), id8, (j | k) != 0);
+                mma_mxfp8(tmem + kColO + c * kHg, vd + (uint64_t)((c * kAtom + (k & 1) * 4096) >> 4),
+                          pd + (uint64_t)((k * 32) >> 4), idesc_mx(k), tmem + kColSfA, tmem + kColSfB + 4 * pb, (j | k) != 0);
               mma_commit(&bar.kv_empty[st][c]);
             }
             mma_commit(&bar.p_empty[pb]);
@@ -746,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
       if (nb == 0) continue;
-      float M = -INFINITY, l = 0.f;
+      float E0 = -INFINITY, l = 0.f;
       int any_valid = 0;
       for (int j = 0; j < nb; ++j, ++g) {
         const int ri = (int)(g % kRing), pb = (int)(g & 1);
@@ -775,31 +796,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         }
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 1));
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 2));
-        const bool raise = ymax > M + kTop;
-        const float Mn = raise ? ymax - kAim : M;
-        const float alpha = raise ? ex2(M - Mn) : 1.f;
-        const int any = __any_sync(0xffffffffu, raise);
-        M = Mn;
-        const float Mu = M == -INFINITY ? 0.f : M;
-        l *= alpha;
-        if (any && m == 0) sm->alpha[pb][hl] = alpha;
-        if (lane == 0) sm->need[pb][hgp] = (uint8_t)(any != 0);
+        const float E = ceilf(ymax) - 8.f;  // -inf: no weight in this block
+        const bool move = E > E0 + kMove;   // (E0 starts at -inf)
+        const float alpha = move ? ex2(E0 - E) : 1.f;
+        const int any = __any_sync(0xffffffffu, move);
+        E0 = move ? E : E0;
+        const float d = fmaxf(E - E0, -120.f);  // beside 2^0, nothing is left of 2^-120
+        if (m == 0) {
+          const uint32_t hi = (uint32_t)(127 + (int)d);
+          sm->sf[pb][hl] = hi * 0x0101u | (hi - 4) * 0x01010000u;
+          if (any) sm->alpha[pb][hl] = alpha;
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.m_full[pb]);
+        if (lane == 0) {
+          sm->need[pb][hgp] = (uint8_t)(any != 0);
+          mbar_arrive(&bar.m_full[pb]);
+        }
+        const float eu = E == -INFINITY ? 0.f : E;
+        float sum = 0.f;
         const uint32_t prow = smem_addr(p_s + pb * kPBytes + hl * 128) + 2 * m;
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
-          const float p0 = ex2(y[2 * jj] - Mu), p1 = ex2(y[2 * jj + 1] - Mu);
+          const float p0 = ex2(y[2 * jj] - eu), p1 = ex2(y[2 * jj + 1] - eu);
           const float2 is = *reinterpret_cast<const float2*>(&sm->isc[ri][8 * jj + 2 * m]);
-          l = fmaf(p0, is.x, l);
-          l = fmaf(p1, is.y, l);
+          sum = fmaf(p0, is.x, sum);
+          sum = fmaf(p1, is.y, sum);
           const uint32_t h = f16x2(p0, p1);
           const uint16_t hi = e4m3_of_f16x2(h);
-          const uint16_t lo = e4m3_of_f16x2(sub_f16x2(h, f16x2_of_e4m3(hi)));
+          const uint16_t lo = e4m3_of_f16x2(mul_f16x2(sub_f16x2(h, f16x2_of_e4m3(hi)), 0x4c004c00u));  // (f16 16.0)
           const uint32_t at = prow + (jj & 1) * 8;
           asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((jj >> 1) ^ (hl & 7)) << 4)), "h"(hi) : "memory");
           asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((4 + (jj >> 1)) ^ (hl & 7)) << 4)), "h"(lo) : "memory");
         }
+        l = fmaf(sum, E == -INFINITY ? 0.f : ex2(E - E0), l * alpha);
         async_fence();
         __syncwarp();
         if (lane == 0) {
@@ -815,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       if (m == 0) {
         sm->lsum[oc & 1][hl] = l == 0.f ? 0.f : 1.f / l;
         const Item I = item_of(p, item);
-        const float v = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+        const float v = l == 0.f ? -INFINITY : (E0 + log2f(l)) * kLn2;
         if (p.splits > 1) p.part_lse[(int64_t)item * kHg + hl] = v;
         else if (p.lse && hl < I.heads) p.lse[(int64_t)I.row * p.H + I.h0 + hl] = v;
       }
@@ -825,9 +854,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
   } else if (warp < kQWarp0) {
     reg_dec<kRegsO>();
-    // ================= O^T: rescales, half of the epilogue =================
+    // ================= O^T: block scales, half of the epilogue =================
     const int t = threadIdx.x - kOWarp0 * 32;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    tmem_st_x2(tmem + lane_base + kColSfA, 0x7f7f7f7fu, 0x7f7f7f7fu);  // V as it stands
+    tmem_st_x2(tmem + lane_base + kColSfA + 2, 0x7f7f7f7fu, 0x7f7f7f7fu);
+    tmem_wait_stores();
+    tc_fence_before();
     int it = 0, oc = 0;
     uint32_t g = 0;
     bool ok = true;
@@ -848,11 +881,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         continue;
       }
       for (int j = 0; j < nb; ++j, ++g) {
-        // told at every block, when its maxima are known and its weights are not yet formed
+        // told at every block, when its scales are known and its weights are not yet formed
         if (!(ok = wait(&bar.m_full[g & 1], (g >> 1) & 1))) break;
         const bool need = j > 0 && __any_sync(0xffffffffu, *reinterpret_cast<const volatile uint64_t*>(sm->need[g & 1]) != 0);
         if (need) {
-          // O^T complete up to the block before: rescale the heads whose maximum rose
+          // O^T complete up to the block before: rescale the heads whose E0 moved
           if (!(ok = wait(&bar.p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1))) break;
           tc_fence_after();
 #pragma unroll 1
@@ -872,13 +905,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
               tmem_st_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
             }
           }
-          tmem_wait_stores();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.corr_done);
         }
+        // the block's scales (the products that read this buffer's last ones are done: the softmax
+        // waited for them before it wrote these)
+        tmem_st_x2(tmem + lane_base + kColSfB + 4 * (g & 1), sm->sf[g & 1][lane], sm->sf[g & 1][32 + lane]);
+        tmem_wait_stores();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.m_empty[g & 1]);
+        if (lane == 0) {
+          mbar_arrive(&bar.sf_full[g & 1]);
+          mbar_arrive(&bar.m_empty[g & 1]);
+        }
       }
       if (!ok || !(ok = epilogue(item, oc))) break;
       ++oc;
