@@ -707,20 +707,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
             id[u] = j < nb && e < p.kk ? __ldg(irow + e) : -1;
           }
         };
-        int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
-        int id[2];
-        load_ids(j, id);
-        for (; j < nb; j += 2) {
-          const uint32_t gj = g + j;
-          const int ri = (int)(gj % kRing);
-          int64_t row[2];
-          float scale[2];
+        // cache rows of ids; the rows' scales, and their lines on the way to L2
+        auto resolve = [&](const int (&id)[2], int64_t (&row)[2]) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             row[u] = id[u] >= 0 && id[u] < p.S ? latent_row(p.cache, I.b, id[u]) : -1;
             if (row[u] < 0 && id[u] != -1) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
           }
-          load_ids(j + 2, id);
+        };
+        auto touch = [&](const int64_t (&row)[2], float (&scale)[2]) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             scale[u] = row[u] >= 0 ? __ldg(p.cache.scales + row[u]) : 0.f;
@@ -731,6 +726,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
               prefetch_l2(p.cache.rope + row[u] * kLatentRope);
             }
           }
+        };
+        int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
+        // each block's ids two, its rows and scales one of this warp's blocks ahead
+        int id[2];
+        int64_t row[2];
+        float scale[2];
+        load_ids(j, id);
+        resolve(id, row);
+        load_ids(j + 2, id);
+        touch(row, scale);
+        for (; j < nb; j += 2) {
+          const uint32_t gj = g + j;
+          const int ri = (int)(gj % kRing);
+          int64_t row_n[2];
+          resolve(id, row_n);
+          load_ids(j + 4, id);
           if (!(ok = wait(&bar.ix_empty[ri], ((gj / kRing) & 1) ^ 1))) break;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -743,6 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           if (lane == 0) sm->valid[ri] = some;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.ix_full[ri]);
+          row[0] = row_n[0];
+          row[1] = row_n[1];
+          touch(row, scale);
         }
         g += nb;
       }
