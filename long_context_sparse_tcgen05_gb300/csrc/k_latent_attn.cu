@@ -12,10 +12,9 @@
 //     The rope part stays bf16 (times 2^k, exact).  S has a hi and a lo row per head (M = 128 for
 //     64 heads): hi . c + r . r and lo . c, added by the softmax.
 //   * the weights: y_j = x_j + log2 s_j carries the row's scale.  A block of 64 keys takes its own
-//     power of two, E = ceil(max y) - 8 per head: p_j = 2^(y_j - E) <= 256, and
-//     p_j = hi + lo / 16 in e4m3 (each rounded to nearest): relative error 2^-8, at most 2^-14
-//     absolute where p_j is small, 2^-21 of the block's largest.  The value product is
-//     block-scaled: its B scales are 2^(E - E0) for the hi and 2^(E - E0 - 4) for the lo terms of a
+//     power of two, E = ceil(max y) - 8 per head: p_j = 2^(y_j - E) <= 256, and p_j = hi + lo in
+//     e4m3 (each rounded to nearest): relative error 2^-8, at most 2^-10 absolute where p_j is
+//     small, 2^-17 of the block's largest.  The value product is block-scaled, the B scale 2^(E - E0) per
 //     head, E0 being the head's E at its first block, so blocks of any size add into the same O
 //     without rescaling it (before, each rise of a running maximum had to rescale O between two
 //     products: in ten of a row's 32 blocks, a third of a decode step).  Only when E passes
@@ -25,9 +24,9 @@
 //
 // Persistent CTAs, one per SM, walk items (query, group of 64 heads, part of the row's blocks of 64
 // keys).  24 warps:
-//   6-7    take the blocks in turn, up to four ahead: resolve positions through the block table, read
-//          the rows' scales, bring the rows to L2 (the three dependent loads a block took as long
-//          as its copies when the copying warps made them)
+//   6-7    take the blocks in turn, up to four ahead: resolve positions through the block table and
+//          read the rows' scales (the three dependent loads a block took as long as its copies when
+//          the copying warps made them)
 //   0-3    copy the rows (16-byte cp.async) into three stages of 40 KB, five 128-byte-swizzled atoms
 //          each, an atom as soon as the products have released it
 //   4      S (hi and lo rows, 128 x 64) = Q K^T: A is Q in tensor memory, so the product reads only
@@ -93,7 +92,7 @@ struct Bars {
   uint64_t ix_full[kRing], ix_empty[kRing];
   uint64_t s_full, s_empty;
   uint64_t p_full[2], p_empty[2];
-  uint64_t o_full, o_empty, m_full[2], m_empty[2], sf_full[2];
+  uint64_t o_full, o_empty, m_full[2], sf_full[2];
   uint64_t l_full[2], l_empty[2];
   uint64_t info_full[2], info_empty[2];
   uint64_t drain[2];
@@ -104,7 +103,7 @@ struct Small {
   alignas(16) int64_t row[kRing][kNB];   // cache row (-1: skipped)
   int valid[kRing];                      // some row of the block counts
   alignas(16) float alpha[2][kHg];       // by block parity: factor of O where `need` is set
-  uint32_t sf[2][kHg];                   // by block parity: the scales of P's four key steps, as exponents + 127
+  uint32_t sf[2][kHg];                   // by block parity: a block's scale, as exponent + 127 in each byte
   alignas(16) float lsum[2][kHg];        // reciprocal row sums, by item parity
   float qs[2][kHg], qnext[kHg];          // 2^-k of the item's heads, and of the converted next one's
   alignas(8) uint8_t need[2][8];         // by block parity and group of 8 heads: O must be rescaled
@@ -133,10 +132,10 @@ __device__ __forceinline__ void mma_mxfp8(uint32_t d, uint64_t a, uint64_t b, ui
       "l"(a), "l"(b), "r"(idesc), "r"(accum), "r"(sfa), "r"(sfb)
       : "memory");
 }
-// Its instruction descriptor: e4m3 operands, A (128 dims) MN-major, N = 64, ue8m0 scales, A's scale
-// byte 0 and B's scale byte `id`.
-__host__ __device__ constexpr uint32_t idesc_mx(uint32_t id) {
-  return (id << 4) | (1u << 15) | ((uint32_t)(64 >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 4) << 24);
+// Its instruction descriptor: e4m3 operands, A (128 dims) MN-major, N = 64, ue8m0 scales, byte 0 of
+// A's and of B's scale words.
+__host__ __device__ constexpr uint32_t idesc_mx() {
+  return (1u << 15) | ((uint32_t)(64 >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 4) << 24);
 }
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
@@ -223,9 +222,6 @@ __device__ __forceinline__ bool named_sync_or(int id, int n, bool pred) {
   return r != 0;
 }
 __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void prefetch_l2(const void* src) {
-  asm volatile("prefetch.global.L2 [%0];\n" ::"l"(reinterpret_cast<uint64_t>(src)) : "memory");
-}
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
@@ -303,6 +299,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity, abort_flag, p.wait));
   };
 
+  // The same, a barrier per lane.
+  auto wait_all = [&](uint64_t* b, uint32_t parity) -> bool {
+    if constexpr (!kPoll) {
+      bool done = mbar_try_wait_sleep(b, parity & 1, kSuspendNs);
+      if (__all_sync(0xffffffffu, done)) return true;
+    }
+    return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity & 1, abort_flag, p.wait));
+  };
+
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 4);
     mbar_init(&bar.q_empty, 1);
@@ -323,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       mbar_init(&bar.p_full[i], kSmWarps);
       mbar_init(&bar.p_empty[i], 1);
       mbar_init(&bar.m_full[i], kSmWarps);
-      mbar_init(&bar.m_empty[i], 4);
       mbar_init(&bar.sf_full[i], 4);
       mbar_init(&bar.l_full[i], kSmWarps);
       mbar_init(&bar.l_empty[i], 8);
@@ -651,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 #pragma unroll
               for (int k = 0; k < 4; ++k)  // keys 0-31 and 32-63 by the hi terms, then by the lo terms
                 mma_mxfp8(tmem + kColO + c * kHg, vd + (uint64_t)((c * kAtom + (k & 1) * 4096) >> 4),
-                          pd + (uint64_t)((k * 32) >> 4), idesc_mx(k), tmem + kColSfA, tmem + kColSfB + 4 * pb, (j | k) != 0);
+                          pd + (uint64_t)((k * 32) >> 4), idesc_mx(), tmem + kColSfA, tmem + kColSfB + 4 * pb, (j | k) != 0);
               mma_commit(&bar.kv_empty[st][c]);
             }
             mma_commit(&bar.p_empty[pb]);
@@ -707,7 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
             id[u] = j < nb && e < p.kk ? __ldg(irow + e) : -1;
           }
         };
-        // cache rows of ids; the rows' scales, and their lines on the way to L2
+        // cache rows of ids, and the rows' scales.  (Bringing the rows' lines to L2 from here cost more in
+        // the load pipe than it saved: 1.15 against 1.09 ms a 4,096-query chunk.)
         auto resolve = [&](const int (&id)[2], int64_t (&row)[2]) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -715,17 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
             if (row[u] < 0 && id[u] != -1) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
           }
         };
-        auto touch = [&](const int64_t (&row)[2], float (&scale)[2]) {
+        auto load_scales = [&](const int64_t (&row)[2], float (&scale)[2]) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            scale[u] = row[u] >= 0 ? __ldg(p.cache.scales + row[u]) : 0.f;
-            if (row[u] >= 0) {
-              const uint8_t* c = p.cache.codes + row[u] * kLatentDim;
-#pragma unroll
-              for (int x = 0; x < 4; ++x) prefetch_l2(c + 128 * x);
-              prefetch_l2(p.cache.rope + row[u] * kLatentRope);
-            }
-          }
+          for (int u = 0; u < 2; ++u) scale[u] = row[u] >= 0 ? __ldg(p.cache.scales + row[u]) : 0.f;
         };
         int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
         // each block's ids two, its rows and scales one of this warp's blocks ahead
@@ -735,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         load_ids(j, id);
         resolve(id, row);
         load_ids(j + 2, id);
-        touch(row, scale);
+        load_scales(row, scale);
         for (; j < nb; j += 2) {
           const uint32_t gj = g + j;
           const int ri = (int)(gj % kRing);
@@ -756,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           if (lane == 0) mbar_arrive(&bar.ix_full[ri]);
           row[0] = row_n[0];
           row[1] = row_n[1];
-          touch(row, scale);
+          load_scales(row, scale);
         }
         g += nb;
       }
@@ -785,14 +782,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       int any_valid = 0;
       for (int j = 0; j < nb; ++j, ++g) {
         const int ri = (int)(g % kRing), pb = (int)(g & 1);
-        // the block's scales are long there, P(g - 2) and its rescales are read: these waits do not
-        // stand between the scores and their softmax
-        if (!(ok = wait(&bar.ix_full[ri], (g / kRing) & 1) && wait(&bar.m_empty[pb], ((g >> 1) & 1) ^ 1) && wait(&bar.p_empty[pb], ((g >> 1) & 1) ^ 1) &&
-                   wait(&bar.s_full, g & 1)))
+        // the block's scales, the release of P(g - 2) (and with it of its scales) and the scores, each
+        // barrier by a quarter of the lanes: one latency for the three
+        if (!(ok = wait_all(lane & 2 ? &bar.s_full : lane & 1 ? &bar.p_empty[pb] : &bar.ix_full[ri],
+                            lane & 2 ? g : lane & 1 ? (g >> 1) ^ 1 : g / kRing)))
           break;
         uint32_t r[32];
         tc_fence_after();
         tmem_ld_16x256b_x8(s_addr, r);
+        float2 sc[16];  // {scale, log2 scale} of this thread's keys, while the scores come
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+          const float4 s = *reinterpret_cast<const float4*>(&sm->sc[ri][8 * jj + 2 * m]);
+          sc[2 * jj] = make_float2(cq * s.x, s.y);
+          sc[2 * jj + 1] = make_float2(cq * s.z, s.w);
+        }
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
@@ -801,11 +805,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         float y[16], ymax = -INFINITY;
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
-          const float4 s = *reinterpret_cast<const float4*>(&sm->sc[ri][8 * jj + 2 * m]);
           const float t0 = fmaf(__uint_as_float(r[4 * jj + 2]), 0.0625f, __uint_as_float(r[4 * jj]));
           const float t1 = fmaf(__uint_as_float(r[4 * jj + 3]), 0.0625f, __uint_as_float(r[4 * jj + 1]));
-          y[2 * jj] = fmaf(t0, cq * s.x, s.y);
-          y[2 * jj + 1] = fmaf(t1, cq * s.z, s.w);
+          y[2 * jj] = fmaf(t0, sc[2 * jj].x, sc[2 * jj].y);
+          y[2 * jj + 1] = fmaf(t1, sc[2 * jj + 1].x, sc[2 * jj + 1].y);
           ymax = fmaxf(ymax, fmaxf(y[2 * jj], y[2 * jj + 1]));
         }
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 1));
@@ -817,8 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         E0 = move ? E : E0;
         const float d = fmaxf(E - E0, -120.f);  // beside 2^0, nothing is left of 2^-120
         if (m == 0) {
-          const uint32_t hi = (uint32_t)(127 + (int)d);
-          sm->sf[pb][hl] = hi * 0x0101u | (hi - 4) * 0x01010000u;
+          sm->sf[pb][hl] = (uint32_t)(127 + (int)d) * 0x01010101u;  // of all four key steps
           if (any) sm->alpha[pb][hl] = alpha;
         }
         __syncwarp();
@@ -837,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           sum = fmaf(p1, is.y, sum);
           const uint32_t h = f16x2(p0, p1);
           const uint16_t hi = e4m3_of_f16x2(h);
-          const uint16_t lo = e4m3_of_f16x2(mul_f16x2(sub_f16x2(h, f16x2_of_e4m3(hi)), 0x4c004c00u));  // (f16 16.0)
+          const uint16_t lo = e4m3_of_f16x2(sub_f16x2(h, f16x2_of_e4m3(hi)));
           const uint32_t at = prow + (jj & 1) * 8;
           asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((jj >> 1) ^ (hl & 7)) << 4)), "h"(hi) : "memory");
           asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((4 + (jj >> 1)) ^ (hl & 7)) << 4)), "h"(lo) : "memory");
@@ -926,10 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         tmem_wait_stores();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar.sf_full[g & 1]);
-          mbar_arrive(&bar.m_empty[g & 1]);
-        }
+        if (lane == 0) mbar_arrive(&bar.sf_full[g & 1]);
       }
       if (!ok || !(ok = epilogue(item, oc))) break;
       ++oc;
