@@ -299,15 +299,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity, abort_flag, p.wait));
   };
 
-  // The same, a barrier per lane.
-  auto wait_all = [&](uint64_t* b, uint32_t parity) -> bool {
-    if constexpr (!kPoll) {
-      bool done = mbar_try_wait_sleep(b, parity & 1, kSuspendNs);
-      if (__all_sync(0xffffffffu, done)) return true;
-    }
-    return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity & 1, abort_flag, p.wait));
-  };
-
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 4);
     mbar_init(&bar.q_empty, 1);
@@ -782,21 +773,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       int any_valid = 0;
       for (int j = 0; j < nb; ++j, ++g) {
         const int ri = (int)(g % kRing), pb = (int)(g & 1);
-        // the block's scales, the release of P(g - 2) (and with it of its scales) and the scores, each
-        // barrier by a quarter of the lanes: one latency for the three
-        if (!(ok = wait_all(lane & 2 ? &bar.s_full : lane & 1 ? &bar.p_empty[pb] : &bar.ix_full[ri],
-                            lane & 2 ? g : lane & 1 ? (g >> 1) ^ 1 : g / kRing)))
+        // the block's scales, the release of P(g - 2) (and with it of its scales), the scores.  (Uniform
+        // waits, one by one: a barrier per lane, for one latency in all, took 2,530 cycles a block, not 2,170.)
+        if (!(ok = wait(&bar.ix_full[ri], (g / kRing) & 1) && wait(&bar.p_empty[pb], ((g >> 1) & 1) ^ 1) && wait(&bar.s_full, g & 1)))
           break;
         uint32_t r[32];
         tc_fence_after();
         tmem_ld_16x256b_x8(s_addr, r);
-        float2 sc[16];  // {scale, log2 scale} of this thread's keys, while the scores come
-#pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-          const float4 s = *reinterpret_cast<const float4*>(&sm->sc[ri][8 * jj + 2 * m]);
-          sc[2 * jj] = make_float2(cq * s.x, s.y);
-          sc[2 * jj + 1] = make_float2(cq * s.z, s.w);
-        }
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
@@ -807,8 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         for (int jj = 0; jj < 8; ++jj) {
           const float t0 = fmaf(__uint_as_float(r[4 * jj + 2]), 0.0625f, __uint_as_float(r[4 * jj]));
           const float t1 = fmaf(__uint_as_float(r[4 * jj + 3]), 0.0625f, __uint_as_float(r[4 * jj + 1]));
-          y[2 * jj] = fmaf(t0, sc[2 * jj].x, sc[2 * jj].y);
-          y[2 * jj + 1] = fmaf(t1, sc[2 * jj + 1].x, sc[2 * jj + 1].y);
+          const float4 s = *reinterpret_cast<const float4*>(&sm->sc[ri][8 * jj + 2 * m]);
+          y[2 * jj] = fmaf(t0, cq * s.x, s.y);
+          y[2 * jj + 1] = fmaf(t1, cq * s.z, s.w);
           ymax = fmaxf(ymax, fmaxf(y[2 * jj], y[2 * jj + 1]));
         }
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 1));

@@ -835,3 +835,28 @@ def test_captured_appends_norms_and_reads_replay():
 def test_synth_latent_shape_is_the_cache_s():
     wl = synth.WORKLOADS["prefill_16k"]
     assert (wl.DQK, wl.DV) == (576, 512)
+
+
+@pytest.mark.parametrize("B,T,H,S,k", [(1, 400, 64, 4000, 512), (2, 1, 128, 4000, 2048), (1, 900, 16, 3000, 64)])
+def test_latent_attn_waits_that_run_out(B, T, H, S, k):
+    """A limit of one cycle: every wait that is not complete at the first look gives up, the kernel
+    ends what it has in flight and raises the flag; the same call with the default limit is right."""
+    cache = _cache(B, S, 64)
+    at = dict(q=_q(B, T, H), cache=cache, scale=1 / 24)
+    idx = _idx(B, T, S, k)
+    want, lse = dsa.dsa_latent_attn(at, idx)
+    assert dsa.read_device_flags(DEV) == 0
+    raised = False
+    for _ in range(3):
+        try:
+            dsa.set_wait_limit(1)
+            dsa.dsa_latent_attn(at, idx)
+            torch.cuda.synchronize()
+        finally:
+            dsa.set_wait_limit(0)
+        flags = dsa.read_device_flags(DEV)  # read, and cleared, after every call
+        raised = raised or bool(flags & dsa.FLAG_TIMEOUT)
+    assert raised
+    o, l = dsa.dsa_latent_attn(at, idx)
+    assert dsa.read_device_flags(DEV) == 0
+    assert torch.equal(o, want) and torch.equal(l, lse)
