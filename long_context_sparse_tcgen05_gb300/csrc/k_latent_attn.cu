@@ -51,6 +51,7 @@
 #include <atomic>
 
 #include "dsa_internal.cuh"
+#include "fp8_rows.cuh"
 #include "latent_cache.cuh"
 #include "sm100.cuh"
 
@@ -69,7 +70,7 @@ constexpr uint32_t kPBytes = kHg * 128;      // P: per head 64 hi bytes, then 64
 // 16-byte words of a row permuted by the row's low bits (a lane reads its row word by word).
 constexpr uint32_t kQCodes = 128 * kLatentDim, kQBytes = kQCodes + 128 * kLatentRope * 2;
 constexpr int kGatherWarps = 4, kSWarp = 4, kPvWarp = 5, kIxWarp0 = 6, kSmWarp0 = 8, kSmWarps = 8, kOWarp0 = 16, kQWarp0 = 20;
-constexpr int kRing = 4;                     // blocks the index warps may be ahead
+constexpr int kRing = 6;                     // blocks the index warps may be ahead
 constexpr int kThreads = 24 * 32;
 // Registers by warpgroup (warps 0-3, 4-7, ..), moved at the start from the kernel's own kRegs each;
 // the softmax warps spilled in their block loop at kRegs.
@@ -81,8 +82,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMove = 60.f;                // E0 moves when a block's E passes it by this
 constexpr int kInfoReaders = kGatherWarps + 2 + kSmWarps + 4 + 4;
 constexpr int kEpiThreads = 256;             // O and query warps store an item's O together
-constexpr uint32_t kOPitch = kLatentDim + 16;  // staged half of an O row: 8 heads' 16-byte pieces in 32 banks
-static_assert(kHg * kOPitch <= kQBytes, "halves of O are staged in the queries' room");
+constexpr uint32_t kOPitch = 2 * kLatentDim + 16;  // a staged O row: 8 heads' 16-byte pieces in 32 banks
+static_assert(kHg * kOPitch <= kQBytes, "O is staged in the queries' room");
 
 struct Bars {
   uint64_t q_full, q_empty, qs_full[2];
@@ -98,9 +99,9 @@ struct Bars {
   uint64_t drain[2];
 };
 struct Small {
-  alignas(16) float2 sc[kRing][kNB];     // {scale, log2 scale} of a block's rows; {0, -inf}: skipped
+  alignas(16) float4 sc[kRing][kNB / 2]; // of two rows of a block: their scales, log2 of them (0 and -inf: skipped)
   alignas(16) float isc[kRing][kNB];     // 1 / scale (0: skipped)
-  alignas(16) int64_t row[kRing][kNB];   // cache row (-1: skipped)
+  int32_t row[kRing][kNB];               // cache row (-1: skipped); 2^31 rows would not fit in memory
   int valid[kRing];                      // some row of the block counts
   alignas(16) float alpha[2][kHg];       // by block parity: factor of O where `need` is set
   uint32_t sf[2][kHg];                   // by block parity: a block's scale, as exponent + 127 in each byte
@@ -203,6 +204,24 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile 
     }
   }
   return true;
+}
+// One look at three phases: their latencies overlap.
+__device__ __forceinline__ bool try_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 r, [%5], %6, %7;\n\t"
+      "and.pred p, p, q;\n\tand.pred p, p, r;\n\tselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(a)), "r"(pa), "r"(smem_addr(b)), "r"(pb), "r"(smem_addr(c)), "r"(pc), "r"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ bool elect_lane() {
   uint32_t r;
@@ -408,9 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
   };
 
-  // An item's O, once its sums and its last value product are there: first dim chunks 0 and 1, then
-  // 2 and 3, one of each by the O warps and the other by the query warps.  false: a wait ran out in
-  // one of them, and all eight leave.
+  // An item's O, once its sums and its last value product are there: dim chunks 0 and 2 by the O warps,
+  // 1 and 3 by the query warps.  false: a wait ran out in one of them, and all eight leave.
   // These warps meet at barrier 1 in step, and once more (meet_last) when they are done or leave for
   // a wait of their own, so none waits there for one that has left.
   bool met_failure = false;
@@ -429,12 +447,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     tc_fence_after();
     float* po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
     // (a head without weights, sum 0, gives zeros whatever its products left)
+    const float* ls = sm->lsum[oc & 1];
+    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const uint32_t o_addr = tmem + ((uint32_t)(q4 * 32) << 16) + kColO + (2 * half + cw) * kHg;
-      const float* ls = sm->lsum[oc & 1];
+    for (int c = cw; c < 4; c += 2) {
+      const uint32_t o_addr = tmem + lanes + kColO + c * kHg;
       if (po) {  // a part: fp32 rows, 32 dims a store (a lane's own heads together: a line per lane)
-        float* out = po + half * 256 + cw * 128 + q4 * 32 + lane;
+        float* out = po + c * 128 + q4 * 32 + lane;
 #pragma unroll 1
         for (int h0 = 0; h0 < I.heads; h0 += 8) {
           uint32_t r[8];
@@ -449,9 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       } else {
         // 16 dims x 16 heads at a time, as 8 x 8 tiles (rows: dims) that stmatrix stores transposed.
         // (Small loops: unrolled, this code ran at the pace of its instruction fetches.)
-        if (half) named_sync(1, kEpiThreads);  // the first half has left the room
         const uint32_t dst = smem_addr(q_s) + (8 * (lane >> 4) + (lane & 7)) * kOPitch +
-                             2 * (cw * 128 + q4 * 32 + 8 * ((lane >> 3) & 1));
+                             2 * (c * 128 + q4 * 32 + 8 * ((lane >> 3) & 1));
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
           const int x = 16 * (i >> 2), h0 = 16 * (i & 3);  // dims, heads
@@ -467,35 +485,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
               const float f = u & 1 ? L.y : L.x;
               o[u] = f == 0.f ? 0.f : __uint_as_float(r[4 * jj + u]) * f;
             }
-            const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
-            w[2 * jj] = *reinterpret_cast<const uint32_t*>(&a);
-            w[2 * jj + 1] = *reinterpret_cast<const uint32_t*>(&b);
+            w[2 * jj] = pack_bf16(o[0], o[1]);
+            w[2 * jj + 1] = pack_bf16(o[2], o[3]);
           }
           asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + h0 * kOPitch + 2 * x),
                        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                        : "memory");
         }
       }
-      if (half) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar.l_empty[oc & 1]);
-          mbar_arrive(&bar.o_empty);
-        }
-      }
-      if (po) continue;
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&bar.l_empty[oc & 1]);
+      mbar_arrive(&bar.o_empty);
+    }
+    if (!po) {
       async_fence();  // the staged rows are read by bulk copies
       named_sync(1, kEpiThreads);
       if (warp >= kQWarp0) {
         const int h = threadIdx.x - kQWarp0 * 32;
         if (h < I.heads) {
-          bulk_store(p.out + ((int64_t)I.row * p.H + I.h0 + h) * kLatentDim + half * 256, smem_addr(q_s) + h * kOPitch, kLatentDim);
+          bulk_store(p.out + ((int64_t)I.row * p.H + I.h0 + h) * kLatentDim, smem_addr(q_s) + h * kOPitch, 2 * kLatentDim);
           asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
           asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
         }
-        if (half) named_sync(2, 128);  // the room may hold converted queries again
-        __syncwarp();
+        named_sync(2, 128);  // the room may hold converted queries again
       }
     }
     return true;
@@ -664,12 +679,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       __syncwarp();
     } else {
       // ================= index: positions to cache rows and scales =================
-      int it = 0;
-      uint32_t g = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+      struct Blocks {  // of an item: its row's ids, its sequence, its first block and their number
+        const int32_t* ids;
+        int b, j0, nb;
+      };
+      auto blocks_of = [&](int item) -> Blocks {
         const Item I = item_of(p, item);
-        const int32_t* irow = p.idx + I.b * p.idx_sb + I.t * p.idx_st;
+        const int32_t* ids = p.idx + I.b * p.idx_sb + I.t * p.idx_st;
         // blocks of the row = 1 + (last entry other than -1) / 64, searched from the end
         int last = -1;
         for (int e0 = p.kk - 1; e0 >= 0 && last < 0; e0 -= 32 * 8) {
@@ -677,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             const int e = e0 - u * 32 - lane;
-            v[u] = e >= 0 ? __ldg(irow + e) : -1;
+            v[u] = e >= 0 ? __ldg(ids + e) : -1;
           }
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
@@ -687,55 +703,73 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         }
         const int nbr = (last + kNB) / kNB;
         const int j0 = (int)((int64_t)I.split * nbr / p.splits);
-        const int nb = (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0;
+        return {ids, I.b, j0, (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0};
+      };
+      Blocks cur = blocks_of(blockIdx.x), next{};
+      // Below, block j >= cur.nb is the next item's block j - cur.nb.
+      auto load_ids = [&](int j, int (&id)[2]) {
+        const bool here = j < cur.nb;
+        const int32_t* ids = here ? cur.ids : next.ids;
+        const int jb = here ? j : j - cur.nb, e0 = ((here ? cur.j0 : next.j0) + jb) * kNB + lane;
+        const bool in = jb < (here ? cur.nb : next.nb);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) id[u] = in && e0 + u * 32 < p.kk ? __ldg(ids + e0 + u * 32) : -1;
+      };
+      auto resolve = [&](int j, const int (&id)[2], int (&row)[2]) {
+        const int b = j < cur.nb ? cur.b : next.b;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          row[u] = id[u] >= 0 && id[u] < p.S ? (int)latent_row(p.cache, b, id[u]) : -1;
+          if (row[u] < 0 && id[u] != -1) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
+        }
+      };
+      // (Bringing the rows' lines to L2 from here cost more in the load pipe than it saved: 1.15 against
+      // 1.09 ms a 4,096-query chunk.)
+      auto load_scales = [&](const int (&row)[2], float (&scale)[2]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) scale[u] = row[u] >= 0 ? __ldg(p.cache.scales + row[u]) : 0.f;
+      };
+      // Each block's ids are loaded two, its rows and scales resolved one of this warp's blocks ahead,
+      // and so across items: the five loads from the end of a row's ids to its first scales, each on
+      // the last one's result, took 9,000 cycles at the start of every row.  (Only where the item had
+      // two blocks or more for this warp; the first blocks of the others' successors wait.)
+      int id[2], row[2];
+      float scale[2];
+      int it = 0;
+      uint32_t g = 0;
+      bool ok = true, ahead = false;  // ahead: id, row and scale are the item's
+      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
         if (warp == kIxWarp0) {
           if (!(ok = wait(&bar.info_empty[it & 1], ((it >> 1) & 1) ^ 1))) break;
           if (lane == 0) {
-            sm->nb[it & 1] = nb;
+            sm->nb[it & 1] = cur.nb;
             mbar_arrive(&bar.info_full[it & 1]);
           }
         }
-        auto load_ids = [&](int j, int (&id)[2]) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int e = (j0 + j) * kNB + u * 32 + lane;
-            id[u] = j < nb && e < p.kk ? __ldg(irow + e) : -1;
-          }
-        };
-        // cache rows of ids, and the rows' scales.  (Bringing the rows' lines to L2 from here cost more in
-        // the load pipe than it saved: 1.15 against 1.09 ms a 4,096-query chunk.)
-        auto resolve = [&](const int (&id)[2], int64_t (&row)[2]) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            row[u] = id[u] >= 0 && id[u] < p.S ? latent_row(p.cache, I.b, id[u]) : -1;
-            if (row[u] < 0 && id[u] != -1) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
-          }
-        };
-        auto load_scales = [&](const int64_t (&row)[2], float (&scale)[2]) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) scale[u] = row[u] >= 0 ? __ldg(p.cache.scales + row[u]) : 0.f;
-        };
         int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
-        // each block's ids two, its rows and scales one of this warp's blocks ahead
-        int id[2];
-        int64_t row[2];
-        float scale[2];
-        load_ids(j, id);
-        resolve(id, row);
-        load_ids(j + 2, id);
-        load_scales(row, scale);
-        for (; j < nb; j += 2) {
-          const uint32_t gj = g + j;
-          const int ri = (int)(gj % kRing);
-          int64_t row_n[2];
-          resolve(id, row_n);
+        if (!ahead && j < cur.nb) {
+          load_ids(j, id);
+          resolve(j, id, row);
+          load_ids(j + 2, id);
+          load_scales(row, scale);
+        }
+        int known = item + G < items ? 0 : 2;  // the last loads that saw the blocks of this or the next item
+        bool seen = known != 0;                // the next item's blocks are known
+        next.nb = 0;
+        for (; j < cur.nb; j += 2) {
+          const int ri = (int)((g + j) % kRing);
+          int row_n[2];
+          resolve(j + 2, id, row_n);
           load_ids(j + 4, id);
-          if (!(ok = wait(&bar.ix_empty[ri], ((gj / kRing) & 1) ^ 1))) break;
+          known = j + 4 < cur.nb || seen ? known + 1 : 0;
+          if (!(ok = wait(&bar.ix_empty[ri], (((g + j) / kRing) & 1) ^ 1))) break;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int r = u * 32 + lane;
             sm->row[ri][r] = row[u];
-            sm->sc[ri][r] = row[u] >= 0 ? make_float2(scale[u], log2f(scale[u])) : make_float2(0.f, -INFINITY);
+            float* sc = reinterpret_cast<float*>(&sm->sc[ri][r >> 1]) + (r & 1);
+            sc[0] = row[u] >= 0 ? scale[u] : 0.f;
+            sc[2] = row[u] >= 0 ? log2f(scale[u]) : -INFINITY;
             sm->isc[ri][r] = row[u] >= 0 ? 1.f / scale[u] : 0.f;
           }
           const bool some = __any_sync(0xffffffffu, row[0] >= 0 || row[1] >= 0);
@@ -745,8 +779,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           row[0] = row_n[0];
           row[1] = row_n[1];
           load_scales(row, scale);
+          if (!seen && j + 6 >= cur.nb) {
+            next = blocks_of(item + G);
+            seen = true;
+          }
         }
-        g += nb;
+        if (!seen) next = blocks_of(item + G);
+        ahead = known >= 2;
+        g += cur.nb;
+        cur = next;
       }
     }
   } else if (warp < kOWarp0) {
@@ -775,8 +816,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         const int ri = (int)(g % kRing), pb = (int)(g & 1);
         // the block's scales, the release of P(g - 2) (and with it of its scales), the scores.  (Uniform
         // waits, one by one: a barrier per lane, for one latency in all, took 2,530 cycles a block, not 2,170.)
-        if (!(ok = wait(&bar.ix_full[ri], (g / kRing) & 1) && wait(&bar.p_empty[pb], ((g >> 1) & 1) ^ 1) && wait(&bar.s_full, g & 1)))
-          break;
+        if (kPoll || !__all_sync(0xffffffffu, try_wait3(&bar.ix_full[ri], (g / kRing) & 1, &bar.p_empty[pb], ((g >> 1) & 1) ^ 1,
+                                                        &bar.s_full, g & 1)))
+          if (!(ok = wait(&bar.ix_full[ri], (g / kRing) & 1) && wait(&bar.p_empty[pb], ((g >> 1) & 1) ^ 1) && wait(&bar.s_full, g & 1)))
+            break;
         uint32_t r[32];
         tc_fence_after();
         tmem_ld_16x256b_x8(s_addr, r);
@@ -785,15 +828,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.s_empty);
         any_valid |= sm->valid[ri];
-        float y[16], ymax = -INFINITY;
+        f32x2 y[8];
+        float ymax = -INFINITY;
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
-          const float t0 = fmaf(__uint_as_float(r[4 * jj + 2]), 0.0625f, __uint_as_float(r[4 * jj]));
-          const float t1 = fmaf(__uint_as_float(r[4 * jj + 3]), 0.0625f, __uint_as_float(r[4 * jj + 1]));
-          const float4 s = *reinterpret_cast<const float4*>(&sm->sc[ri][8 * jj + 2 * m]);
-          y[2 * jj] = fmaf(t0, cq * s.x, s.y);
-          y[2 * jj + 1] = fmaf(t1, cq * s.z, s.w);
-          ymax = fmaxf(ymax, fmaxf(y[2 * jj], y[2 * jj + 1]));
+          const float4 s = sm->sc[ri][4 * jj + m];
+          const f32x2 t = fma_2(pair(__uint_as_float(r[4 * jj + 2]), __uint_as_float(r[4 * jj + 3])), pair(0.0625f, 0.0625f),
+                                pair(__uint_as_float(r[4 * jj]), __uint_as_float(r[4 * jj + 1])));
+          y[jj] = fma_2(t, mul_2(pair(cq, cq), pair(s.x, s.y)), pair(s.z, s.w));
+          ymax = max3(ymax, lo_of(y[jj]), hi_of(y[jj]));
         }
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 1));
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 2));
@@ -813,21 +856,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           mbar_arrive(&bar.m_full[pb]);
         }
         const float eu = E == -INFINITY ? 0.f : E;
-        float sum = 0.f;
-        const uint32_t prow = smem_addr(p_s + pb * kPBytes + hl * 128) + 2 * m;
+        f32x2 sum2 = 0;
+        const uint32_t at = smem_addr(p_s + pb * kPBytes + hl * 128) + ((hl & 7) << 4) + 2 * m;
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
-          const float p0 = ex2(y[2 * jj] - eu), p1 = ex2(y[2 * jj + 1] - eu);
+          const f32x2 x = add_2(y[jj], pair(-eu, -eu));
+          const float p0 = ex2(lo_of(x)), p1 = ex2(hi_of(x));
           const float2 is = *reinterpret_cast<const float2*>(&sm->isc[ri][8 * jj + 2 * m]);
-          sum = fmaf(p0, is.x, sum);
-          sum = fmaf(p1, is.y, sum);
+          sum2 = fma_2(pair(p0, p1), pair(is.x, is.y), sum2);
           const uint32_t h = f16x2(p0, p1);
           const uint16_t hi = e4m3_of_f16x2(h);
           const uint16_t lo = e4m3_of_f16x2(sub_f16x2(h, f16x2_of_e4m3(hi)));
-          const uint32_t at = prow + (jj & 1) * 8;
-          asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((jj >> 1) ^ (hl & 7)) << 4)), "h"(hi) : "memory");
-          asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + (((4 + (jj >> 1)) ^ (hl & 7)) << 4)), "h"(lo) : "memory");
+          asm volatile("st.shared.b16 [%0], %1;\n" ::"r"((at ^ ((jj >> 1) << 4)) + (jj & 1) * 8), "h"(hi) : "memory");
+          asm volatile("st.shared.b16 [%0], %1;\n" ::"r"((at ^ ((4 + (jj >> 1)) << 4)) + (jj & 1) * 8), "h"(lo) : "memory");
         }
+        const float sum = lo_of(sum2) + hi_of(sum2);
         l = fmaf(sum, E == -INFINITY ? 0.f : ex2(E - E0), l * alpha);
         async_fence();
         __syncwarp();
