@@ -180,11 +180,13 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// 16 lanes x 16 columns, distributed the same way.
-__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
+// 16 lanes x 32 columns, distributed the same way.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
@@ -241,6 +243,7 @@ __device__ __forceinline__ bool named_sync_or(int id, int n, bool pred) {
   return r != 0;
 }
 __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void named_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
@@ -438,6 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   auto epilogue = [&](int item, int oc) -> bool {
     const int q4 = warp & 3, cw = warp < kQWarp0 ? 0 : 1;
     const Item I = item_of(p, item);
+    float* const po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
+    const float* ls = sm->lsum[oc & 1];
+    const uint32_t o_addr = tmem + ((uint32_t)(q4 * 32) << 16) + kColO + cw * kHg;
     const bool ok = wait(&bar.l_full[oc & 1], (oc >> 1) & 1) && wait(&bar.o_full, oc & 1);
     // (here the query warps are past the read of their converted queries)
     if (named_sync_or(1, kEpiThreads, !ok)) {
@@ -445,19 +451,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       return false;
     }
     tc_fence_after();
-    float* po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
     // (a head without weights, sum 0, gives zeros whatever its products left)
-    const float* ls = sm->lsum[oc & 1];
-    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+    const bool none = __any_sync(0xffffffffu, ls[lane] == 0.f || ls[32 + lane] == 0.f);
+    if (po) {  // a part: fp32 rows, 32 dims a store (a lane's own heads together: a line per lane)
 #pragma unroll 1
-    for (int c = cw; c < 4; c += 2) {
-      const uint32_t o_addr = tmem + lanes + kColO + c * kHg;
-      if (po) {  // a part: fp32 rows, 32 dims a store (a lane's own heads together: a line per lane)
-        float* out = po + c * 128 + q4 * 32 + lane;
+      for (int c = 0; c < 2; ++c) {
+        float* out = po + (2 * c + cw) * 128 + q4 * 32 + lane;
 #pragma unroll 1
         for (int h0 = 0; h0 < I.heads; h0 += 8) {
           uint32_t r[8];
-          tmem_ld_x8(o_addr + h0, r);
+          tmem_ld_x8(o_addr + 2 * c * kHg + h0, r);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -465,32 +468,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
             out[(h0 + i) * kLatentDim] = f == 0.f ? 0.f : __uint_as_float(r[i]) * f;
           }
         }
-      } else {
-        // 16 dims x 16 heads at a time, as 8 x 8 tiles (rows: dims) that stmatrix stores transposed.
-        // (Small loops: unrolled, this code ran at the pace of its instruction fetches.)
-        const uint32_t dst = smem_addr(q_s) + (8 * (lane >> 4) + (lane & 7)) * kOPitch +
-                             2 * (c * 128 + q4 * 32 + 8 * ((lane >> 3) & 1));
+      }
+    } else {
+      // 16 dims x 32 heads at a time, as 8 x 8 tiles (rows: dims) that stmatrix stores transposed.
+      // (A small loop: unrolled, this code ran at the pace of its instruction fetches.)
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          const int x = 16 * (i >> 2), h0 = 16 * (i & 3);  // dims, heads
-          uint32_t r[8], w[4];
-          tmem_ld_16x256b_x2(o_addr + h0 + ((uint32_t)x << 16), r);
+      for (int h0 = 0; h0 < kHg; h0 += 32) {
+        const uint32_t dst = smem_addr(q_s) + (h0 + 8 * (lane >> 4) + (lane & 7)) * kOPitch +
+                             2 * (cw * 128 + q4 * 32 + 8 * ((lane >> 3) & 1));
+        f32x2 f[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) f[t] = *reinterpret_cast<const f32x2*>(ls + h0 + 8 * t + 2 * (lane & 3));
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int x = 16 * (i & 1), c = i >> 1;  // dims, of this warp's chunks
+          uint32_t r[16], w[8];
+          tmem_ld_16x256b_x4(o_addr + 2 * c * kHg + h0 + ((uint32_t)x << 16), r);
           tmem_wait_ld();
+          if (none) {
 #pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const float2 L = *reinterpret_cast<const float2*>(ls + h0 + 8 * jj + 2 * (lane & 3));
-            float o[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float f = u & 1 ? L.y : L.x;
-              o[u] = f == 0.f ? 0.f : __uint_as_float(r[4 * jj + u]) * f;
-            }
-            w[2 * jj] = pack_bf16(o[0], o[1]);
-            w[2 * jj + 1] = pack_bf16(o[2], o[3]);
+            for (int u = 0; u < 16; ++u)
+              if ((u & 1 ? hi_of(f[u >> 2]) : lo_of(f[u >> 2])) == 0.f) r[u] = 0;
           }
-          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + h0 * kOPitch + 2 * x),
-                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const f32x2 v = mul_2(pair(__uint_as_float(r[2 * u]), __uint_as_float(r[2 * u + 1])), f[u >> 1]);
+            w[u] = pack_bf16(lo_of(v), hi_of(v));
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + 16 * k * kOPitch + 2 * x + 512 * c),
+                         "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
+                         : "memory");
         }
       }
     }
@@ -502,8 +511,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
     if (!po) {
       async_fence();  // the staged rows are read by bulk copies
-      named_sync(1, kEpiThreads);
-      if (warp >= kQWarp0) {
+      if (warp < kQWarp0) {
+        named_arrive(4, kEpiThreads);  // (the next arrival here comes after the next meeting at barrier 1)
+      } else {
+        named_sync(4, kEpiThreads);
         const int h = threadIdx.x - kQWarp0 * 32;
         if (h < I.heads) {
           bulk_store(p.out + ((int64_t)I.row * p.H + I.h0 + h) * kLatentDim, smem_addr(q_s) + h * kOPitch, 2 * kLatentDim);
@@ -912,8 +923,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       const int nb = sm->nb[it & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
-      const Item I = item_of(p, item);
       if (nb == 0) {  // nothing selected: O = 0, LSE = -inf
+        const Item I = item_of(p, item);
         uint16_t* og = p.out + ((int64_t)I.row * p.H + I.h0) * kLatentDim;
         if (p.splits > 1) {  // the combine reads no part whose weight is 0
           if (t < kHg) p.part_lse[(int64_t)item * kHg + t] = -INFINITY;
