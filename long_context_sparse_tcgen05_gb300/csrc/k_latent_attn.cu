@@ -480,26 +480,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 #pragma unroll
         for (int t = 0; t < 4; ++t) f[t] = *reinterpret_cast<const f32x2*>(ls + h0 + 8 * t + 2 * (lane & 3));
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const int x = 16 * (i & 1), c = i >> 1;  // dims, of this warp's chunks
-          uint32_t r[16], w[8];
-          tmem_ld_16x256b_x4(o_addr + 2 * c * kHg + h0 + ((uint32_t)x << 16), r);
+        for (int c = 0; c < 2; ++c) {  // this warp's chunks: dims 0-15 and 16-31 of its quarter together
+          uint32_t r[2][16], w[8];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) tmem_ld_16x256b_x4(o_addr + 2 * c * kHg + h0 + (x << 20), r[x]);
           tmem_wait_ld();
-          if (none) {
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
-              if ((u & 1 ? hi_of(f[u >> 2]) : lo_of(f[u >> 2])) == 0.f) r[u] = 0;
+          for (int x = 0; x < 2; ++x) {
+            if (none) {
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                if ((u & 1 ? hi_of(f[u >> 2]) : lo_of(f[u >> 2])) == 0.f) r[x][u] = 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const f32x2 v = mul_2(pair(__uint_as_float(r[x][2 * u]), __uint_as_float(r[x][2 * u + 1])), f[u >> 1]);
+              w[u] = pack_bf16(lo_of(v), hi_of(v));
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + 16 * k * kOPitch + 32 * x + 512 * c),
+                           "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
+                           : "memory");
           }
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const f32x2 v = mul_2(pair(__uint_as_float(r[2 * u]), __uint_as_float(r[2 * u + 1])), f[u >> 1]);
-            w[u] = pack_bf16(lo_of(v), hi_of(v));
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + 16 * k * kOPitch + 2 * x + 512 * c),
-                         "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
-                         : "memory");
         }
       }
     }
@@ -510,11 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       mbar_arrive(&bar.o_empty);
     }
     if (!po) {
-      async_fence();  // the staged rows are read by bulk copies
       if (warp < kQWarp0) {
         named_arrive(4, kEpiThreads);  // (the next arrival here comes after the next meeting at barrier 1)
       } else {
         named_sync(4, kEpiThreads);
+        async_fence();  // the staged rows, all warps', are read by bulk copies
         const int h = threadIdx.x - kQWarp0 * 32;
         if (h < I.heads) {
           bulk_store(p.out + ((int64_t)I.row * p.H + I.h0 + h) * kLatentDim, smem_addr(q_s) + h * kOPitch, 2 * kLatentDim);
@@ -663,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           if (!(ok = wait(&bar.kv_full[st], (g / kStages) & 1) && wait(&bar.sf_full[pb], (g >> 1) & 1) &&
                      wait(&bar.p_full[pb], (g >> 1) & 1)))
             break;
-          async_fence();
+          async_fence();  // P was written by plain stores, the stage by cp.async
           tc_fence_after();
           if (elect_lane()) {
             const uint64_t vd = v_desc + (uint64_t)((st * kStage) >> 4), pd = p_desc + (uint64_t)((pb * kPBytes) >> 4);
@@ -883,7 +886,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         }
         const float sum = lo_of(sum2) + hi_of(sum2);
         l = fmaf(sum, E == -INFINITY ? 0.f : ex2(E - E0), l * alpha);
-        async_fence();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&bar.p_full[pb]);
