@@ -90,7 +90,7 @@ struct Bars {
   // kv_empty[st][c]: atom c of stage st may be refilled (0-3 codes, after the value product's dim
   // chunk c; 4 rope values, after the score product)
   uint64_t kv_full[kStages], kv_empty[kStages][5];
-  uint64_t ix_full[kRing], ix_empty[kRing];
+  uint64_t ix_row[kRing], ix_full[kRing], ix_empty[kRing];  // a block's rows; its scales too
   uint64_t s_full, s_empty;
   uint64_t p_full[2], p_empty[2];
   uint64_t o_full, o_empty, m_full[2], sf_full[2];
@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity, abort_flag, p.wait));
   };
 
+  asm volatile("griddepcontrol.launch_dependents;\n");  // (k_latent_combine waits for this grid's end itself)
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 4);
     mbar_init(&bar.q_empty, 1);
@@ -333,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       for (int c = 0; c < 5; ++c) mbar_init(&bar.kv_empty[i][c], 1);
     }
     for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar.ix_row[i], 1);
       mbar_init(&bar.ix_full[i], 1);
       mbar_init(&bar.ix_empty[i], kSmWarps);
     }
@@ -453,19 +455,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     tc_fence_after();
     // (a head without weights, sum 0, gives zeros whatever its products left)
     const bool none = __any_sync(0xffffffffu, ls[lane] == 0.f || ls[32 + lane] == 0.f);
-    if (po) {  // a part: fp32 rows, 32 dims a store (a lane's own heads together: a line per lane)
+    if (po) {  // a part: fp32 rows, 32 dims of a head a store
 #pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        float* out = po + (2 * c + cw) * 128 + q4 * 32 + lane;
-#pragma unroll 1
-        for (int h0 = 0; h0 < I.heads; h0 += 8) {
-          uint32_t r[8];
-          tmem_ld_x8(o_addr + 2 * c * kHg + h0, r);
-          tmem_wait_ld();
+      for (int i = 0; i < 4; ++i) {
+        const int c = i >> 1, h0 = 32 * (i & 1);
+        float* out = po + (int64_t)h0 * kLatentDim + (2 * c + cw) * 128 + q4 * 32 + lane;
+        uint32_t r[32];
+        tmem_ld32(o_addr + 2 * c * kHg + h0, r);
+        tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float f = ls[h0 + i];
-            out[(h0 + i) * kLatentDim] = f == 0.f ? 0.f : __uint_as_float(r[i]) * f;
+        for (int u = 0; u < 32; u += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(ls + h0 + u);
+          const float a[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (none && a[x] == 0.f) r[u + x] = 0;
+            if (h0 + u + x < I.heads) out[(u + x) * kLatentDim] = __uint_as_float(r[u + x]) * a[x];
           }
         }
       }
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
       for (int j = 0; j < nb; ++j, ++g) {
         const int st = (int)(g % kStages), ri = (int)(g % kRing);
-        if (!(ok = wait(&bar.ix_full[ri], (g / kRing) & 1))) break;
+        if (!(ok = wait(&bar.ix_row[ri], (g / kRing) & 1))) break;
         const int cc = lane & 7;
         uint8_t* stage = kv_s + st * kStage;
         // atom by atom (the rope atom is free first), 8 lanes per row, 4 rows per pass
@@ -719,6 +724,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         const int j0 = (int)((int64_t)I.split * nbr / p.splits);
         return {ids, I.b, j0, (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0};
       };
+      // The first item's first ids, where they are if its row is full, beside the search for its end.
+      int id[2], row[2], id_full[2];
+      float scale[2];
+      const Item first = item_of(p, blockIdx.x);
+      const int j_full = first.split * ((p.kk + kNB - 1) / kNB) / p.splits;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int e = (j_full + warp - kIxWarp0) * kNB + u * 32 + lane;
+        id_full[u] = e < p.kk ? __ldg(p.idx + first.b * p.idx_sb + first.t * p.idx_st + e) : -1;
+      }
       Blocks cur = blocks_of(blockIdx.x), next{};
       // Below, block j >= cur.nb is the next item's block j - cur.nb.
       auto load_ids = [&](int j, int (&id)[2]) {
@@ -747,8 +762,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       // and so across items: the five loads from the end of a row's ids to its first scales, each on
       // the last one's result, took 9,000 cycles at the start of every row.  (Only where the item had
       // two blocks or more for this warp; the first blocks of the others' successors wait.)
-      int id[2], row[2];
-      float scale[2];
       int it = 0;
       uint32_t g = 0;
       bool ok = true, ahead = false;  // ahead: id, row and scale are the item's
@@ -762,7 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         }
         int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
         if (!ahead && j < cur.nb) {
-          load_ids(j, id);
+          if (it == 0 && cur.j0 == j_full) id[0] = id_full[0], id[1] = id_full[1];
+          else load_ids(j, id);
           resolve(j, id, row);
           load_ids(j + 2, id);
           load_scales(row, scale);
@@ -772,22 +786,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         next.nb = 0;
         for (; j < cur.nb; j += 2) {
           const int ri = (int)((g + j) % kRing);
+          if (!(ok = wait(&bar.ix_empty[ri], (((g + j) / kRing) & 1) ^ 1))) break;
+          sm->row[ri][lane] = row[0];
+          sm->row[ri][32 + lane] = row[1];
+          const bool some = __any_sync(0xffffffffu, row[0] >= 0 || row[1] >= 0);
+          if (lane == 0) sm->valid[ri] = some;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.ix_row[ri]);  // the copies do not wait for the scales
           int row_n[2];
           resolve(j + 2, id, row_n);
           load_ids(j + 4, id);
           known = j + 4 < cur.nb || seen ? known + 1 : 0;
-          if (!(ok = wait(&bar.ix_empty[ri], (((g + j) / kRing) & 1) ^ 1))) break;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int r = u * 32 + lane;
-            sm->row[ri][r] = row[u];
             float* sc = reinterpret_cast<float*>(&sm->sc[ri][r >> 1]) + (r & 1);
             sc[0] = row[u] >= 0 ? scale[u] : 0.f;
             sc[2] = row[u] >= 0 ? log2f(scale[u]) : -INFINITY;
             sm->isc[ri][r] = row[u] >= 0 ? 1.f / scale[u] : 0.f;
           }
-          const bool some = __any_sync(0xffffffffu, row[0] >= 0 || row[1] >= 0);
-          if (lane == 0) sm->valid[ri] = some;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.ix_full[ri]);
           row[0] = row_n[0];
@@ -1032,6 +1049,7 @@ static_assert(kColQR == kColQ + 128, "the converted query row is stored in one r
 constexpr int kCombHeads = 4;
 __global__ void __launch_bounds__(kCombHeads * 128) k_latent_combine(LatentAttnLaunch p) {
   __shared__ float wgt[kMaxLatentSplits][kCombHeads];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the parts are complete and visible
   const int row = blockIdx.x, h0 = blockIdx.y * kCombHeads, S = p.splits;
   const int64_t part0 = ((int64_t)row * p.groups + h0 / kHg) * S;
   const int hl0 = h0 % kHg;
@@ -1125,7 +1143,17 @@ cudaError_t launch_latent_attn(LatentAttnLaunch p, float* part, cudaStream_t st)
   kern<<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, st>>>(p);
   count_launches(1);
   if ((e = cudaGetLastError()) != cudaSuccess || p.splits <= 1) return e;
-  k_latent_combine<<<dim3((unsigned)(p.B * p.T), (unsigned)((p.H + kCombHeads - 1) / kCombHeads)), kCombHeads * 128, 0, st>>>(p);
+  // launched while the parts are being computed: its blocks stand ready when the last part ends
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(p.B * p.T), (unsigned)((p.H + kCombHeads - 1) / kCombHeads));
+  cfg.blockDim = dim3(kCombHeads * 128);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, k_latent_combine, p)) != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
 }
