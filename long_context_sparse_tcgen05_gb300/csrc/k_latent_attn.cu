@@ -28,7 +28,7 @@
 //          read the rows' scales (the three dependent loads a block took as long as its copies when
 //          the copying warps made them)
 //   0-3    copy the rows (16-byte cp.async) into three stages of 40 KB, five 128-byte-swizzled atoms
-//          each, an atom as soon as the products have released it
+//          each, as soon as the products have released them
 //   4      S (hi and lo rows, 128 x 64) = Q K^T: A is Q in tensor memory, so the product reads only
 //          the codes from shared memory; 16 FP8 steps and 4 bf16 steps for the rope part
 //   5      O^T (512 x 64) += V^T P^T: four chunks of 128 dims, 2 key steps, hi and lo
@@ -87,9 +87,9 @@ static_assert(kHg * kOPitch <= kQBytes, "O is staged in the queries' room");
 
 struct Bars {
   uint64_t q_full, q_empty, qs_full[2];
-  // kv_empty[st][c]: atom c of stage st may be refilled (0-3 codes, after the value product's dim
-  // chunk c; 4 rope values, after the score product)
-  uint64_t kv_full[kStages], kv_empty[kStages][5];
+  // kv_empty[st][c]: atoms of stage st that may be refilled (0, 1: two of codes, after the value
+  // product's dim chunks 1 and 3; 2: the rope values, after the score product)
+  uint64_t kv_full[kStages], kv_empty[kStages][3];
   uint64_t ix_row[kRing], ix_full[kRing], ix_empty[kRing];  // a block's rows; its scales too
   uint64_t s_full, s_empty;
   uint64_t p_full[2], p_empty[2];
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     mbar_init(&bar.o_empty, 8);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.kv_full[i], kGatherWarps * 32);
-      for (int c = 0; c < 5; ++c) mbar_init(&bar.kv_empty[i][c], 1);
+      for (int c = 0; c < 3; ++c) mbar_init(&bar.kv_empty[i][c], 1);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar.ix_row[i], 1);
@@ -584,7 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         if (!(ok = wait(&bar.ix_row[ri], (g / kRing) & 1))) break;
         const int cc = lane & 7;
         uint8_t* stage = kv_s + st * kStage;
-        // atom by atom (the rope atom is free first), 8 lanes per row, 4 rows per pass
+        // atom by atom, 8 lanes per row, 4 rows per pass; the rope atom is free first.  (Waits and commits
+        // for each atom of codes cost more than they bring: 1.05 against 0.99 ms a 4,096-query chunk; one
+        // for all four: 1.00.)
         int64_t row[4];
         uint32_t dst[4], n[4];
 #pragma unroll
@@ -598,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
           const int a = i == 0 ? 4 : i - 1;
-          ok &= bar_wait<kPoll>(&bar.kv_empty[st][a], ((g / kStages) & 1) ^ 1, abort_flag, p.wait);
+          if (i == 0 || i == 1 || i == 3)
+            ok &= bar_wait<kPoll>(&bar.kv_empty[st][i == 0 ? 2 : i >> 1], ((g / kStages) & 1) ^ 1, abort_flag, p.wait);
 #pragma unroll
           for (int pass = 0; pass < 4; ++pass)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst[pass] + a * kAtom),
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
             for (int k = 0; k < 4; ++k)
               mma_bf16_ts(tmem + kColS, tmem + kColQR + 8 * k, kd + (uint64_t)((4 * kAtom + k * 32) >> 4), id16, 1);
             mma_commit(&bar.s_full);
-            mma_commit(&bar.kv_empty[st][4]);
+            mma_commit(&bar.kv_empty[st][2]);
             if (j == nb - 1) mma_commit(&bar.q_empty);
           }
           __syncwarp();
@@ -681,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
               for (int k = 0; k < 4; ++k)  // keys 0-31 and 32-63 by the hi terms, then by the lo terms
                 mma_mxfp8(tmem + kColO + c * kHg, vd + (uint64_t)((c * kAtom + (k & 1) * 4096) >> 4),
                           pd + (uint64_t)((k * 32) >> 4), idesc_mx(), tmem + kColSfA, tmem + kColSfB + 4 * pb, (j | k) != 0);
-              mma_commit(&bar.kv_empty[st][c]);
+              if (c & 1) mma_commit(&bar.kv_empty[st][c >> 1]);
             }
             mma_commit(&bar.p_empty[pb]);
             if (j == nb - 1) mma_commit(&bar.o_full);
@@ -724,16 +727,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         const int j0 = (int)((int64_t)I.split * nbr / p.splits);
         return {ids, I.b, j0, (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0};
       };
-      // The first item's first ids, where they are if its row is full, beside the search for its end.
-      int id[2], row[2], id_full[2];
-      float scale[2];
-      const Item first = item_of(p, blockIdx.x);
-      const int j_full = first.split * ((p.kk + kNB - 1) / kNB) / p.splits;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int e = (j_full + warp - kIxWarp0) * kNB + u * 32 + lane;
-        id_full[u] = e < p.kk ? __ldg(p.idx + first.b * p.idx_sb + first.t * p.idx_st + e) : -1;
-      }
       Blocks cur = blocks_of(blockIdx.x), next{};
       // Below, block j >= cur.nb is the next item's block j - cur.nb.
       auto load_ids = [&](int j, int (&id)[2]) {
@@ -744,12 +737,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 #pragma unroll
         for (int u = 0; u < 2; ++u) id[u] = in && e0 + u * 32 < p.kk ? __ldg(ids + e0 + u * 32) : -1;
       };
-      auto resolve = [&](int j, const int (&id)[2], int (&row)[2]) {
+      auto load_pages = [&](int j, const int (&id)[2], int (&page)[2], int (&off)[2]) {
         const int b = j < cur.nb ? cur.b : next.b;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          row[u] = id[u] >= 0 && id[u] < p.S ? (int)latent_row(p.cache, b, id[u]) : -1;
-          if (row[u] < 0 && id[u] != -1) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
+          off[u] = -1;
+          if (id[u] >= 0 && id[u] < p.S) page[u] = latent_page(p.cache, b, id[u], off[u]);
+          if (off[u] < 0 && id[u] != -1) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
+        }
+      };
+      auto resolve = [&](const int (&page)[2], const int (&off)[2], int (&row)[2]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          row[u] = off[u] >= 0 ? (int)latent_row_of(p.cache, page[u], off[u]) : -1;
+          if (row[u] < 0 && off[u] >= 0) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
         }
       };
       // (Bringing the rows' lines to L2 from here cost more in the load pipe than it saved: 1.15 against
@@ -758,13 +759,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 #pragma unroll
         for (int u = 0; u < 2; ++u) scale[u] = row[u] >= 0 ? __ldg(p.cache.scales + row[u]) : 0.f;
       };
-      // Each block's ids are loaded two, its rows and scales resolved one of this warp's blocks ahead,
-      // and so across items: the five loads from the end of a row's ids to its first scales, each on
-      // the last one's result, took 9,000 cycles at the start of every row.  (Only where the item had
-      // two blocks or more for this warp; the first blocks of the others' successors wait.)
+      // The four loads behind a block, each on the last one's result (its ids, their pages, the rows'
+      // scales; the copies wait for the rows only), are made one of this warp's blocks apart, so a block
+      // costs one latency, not all; and so across items.  (One latency after the other took 2,400 cycles
+      // a block in a decode step, and 9,000 at the start of every row.)  Only where the item had three
+      // blocks or more for this warp; the first blocks of the others' successors wait.
+      int id[2], page[2], off[2], row[2];
+      float scale[2];
       int it = 0;
       uint32_t g = 0;
-      bool ok = true, ahead = false;  // ahead: id, row and scale are the item's
+      bool ok = true, ahead = false;  // ahead: id, page, off, row and scale are the item's
       for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
         if (warp == kIxWarp0) {
           if (!(ok = wait(&bar.info_empty[it & 1], ((it >> 1) & 1) ^ 1))) break;
@@ -775,13 +779,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         }
         int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
         if (!ahead && j < cur.nb) {
-          if (it == 0 && cur.j0 == j_full) id[0] = id_full[0], id[1] = id_full[1];
-          else load_ids(j, id);
-          resolve(j, id, row);
-          load_ids(j + 2, id);
+          int id_0[2], id_2[2];
+          load_ids(j, id_0);
+          load_ids(j + 2, id_2);
+          load_ids(j + 4, id);
+          load_pages(j, id_0, page, off);
+          resolve(page, off, row);
           load_scales(row, scale);
+          load_pages(j + 2, id_2, page, off);
         }
-        int known = item + G < items ? 0 : 2;  // the last loads that saw the blocks of this or the next item
+        int known = item + G < items ? 0 : 3;  // the last loads that saw the blocks of this or the next item
         bool seen = known != 0;                // the next item's blocks are known
         next.nb = 0;
         for (; j < cur.nb; j += 2) {
@@ -793,10 +800,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           if (lane == 0) sm->valid[ri] = some;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.ix_row[ri]);  // the copies do not wait for the scales
-          int row_n[2];
-          resolve(j + 2, id, row_n);
-          load_ids(j + 4, id);
-          known = j + 4 < cur.nb || seen ? known + 1 : 0;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int r = u * 32 + lane;
@@ -807,16 +810,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.ix_full[ri]);
-          row[0] = row_n[0];
-          row[1] = row_n[1];
+          resolve(page, off, row);
           load_scales(row, scale);
-          if (!seen && j + 6 >= cur.nb) {
+          load_pages(j + 4, id, page, off);
+          load_ids(j + 6, id);
+          known = j + 6 < cur.nb || seen ? known + 1 : 0;
+          if (!seen && j + 8 >= cur.nb) {
             next = blocks_of(item + G);
             seen = true;
           }
         }
         if (!seen) next = blocks_of(item + G);
-        ahead = known >= 2;
+        ahead = known >= 3;
         g += cur.nb;
         cur = next;
       }
@@ -1047,7 +1052,7 @@ static_assert(kColQR == kColQ + 128, "the converted query row is stored in one r
 // Joins a split item's parts: O = sum_s w_s O_s with w_s = e^(lse_s - lse).  One CTA per (query, 4
 // heads): few queries must still fill the GPU.
 constexpr int kCombHeads = 4;
-__global__ void __launch_bounds__(kCombHeads * 128) k_latent_combine(LatentAttnLaunch p) {
+__global__ void __launch_bounds__(kCombHeads * 128, 4) k_latent_combine(LatentAttnLaunch p) {
   __shared__ float wgt[kMaxLatentSplits][kCombHeads];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the parts are complete and visible
   const int row = blockIdx.x, h0 = blockIdx.y * kCombHeads, S = p.splits;
@@ -1070,24 +1075,28 @@ __global__ void __launch_bounds__(kCombHeads * 128) k_latent_combine(LatentAttnL
   const int hl = threadIdx.x >> 7, i = threadIdx.x & 127;
   const float4* src = reinterpret_cast<const float4*>(p.part_o + (part0 * kHg + hl0 + hl) * kLatentDim) + i;
   const bool live = h0 + hl < p.H;
-  float4 v[8];
+  float4 v[4];
+  auto load = [&](int s0) {
 #pragma unroll
-  for (int s = 0; s < 8; ++s)
-    if (live && s < S) v[s] = src[(int64_t)s * kHg * kLatentDim / 4];
+    for (int s = 0; s < 4; ++s)
+      if (live && s0 + s < S) v[s] = __ldcs(src + (int64_t)(s0 + s) * kHg * kLatentDim / 4);
+  };
+  load(0);
   __syncthreads();
   if (!live) return;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float4 x, float w) {
-    if (w == 0.f) return;  // an empty part wrote no values
-    acc.x += w * x.x;
-    acc.y += w * x.y;
-    acc.z += w * x.z;
-    acc.w += w * x.w;
-  };
+  for (int s0 = 0; s0 < S; s0 += 4) {
 #pragma unroll
-  for (int s = 0; s < 8; ++s)
-    if (s < S) add(v[s], wgt[s][hl]);
-  for (int s = 8; s < S; ++s) add(src[(int64_t)s * kHg * kLatentDim / 4], wgt[s][hl]);
+    for (int s = 0; s < 4; ++s) {
+      const float w = s0 + s < S ? wgt[s0 + s][hl] : 0.f;
+      if (w == 0.f) continue;  // an empty part wrote no values
+      acc.x += w * v[s].x;
+      acc.y += w * v[s].y;
+      acc.z += w * v[s].z;
+      acc.w += w * v[s].w;
+    }
+    load(s0 + 4);
+  }
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), b = __floats2bfloat162_rn(acc.z, acc.w);
   reinterpret_cast<uint2*>(p.out + ((int64_t)row * p.H + h0 + hl) * kLatentDim)[i] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
