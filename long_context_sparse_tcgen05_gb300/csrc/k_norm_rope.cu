@@ -54,9 +54,10 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // (mean, factor) with y = (x - mean) * factor * weight + bias, over a head held by G lanes as U units
-// each, unit u of lane l at (u G + l) 8.  raw: zero where there is no unit.
+// each, unit u of lane l at (u G + l) 8.  raw: zero where there is no unit.  inv_d: 1 / d (a division a
+// head is a tenth of the work; half a step of the reciprocal is 2^-24 of the variance).
 template <int kNorm, int G, int U>
-__device__ __forceinline__ float2 head_stats(const NormRopeLaunch& p, const uint4 (&raw)[U], int l) {
+__device__ __forceinline__ float2 head_stats(const NormRopeLaunch& p, const uint4 (&raw)[U], int l, float inv_d) {
   float mean = 0.f;
   if (kNorm == DSA_NORM_LAYER) {
     f32x2 s = 0;
@@ -66,7 +67,7 @@ __device__ __forceinline__ float2 head_stats(const NormRopeLaunch& p, const uint
 #pragma unroll
       for (int e = 0; e < 4; ++e) s = add_2(s, x.p[e]);
     }
-    mean = group_sum<G>(lo_of(s) + hi_of(s)) / (float)p.d;
+    mean = group_sum<G>(lo_of(s) + hi_of(s)) * inv_d;
   }
   f32x2 ss = 0;  // squares about the mean: no cancellation between mean^2 and the second moment
 #pragma unroll
@@ -80,7 +81,7 @@ __device__ __forceinline__ float2 head_stats(const NormRopeLaunch& p, const uint
       }
     }
   }
-  return make_float2(mean, rsqrtf(group_sum<G>(lo_of(ss) + hi_of(ss)) / (float)p.d + p.eps));
+  return make_float2(mean, rsqrtf(fmaf(group_sum<G>(lo_of(ss) + hi_of(ss)), inv_d, p.eps)));
 }
 
 // What a lane needs of a unit whatever its head: the norm's weights, and the factors of its rotation
@@ -201,6 +202,7 @@ template <int G, int U, int R, int kNorm>
 __global__ void __launch_bounds__(kThreads, U == 1 ? 4 : 2) k_norm_rope_bf16(NormRopeLaunch p) {
   constexpr int kHeads = 32 / G;
   const int lane = threadIdx.x & 31, l = lane % G, hsub = lane / G;
+  const float inv_d = 1.f / (float)p.d;
   const uint32_t chunks = (uint32_t)(p.H + kHeads * R - 1) / (kHeads * R);
   const uint32_t tasks = (uint32_t)p.B * p.n * chunks;  // (below 2^31: checked by the caller)
   const uint32_t step = gridDim.x * (kThreads / 32);
@@ -212,37 +214,37 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 4 : 2) k_norm_rope_bf16(Nor
     const uint32_t tok = task / chunks;
     const int h0 = (int)(task - tok * chunks) * kHeads * R + hsub;
     const int b = (int)(tok / (uint32_t)p.n), i = (int)(tok - (uint32_t)b * (uint32_t)p.n);
-    const uint16_t* x = p.x + b * p.x_sb + i * p.x_st;
+    const uint16_t* x = p.x + b * p.x_sb + i * p.x_st + h0 * p.x_sh;
     uint4 raw[R][U], par[R][U];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r, x += kHeads * p.x_sh)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = h0 + r * kHeads, at = (u * G + l) * 8;
-        const bool in = h < p.H && at < p.d;
+        const int at = (u * G + l) * 8;
+        const bool in = h0 + r * kHeads < p.H && at < p.d;
         // plain loads: out may be x
-        raw[r][u] = in ? *reinterpret_cast<const uint4*>(x + h * p.x_sh + at) : make_uint4(0, 0, 0, 0);
+        raw[r][u] = in ? *reinterpret_cast<const uint4*>(x + at) : make_uint4(0, 0, 0, 0);
         par[r][u] = U > 1 && in && !p.interleaved && in_rope(p, at)
-                        ? *reinterpret_cast<const uint4*>(x + h * p.x_sh + partner_at(p, at))
+                        ? *reinterpret_cast<const uint4*>(x + partner_at(p, at))
                         : make_uint4(0, 0, 0, 0);
       }
     const int64_t pos = checked_pos(p, p.positions ? __ldg(p.positions + tok) : p.pos0 + i, lane == 0 && h0 == 0);
     if (pos < 0) continue;  // uniform over the warp
     if (U == 1 && turn) tab.angles(p, l * 8, pos);
     __syncwarp();  // in place: every load of these heads comes before their stores
-    uint16_t* out = p.out + b * p.o_sb + i * p.o_st;
+    uint16_t* out = p.out + b * p.o_sb + i * p.o_st + h0 * p.o_sh;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int h = h0 + r * kHeads;
-      const float2 st = kNorm ? head_stats<kNorm, G, U>(p, raw[r], l) : make_float2(0.f, 1.f);
+    for (int r = 0; r < R; ++r, out += kHeads * p.o_sh) {
+      if (h0 - hsub + r * kHeads >= p.H) break;  // (uniform over the warp)
+      const float2 st = kNorm ? head_stats<kNorm, G, U>(p, raw[r], l, inv_d) : make_float2(0.f, 1.f);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int at = (u * G + l) * 8;
         Vec8 y;
         if constexpr (U == 1) y = unit_result<G, kNorm>(p, raw[r][u], st, src, turn, tab);
-        if (h >= p.H || at >= p.d) continue;
+        if (h0 + r * kHeads >= p.H || at >= p.d) continue;
         if constexpr (U > 1) y = unit_result_wide<kNorm>(p, raw[r][u], par[r][u], st, at, pos);
-        *reinterpret_cast<uint4*>(out + h * p.o_sh + at) = pack8(y);
+        *reinterpret_cast<uint4*>(out + at) = pack8(y);
       }
     }
   }
@@ -262,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
   constexpr int kHeads = kTeam / G;         // heads per pass
   const int lane = threadIdx.x & 31, t = threadIdx.x % kTeam, l = t % G, hsub = t / G;
   const uint32_t toks = (uint32_t)p.B * p.n;  // (below 2^31: checked by the caller)
+  const float inv_d = 1.f / (float)p.d;
   UnitTables<kNorm> tab;
   if (U == 1 && l * 8 < p.d) tab.affine(p, l * 8);
   const bool turn = p.rope_dim > 0 && in_rope(p, l * 8);  // (U = 1: of this lane's unit)
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
 #pragma unroll
     for (int s = 0; s < NP; ++s) {
       const int h = hsub + s * kHeads;
-      const float2 st = kNorm ? head_stats<kNorm, G, U>(p, raw[s], l) : make_float2(0.f, 1.f);
+      const float2 st = kNorm ? head_stats<kNorm, G, U>(p, raw[s], l, inv_d) : make_float2(0.f, 1.f);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int at = (u * G + l) * 8;
