@@ -587,10 +587,17 @@ def _tables(cos, sin, dev):
 _NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
+def _strides(t, axes: int):
+    """_stride of the leading axes.  A broadcast axis is refused: its stride 0 means dense to the library."""
+    s = tuple(_stride(t, i) for i in range(axes))
+    assert all(v > 0 or t.shape[i] <= 1 for i, v in enumerate(s)), "broadcast axes are not supported: use a copy"
+    return s
+
+
 def _head_strides(t):
     """Strides of a [B,n,H,d] tensor with a dense last axis (0 along an axis of size 1)."""
     assert t.dim() == 4 and (t.shape[3] == 1 or t.stride(3) == 1), "[B, n, H, d] with dense heads is expected"
-    return _stride(t, 0), _stride(t, 1), _stride(t, 2)
+    return _strides(t, 3)
 
 
 def _norm_rope_struct(x, norm, weight, bias, eps, cos, sin, rope_off, interleaved, pos0, positions):
@@ -669,7 +676,7 @@ def dsa_latent_append(x: torch.Tensor, cache: dict, *, weight: torch.Tensor | No
     assert cache["codes"].device == dev
     c, s, rows, angles = _tables(cos, sin, dev)
     assert c is None or angles == 32, "cos and sin: 32 angles for the 64 rope values"
-    a = LatentAppendArgs(B, n, x.data_ptr(), _stride(x, 0), _stride(x, 1), _addr(weight, dev, torch.float32, "weight", 512),
+    a = LatentAppendArgs(B, n, x.data_ptr(), *_strides(x, 2), _addr(weight, dev, torch.float32, "weight", 512),
                          eps, c, s, interleaved, rows, _addr(positions, dev, torch.int64, "positions", B * n), pos0)
     if n:
         ws = _flag_word(dev)
@@ -713,7 +720,8 @@ def latent_attn_struct(at: dict, idx: torch.Tensor) -> LatentAttnArgs:
     S = at.get("S")
     if S is None:
         S = min((lc.table_ld if lc.block_table else 1) * lc.page_size, 2 ** 31 - 1)
-    return LatentAttnArgs(B, T, int(S), H, at["scale"], q.data_ptr(), _stride(q, 0), _stride(q, 1), lc, idx.shape[1], None)
+    assert 0 < S < 2 ** 31, "S: between 1 and 2^31 - 1 positions"
+    return LatentAttnArgs(B, T, int(S), H, at["scale"], q.data_ptr(), *_strides(q, 2), lc, idx.shape[1], None)
 
 
 def dsa_latent_attn(at: dict, idx: torch.Tensor, out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = True,

@@ -80,9 +80,9 @@ dsa_status norm_rope_launch(const dsa_norm_rope_args* a, dsa::NormRopeLaunch& P)
   if (!aligned(a->weight, 16) || !aligned(a->bias, 16))
     return fail(DSA_ERR_MISALIGNED, "weight and bias must be 16-byte aligned");
   if (!aligned(a->positions, 8)) return fail(DSA_ERR_MISALIGNED, "positions must be 8-byte aligned");
-  // (a warp of the kernel takes at least four heads of a token)
-  const dsa_status s = check_count((int64_t)a->B * a->n, a->H / 4 + 1);
-  if (s != DSA_OK) return s;
+  // (a warp of the kernel takes at least four heads of a token, of wide heads one)
+  dsa_status s = check_count((int64_t)a->B * a->n, a->d <= 256 ? a->H / 4 + 1 : a->H);
+  if (s != DSA_OK || (!a->positions && (s = check_range(a->pos0, a->n, 0, "the tokens")) != DSA_OK)) return s;
   P.B = a->B; P.n = a->n; P.H = a->H; P.d = a->d;
   P.x = static_cast<const uint16_t*>(a->x);
   P.x_sh = a->x_stride_h ? a->x_stride_h : a->d;

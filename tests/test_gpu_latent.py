@@ -860,3 +860,23 @@ def test_latent_attn_waits_that_run_out(B, T, H, S, k):
     o, l = dsa.dsa_latent_attn(at, idx)
     assert dsa.read_device_flags(DEV) == 0
     assert torch.equal(o, want) and torch.equal(l, lse)
+
+
+def test_broadcast_operands_are_refused():
+    """A stride of 0 means dense to the library: a broadcast view would be read past its end."""
+    x = torch.zeros(1, 3, 4, 64, device=DEV, dtype=torch.bfloat16)
+    for view in (x.expand(2, 3, 4, 64), x[:, :1].expand(1, 5, 4, 64), x[:, :, :1].expand(1, 3, 7, 64)):
+        with pytest.raises(AssertionError, match="broadcast"):
+            dsa.dsa_norm_rope(view)
+        with pytest.raises(AssertionError, match="broadcast"):
+            dsa.dsa_norm_rope(torch.zeros(view.shape, device=DEV, dtype=torch.bfloat16), out=view)
+    cache = _cache(2, 20, 16)
+    row = torch.zeros(1, 1, 576, device=DEV, dtype=torch.bfloat16)
+    for view in (row.expand(2, 1, 576), row.expand(2, 4, 576)):
+        with pytest.raises(AssertionError, match="broadcast"):
+            dsa.dsa_latent_append(view, cache)
+    at = dict(q=_q(1, 1, 8).expand(2, 1, 8, 576), cache=cache, scale=0.05)
+    with pytest.raises(AssertionError, match="broadcast"):
+        dsa.dsa_latent_attn(at, _idx(2, 1, 20, 4))
+    with pytest.raises(AssertionError):
+        dsa.dsa_latent_attn(dict(at, q=_q(2, 1, 8), S=2 ** 32 + 5), _idx(2, 1, 20, 4))

@@ -73,6 +73,15 @@ def test_norm_rope_refusals(lib, edits, status):
     assert lib.dsa_last_error() and lib.dsa_launch_count() == before
 
 
+@pytest.mark.parametrize("edits,status", [
+    (dict(B=1 << 16, n=1 << 13, H=16, d=64), UNSUPPORTED), (dict(B=1 << 16, n=1 << 13, H=4, d=512, rope_dim=64), UNSUPPORTED),
+    (dict(positions=None, pos0=-1, rope_dim=0), INVALID),
+])
+def test_norm_rope_refuses_what_its_kernels_cannot_count(lib, edits, status):
+    a = _norm(**edits)
+    assert lib.dsa_norm_rope(ctypes.byref(a), FAKE, 0, 0, 0, FAKE, 256, None) == status
+
+
 def test_norm_rope_output_refusals(lib):
     a = ctypes.byref(_norm())
     call = lambda out=FAKE, sb=0, st=0, sh=0, ws=FAKE, n=256: lib.dsa_norm_rope(a, out, sb, st, sh, ws, n, None)  # noqa: E731
