@@ -571,7 +571,7 @@ def _addr(t, dev, dtype, what: str, n: int | None = None):
     """Device address of an optional dense operand, checked against `dev`, dtype and size."""
     if t is None:
         return None
-    assert t.device == dev and t.dtype == dtype and t.is_contiguous(), f"{what}: a dense {dtype} tensor on {dev} is expected"
+    assert t.dtype == dtype and t.is_contiguous() and t.device == dev, f"{what}: a dense {dtype} tensor on {dev} is expected"
     assert n is None or t.numel() == n, f"{what}: {n} values are expected"
     return t.data_ptr()
 
@@ -587,17 +587,23 @@ def _tables(cos, sin, dev):
 _NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
-def _strides(t, axes: int):
-    """_stride of the leading axes.  A broadcast axis is refused: its stride 0 means dense to the library."""
-    s = tuple(_stride(t, i) for i in range(axes))
-    assert all(v > 0 or t.shape[i] <= 1 for i, v in enumerate(s)), "broadcast axes are not supported: use a copy"
-    return s
+_BROADCAST = "broadcast axes are not supported: use a copy"  # (their stride 0 means dense to the library)
 
 
 def _head_strides(t):
     """Strides of a [B,n,H,d] tensor with a dense last axis (0 along an axis of size 1)."""
-    assert t.dim() == 4 and (t.shape[3] == 1 or t.stride(3) == 1), "[B, n, H, d] with dense heads is expected"
-    return _strides(t, 3)
+    assert t.dim() == 4, "[B, n, H, d] with dense heads is expected"
+    (B, n, H, d), (sb, st, sh, sd) = t.shape, t.stride()
+    assert sd == 1 or d == 1, "[B, n, H, d] with dense heads is expected"
+    assert (sb or B < 2) and (st or n < 2) and (sh or H < 2), _BROADCAST
+    return sb if B > 1 else 0, st if n > 1 else 0, sh if H > 1 else 0
+
+
+def _token_strides(t):
+    """The first two strides of a [B,n,...] tensor (0 along an axis of size 1)."""
+    (B, n), (sb, st) = t.shape[:2], t.stride()[:2]
+    assert (sb or B < 2) and (st or n < 2), _BROADCAST
+    return sb if B > 1 else 0, st if n > 1 else 0
 
 
 def _norm_rope_struct(x, norm, weight, bias, eps, cos, sin, rope_off, interleaved, pos0, positions):
@@ -676,7 +682,7 @@ def dsa_latent_append(x: torch.Tensor, cache: dict, *, weight: torch.Tensor | No
     assert cache["codes"].device == dev
     c, s, rows, angles = _tables(cos, sin, dev)
     assert c is None or angles == 32, "cos and sin: 32 angles for the 64 rope values"
-    a = LatentAppendArgs(B, n, x.data_ptr(), *_strides(x, 2), _addr(weight, dev, torch.float32, "weight", 512),
+    a = LatentAppendArgs(B, n, x.data_ptr(), *_token_strides(x), _addr(weight, dev, torch.float32, "weight", 512),
                          eps, c, s, interleaved, rows, _addr(positions, dev, torch.int64, "positions", B * n), pos0)
     if n:
         ws = _flag_word(dev)
@@ -721,7 +727,7 @@ def latent_attn_struct(at: dict, idx: torch.Tensor) -> LatentAttnArgs:
     if S is None:
         S = min((lc.table_ld if lc.block_table else 1) * lc.page_size, 2 ** 31 - 1)
     assert 0 < S < 2 ** 31, "S: between 1 and 2^31 - 1 positions"
-    return LatentAttnArgs(B, T, int(S), H, at["scale"], q.data_ptr(), *_strides(q, 2), lc, idx.shape[1], None)
+    return LatentAttnArgs(B, T, int(S), H, at["scale"], q.data_ptr(), *_token_strides(q), lc, idx.shape[1], None)
 
 
 def dsa_latent_attn(at: dict, idx: torch.Tensor, out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = True,
