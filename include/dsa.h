@@ -446,10 +446,9 @@ dsa_status dsa_latent_read(const dsa_latent_cache* cache, int32_t B, int32_t n, 
  *        skipped and raise DSA_FLAG_BAD_INDEX.  A position listed twice counts twice.
  *   out  [B,T,H,512] bf16 (16-byte aligned); lse [B,T,H] fp32 (natural log) or NULL
  * 1 <= k <= 65536.  A row with no valid entry gets out = 0, lse = -inf.  Scores and the softmax's
- * sums are fp32.  ws: dsa_latent_attn_workspace_size bytes are preferred (DSA_WS_MIN plus room for
- * the parts of rows split over CTAs when there are few); at least DSA_WS_MIN.  flags: DEVICE word
- * for DSA_FLAG_* bits, or NULL for the workspace's flag word; with it ws needs no zero fill, so
- * calls that may overlap can each take scratch of their own and share one flag word. */
+ * sums are fp32.  ws: dsa_latent_attn_workspace_size bytes (DSA_WS_MIN: its flag word is all that the
+ * call uses, so calls that may overlap can share one).  flags: DEVICE word for DSA_FLAG_* bits, or
+ * NULL for the workspace's flag word. */
 typedef struct {
   int32_t B, T, S, H;
   float scale;

@@ -254,7 +254,7 @@ _flags = {}
 
 def _flag_word(dev) -> torch.Tensor:
     """The device's flag workspace (WS_MIN zeroed bytes): allocated once and kept, so a captured
-    graph may hold its address.  Calls that use it allocate their scratch themselves."""
+    graph may hold its address."""
     t = _flags.get(dev)
     if t is None:
         if torch.cuda.is_current_stream_capturing():
@@ -734,7 +734,7 @@ def dsa_latent_attn(at: dict, idx: torch.Tensor, out: torch.Tensor | None = None
                     ws: torch.Tensor | None = None):
     """Sparse attention over the rows idx [B,T,k] (or [B,1,k], shared by a sequence's T queries) of
     a paged FP8 latent cache: (out [B,T,H,512] bf16, lse [B,T,H] fp32 or None).  `ws`: a workspace
-    to use (uint8, zero-filled once) instead of scratch allocated by the call."""
+    whose flag word to use (uint8, zero-filled once) instead of the device's."""
     lib = load_library()
     a = latent_attn_struct(at, idx)
     dev = at["q"].device
@@ -750,13 +750,7 @@ def dsa_latent_attn(at: dict, idx: torch.Tensor, out: torch.Tensor | None = None
         lse = None
     lp = _addr(lse, dev, torch.float32, "lse", a.B * a.T * a.H)
     if ws is None:
-        # scratch from the caching allocator, private to this call on its stream (and to its graph,
-        # when one is being captured); the flag word is the device's
-        ws = flags = _flag_word(dev)
-        need = int(lib.dsa_latent_attn_workspace_size(_c.byref(a), k))
-        if need > WS_MIN:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        a.flags = flags.data_ptr()
+        ws = _flag_word(dev)
     assert ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous()
     _launch(dev, lib.dsa_latent_attn, _c.byref(a), ip, k, op, lp, ws.data_ptr(), ws.numel())
     return out, lse

@@ -308,17 +308,12 @@ struct LatentAttnLaunch {
   uint16_t* out;
   float* lse;
   uint32_t* flags;
-  // filled by launch_latent_attn: groups of 64 heads; with splits > 1 an item is a part of a
-  // (query, group), and part i writes its normalised output to part_o[i * 64 * 512 ..] and its LSE
-  // to part_lse[i * 64 ..]
+  // filled by launch_latent_attn: groups of 64 heads; with splits > 1 an item is a part of a (query,
+  // group), and the CTAs of a cluster hold a row's parts
   int groups, splits;
-  float* part_o;
-  float* part_lse;
   long long wait;
 };
-constexpr int kMaxLatentSplits = 16;
-int latent_attn_splits(const LatentAttnLaunch& p);
-size_t latent_attn_part_bytes(const LatentAttnLaunch& p, int splits);
-cudaError_t launch_latent_attn(LatentAttnLaunch p, float* part, cudaStream_t st);
+constexpr int kMaxLatentSplits = 8;
+cudaError_t launch_latent_attn(LatentAttnLaunch p, cudaStream_t st);
 
 }  // namespace dsa

@@ -241,13 +241,7 @@ dsa_status dsa_latent_read(const dsa_latent_cache* cache, int32_t B, int32_t n, 
   return done(dsa::launch_latent_read(P, static_cast<cudaStream_t>(stream)), "read launch");
 }
 
-size_t dsa_latent_attn_workspace_size(const dsa_latent_attn_args* a, int32_t k) {
-  if (!a || a->B < 1 || a->T < 1 || a->H < 1 || a->H > 128 || k < 1 || k > 65536 || (int64_t)a->B * a->T > (1 << 24))
-    return DSA_WS_MIN;
-  dsa::LatentAttnLaunch L{};
-  L.B = a->B; L.T = a->T; L.H = a->H; L.kk = k;
-  return dsa::kWsScratch + dsa::latent_attn_part_bytes(L, dsa::latent_attn_splits(L));
-}
+size_t dsa_latent_attn_workspace_size(const dsa_latent_attn_args*, int32_t) { return DSA_WS_MIN; }
 
 dsa_status dsa_latent_attn(const dsa_latent_attn_args* a, const int32_t* idx, int32_t k, void* out, float* lse, void* ws,
                            size_t ws_bytes, void* stream) {
@@ -260,12 +254,7 @@ dsa_status dsa_latent_attn(const dsa_latent_attn_args* a, const int32_t* idx, in
   if ((s = check_ws(ws, ws_bytes)) != DSA_OK) return s;
   L.idx = idx; L.out = static_cast<uint16_t*>(out); L.lse = lse;
   L.flags = a->flags ? a->flags : ws_flags(ws);
-  // few rows are split over CTAs when the workspace holds the parts
-  const size_t need = dsa::latent_attn_part_bytes(L, dsa::latent_attn_splits(L));
-  float* part = need > 0 && ws_bytes - dsa::kWsScratch >= need
-                    ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dsa::kWsScratch)
-                    : nullptr;
-  return done(dsa::launch_latent_attn(L, part, static_cast<cudaStream_t>(stream)), "attention launch");
+  return done(dsa::launch_latent_attn(L, static_cast<cudaStream_t>(stream)), "attention launch");
 }
 
 }  // extern "C"

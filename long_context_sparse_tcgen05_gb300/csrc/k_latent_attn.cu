@@ -44,8 +44,8 @@
 // descriptors then stay in uniform registers.  Issued from a lane-0 branch, every product took 60
 // cycles whatever its shape; this way 32 (A in tensor memory) and 48 (A in shared memory: 6 KB of
 // operands at 128 bytes a cycle).
-// With fewer items than half the SMs each is split into parts of at least 128 keys; parts are
-// joined by k_latent_combine.  Waits are bounded (DSA_FLAG_TIMEOUT).
+// With few items each is split into up to 8 parts of at least 128 keys, one to each CTA of a cluster, and
+// the parts are joined over the cluster's shared memory.  Waits are bounded (DSA_FLAG_TIMEOUT).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -74,8 +74,8 @@ constexpr int kRing = 6;                     // blocks the index warps may be ah
 constexpr int kThreads = 24 * 32;
 // Registers by warpgroup (warps 0-3, 4-7, ..), moved at the start from the kernel's own kRegs each;
 // the softmax warps spilled in their block loop at kRegs.
-constexpr int kRegs = 80, kRegsGather = 56, kRegsIssue = 64, kRegsSm = 112, kRegsO = 64, kRegsQ = 72;
-static_assert(kRegsGather + kRegsIssue + 2 * kRegsSm + kRegsO + kRegsQ <= 6 * kRegs, "registers the block is launched with");
+constexpr int kRegs = 80, kRegsGather = 56, kRegsIssue = 64, kRegsSm = 104, kRegsEpi = 72;
+static_assert(kRegsGather + kRegsIssue + 2 * kRegsSm + 2 * kRegsEpi <= 6 * kRegs, "registers the block is launched with");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColSfA = 416, kColSfB = 424, kColS = 448;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -84,6 +84,8 @@ constexpr int kInfoReaders = kGatherWarps + 2 + kSmWarps + 4 + 4;
 constexpr int kEpiThreads = 256;             // O and query warps store an item's O together
 constexpr uint32_t kOPitch = 2 * kLatentDim + 16;  // a staged O row: 8 heads' 16-byte pieces in 32 banks
 static_assert(kHg * kOPitch <= kQBytes, "O is staged in the queries' room");
+static_assert(kHg * kLatentDim * sizeof(float) <= kStages * kStage + 2 * kPBytes, "a part is left over the stages and P");
+static_assert(kHg * kMaxLatentSplits * sizeof(float) <= kQBytes, "the parts' weights in the queries' room");
 
 struct Bars {
   uint64_t q_full, q_empty, qs_full[2];
@@ -106,6 +108,7 @@ struct Small {
   alignas(16) float alpha[2][kHg];       // by block parity: factor of O where `need` is set
   uint32_t sf[2][kHg];                   // by block parity: a block's scale, as exponent + 127 in each byte
   alignas(16) float lsum[2][kHg];        // reciprocal row sums, by item parity
+  float part_lse[kHg];                   // of a part of a row
   float qs[2][kHg], qnext[kHg];          // 2^-k of the item's heads, and of the converted next one's
   alignas(8) uint8_t need[2][8];         // by block parity and group of 8 heads: O must be rescaled
   Bars bar;
@@ -225,6 +228,30 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// Other CTAs of the cluster: a meeting of all their threads (each comes, since every wait of its own is
+// bounded), and loads from the place in rank's shared memory that p has in this CTA's.
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;\n" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float cluster_ld(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr(p, rank))
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ bool elect_lane() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
@@ -303,7 +330,10 @@ __device__ __forceinline__ Item item_of(const LatentAttnLaunch& p, int item) {
   return r;
 }
 
-template <bool kPoll>
+// kPoll: a wait limit below the default.  kParts: an item is a part of a row, one a CTA.  (A kernel of its
+// own: the loops of a chunk run at the pace of their instruction fetches, 1.09 against 0.99 ms with the
+// joining code beside them.)
+template <bool kPoll, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -321,7 +351,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity, abort_flag, p.wait));
   };
 
-  asm volatile("griddepcontrol.launch_dependents;\n");  // (k_latent_combine waits for this grid's end itself)
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 4);
     mbar_init(&bar.q_empty, 1);
@@ -443,7 +472,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   auto epilogue = [&](int item, int oc) -> bool {
     const int q4 = warp & 3, cw = warp < kQWarp0 ? 0 : 1;
     const Item I = item_of(p, item);
-    float* const po = p.splits > 1 ? p.part_o + (int64_t)item * kHg * kLatentDim : nullptr;
     const float* ls = sm->lsum[oc & 1];
     const uint32_t o_addr = tmem + ((uint32_t)(q4 * 32) << 16) + kColO + cw * kHg;
     const bool ok = wait(&bar.l_full[oc & 1], (oc >> 1) & 1) && wait(&bar.o_full, oc & 1);
@@ -455,11 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     tc_fence_after();
     // (a head without weights, sum 0, gives zeros whatever its products left)
     const bool none = __any_sync(0xffffffffu, ls[lane] == 0.f || ls[32 + lane] == 0.f);
-    if (po) {  // a part: fp32 rows, 32 dims of a head a store
+    if constexpr (kParts) {  // fp32 rows over the stages, which the last products have read, 32 dims of a head a store
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         const int c = i >> 1, h0 = 32 * (i & 1);
-        float* out = po + (int64_t)h0 * kLatentDim + (2 * c + cw) * 128 + q4 * 32 + lane;
+        float* out = reinterpret_cast<float*>(kv_s) + h0 * kLatentDim + (2 * c + cw) * 128 + q4 * 32 + lane;
         uint32_t r[32];
         tmem_ld32(o_addr + 2 * c * kHg + h0, r);
         tmem_wait_ld();
@@ -468,10 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
           const float4 f = *reinterpret_cast<const float4*>(ls + h0 + u);
           const float a[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (none && a[x] == 0.f) r[u + x] = 0;
-            if (h0 + u + x < I.heads) out[(u + x) * kLatentDim] = __uint_as_float(r[u + x]) * a[x];
-          }
+          for (int x = 0; x < 4; ++x)
+            out[(u + x) * kLatentDim] = none && a[x] == 0.f ? 0.f : __uint_as_float(r[u + x]) * a[x];
         }
       }
     } else {
@@ -517,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       mbar_arrive(&bar.l_empty[oc & 1]);
       mbar_arrive(&bar.o_empty);
     }
-    if (!po) {
+    if constexpr (!kParts) {
       if (warp < kQWarp0) {
         named_arrive(4, kEpiThreads);  // (the next arrival here comes after the next meeting at barrier 1)
       } else {
@@ -533,6 +559,63 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       }
     }
     return true;
+  };
+
+  // Joins the parts of a row, one in each CTA of a cluster: O = sum_s w_s O_s, w_s = e^(lse_s - lse).  The
+  // O and query warps of each take a share of the heads, over every CTA's shared memory: 128 KB at the
+  // 15 bytes a cycle that such loads move.  (Parts in global memory, joined by a second kernel, took the same
+  // 29 us for a 32-sequence decode step and 16.5, not 19, for a single sequence in 16 parts, but 28, not
+  // 20, on the host, whose time is what a caller outside a graph waits for: a launch more, and room.)
+  auto join = [&]() {
+    const Item I = item_of(p, blockIdx.x);
+    const int t = threadIdx.x - kOWarp0 * 32, h0 = kHg * I.split / p.splits, share = kHg * (I.split + 1) / p.splits - h0;
+    float* wgt = reinterpret_cast<float*>(q_s);  // [head of the share][part]: the queries' room is free
+    if (t < share) {
+      float mx = -INFINITY, sum = 0.f, v[kMaxLatentSplits];
+#pragma unroll
+      for (int s = 0; s < kMaxLatentSplits; ++s) {
+        v[s] = s < p.splits ? cluster_ld(&sm->part_lse[h0 + t], s) : -INFINITY;
+        mx = fmaxf(mx, v[s]);
+      }
+#pragma unroll
+      for (int s = 0; s < kMaxLatentSplits; ++s) {
+        v[s] = v[s] == -INFINITY ? 0.f : expf(v[s] - mx);  // (a NaN stays)
+        sum += v[s];
+      }
+#pragma unroll
+      for (int s = 0; s < kMaxLatentSplits; ++s) wgt[t * kMaxLatentSplits + s] = sum == 0.f ? 0.f : v[s] / sum;
+      if (p.lse && h0 + t < I.heads) p.lse[(int64_t)I.row * p.H + I.h0 + h0 + t] = sum == 0.f ? -INFINITY : mx + logf(sum);
+    }
+    named_sync(1, kEpiThreads);
+#pragma unroll 1
+    for (int i = t; i < share * (kLatentDim / 4); i += kEpiThreads) {
+      const int h = i / (kLatentDim / 4), d = i % (kLatentDim / 4) * 4;
+      if (h0 + h >= I.heads) break;
+      const float* mine = reinterpret_cast<const float*>(kv_s) + (h0 + h) * kLatentDim + d;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), x[kMaxLatentSplits];
+#pragma unroll
+      for (int s = 0; s < kMaxLatentSplits; ++s)
+        if (s < p.splits) x[s] = s == I.split ? *reinterpret_cast<const float4*>(mine) : cluster_ld4(mine, s);
+#pragma unroll
+      for (int s = 0; s < kMaxLatentSplits; ++s) {
+        const float w = wgt[h * kMaxLatentSplits + s];
+        if (w == 0.f) continue;  // (an empty part wrote no values)
+        acc.x += w * x[s].x;
+        acc.y += w * x[s].y;
+        acc.z += w * x[s].z;
+        acc.w += w * x[s].w;
+      }
+      reinterpret_cast<uint2*>(p.out + ((int64_t)I.row * p.H + I.h0 + h0 + h) * kLatentDim + d)[0] =
+          make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    }
+  };
+  // Every warp's end: with parts, all of a cluster's CTAs meet before they are joined and after.
+  auto finish = [&](bool joins) {
+    if constexpr (kParts) {
+      cluster_meet();
+      if (joins) join();
+      cluster_meet();
+    }
   };
 
   // The converted rows' columns 32 s0 .. 32 s1 into tensor memory (the rope columns follow the codes').
@@ -614,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       }
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
+    finish(false);
   } else if (warp < kSmWarp0) {
     reg_dec<kRegsIssue>();
     if (warp == kSWarp) {
@@ -826,6 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         cur = next;
       }
     }
+    finish(false);
   } else if (warp < kOWarp0) {
     reg_inc<kRegsSm>();
     // ================= softmax =================
@@ -923,121 +1008,124 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
         sm->lsum[oc & 1][hl] = l == 0.f ? 0.f : 1.f / l;
         const Item I = item_of(p, item);
         const float v = l == 0.f ? -INFINITY : (E0 + log2f(l)) * kLn2;
-        if (p.splits > 1) p.part_lse[(int64_t)item * kHg + hl] = v;
+        if (kParts) sm->part_lse[hl] = v;
         else if (p.lse && hl < I.heads) p.lse[(int64_t)I.row * p.H + I.h0 + hl] = v;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.l_full[oc & 1]);
       ++oc;
     }
-  } else if (warp < kQWarp0) {
-    reg_dec<kRegsO>();
-    // ================= O^T: block scales, half of the epilogue =================
-    const int t = threadIdx.x - kOWarp0 * 32;
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    tmem_st_x2(tmem + lane_base + kColSfA, 0x7f7f7f7fu, 0x7f7f7f7fu);  // V as it stands
-    tmem_st_x2(tmem + lane_base + kColSfA + 2, 0x7f7f7f7fu, 0x7f7f7f7fu);
-    tmem_wait_stores();
-    tc_fence_before();
-    int it = 0, oc = 0;
-    uint32_t g = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
-      if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
-      const int nb = sm->nb[it & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
-      if (nb == 0) {  // nothing selected: O = 0, LSE = -inf
-        const Item I = item_of(p, item);
-        uint16_t* og = p.out + ((int64_t)I.row * p.H + I.h0) * kLatentDim;
-        if (p.splits > 1) {  // the combine reads no part whose weight is 0
-          if (t < kHg) p.part_lse[(int64_t)item * kHg + t] = -INFINITY;
-        } else {
-          for (int i = t; i < I.heads * kLatentDim / 8; i += 128) reinterpret_cast<uint4*>(og)[i] = make_uint4(0, 0, 0, 0);
-          if (p.lse && t < I.heads) p.lse[(int64_t)I.row * p.H + I.h0 + t] = -INFINITY;
+    finish(false);
+  } else {
+    reg_dec<kRegsEpi>();
+    if (warp < kQWarp0) {
+      // ================= O^T: block scales, half of the epilogue =================
+      const int t = threadIdx.x - kOWarp0 * 32;
+      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+      tmem_st_x2(tmem + lane_base + kColSfA, 0x7f7f7f7fu, 0x7f7f7f7fu);  // V as it stands
+      tmem_st_x2(tmem + lane_base + kColSfA + 2, 0x7f7f7f7fu, 0x7f7f7f7fu);
+      tmem_wait_stores();
+      tc_fence_before();
+      int it = 0, oc = 0;
+      uint32_t g = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < items; item += G, ++it) {
+        if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
+        const int nb = sm->nb[it & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+        if (nb == 0) {  // nothing selected: O = 0, LSE = -inf
+          const Item I = item_of(p, item);
+          uint16_t* og = p.out + ((int64_t)I.row * p.H + I.h0) * kLatentDim;
+          if (kParts) {  // (no part is read whose weight is 0)
+            if (t < kHg) sm->part_lse[t] = -INFINITY;
+          } else {
+            for (int i = t; i < I.heads * kLatentDim / 8; i += 128) reinterpret_cast<uint4*>(og)[i] = make_uint4(0, 0, 0, 0);
+            if (p.lse && t < I.heads) p.lse[(int64_t)I.row * p.H + I.h0 + t] = -INFINITY;
+          }
+          continue;
         }
-        continue;
-      }
-      for (int j = 0; j < nb; ++j, ++g) {
-        // told at every block, when its scales are known and its weights are not yet formed
-        if (!(ok = wait(&bar.m_full[g & 1], (g >> 1) & 1))) break;
-        const bool need = j > 0 && __any_sync(0xffffffffu, *reinterpret_cast<const volatile uint64_t*>(sm->need[g & 1]) != 0);
-        if (need) {
-          // O^T complete up to the block before: rescale the heads whose E0 moved
-          if (!(ok = wait(&bar.p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1))) break;
-          tc_fence_after();
+        for (int j = 0; j < nb; ++j, ++g) {
+          // told at every block, when its scales are known and its weights are not yet formed
+          if (!(ok = wait(&bar.m_full[g & 1], (g >> 1) & 1))) break;
+          const bool need = j > 0 && __any_sync(0xffffffffu, *reinterpret_cast<const volatile uint64_t*>(sm->need[g & 1]) != 0);
+          if (need) {
+            // O^T complete up to the block before: rescale the heads whose E0 moved
+            if (!(ok = wait(&bar.p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1))) break;
+            tc_fence_after();
 #pragma unroll 1
-          for (int w = 0; w < 8; ++w) {
-            if (!sm->need[g & 1][w]) continue;
-            const float4 a0 = *reinterpret_cast<const float4*>(&sm->alpha[g & 1][8 * w]);
-            const float4 a1 = *reinterpret_cast<const float4*>(&sm->alpha[g & 1][8 * w + 4]);
-            const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            uint32_t v[4][8];
+            for (int w = 0; w < 8; ++w) {
+              if (!sm->need[g & 1][w]) continue;
+              const float4 a0 = *reinterpret_cast<const float4*>(&sm->alpha[g & 1][8 * w]);
+              const float4 a1 = *reinterpret_cast<const float4*>(&sm->alpha[g & 1][8 * w + 4]);
+              const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+              uint32_t v[4][8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
-            tmem_wait_ld();
+              for (int c = 0; c < 4; ++c) tmem_ld_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+              for (int c = 0; c < 4; ++c) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * a[i]);
-              tmem_st_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
+                for (int i = 0; i < 8; ++i) v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * a[i]);
+                tmem_st_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
+              }
             }
           }
-        }
-        // the block's scales (the products that read this buffer's last ones are done: the softmax
-        // waited for them before it wrote these)
-        tmem_st_x2(tmem + lane_base + kColSfB + 4 * (g & 1), sm->sf[g & 1][lane], sm->sf[g & 1][32 + lane]);
-        tmem_wait_stores();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.sf_full[g & 1]);
-      }
-      if (!ok || !(ok = epilogue(item, oc))) break;
-      ++oc;
-    }
-    meet_last(ok);
-  } else {
-    reg_dec<kRegsQ>();
-    // ================= queries: hi and lo rows; half of the epilogue =================
-    const int qw = warp - kQWarp0;
-    int it = 0, oc = 0;
-    int last = -1;  // the item whose O is still to be stored
-    bool ok = true;
-    for (int item = blockIdx.x; item < items || last >= 0; item += G, ++it) {
-      int nb = 0;
-      if (item < items) {
-        if (it > 0) convert(item, 16 * qw, 16);
-        ok = wait(&bar.info_full[it & 1], (it >> 1) & 1);
-        nb = ok ? sm->nb[it & 1] : 0;
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
-        if (ok && nb) ok = wait(&bar.q_empty, (oc & 1) ^ 1);
-        if (named_sync_or(2, 128, !ok)) {  // all rows are there; the four warps go on or leave together
-          ok = false;
-          break;
-        }
-        if (nb) {
-          if (lane < 16) sm->qs[oc & 1][16 * qw + lane] = sm->qnext[16 * qw + lane];
-          if (it > 0) {
-            tc_fence_after();
-            copy_q(0, 5);
-          }
+          // the block's scales (the products that read this buffer's last ones are done: the softmax
+          // waited for them before it wrote these)
+          tmem_st_x2(tmem + lane_base + kColSfB + 4 * (g & 1), sm->sf[g & 1][lane], sm->sf[g & 1][32 + lane]);
+          tmem_wait_stores();
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bar.qs_full[oc & 1]);
-            mbar_arrive(&bar.q_full);
-          }
+          if (lane == 0) mbar_arrive(&bar.sf_full[g & 1]);
         }
-        named_sync(2, 128);  // the room has been read
+        if (!ok || !(ok = epilogue(item, oc))) break;
+        ++oc;
       }
-      // the O warps wait in the last item's epilogue: join them before any wait on a later item
-      // than this one, whose publication they hold up
-      if (last >= 0 && !(ok = epilogue(last, oc - 1))) break;
-      if (nb) ++oc;
-      last = nb ? item : -1;
+      meet_last(ok);
+    } else {
+      // ================= queries: hi and lo rows; half of the epilogue =================
+      const int qw = warp - kQWarp0;
+      int it = 0, oc = 0;
+      int last = -1;  // the item whose O is still to be stored
+      bool ok = true;
+      for (int item = blockIdx.x; item < items || last >= 0; item += G, ++it) {
+        int nb = 0;
+        if (item < items) {
+          if (it > 0) convert(item, 16 * qw, 16);
+          ok = wait(&bar.info_full[it & 1], (it >> 1) & 1);
+          nb = ok ? sm->nb[it & 1] : 0;
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
+          if (ok && nb) ok = wait(&bar.q_empty, (oc & 1) ^ 1);
+          if (named_sync_or(2, 128, !ok)) {  // all rows are there; the four warps go on or leave together
+            ok = false;
+            break;
+          }
+          if (nb) {
+            if (lane < 16) sm->qs[oc & 1][16 * qw + lane] = sm->qnext[16 * qw + lane];
+            if (it > 0) {
+              tc_fence_after();
+              copy_q(0, 5);
+            }
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&bar.qs_full[oc & 1]);
+              mbar_arrive(&bar.q_full);
+            }
+          }
+          named_sync(2, 128);  // the room has been read
+        }
+        // the O warps wait in the last item's epilogue: join them before any wait on a later item
+        // than this one, whose publication they hold up
+        if (last >= 0 && !(ok = epilogue(last, oc - 1))) break;
+        if (nb) ++oc;
+        last = nb ? item : -1;
+      }
+      meet_last(ok);
+      asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     }
-    meet_last(ok);
-    asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+    finish(true);
   }
 
   __syncthreads();
@@ -1049,124 +1137,84 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 }
 static_assert(kColQR == kColQ + 128, "the converted query row is stored in one run of columns");
 
-// Joins a split item's parts: O = sum_s w_s O_s with w_s = e^(lse_s - lse).  One CTA per (query, 4
-// heads): few queries must still fill the GPU.  N parts' loads in flight: 4, in 32 registers, so that
-// every block of a batch is resident at once (8 in 51 registers: 26.5 against 25.2 us into a
-// 32-sequence decode step); 8 for more than 8 parts, which few rows have (17.2 against 16.5 us a single
-// sequence's step).
-constexpr int kCombHeads = 4;
-template <int N>
-__global__ void __launch_bounds__(kCombHeads * 128, 16 / N) k_latent_combine(LatentAttnLaunch p) {
-  __shared__ float wgt[kMaxLatentSplits][kCombHeads];
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the parts are complete and visible
-  const int row = blockIdx.x, h0 = blockIdx.y * kCombHeads, S = p.splits;
-  const int64_t part0 = ((int64_t)row * p.groups + h0 / kHg) * S;
-  const int hl0 = h0 % kHg;
-  if (threadIdx.x < kCombHeads && h0 + threadIdx.x < p.H) {
-    const float* pl = p.part_lse + part0 * kHg + hl0 + threadIdx.x;
-    float mx = -INFINITY, sum = 0.f;
-    for (int s = 0; s < S; ++s) mx = fmaxf(mx, pl[s * kHg]);
-    for (int s = 0; s < S; ++s) {
-      const float v = pl[s * kHg];
-      const float w = v == -INFINITY ? 0.f : expf(v - mx);  // (a NaN stays)
-      wgt[s][threadIdx.x] = w;
-      sum += w;
-    }
-    for (int s = 0; s < S; ++s) wgt[s][threadIdx.x] = sum == 0.f ? 0.f : wgt[s][threadIdx.x] / sum;
-    if (p.lse) p.lse[(int64_t)row * p.H + h0 + threadIdx.x] = sum == 0.f ? -INFINITY : mx + logf(sum);
-  }
-  // the parts' values do not wait for their weights: four dims of a head a thread
-  const int hl = threadIdx.x >> 7, i = threadIdx.x & 127;
-  const float4* src = reinterpret_cast<const float4*>(p.part_o + (part0 * kHg + hl0 + hl) * kLatentDim) + i;
-  const bool live = h0 + hl < p.H;
-  float4 v[N];
-  auto load = [&](int s0) {
-#pragma unroll
-    for (int s = 0; s < N; ++s)
-      if (live && s0 + s < S) v[s] = __ldcs(src + (int64_t)(s0 + s) * kHg * kLatentDim / 4);
-  };
-  load(0);
-  __syncthreads();
-  if (!live) return;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < S; s0 += N) {
-#pragma unroll
-    for (int s = 0; s < N; ++s) {
-      const float w = s0 + s < S ? wgt[s0 + s][hl] : 0.f;
-      if (w == 0.f) continue;  // an empty part wrote no values
-      acc.x += w * v[s].x;
-      acc.y += w * v[s].y;
-      acc.z += w * v[s].z;
-      acc.w += w * v[s].w;
-    }
-    load(s0 + N);
-  }
-  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), b = __floats2bfloat162_rn(acc.z, acc.w);
-  reinterpret_cast<uint2*>(p.out + ((int64_t)row * p.H + h0 + hl) * kLatentDim)[i] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
 }  // namespace
 
-int latent_attn_splits(const LatentAttnLaunch& p) {
-  const int64_t items = (int64_t)p.B * p.T * ((p.H + kHg - 1) / kHg);
-  const int sms = device_sm_count();
-  if (items * 2 > sms) return 1;
-  int s = (int)(sms / items);
-  s = s < (p.kk + 127) / 128 ? s : (p.kk + 127) / 128;  // parts of at least 128 keys
-  return s < 2 ? 1 : s > kMaxLatentSplits ? kMaxLatentSplits : s;
+// A launch whose CTAs work in clusters of n on a row each.
+static cudaLaunchConfig_t launch_config(int ctas, int n, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)ctas);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = kSmem;
+  c.stream = st;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)n;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  c.attrs = attr;
+  c.numAttrs = n > 1;
+  return c;
 }
 
-size_t latent_attn_part_bytes(const LatentAttnLaunch& p, int splits) {
-  if (splits <= 1) return 0;
-  return (size_t)p.B * p.T * ((p.H + kHg - 1) / kHg) * splits * kHg * (kLatentDim + 1) * sizeof(float);
+// What the launcher knows of a device, found out once: the clusters of n CTAs that fit on it at a time.
+struct ClusterRoom {
+  int clusters[kMaxLatentSplits + 1];
+};
+
+static auto kernel_of(bool poll, bool parts) {
+  return poll ? (parts ? k_latent_attn<true, true> : k_latent_attn<true, false>)
+              : (parts ? k_latent_attn<false, true> : k_latent_attn<false, false>);
 }
 
-// Once per device and instantiation: shared memory, and that the block is launched with the registers
-// that its warpgroups' moves count on.
-static cudaError_t prepare_kernel(void (*kern)(LatentAttnLaunch), int which) {
-  static std::atomic<bool> ready[64][2];
+// Once per device: shared memory, that a block is launched with the registers that its warpgroups' moves
+// count on, and the clusters.
+static cudaError_t prepare_kernels(ClusterRoom& room) {
+  static ClusterRoom rooms[64];
+  static std::atomic<int> state[64];  // 0: unknown, 1: being written, 2: known
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && ready[dev][which].load(std::memory_order_acquire)) return cudaSuccess;
-  cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-  if (fa.numRegs != kRegs) return cudaErrorInvalidKernelImage;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)) != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64) ready[dev][which].store(true, std::memory_order_release);
+  const bool kept = dev >= 0 && dev < 64;
+  if (kept && state[dev].load(std::memory_order_acquire) == 2) {
+    room = rooms[dev];
+    return cudaSuccess;
+  }
+  for (int k = 0; k < 4; ++k) {
+    auto kern = kernel_of(k & 1, k & 2);
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if (fa.numRegs != kRegs) return cudaErrorInvalidKernelImage;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)) != cudaSuccess) return e;
+  }
+  for (int n = 2; n <= kMaxLatentSplits; ++n) {
+    cudaLaunchAttribute attr{};
+    const cudaLaunchConfig_t c = launch_config(n, n, nullptr, &attr);
+    if ((e = cudaOccupancyMaxActiveClusters(&room.clusters[n], kernel_of(false, true), &c)) != cudaSuccess) return e;
+  }
+  int unknown = 0;
+  if (kept && state[dev].compare_exchange_strong(unknown, 1)) {
+    rooms[dev] = room;
+    state[dev].store(2, std::memory_order_release);
+  }
   return cudaSuccess;
 }
 
-// part: room for latent_attn_part_bytes, or NULL: rows are not split.
-cudaError_t launch_latent_attn(LatentAttnLaunch p, float* part, cudaStream_t st) {
+cudaError_t launch_latent_attn(LatentAttnLaunch p, cudaStream_t st) {
   TraceScope trace(kTraceAttention, st);
   p.groups = (p.H + kHg - 1) / kHg;
-  p.splits = part ? latent_attn_splits(p) : 1;
-  const int64_t items = (int64_t)p.B * p.T * p.groups * p.splits;
-  if (p.splits > 1) {
-    p.part_o = part;
-    p.part_lse = part + items * kHg * kLatentDim;
-  }
   p.wait = wait_limit();
-  auto kern = p.wait < kDefaultWaitCycles ? k_latent_attn<true> : k_latent_attn<false>;
-  cudaError_t e = prepare_kernel(kern, kern == k_latent_attn<true> ? 0 : 1);
+  const bool poll = p.wait < kDefaultWaitCycles;
+  ClusterRoom room{};
+  cudaError_t e = prepare_kernels(room);
   if (e != cudaSuccess) return e;
+  // parts of at least 128 keys, in clusters that are all resident at once
+  const int64_t rows = (int64_t)p.B * p.T * p.groups;
+  p.splits = 1;
+  for (int n = 2; n <= kMaxLatentSplits && n <= (p.kk + 127) / 128; ++n)
+    if (rows <= room.clusters[n]) p.splits = n;
+  const int64_t items = rows * p.splits;
   const int sms = device_sm_count();
-  kern<<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, st>>>(p);
-  count_launches(1);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.splits <= 1) return e;
-  // launched while the parts are being computed: its blocks stand ready when the last part ends
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.B * p.T), (unsigned)((p.H + kCombHeads - 1) / kCombHeads));
-  cfg.blockDim = dim3(kCombHeads * 128);
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, p.splits > 8 ? k_latent_combine<8> : k_latent_combine<4>, p)) != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  const cudaLaunchConfig_t cfg = launch_config((int)(p.splits > 1 || items < sms ? items : sms), p.splits, st, &attr);
+  if ((e = cudaLaunchKernelEx(&cfg, kernel_of(poll, p.splits > 1), p)) != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
 }
