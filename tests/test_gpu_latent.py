@@ -880,3 +880,21 @@ def test_broadcast_operands_are_refused():
         dsa.dsa_latent_attn(at, _idx(2, 1, 20, 4))
     with pytest.raises(AssertionError):
         dsa.dsa_latent_attn(dict(at, q=_q(2, 1, 8), S=2 ** 32 + 5), _idx(2, 1, 20, 4))
+
+
+@pytest.mark.parametrize("rows", [2, 16, 21, 26, 33, 45, 60, 76, 77, 153])
+@pytest.mark.parametrize("H", [64, 20, 128])
+def test_latent_attn_rows_of_every_split(rows, H):
+    """From eight parts a row to one: rows cut short, so that parts are empty, and empty rows."""
+    S, k = 1500, 1100
+    cache = _cache(1, S, 48)
+    idx = _idx(1, rows, S, k)
+    n = torch.randint(0, k + 1, (rows,), generator=_gen(rows), device=DEV)
+    n[0], n[-1], n[rows // 2] = 130, k, 0
+    idx[0][torch.arange(k, device=DEV) >= n[:, None]] = -1
+    at = dict(q=_q(1, rows, H), cache=cache, scale=1 / 24)
+    _check_attn(at, idx)
+    o, l = dsa.dsa_latent_attn(at, idx)
+    o2, l2 = dsa.dsa_latent_attn(at, idx)
+    assert torch.equal(o, o2) and torch.equal(l, l2)
+    assert bool((o[0, n == 0] == 0).all()) and bool((l[0, n == 0] == -math.inf).all())
