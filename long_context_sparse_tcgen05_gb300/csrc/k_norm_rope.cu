@@ -279,21 +279,20 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
   };
   const uint32_t first = blockIdx.x * kTeams + threadIdx.x / kTeam;
   int64_t next = position(first, at_row.i);
-  // unit (s, u) of the token at row w, and whether there is one
-  auto unit_at = [&](uint32_t tok, const RowWalk& w, int s, int u, bool& in) -> const uint16_t* {
-    const int h = hsub + s * kHeads, at = (u * G + l) * 8;
-    in = tok < toks && h < p.H && at < p.d;
-    return in ? p.x + w.b * p.x_sb + w.i * p.x_st + h * p.x_sh + at : p.x;
-  };
+  // this thread's first unit of the token at row w, and its unit (s, u)
+  const uint16_t* const mine = p.x + hsub * p.x_sh + l * 8;
+  auto units_of = [&](const RowWalk& w) { return mine + w.b * p.x_sb + w.i * p.x_st; };
+  auto unit_at = [&](const uint16_t* x, int s, int u) { return x + s * kHeads * p.x_sh + u * G * 8; };
+  auto has_unit = [&](uint32_t tok, int s, int u) { return tok < toks && hsub + s * kHeads < p.H && (u * G + l) * 8 < p.d; };
   auto fetch = [&](uint32_t tok, const RowWalk& w, int slot) {
     if constexpr (kAhead) {
+      const uint16_t* x = units_of(w);
 #pragma unroll
       for (int s = 0; s < NP; ++s)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          bool in;
-          const uint16_t* src = unit_at(tok, w, s, u, in);
-          copy16_async(&ahead[slot][s * U + u][threadIdx.x], src, in);
+          const bool in = has_unit(tok, s, u);
+          copy16_async(&ahead[slot][s * U + u][threadIdx.x], in ? unit_at(x, s, u) : p.x, in);
         }
       copies_commit();
     }
@@ -306,14 +305,12 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
     const int b = live ? (int)at_row.b : 0, i = live ? (int)at_row.i : 0;
     uint4 raw[NP][U];
     if constexpr (!kAhead) {
+      const uint16_t* x = units_of(at_row);
 #pragma unroll
       for (int s = 0; s < NP; ++s)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          bool in;
-          const uint16_t* src = unit_at(tok, at_row, s, u, in);
-          raw[s][u] = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
-        }
+        for (int u = 0; u < U; ++u)
+          raw[s][u] = has_unit(tok, s, u) ? __ldg(reinterpret_cast<const uint4*>(unit_at(x, s, u))) : make_uint4(0, 0, 0, 0);
     }
     at_row.next();
     const int64_t pos = checked_pos(p, next, t == 0);
@@ -364,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
     const float q = amax / 448.f;
     const float scale = q == 0.f ? 1.f : q;  // (a NaN stays)
     const int64_t dst = (int64_t)b * p.S_cap + (p.at_position ? pos : i);
-    uint8_t* codes = p.codes + dst * (int64_t)p.H * p.d;
+    uint8_t* codes = p.codes + dst * (int64_t)p.H * p.d + (int64_t)hsub * p.d + l * 8;
     with_quotient(scale, [&](auto div) {
 #pragma unroll
       for (int s = 0; s < NP; ++s)
@@ -373,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, NP * U >= 8 ? 1 : 3) k_norm_rope_e4m
           const int h = hsub + s * kHeads, at = (u * G + l) * 8;
           if (h >= p.H || at >= p.d) continue;
           const f32x2* v = y[s][u].p;
-          *reinterpret_cast<uint2*>(codes + (int64_t)h * p.d + at) = make_uint2(codes4(div, v[0], v[1]), codes4(div, v[2], v[3]));
+          *reinterpret_cast<uint2*>(codes + s * kHeads * p.d + u * G * 8) = make_uint2(codes4(div, v[0], v[1]), codes4(div, v[2], v[3]));
         }
     });
     if (t == 0) p.scales[dst] = scale;
