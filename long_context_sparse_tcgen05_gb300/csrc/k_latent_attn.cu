@@ -400,20 +400,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm->tmem, 0);
 
-  // Heads h0 .. h0 + n - 1 of an item's queries to hi and lo rows in shared memory: a warp takes a head
-  // at a time, 16 latent values and 2 rope values a lane.  Row of head h's hi codes: 32 (h / 16) +
-  // 16 (h / 8 % 2) + h % 8; its lo codes 8 rows on, so that a softmax thread's one load gives it both.
-  auto convert = [&](int item, int h0, int n) {
+  // Every n-th head of an item's queries, from w on, to hi and lo rows in shared memory (so few heads are
+  // spread over the warps too; zeros where there is none).  Two heads at a time, 16 latent values and 2
+  // rope values of each a lane.  Row of head h's hi codes: row_of(h); its lo codes 8 rows on, so that a
+  // softmax thread's one load gives it both.
+  auto row_of = [](int h) -> uint32_t { return 32 * (h >> 4) + 16 * ((h >> 3) & 1) + (h & 7); };
+  auto convert = [&](int item, int w, int n) {
     const Item I = item_of(p, item);
     const uint16_t* q0 = p.q + I.b * p.q_sb + I.t * p.q_st + (int64_t)I.h0 * kD;
     const uint32_t sixteen = 0x4c004c00u;  // f16 16.0 twice
     uint4 nx[2][2];
     uint32_t nr[2];
-    auto load = [&](int h0_) {  // two heads
+    auto load = [&](int h) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const bool live = h0_ + k < min(I.heads, h0 + n);
-        const uint4* q = reinterpret_cast<const uint4*>(q0 + (int64_t)(h0_ + k) * kD);
+        const bool live = h + k * n < I.heads;
+        const uint4* q = reinterpret_cast<const uint4*>(q0 + (int64_t)(h + k * n) * kD);
         nx[k][0] = live ? __ldg(q + lane) : make_uint4(0, 0, 0, 0);
         nx[k][1] = live ? __ldg(q + 32 + lane) : make_uint4(0, 0, 0, 0);
         nr[k] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + kLatentDim / 8) + lane) : 0u;
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       const bool finite = (top >> 7) < 255;
       const float mul = finite ? __uint_as_float((uint32_t)(7 - e + 127) << 23) : __uint_as_float(0x7fc00000u);
       if (lane == 0) sm->qnext[h] = finite ? __uint_as_float((uint32_t)(e - 7 + 127) << 23) : 1.f;
-      const uint32_t row = 32 * (h >> 4) + 16 * ((h >> 3) & 1) + (h & 7);
+      const uint32_t row = row_of(h);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
@@ -459,14 +461,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(&h2);
       *reinterpret_cast<uint32_t*>(dst + 8 * 2 * kLatentRope) = *reinterpret_cast<const uint32_t*>(&l2);
     };
-    load(h0);
+    load(w);
 #pragma unroll 1
-    for (int h = h0; h < h0 + n; h += 2) {
+    for (int h = w; h < I.heads; h += 2 * n) {
       const uint4 a[2] = {nx[0][0], nx[0][1]}, b[2] = {nx[1][0], nx[1][1]};
       const uint32_t ra = nr[0], rb = nr[1];
-      load(h + 2);
+      load(h + 2 * n);
       one(h, a, ra);
-      one(h + 1, b, rb);
+      one(h + n, b, rb);  // (a place below 64: an even number of them a warp)
+    }
+    if (I.heads == kHg) return;
+#pragma unroll 1
+    for (int h = w; h < kHg; h += n) {
+      if (h < I.heads) continue;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        *reinterpret_cast<uint4*>(q_s + (row_of(h) + 8 * k) * kLatentDim + lane * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint32_t*>(q_s + kQCodes + (row_of(h) + 8 * k) * (2 * kLatentRope) + lane * 4) = 0u;
+      }
+      if (lane == 0) sm->qnext[h] = 1.f;
     }
   };
 
@@ -496,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         const int c = i >> 1, h0 = 32 * (i & 1);
+        if (h0 >= I.heads) continue;
         float* out = reinterpret_cast<float*>(kv_s) + h0 * kLatentDim + (2 * c + cw) * 128 + q4 * 32 + lane;
         uint32_t r[32];
         tmem_ld32(o_addr + 2 * c * kHg + h0, r);
@@ -513,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       // 16 dims x 32 heads at a time, as 8 x 8 tiles (rows: dims) that stmatrix stores transposed.
       // (A small loop: unrolled, this code ran at the pace of its instruction fetches.)
 #pragma unroll 1
-      for (int h0 = 0; h0 < kHg; h0 += 32) {
+      for (int h0 = 0; h0 < I.heads; h0 += 32) {
         const uint32_t dst = smem_addr(q_s) + (h0 + 8 * (lane >> 4) + (lane & 7)) * kOPitch +
                              2 * (cw * 128 + q4 * 32 + 8 * ((lane >> 3) & 1));
         f32x2 f[4];
@@ -650,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   // The first item's queries: sixteen warps that have nothing else to do yet convert four heads each,
   // eight of them store the rows (a single decode step waits for nothing longer).
   if (warp >= kSmWarp0) {
-    convert(blockIdx.x, 4 * (warp - kSmWarp0), 4);
+    convert(blockIdx.x, warp - kSmWarp0, 16);
     named_sync(3, 512);
     if (warp >= kOWarp0) {
       copy_q(warp < kQWarp0 ? 0 : 3, warp < kQWarp0 ? 3 : 5);
@@ -1101,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       for (int item = blockIdx.x; item < items || last >= 0; item += G, ++it) {
         int nb = 0;
         if (item < items) {
-          if (it > 0) convert(item, 16 * qw, 16);
+          if (it > 0) convert(item, qw, 4);
           ok = wait(&bar.info_full[it & 1], (it >> 1) & 1);
           nb = ok ? sm->nb[it & 1] : 0;
           __syncwarp();
