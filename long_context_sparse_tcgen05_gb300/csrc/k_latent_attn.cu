@@ -46,8 +46,8 @@
 // With few items each is split into up to 8 parts of at least 128 keys, one to each CTA of a cluster, and
 // the parts are joined over the cluster's shared memory.  Waits are bounded (DSA_FLAG_TIMEOUT).
 //
-// Measured (64 heads, k = 2,048): 4,096 queries over 131,072 rows 1.00 ms, 1,160 TFLOP/s, the tensor pipe
-// 51% busy; 32 single tokens over 200,000 rows 29.0 us; one over 20,000 rows 18.6 us.  What bounds it: a
+// Measured (64 heads, k = 2,048): 4,096 queries over 131,072 rows 0.99 ms, 1,170 TFLOP/s, the tensor pipe
+// 51% busy; 32 single tokens over 200,000 rows 28.8 us; one over 20,000 rows 18.7 us.  What bounds it: a
 // block's products need 1,360 cycles of the tensor pipe, a block takes 2,000: a softmax warp's waits
 // (200), loads (170), scores and maxima (680), exponentials and stores (740) follow one another, and
 // tensor memory (512 columns in use) has no room for a second score buffer to overlap them with.  A
