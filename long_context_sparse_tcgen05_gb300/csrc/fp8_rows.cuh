@@ -63,9 +63,10 @@ __device__ __forceinline__ f32x2 unpack_bf16(uint32_t v) { return pair(bf_lo(v),
 // a = fl(y r), the remainder y - a s is exact in one fma, and fl(a + r (y - a s)) is the rounded
 // quotient (Markstein 1990, "Computation of elementary functions on the IBM RISC System/6000
 // processor", theorem on division) -- three instructions a pair.  It needs a quotient and a remainder
-// inside the normal range: scales outside [2^-60, 2^60] (and NaN) divide; a quotient small enough for
-// its remainder to be subnormal is far below the least e4m3 value.  (with_quotient picks one of the
-// two for a whole row.)
+// inside the normal range, and gives NaN where the quotient is infinite.  So it is for values that the
+// row's scale bounds, and for scales in [2^-60, 2^60] (others, and NaN, divide): of those a quotient too
+// small for its remainder is far below the least e4m3 value.  Values that the scale does not bound go
+// through any_quotient.  (with_quotient picks one of the two for a whole row.)
 struct FastQuotient {
   f32x2 minus_s, r;
   __device__ __forceinline__ explicit FastQuotient(float s) : minus_s(pair(-s, -s)) {
@@ -85,6 +86,13 @@ template <class F>
 __device__ __forceinline__ void with_quotient(float s, F&& f) {
   if (s >= 0x1p-60f && s <= 0x1p60f) f(FastQuotient(s));
   else f(PlainQuotient{s});
+}
+// y / s where s does not bound y: the division itself for a pair that has a value outside [2^-60, 2^60]
+// (zeros, infinities and NaN among them), whose quotient may pass the range the correction needs.
+template <class Q>
+__device__ __forceinline__ f32x2 any_quotient(const Q& q, f32x2 y, float s) {
+  const float lo = fabsf(lo_of(y)), hi = fabsf(hi_of(y));
+  return max_nan(lo, hi) <= 0x1p60f && fminf(lo, hi) >= 0x1p-60f ? q(y) : PlainQuotient{s}(y);
 }
 // four quotients as e4m3 codes
 template <class Q>

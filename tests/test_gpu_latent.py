@@ -898,3 +898,53 @@ def test_latent_attn_rows_of_every_split(rows, H):
     o2, l2 = dsa.dsa_latent_attn(at, idx)
     assert torch.equal(o, o2) and torch.equal(l, l2)
     assert bool((o[0, n == 0] == 0).all()) and bool((l[0, n == 0] == -math.inf).all())
+
+
+# --- rope values that the row's scale does not bound ---------------------------------------------
+
+def _append_rope(rope, top, **kw):
+    """(stored rope values, scales) of rows with the rope values `rope` [n, 64] and latent values
+    whose largest is `top`, on the host."""
+    cache = _cache(1, rope.shape[0], 0, fill=False)
+    x = torch.zeros((1, rope.shape[0], 576), device=DEV, dtype=torch.bfloat16)
+    x[0, :, 3] = top
+    x[0, :, 512:] = rope.to(DEV)
+    dsa.dsa_latent_append(x, cache, **kw)
+    return cache["rope"][0].cpu(), cache["scales"][0].cpu()
+
+
+def _assert_same(got, want):
+    bad = ~((got == want) | (got.isnan() & want.isnan()))
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} differ, first {got[bad][:4]} for {want[bad][:4]}"
+
+
+def _bf16_values():
+    """Every bf16 value, in rows of 64."""
+    return torch.arange(-2 ** 15, 2 ** 15).to(torch.int16).view(torch.bfloat16).reshape(-1, 64)
+
+
+# scales of 2^-60 (an all-zero latent row), 2^-52, ordinary ones, 2^50, 2^60 and beyond
+LATENT_TOPS = [0.0, 448 * 2.0 ** -52, 0.01, 1.0, 3.0, 448 * 2.0 ** 50, 448 * 2.0 ** 60, 1e30, 3e38]
+
+
+@pytest.mark.parametrize("top", LATENT_TOPS)
+def test_latent_append_rope_is_the_ieee_quotient(top):
+    """rope = bf16(value / scale), bit for bit, for every finite bf16 value: quotients that overflow
+    are infinite, not NaN."""
+    v = _bf16_values()
+    v = torch.where(v.isfinite(), v, 0.0)
+    got, s = _append_rope(v, top)
+    _assert_same(got, (v.float() / s[:, None]).bfloat16())
+
+
+@pytest.mark.parametrize("top", LATENT_TOPS)
+@pytest.mark.parametrize("inter", [False, True])
+def test_latent_append_infinite_rope_values_stay_infinite(top, inter):
+    """A pair (inf, c) turned by an angle whose cosine and sine are both positive is (inf, inf)."""
+    v = torch.ones((4, 64))
+    a = slice(0, None, 2) if inter else slice(0, 32)
+    v[1, a], v[2, a], v[3, a] = math.inf, -math.inf, math.nan
+    cos, sin = torch.full((4, 32), 0.6, device=DEV), torch.full((4, 32), 0.8, device=DEV)
+    got, _ = _append_rope(v.bfloat16(), top, cos=cos, sin=sin, interleaved=inter)
+    assert bool(got[0].isfinite().all())
+    assert bool((got[1] == math.inf).all()) and bool((got[2] == -math.inf).all()) and bool(got[3].isnan().all())
