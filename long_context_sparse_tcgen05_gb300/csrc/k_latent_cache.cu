@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p
       *reinterpret_cast<uint2*>(codes + lane * 8) = make_uint2(codes4(div, y[0], y[1]), codes4(div, y[2], y[3]));
       *reinterpret_cast<uint2*>(codes + 256 + lane * 8) = make_uint2(codes4(div, y[4], y[5]), codes4(div, y[6], y[7]));
       // (the scale is the latent values': it does not bound these)
-      const f32x2 r = any_quotient(div, pair(a * cs - c * sn, c * cs + a * sn), scale);
+      // (without tables the values themselves: 1 and 0 as angles would spread an infinity or NaN over the pair)
+      const f32x2 r = any_quotient(div, p.cos ? pair(a * cs - c * sn, c * cs + a * sn) : pair(a, c), scale);
       const uint32_t rr = pack_bf16(lo_of(r), hi_of(r));
       uint16_t* rope = p.cache.rope + row * kLatentRope;
       if (p.interleaved) {

@@ -948,3 +948,14 @@ def test_latent_append_infinite_rope_values_stay_infinite(top, inter):
     got, _ = _append_rope(v.bfloat16(), top, cos=cos, sin=sin, interleaved=inter)
     assert bool(got[0].isfinite().all())
     assert bool((got[1] == math.inf).all()) and bool((got[2] == -math.inf).all()) and bool(got[3].isnan().all())
+
+
+@pytest.mark.parametrize("top", LATENT_TOPS)
+def test_latent_append_without_rotation_keeps_each_rope_value_to_itself(top):
+    """Every bf16 value, infinities and NaN among them, beside finite partners in both pairings."""
+    v = _bf16_values()
+    for rows in (v, torch.stack((v, torch.ones_like(v)), -1).reshape(-1, 64),
+                 torch.cat((v.reshape(-1, 32), torch.ones_like(v).reshape(-1, 32)), -1)):
+        for inter in (False, True):
+            got, s = _append_rope(rows, top, interleaved=inter)
+            _assert_same(got, (rows.float() / s[:, None]).bfloat16())
