@@ -388,7 +388,8 @@ dsa_status dsa_norm_rope_e4m3(const dsa_norm_rope_args* a, uint8_t* codes, float
  * row stands for scale * [codes (512 e4m3) | rope (64 bf16)]: the one scale serves both, so
  * attention multiplies a whole row's score by it.
  *   codes   [n_pages, page_size, 512] (16-byte aligned)
- *   scales  [n_pages, page_size] fp32 (4-byte aligned); positive and finite where rows are used
+ *   scales  [n_pages, page_size] fp32 (4-byte aligned); where rows are used finite and at least 2^-60,
+ *           as dsa_latent_append writes them (attention divides its weights by them)
  *   rope    [n_pages, page_size, 64] bf16 (16-byte aligned)
  *   block_table  DEVICE int32 [B, table_ld]: position p of sequence b is row p % page_size of page
  *                block_table[b * table_ld + p / page_size].  NULL: sequence b is page b

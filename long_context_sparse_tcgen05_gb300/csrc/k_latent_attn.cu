@@ -18,7 +18,7 @@
 //     head, E0 being the head's E at its first block, so blocks of any size add into the same O
 //     without rescaling it (before, each rise of a running maximum had to rescale O between two
 //     products: in ten of a row's 32 blocks, a third of a decode step).  Only when E passes
-//     E0 + 60 is O rescaled and E0 moved.  Row sums take p_j / s_j, times 2^(E - E0), in fp32.
+//     E0 + 40 is O rescaled and E0 moved.  Row sums take p_j / s_j, times 2^(E - E0), in fp32.
 // FP8 products accumulate exactly enough in fp32 (sums of 2,048 products of mixed size came out
 // equal to the 64-bit sum).
 //
@@ -88,7 +88,10 @@ static_assert(kRegsGather + kRegsIssue + 2 * kRegsSm + 2 * kRegsEpi <= 6 * kRegs
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColSfA = 416, kColSfB = 424, kColS = 448;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kMove = 60.f;                // E0 moves when a block's E passes it by this
+// E0 moves when a block's E passes it by this.  A row sum holds up to 1,024 blocks of 64 weights
+// p_j / s_j <= 2^8 / 2^-60 (the append's least scale), times 2^(E - E0): 2^(10 + 6 + 8 + 60 + 40) = 2^124,
+// within fp32 (with 60 it passed 2^128).
+constexpr float kMove = 40.f;
 constexpr int kInfoReaders = kGatherWarps + 2 + kSmWarps + 4 + 4;
 constexpr int kEpiThreads = 256;             // O and query warps store an item's O together
 constexpr uint32_t kOPitch = 2 * kLatentDim + 16;  // a staged O row: 8 heads' 16-byte pieces in 32 banks

@@ -959,3 +959,24 @@ def test_latent_append_without_rotation_keeps_each_rope_value_to_itself(top):
         for inter in (False, True):
             got, s = _append_rope(rows, top, interleaved=inter)
             _assert_same(got, (rows.float() / s[:, None]).bfloat16())
+
+
+# --- attention: sums and accuracy ----------------------------------------------------------------
+
+@pytest.mark.parametrize("T", [1, 160])
+def test_latent_attn_rows_of_the_least_scale_far_above_the_first_block(T):
+    """Ordinary rows, then rows with nothing but rope values (an all-zero latent row's scale is 2^-60)
+    whose scores lie 30 to 110 nats above them: the row sums, which weigh a row by 1 / scale, stay
+    finite whatever the distance, in one part (T = 160) and in several."""
+    S, first = 2048, 64
+    cache = _cache(1, S, 64)
+    cache["rope"].zero_()
+    cache["scales"].fill_(0.01)
+    at = _flat(cache, torch.zeros(S - first, dtype=torch.long, device=DEV), torch.arange(first, S, device=DEV))
+    cache["codes"].view(torch.uint8).view(-1, 512)[at] = 0
+    cache["scales"].view(-1)[at] = 2.0 ** -60
+    cache["rope"].view(-1, 64)[at, 0] = 2.0 ** 60  # a rope value of 1
+    q = torch.zeros((1, T, 64, 576), device=DEV, dtype=torch.bfloat16)
+    q[..., 512] = torch.linspace(30, 110, 64, device=DEV).bfloat16()
+    _check_attn(dict(q=q, cache=cache, scale=1.0), _idx(1, T, S, S, holes=False))
+    assert dsa.read_device_flags(DEV) == 0
