@@ -805,16 +805,18 @@ def trace_disable() -> None:
 
 
 def read_device_flags(device=None) -> int:
-    """Flag words of the cached workspace and of the calls that take none from it (cleared by the
-    read).  Synchronises."""
+    """Flag words of the device's cached workspace and of the calls that take none from it (cleared
+    by the read), once the work before it on the device's current stream is done.  Synchronises."""
     lib = load_library()
-    ws = workspace(WS_MIN, device)
-    v = _c.c_uint32()
-    _check(lib.dsa_read_device_flags(_ptr(ws), _c.byref(v), _stream()))
-    found = int(v.value)
-    if ws.device in _flags:
-        _check(lib.dsa_read_device_flags(_ptr(_flags[ws.device]), _c.byref(v), _stream()))
-        found |= int(v.value)
+    dev = torch.device("cuda" if device is None else device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    v, found = _c.c_uint32(), 0
+    with torch.cuda.device(dev):
+        for ws in (workspace(WS_MIN, dev), _flags.get(dev)):
+            if ws is not None:
+                _check(lib.dsa_read_device_flags(_ptr(ws), _c.byref(v), _stream()))
+                found |= int(v.value)
     return found
 
 

@@ -1,10 +1,13 @@
 """C-ABI checks of the latent cache and norm entry points that need no GPU: struct layouts, and the
 host-side validation that rejects a bad call before any launch."""
+import contextlib
 import ctypes
 import os
 import subprocess
+import types
 
 import pytest
+import torch
 
 import long_context_sparse_tcgen05_gb300 as dsa
 from long_context_sparse_tcgen05_gb300 import build as dsa_build
@@ -192,3 +195,47 @@ def test_latent_attn_workspace_query(lib):
     size = lambda a, k: lib.dsa_latent_attn_workspace_size(a and ctypes.byref(a), k)  # noqa: E731
     assert size(None, 16) == 256 and size(_attn(H=0), 16) == 256 and size(_attn(), 0) == 256
     assert size(_attn(), 2048) >= 256
+
+
+@pytest.mark.parametrize("device,index", [("cuda:1", 1), ("cuda:0", 0), ("cuda", 0), (None, 0)])
+def test_read_device_flags_reads_the_named_device_on_its_own_stream(monkeypatch, device, index):
+    """Device 0 is current; each device has its workspace, its flag word and its current stream."""
+    current, reads = [0], []
+    words = {(i, kind): FAKE + 4096 * i + 256 * kind for i in (0, 1) for kind in (0, 1)}
+    bits = {words[i, 0]: 1 << i for i in (0, 1)} | {words[i, 1]: 4 << i for i in (0, 1)}
+
+    class Memory:
+        def __init__(self, i, kind):
+            self.device, self._addr = torch.device("cuda", i), words[i, kind]
+
+        def data_ptr(self):
+            return self._addr
+
+    class Library:
+        def dsa_read_device_flags(self, ws, out, stream):
+            addr = ctypes.cast(ws, ctypes.c_void_p).value
+            out._obj.value = bits[addr]
+            reads.append((addr, stream.value, current[0]))
+            return 0
+
+    @contextlib.contextmanager
+    def on(dev):
+        before, current[0] = current[0], dev.index
+        yield
+        current[0] = before
+
+    def stream_of(dev=None):
+        return types.SimpleNamespace(cuda_stream=1000 + (current[0] if dev is None else dev.index))
+
+    def workspace(nbytes=256, device=None):
+        i = None if device is None else torch.device(device).index
+        return Memory(current[0] if i is None else i, 0)
+
+    monkeypatch.setattr(dsa, "load_library", Library)
+    monkeypatch.setattr(dsa, "workspace", workspace)
+    monkeypatch.setattr(dsa, "_flags", {torch.device("cuda", i): Memory(i, 1) for i in (0, 1)})
+    monkeypatch.setattr(torch.cuda, "device", on)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", stream_of)
+    assert dsa.read_device_flags(device) == 5 << index
+    assert sorted(reads) == [(words[index, kind], 1000 + index, index) for kind in (0, 1)]
