@@ -448,8 +448,8 @@ dsa_status dsa_latent_read(const dsa_latent_cache* cache, int32_t B, int32_t n, 
  *   out  [B,T,H,512] bf16 (16-byte aligned); lse [B,T,H] fp32 (natural log) or NULL
  * 1 <= k <= 65536.  A row with no valid entry gets out = 0, lse = -inf.  Scores and the softmax's
  * sums are fp32.  ws: dsa_latent_attn_workspace_size bytes (DSA_WS_MIN: its flag word is all that the
- * call uses, so calls that may overlap can share one).  flags: DEVICE word for DSA_FLAG_* bits, or
- * NULL for the workspace's flag word. */
+ * call uses, so calls that may overlap can share one, and a read of that word then reports the bits
+ * of all of them).  flags: DEVICE word for DSA_FLAG_* bits, or NULL for the workspace's flag word. */
 typedef struct {
   int32_t B, T, S, H;
   float scale;
@@ -463,8 +463,11 @@ dsa_status dsa_latent_attn(const dsa_latent_attn_args* a, const int32_t* idx, in
                            void* ws, size_t ws_bytes, void* stream);
 size_t dsa_latent_attn_workspace_size(const dsa_latent_attn_args* a, int32_t k);
 
-/* Reads the device flag word of a workspace into *flags_out (host) and clears it.
- * Synchronises `stream`. */
+/* Reads the device flag word of a workspace (memory of the current device) into *flags_out (host)
+ * and clears it, once the work before it on `stream` is done; synchronises `stream`.  Reading and
+ * clearing are one step, so a bit that a call on another stream raises meanwhile is in this read or
+ * in the next.  The word does not say which call raised a bit: calls whose flags are to be told
+ * apart need words of their own. */
 dsa_status dsa_read_device_flags(void* ws, uint32_t* flags_out, void* stream);
 
 /* Bound on every wait inside the library's kernels (a wait for a copy, a tensor-core

@@ -254,7 +254,8 @@ _flags = {}
 
 def _flag_word(dev) -> torch.Tensor:
     """The device's flag workspace (WS_MIN zeroed bytes): allocated once and kept, so a captured
-    graph may hold its address."""
+    graph may hold its address.  All its streams share it: a read reports the bits of every call that
+    has ended, whichever stream it ran on."""
     t = _flags.get(dev)
     if t is None:
         if torch.cuda.is_current_stream_capturing():

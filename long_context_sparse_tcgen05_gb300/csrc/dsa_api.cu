@@ -7,6 +7,7 @@
 #include <atomic>
 #include <climits>
 #include <cstring>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -41,6 +42,11 @@ dsa_status cuda_fail(cudaError_t e, const char* what) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
+
+// A flag word's bits, and zero in their place, in one step: kernels on other streams may raise bits
+// meanwhile, and one raised between a copy and a clear would be lost.  One reader at a time.
+__device__ uint32_t g_taken_flags;
+__global__ void k_take_flags(uint32_t* word) { g_taken_flags = atomicExch(word, 0u); }
 
 uint32_t* ws_flags(void* ws) { return reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + dsa::kWsFlags); }
 
@@ -882,8 +888,20 @@ dsa_status indexshare_schedule_search(const double* overlap, int32_t n, int32_t 
 dsa_status dsa_read_device_flags(void* ws, uint32_t* flags_out, void* stream) {
   if (!ws || !flags_out) return fail(DSA_ERR_INVALID_ARG, "ws and flags_out must be non-NULL");
   cudaStream_t st = as_stream(stream);
-  cudaError_t e = cudaMemcpyAsync(flags_out, ws_flags(ws), sizeof(uint32_t), cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(ws_flags(ws), 0, sizeof(uint32_t), st);
+  int dev = 0;
+  cudaPointerAttributes at{};
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaPointerGetAttributes(&at, ws);
+  if (e != cudaSuccess) return cuda_fail(e, "reading device flags");
+  if (at.type == cudaMemoryTypeUnregistered || (at.type == cudaMemoryTypeDevice && at.device != dev))
+    return fail(DSA_ERR_INVALID_ARG, "the workspace is not memory of the current device, %d", dev);
+  // (the work before the read is waited for outside the lock, which then covers a few microseconds)
+  if ((e = cudaStreamSynchronize(st)) != cudaSuccess) return cuda_fail(e, "reading device flags");
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  k_take_flags<<<1, 1, 0, st>>>(ws_flags(ws));
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(flags_out, g_taken_flags, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "reading device flags");
 }

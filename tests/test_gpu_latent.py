@@ -5,6 +5,7 @@ attention over selected rows of it.  Tolerances count roundings: a bf16 result i
 work before it by a few 2^-24 of the largest term (2^-18 covers sums of up to 1,024 terms)."""
 import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -980,3 +981,57 @@ def test_latent_attn_rows_of_the_least_scale_far_above_the_first_block(T):
     q[..., 512] = torch.linspace(30, 110, 64, device=DEV).bfloat16()
     _check_attn(dict(q=q, cache=cache, scale=1.0), _idx(1, T, S, S, holes=False))
     assert dsa.read_device_flags(DEV) == 0
+
+
+# --- flag words ----------------------------------------------------------------------------------
+
+def _read_flags(ws):
+    """The flag word of a workspace, on the calling thread's current stream."""
+    v = ctypes.c_uint32()
+    status = dsa.load_library().dsa_read_device_flags(ctypes.c_void_p(ws.data_ptr()), ctypes.byref(v),
+                                                      ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert status == 0
+    return int(v.value)
+
+
+def test_flags_raised_while_another_stream_reads_are_not_lost():
+    """One thread reads the word without pause while calls with a bad index raise it on a stream of
+    their own: each raised bit is in one of the reads, the reader's or the caller's own."""
+    cache = _cache(1, 20, 16)
+    at = dict(q=_q(1, 1, 1), cache=cache, scale=0.05)
+    idx = torch.tensor([[[5, 40]]], device=DEV, dtype=torch.int32)  # 40: past the 32 rows of the sequence
+    ws = torch.zeros(dsa.WS_MIN, dtype=torch.uint8, device=DEV)
+    dsa.dsa_latent_attn(at, idx, ws=ws)
+    assert _read_flags(ws) == dsa.FLAG_BAD_INDEX and _read_flags(ws) == 0
+    rounds, seen, stop = [0], [0], threading.Event()
+
+    def reader():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            while not stop.is_set():
+                seen[0] += _read_flags(ws) != 0
+                rounds[0] += 1
+
+    t = threading.Thread(target=reader)
+    t.start()
+    lost = 0
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(500):
+                before = seen[0]
+                dsa.dsa_latent_attn(at, idx, ws=ws)
+                own = _read_flags(ws)
+                now = rounds[0]
+                while rounds[0] < now + 2 and t.is_alive():  # a read that was under way has been counted
+                    pass
+                lost += seen[0] == before and not own
+    finally:
+        stop.set()
+        t.join()
+    assert lost == 0 and _read_flags(ws) == 0
+    assert dsa.read_device_flags(DEV) == 0
+
+
+def test_read_device_flags_refuses_host_memory():
+    ws = torch.zeros(dsa.WS_MIN, dtype=torch.uint8)
+    v = ctypes.c_uint32()
+    assert dsa.load_library().dsa_read_device_flags(ctypes.c_void_p(ws.data_ptr()), ctypes.byref(v), None) == 1
