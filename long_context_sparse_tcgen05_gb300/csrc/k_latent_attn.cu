@@ -43,8 +43,9 @@
 // descriptors then stay in uniform registers.  Issued from a lane-0 branch, every product took 60
 // cycles whatever its shape; this way 32 (A in tensor memory) and 48 (A in shared memory: 6 KB of
 // operands at 128 bytes a cycle).
-// With few items each is split into up to 8 parts of at least 128 keys, one to each CTA of a cluster, and
-// the parts are joined over the cluster's shared memory.  Waits are bounded (DSA_FLAG_TIMEOUT).
+// With few items of long index rows each is split into up to 8 parts of about 128 keys or more, one to each
+// CTA of a cluster, and the parts are joined over the cluster's shared memory.
+// Waits are bounded (DSA_FLAG_TIMEOUT).
 //
 // Measured (64 heads, k = 2,048): 4,096 queries over 131,072 rows 0.99 ms, 1,170 TFLOP/s, the tensor pipe
 // 51% busy; 32 single tokens over 200,000 rows 28.8 us; one over 20,000 rows 18.7 us.  What bounds it: a
@@ -1190,6 +1191,19 @@ static auto kernel_of(bool poll, bool parts) {
               : (parts ? k_latent_attn<false, true> : k_latent_attn<false, false>);
 }
 
+// Whether index rows of kk entries are worth n parts: about 128 keys a part (one block at least), and the
+// keys of six blocks less for a CTA to walk, which is what leaving and joining the parts takes.  Unsplit
+// against split as by the first condition alone, us (64 heads; the inputs in L2):
+//   kk           129          192          257          384          448          512          768
+//   1 row        11.5 / 16.7  11.5 / 16.7  13.6 / 16.2  14.6 / 16.3  15.5 / 15.8  16.5 / 15.8  20.7 / 16.0
+//   16 rows      11.7 / 17.3  11.6 / 17.3  13.7 / 16.5  14.6 / 16.5  15.7 / 16.1  16.6 / 16.0  20.9 / 16.7
+//   70 (2 parts) 12.1 / 18.5  12.2 / 18.3  14.3 / 19.5  15.3 / 19.6  16.4 / 20.6  17.3 / 20.6  21.8 / 23.0
+// and 70 rows of 1,024 25.5 / 25.2, of 2,048 43.7 / 35.4.
+static bool splits_pay(int kk, int n) {
+  const int blocks = (kk + kNB - 1) / kNB;
+  return n <= (kk + 127) / 128 && kk - (blocks + n - 1) / n * kNB >= 6 * kNB;
+}
+
 // Once per device: shared memory, that a block is launched with the registers that its warpgroups' moves
 // count on, and the clusters.
 static cudaError_t prepare_kernels(ClusterRoom& room) {
@@ -1231,11 +1245,10 @@ cudaError_t launch_latent_attn(LatentAttnLaunch p, cudaStream_t st) {
   ClusterRoom room{};
   cudaError_t e = prepare_kernels(room);
   if (e != cudaSuccess) return e;
-  // parts of at least 128 keys, in clusters that are all resident at once
   const int64_t rows = (int64_t)p.B * p.T * p.groups;
   p.splits = 1;
-  for (int n = 2; n <= kMaxLatentSplits && n <= (p.kk + 127) / 128; ++n)
-    if (rows <= room.clusters[n]) p.splits = n;
+  for (int n = 2; n <= kMaxLatentSplits; ++n)
+    if (rows <= room.clusters[n] && splits_pay(p.kk, n)) p.splits = n;
   const int64_t items = rows * p.splits;
   const int sms = device_sm_count();
   cudaLaunchAttribute attr{};

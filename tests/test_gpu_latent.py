@@ -983,6 +983,24 @@ def test_latent_attn_rows_of_the_least_scale_far_above_the_first_block(T):
     assert dsa.read_device_flags(DEV) == 0
 
 
+@pytest.mark.parametrize("k", [64, 129, 192, 257, 384, 448, 511])
+def test_latent_attn_short_index_rows_are_not_split(k):
+    """Joining parts takes as long as six blocks of keys: a single row of up to 511 entries is one
+    part, so it comes out bit for bit as it does among many rows."""
+    cache = _cache(1, 3000, 64, seed=k)
+    q, idx = _q(1, 200, 64, seed=k), _idx(1, 200, 3000, k, seed=k)
+    want, wl = dsa.dsa_latent_attn(dict(q=q, cache=cache, scale=1 / 24), idx)
+    got, gl = dsa.dsa_latent_attn(dict(q=q[:, 7:8], cache=cache, scale=1 / 24), idx[:, 7:8].contiguous())
+    assert torch.equal(got, want[:, 7:8]) and torch.equal(gl, wl[:, 7:8])
+
+
+@pytest.mark.parametrize("k", [512, 513, 575, 576, 640, 767, 768, 1025])
+@pytest.mark.parametrize("rows", [1, 30, 70])
+def test_latent_attn_around_the_lengths_that_are_split(k, rows):
+    cache = _cache(1, 1200, 48, seed=k)
+    _check_attn(dict(q=_q(1, rows, 64), cache=cache, scale=1 / 24), _idx(1, rows, 1200, k, seed=rows))
+
+
 # --- flag words ----------------------------------------------------------------------------------
 
 def _read_flags(ws):
