@@ -446,10 +446,15 @@ dsa_status dsa_latent_read(const dsa_latent_cache* cache, int32_t B, int32_t n, 
  *        -1 is skipped; other entries out of range, and positions without a valid page, are
  *        skipped and raise DSA_FLAG_BAD_INDEX.  A position listed twice counts twice.
  *   out  [B,T,H,512] bf16 (16-byte aligned); lse [B,T,H] fp32 (natural log) or NULL
- * 1 <= k <= 65536.  A row with no valid entry gets out = 0, lse = -inf.  Scores and the softmax's
- * sums are fp32.  ws: dsa_latent_attn_workspace_size bytes (DSA_WS_MIN: its flag word is all that the
- * call uses, so calls that may overlap can share one, and a read of that word then reports the bits
- * of all of them).  flags: DEVICE word for DSA_FLAG_* bits, or NULL for the workspace's flag word. */
+ * 1 <= k <= 65536.  A row with no valid entry, or whose every score is -inf, gets out = 0, lse = -inf.
+ * Precision: scores, lse and the softmax's sums are fp32.  Queries are taken exactly down to 2^-21 of
+ * their head's largest value.  In the product with the values an entry's weight times its row's scale
+ * is two e4m3 terms: off by about 2^-8 of itself, or, where it is small, by 2^-18 of the largest of
+ * its 64 neighbours in idx (entries 64 i .. 64 i + 63); what is below 2^-120 of the row's first 64
+ * entries counts as that.  Against exact arithmetic that is what bf16 weights give.
+ * ws: dsa_latent_attn_workspace_size bytes (DSA_WS_MIN: its flag word is all that the call uses, so
+ * calls that may overlap can share one, and a read of that word then reports the bits of all of
+ * them).  flags: DEVICE word for DSA_FLAG_* bits, or NULL for the workspace's flag word. */
 typedef struct {
   int32_t B, T, S, H;
   float scale;

@@ -1001,6 +1001,49 @@ def test_latent_attn_around_the_lengths_that_are_split(k, rows):
     _check_attn(dict(q=_q(1, rows, 64), cache=cache, scale=1 / 24), _idx(1, rows, 1200, k, seed=rows))
 
 
+@pytest.mark.parametrize("T", [1, 40, 200])
+@pytest.mark.parametrize("mul", [1e-3, 0.25])
+def test_latent_attn_flat_rows_norm_wise(T, mul):
+    """Heads that weigh all of 2,048 rows alike: the sum of independent values of either sign is some
+    45 times smaller than the sum of their magnitudes, which bounds no such result.  Rounding the
+    result takes 2^-8 of its norm.  A weight is off by 2^-8 of itself at most; equal weights are off
+    alike, which scales the result, and unequal ones add up like the independent values they weigh:
+    2^-8 of the norm again, a third more for the spread of 512 products' norms.  (Without its second
+    term a weight is off by 2^-4, and a lost row of 2,048 takes 2^-5.5.)"""
+    cache = _cache(1, 4000, 64)
+    at = dict(q=_q(1, T, 64, mul), cache=cache, scale=1 / 24)
+    idx = _idx(1, T, 4000, 2048, holes=False)
+    o, _ = dsa.dsa_latent_attn(at, idx)
+    ref, _, _ = _attn64(at, idx)
+    off = (o.double() - ref).norm(dim=-1)
+    assert bool((off <= (1 + 4 / 3) * BF16_STEP * ref.norm(dim=-1)).all()), f"{float((off / ref.norm(dim=-1)).max()):.3g}"
+
+
+def test_latent_attn_longest_index_row():
+    cache = _cache(1, 70000, 64)
+    _check_attn(dict(q=_q(1, 1, 20), cache=cache, scale=1 / 24), _idx(1, 1, 70000, 65536))
+
+
+@pytest.mark.parametrize("T", [1, 170])
+def test_latent_attn_rows_whose_every_score_is_minus_infinity_are_empty(T):
+    cache = _cache(1, 900, 64)
+    cache["rope"][..., 5] = -math.inf
+    q = _q(1, T, 64)
+    q[..., 517] = q[..., 517].abs() + 0.5
+    o, l = dsa.dsa_latent_attn(dict(q=q, cache=cache, scale=0.05), _idx(1, T, 900, 700))
+    assert bool((o == 0).all()) and bool((l == -math.inf).all())
+
+
+def test_latent_attn_of_very_large_and_very_small_queries():
+    """Powers of two moved from the softmax scale into the queries change nothing."""
+    cache = _cache(2, 600, 64)
+    q, idx = _q(2, 3, 64, 1.0), _idx(2, 3, 600, 300)
+    want, wl = dsa.dsa_latent_attn(dict(q=q, cache=cache, scale=1 / 24), idx)
+    for e in (90, -80):
+        o, l = dsa.dsa_latent_attn(dict(q=(q.float() * 2.0 ** e).bfloat16(), cache=cache, scale=2.0 ** -e / 24), idx)
+        assert torch.equal(o, want) and torch.equal(l, wl)
+
+
 # --- flag words ----------------------------------------------------------------------------------
 
 def _read_flags(ws):
@@ -1046,6 +1089,30 @@ def test_flags_raised_while_another_stream_reads_are_not_lost():
         stop.set()
         t.join()
     assert lost == 0 and _read_flags(ws) == 0
+    assert dsa.read_device_flags(DEV) == 0
+
+
+def test_latent_attn_flags_go_to_the_word_that_the_call_names():
+    """The size query asks for the flag word only; a caller's workspace, or the word that the arguments
+    name, takes the call's flags, and the device's own word stays clean."""
+    cache = _cache(1, 20, 16)
+    at = dict(q=_q(1, 1, 8), cache=cache, scale=0.05)
+    bad = torch.tensor([[[5, 40]]], device=DEV, dtype=torch.int32)  # 40: past the 32 rows of the sequence
+    lib = dsa.load_library()
+    a = dsa.latent_attn_struct(at, bad)
+    assert lib.dsa_latent_attn_workspace_size(ctypes.byref(a), 2) == dsa.WS_MIN
+    ws = torch.zeros(dsa.WS_MIN, dtype=torch.uint8, device=DEV)
+    dsa.dsa_latent_attn(at, bad, ws=ws)
+    assert dsa.read_device_flags(DEV) == 0 and _read_flags(ws) == dsa.FLAG_BAD_INDEX
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = torch.empty((1, 1, 8, 512), dtype=torch.bfloat16, device=DEV)
+    a.flags = word.data_ptr()
+    assert lib.dsa_latent_attn(ctypes.byref(a), bad.data_ptr(), 2, out.data_ptr(), None, ws.data_ptr(), dsa.WS_MIN,
+                               torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert int(word) == dsa.FLAG_BAD_INDEX and _read_flags(ws) == 0
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_latent_attn(at, bad, ws=ws[:-16])
     assert dsa.read_device_flags(DEV) == 0
 
 
