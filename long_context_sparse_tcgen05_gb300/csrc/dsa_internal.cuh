@@ -314,6 +314,7 @@ struct LatentAttnLaunch {
   long long wait;
 };
 constexpr int kMaxLatentSplits = 8;
+constexpr int kLatentAttnRegs = 80;  // a thread's registers, which the kernel's warpgroups share out
 cudaError_t launch_latent_attn(LatentAttnLaunch p, cudaStream_t st);
 
 }  // namespace dsa

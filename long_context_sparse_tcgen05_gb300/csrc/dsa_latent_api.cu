@@ -254,7 +254,11 @@ dsa_status dsa_latent_attn(const dsa_latent_attn_args* a, const int32_t* idx, in
   if ((s = check_ws(ws, ws_bytes)) != DSA_OK) return s;
   L.idx = idx; L.out = static_cast<uint16_t*>(out); L.lse = lse;
   L.flags = a->flags ? a->flags : ws_flags(ws);
-  return done(dsa::launch_latent_attn(L, static_cast<cudaStream_t>(stream)), "attention launch");
+  const cudaError_t e = dsa::launch_latent_attn(L, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidKernelImage)  // (returned by the launcher's own look at the kernels, too)
+    return fail(DSA_ERR_CUDA, "attention launch: the kernel is not built for this device, or not with the %d registers a "
+                "thread that its warpgroups share out (build it with the package's own build step)", dsa::kLatentAttnRegs);
+  return done(e, "attention launch");
 }
 
 }  // extern "C"

@@ -84,7 +84,7 @@ constexpr int kRing = 6;                     // blocks the index warps may be ah
 constexpr int kThreads = 24 * 32;
 // Registers by warpgroup (warps 0-3, 4-7, ..), moved at the start from the kernel's own kRegs each;
 // the softmax warps spilled in their block loop at kRegs.
-constexpr int kRegs = 80, kRegsGather = 56, kRegsIssue = 64, kRegsSm = 104, kRegsEpi = 72;
+constexpr int kRegs = kLatentAttnRegs, kRegsGather = 56, kRegsIssue = 64, kRegsSm = 104, kRegsEpi = 72;
 static_assert(kRegsGather + kRegsIssue + 2 * kRegsSm + 2 * kRegsEpi <= 6 * kRegs, "registers the block is launched with");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColSfA = 416, kColSfB = 424, kColS = 448;
