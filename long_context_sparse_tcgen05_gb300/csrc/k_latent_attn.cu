@@ -205,6 +205,10 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+// Before the asynchronous proxy (a product, a bulk copy) reads what threads wrote to shared memory.  The order
+// of the write before the read wants one proxy fence anywhere between them, so the reading thread makes it,
+// after the barrier that the writers arrived at: one a block instead of one in each writing warp (with a
+// second load of O in flight, 1.02 -> 0.99 ms a 4,096-query chunk).
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 // mbar_wait in few instructions: 24 warps of seven kinds run at a time, and their loops compete for
 // the instruction caches.  The abort word and the bound are read at each wake.

@@ -2,9 +2,10 @@
 // the block table in one pass) and reading rows back.  A warp takes a token: 16 latent values per
 // lane (two 16-byte loads) and one rotated pair, so the sum of squares and the largest magnitude
 // are warp shuffles.  HBM-bound: 1,152 bytes in and 644 out per appended token (the other way
-// round to read), plus a 256-byte table row.  Measured: 131,072 tokens appended in 55.7 us (4.8 TB/s;
-// 74% of the issue slots) and read back in 40.7 us (5.8 TB/s); 32 x 2,048 selected rows read in 22.8 us
-// (5.2 TB/s); one token each of 32 sequences appended in 3.5 us.
+// round to read), plus a 256-byte table row.  Measured: 131,072 tokens appended in 55.6 us (4.9 TB/s;
+// 75% of the issue slots, 370 instructions a token, 27 of them quotients) and read back in 41.2 us
+// (5.7 TB/s); 32 x 2,048 selected rows read in 22.6 us (5.2 TB/s); one token each of 32 sequences appended
+// in 3.5 us.
 #include <algorithm>
 
 #include "dsa_internal.cuh"
@@ -21,7 +22,8 @@ constexpr float kMinScale = 0x1p-60f;  // rope / scale stays finite in bf16 for 
 // the warp's part of shared memory, its angles and block table entry in registers (its position one
 // token earlier still).  Loaded when its turn came, a token took a warp three dependent loads.
 // kTurn: with rotation tables.  (Without them the rope values stay as they are: an angle of zero, 1 and 0,
-// would spread an infinity or NaN over its pair.  Chosen inside the kernel it cost 59.5, not 58.2 us.)
+// would spread an infinity or NaN over its pair.  Chosen inside the kernel, a call of 131,072 rows took 59.5,
+// not 57.2 us.)
 template <bool kTurn>
 __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p) {
   constexpr int kRow = kLatentDim + kLatentRope;

@@ -7,8 +7,8 @@
 // wide), or are read a second time and normed with the same statistics (wider heads).
 // x is read once and the result written once; the tables and weights are read from L1, once per lane
 // for all the heads of a token.  Measured (device time, inputs of 3 calls past L2):
-//   16,384 tokens x 64 x 128 to e4m3, half-split rotation   101 us, 4.0 TB/s: issue (60% of the slots, 144
-//       instructions for a lane's 8 values) and, at 24 warps an SM, the loads' latency; 260 us before
+//   16,384 tokens x 64 x 128 to e4m3, half-split rotation   101 us, 4.0 TB/s: issue (61% of the slots, 141
+//       instructions for a lane's 8 values, 12 of them quotients) and, at 24 warps an SM, the loads' latency; 260 us before
 //       the next token's values were copied ahead and two values went into an instruction
 //   8,192 tokens x 64 x 64 to bf16 among 576-wide rows      25.6 us, 5.3 TB/s (53% of the issue slots)
 //   6,455 tokens x 20 x 96, RMS norm                        19.3 us, 2.6 TB/s: issue (68%); heads of 96
