@@ -468,6 +468,71 @@ dsa_status dsa_latent_attn(const dsa_latent_attn_args* a, const int32_t* idx, in
                            void* ws, size_t ws_bytes, void* stream);
 size_t dsa_latent_attn_workspace_size(const dsa_latent_attn_args* a, int32_t k);
 
+/* Attention over every row that a query sees of the paged FP8 cache, for layers without an indexer and for
+ * contexts that a selection would not shorten.  As dsa_latent_attn, with instead of index rows
+ *   lens    DEVICE int32 [B]: rows that each sequence holds, 0 <= lens[b] <= S (a value outside counts as the
+ *           nearer end and raises DSA_FLAG_BAD_INDEX); rows behind them are not read
+ *   causal  != 0: the T queries are the sequence's last T rows and query t sees positions
+ *           [0, lens[b] - T + 1 + t): itself and what precedes it; 0: every query sees [0, lens[b])
+ * A query that sees nothing gets out = 0, lse = -inf; positions without a valid page are skipped and raise
+ * DSA_FLAG_BAD_INDEX.  The args' idx_T is not read.  Precision as dsa_latent_attn (the 64 neighbours: positions
+ * 64 i .. 64 i + 63).  The rows of all queries are divided evenly over the SMs, whatever the lengths, and
+ * partial results are joined in a fixed order: results do not vary from run to run on one kind of device.
+ * ws: dsa_latent_attn_dense_workspace_size bytes (of the current device): the flag word, and scratch that calls
+ * which may overlap must not share. */
+dsa_status dsa_latent_attn_dense(const dsa_latent_attn_args* a, const int32_t* lens, int32_t causal, void* out, float* lse,
+                                 void* ws, size_t ws_bytes, void* stream);
+size_t dsa_latent_attn_dense_workspace_size(int32_t B, int32_t T, int32_t S, int32_t H);
+
+/* Paged 4-bit cache of latent KV rows: 404 bytes a row where the FP8 cache has 644.  A stored row stands for
+ * scale * [code_i * 2^(groups[i / 32] - 127), i < 512 | rope (64 bf16)].
+ *   codes   [n_pages, page_size, 256] (16-byte aligned): e2m1 codes (OCP MX FP4: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a
+ *           sign), two a byte, value 2 i in the low half of byte i
+ *   groups  [n_pages, page_size, 16]: a power of two for 32 values, as exponent + 127; where rows are used 122 to
+ *           133 (2^-5 to 2^6), as dsa_latent4_append writes them, so that code * 2^(group - 127) is an e4m3 value
+ *   scales, rope, block_table, page_size: as dsa_latent_cache */
+typedef struct {
+  int32_t n_pages, page_size, table_ld;
+  uint8_t* codes;
+  uint8_t* groups;
+  float* scales;
+  void* rope;
+  const int32_t* block_table;
+} dsa_latent4_cache;
+
+/* dsa_latent_append into the 4-bit cache (same args): with y the 512 normed values (fp32, IEEE division),
+ * scale = max(amax / 384, 2^-60), z = y / scale; a group's exponent is the least e in [-5, 6] with
+ * 6 * 2^e >= max |z| of its 32 values; codes = e2m1(z / 2^e), nearest, ties to even, at most 6;
+ * rope = bf16(rotated / scale).  A row with a NaN or an infinity among the 512 gets a NaN scale (e2m1 has neither). */
+dsa_status dsa_latent4_append(const dsa_latent_append_args* a, const dsa_latent4_cache* cache, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* dsa_latent_read of the 4-bit cache. */
+dsa_status dsa_latent4_read(const dsa_latent4_cache* cache, int32_t B, int32_t n, const int32_t* idx, int64_t pos0,
+                            void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* The same rows in the FP8 cache's form, exactly: codes [B,n,512] e4m3 (code * 2^(group - 127)), scales [B,n] and rope
+ * [B,n,64] as stored, dense, codes and rope 16-byte aligned -- B contiguous sequences of a dsa_latent_cache whose
+ * page_size is n.  A position without a row gives zeros under scale 1 (and DSA_FLAG_BAD_INDEX unless it is -1). */
+dsa_status dsa_latent4_unpack(const dsa_latent4_cache* cache, int32_t B, int32_t n, const int32_t* idx, int64_t pos0,
+                              uint8_t* codes, float* scales, void* rope, void* ws, size_t ws_bytes, void* stream);
+
+/* dsa_latent_attn and dsa_latent_attn_dense over the 4-bit cache (workspaces as theirs): the tensor cores read the e4m3
+ * values that the codes stand for, so results are those of dsa_latent_attn over the unpacked rows. */
+typedef struct {
+  int32_t B, T, S, H;
+  float scale;
+  const void* q;
+  int64_t q_stride_b, q_stride_t;
+  dsa_latent4_cache cache;
+  int32_t idx_T;
+  uint32_t* flags;
+} dsa_latent4_attn_args;
+dsa_status dsa_latent4_attn(const dsa_latent4_attn_args* a, const int32_t* idx, int32_t k, void* out, float* lse, void* ws,
+                            size_t ws_bytes, void* stream);
+dsa_status dsa_latent4_attn_dense(const dsa_latent4_attn_args* a, const int32_t* lens, int32_t causal, void* out, float* lse,
+                                  void* ws, size_t ws_bytes, void* stream);
+
 /* Reads the device flag word of a workspace (memory of the current device) into *flags_out (host)
  * and clears it, once the work before it on `stream` is done; synchronises `stream`.  Reading and
  * clearing are one step, so a bit that a call on another stream raises meanwhile is in this read or

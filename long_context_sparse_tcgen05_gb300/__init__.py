@@ -23,9 +23,13 @@ Calls (same names as the C ABI):
   dsa_latent_append(x, cache, ...)        -> norm + rotation + quantisation into a paged FP8 cache
   dsa_latent_read(cache, idx | n, pos0)   -> bf16 rows [B,n,576] of that cache
   dsa_latent_attn(at, idx)                -> (out [B,T,H,512] bf16, lse): sparse attention over it
+  dsa_latent_attn_dense(at, lens)         -> the same over every row that a query sees
+  dsa_latent4_append, dsa_latent4_read, dsa_latent4_attn, dsa_latent4_attn_dense: the same calls on
+                                             a 4-bit cache
+  dsa_latent4_unpack(cache, idx | n, pos0) -> its rows as a contiguous FP8 cache
 A latent cache is a dict: codes [pages, page, 512] float8_e4m3fn or uint8, scales [pages, page]
 fp32, rope [pages, page, 64] bf16 and block_table [B, pages per sequence] int32 (None: sequence b
-is page b).
+is page b).  A 4-bit one has codes [pages, page, 256] uint8 and groups [pages, page, 16] uint8.
 Operand dicts use the keys produced by ``synth``: an indexer dict holds q, w, k, q_scale,
 k_scale, q_pos0, diag; an attention dict holds q, k, v (None: latent KV), d_v, scale.
 """
@@ -100,6 +104,17 @@ class LatentAppendArgs(_c.Structure):
 class LatentAttnArgs(_c.Structure):
     _fields_ = [("B", _c.c_int32), ("T", _c.c_int32), ("S", _c.c_int32), ("H", _c.c_int32), ("scale", _c.c_float),
                 ("q", _P), ("q_stride_b", _c.c_int64), ("q_stride_t", _c.c_int64), ("cache", LatentCache),
+                ("idx_T", _c.c_int32), ("flags", _P)]
+
+
+class Latent4Cache(_c.Structure):
+    _fields_ = [("n_pages", _c.c_int32), ("page_size", _c.c_int32), ("table_ld", _c.c_int32), ("codes", _P),
+                ("groups", _P), ("scales", _P), ("rope", _P), ("block_table", _P)]
+
+
+class Latent4AttnArgs(_c.Structure):
+    _fields_ = [("B", _c.c_int32), ("T", _c.c_int32), ("S", _c.c_int32), ("H", _c.c_int32), ("scale", _c.c_float),
+                ("q", _P), ("q_stride_b", _c.c_int64), ("q_stride_t", _c.c_int64), ("cache", Latent4Cache),
                 ("idx_T", _c.c_int32), ("flags", _P)]
 
 
@@ -192,6 +207,22 @@ def load_library(path: str = LIB_PATH):
             lib.dsa_latent_attn.argtypes = [_c.POINTER(LatentAttnArgs), _P, _c.c_int32, _P, _P, _P, _c.c_size_t, _P]
             lib.dsa_latent_attn_workspace_size.restype = _c.c_size_t
             lib.dsa_latent_attn_workspace_size.argtypes = [_c.POINTER(LatentAttnArgs), _c.c_int32]
+            lib.dsa_latent_attn_dense.restype = S
+            lib.dsa_latent_attn_dense.argtypes = [_c.POINTER(LatentAttnArgs), _P, _c.c_int32, _P, _P, _P, _c.c_size_t, _P]
+            lib.dsa_latent_attn_dense_workspace_size.restype = _c.c_size_t
+            lib.dsa_latent_attn_dense_workspace_size.argtypes = [_c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32]
+            lib.dsa_latent4_append.restype = S
+            lib.dsa_latent4_append.argtypes = [_c.POINTER(LatentAppendArgs), _c.POINTER(Latent4Cache), _P, _c.c_size_t, _P]
+            lib.dsa_latent4_read.restype = S
+            lib.dsa_latent4_read.argtypes = [_c.POINTER(Latent4Cache), _c.c_int32, _c.c_int32, _P, _c.c_int64, _P, _P,
+                                             _c.c_size_t, _P]
+            lib.dsa_latent4_unpack.restype = S
+            lib.dsa_latent4_unpack.argtypes = [_c.POINTER(Latent4Cache), _c.c_int32, _c.c_int32, _P, _c.c_int64, _P, _P,
+                                               _P, _P, _c.c_size_t, _P]
+            lib.dsa_latent4_attn.restype = S
+            lib.dsa_latent4_attn.argtypes = [_c.POINTER(Latent4AttnArgs), _P, _c.c_int32, _P, _P, _P, _c.c_size_t, _P]
+            lib.dsa_latent4_attn_dense.restype = S
+            lib.dsa_latent4_attn_dense.argtypes = [_c.POINTER(Latent4AttnArgs), _P, _c.c_int32, _P, _P, _P, _c.c_size_t, _P]
             lib.dsa_read_device_flags.restype = S
             lib.dsa_read_device_flags.argtypes = [_P, _c.POINTER(_c.c_uint32), _P]
             lib.dsa_status_string.restype = _c.c_char_p
@@ -656,18 +687,50 @@ def dsa_norm_rope_e4m3(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
     return codes, scales
 
 
-def latent_cache_struct(cache: dict, B: int | None = None):
-    """(C struct, sequences) of a latent cache dict."""
+def _cache_parts(cache, B):
+    """(pages, page size, table entries a sequence, addresses of scales, rope and table, sequences) of a cache dict."""
     codes, scales, rope, table = cache["codes"], cache["scales"], cache["rope"], cache.get("block_table")
     dev = codes.device
     pages, page = scales.shape
-    assert codes.is_cuda and codes.dtype in (torch.float8_e4m3fn, torch.uint8) and codes.is_contiguous()
-    assert codes.shape == (pages, page, 512) and rope.shape == (pages, page, 64)
+    assert codes.is_cuda and codes.is_contiguous() and codes.shape[:2] == scales.shape and rope.shape == (pages, page, 64)
     seqs = pages if table is None else table.shape[0]
     assert B is None or (B <= seqs if table is None else B == seqs), "the cache's sequences and the call's differ"
-    return LatentCache(pages, page, 0 if table is None else table.shape[1], codes.data_ptr(),
-                       _addr(scales, dev, torch.float32, "scales"), _addr(rope, dev, torch.bfloat16, "rope"),
-                       _addr(table, dev, torch.int32, "block_table")), seqs
+    return (pages, page, 0 if table is None else table.shape[1], _addr(scales, dev, torch.float32, "scales"),
+            _addr(rope, dev, torch.bfloat16, "rope"), _addr(table, dev, torch.int32, "block_table"), seqs)
+
+
+def latent_cache_struct(cache: dict, B: int | None = None):
+    """(C struct, sequences) of a latent cache dict."""
+    codes = cache["codes"]
+    assert codes.dtype in (torch.float8_e4m3fn, torch.uint8) and codes.shape[2] == 512, "codes: [pages, page, 512] e4m3"
+    pages, page, ld, scales, rope, table, seqs = _cache_parts(cache, B)
+    return LatentCache(pages, page, ld, codes.data_ptr(), scales, rope, table), seqs
+
+
+def latent4_cache_struct(cache: dict, B: int | None = None):
+    """(C struct, sequences) of a 4-bit latent cache dict."""
+    codes, groups = cache["codes"], cache["groups"]
+    assert codes.dtype == torch.uint8 and codes.shape[2] == 256, "codes: [pages, page, 256] uint8, two codes a byte"
+    pages, page, ld, scales, rope, table, seqs = _cache_parts(cache, B)
+    assert groups.shape == (pages, page, 16)
+    return Latent4Cache(pages, page, ld, codes.data_ptr(), _addr(groups, codes.device, torch.uint8, "groups"), scales, rope,
+                        table), seqs
+
+
+def _append_rows(struct, call, x, cache, weight, eps, cos, sin, interleaved, pos0, positions):
+    dev = x.device
+    assert x.is_cuda and x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[2] == 576 and x.stride(2) == 1
+    B, n = x.shape[:2]
+    lc, _ = struct(cache, B)
+    assert cache["codes"].device == dev
+    c, s, rows, angles = _tables(cos, sin, dev)
+    assert c is None or angles == 32, "cos and sin: 32 angles for the 64 rope values"
+    a = LatentAppendArgs(B, n, x.data_ptr(), *_token_strides(x), _addr(weight, dev, torch.float32, "weight", 512),
+                         eps, c, s, interleaved, rows, _addr(positions, dev, torch.int64, "positions", B * n), pos0)
+    if n:
+        ws = _flag_word(dev)
+        _launch(dev, getattr(load_library(), call), _c.byref(a), _c.byref(lc), ws.data_ptr(), WS_MIN)
+    return cache
 
 
 def dsa_latent_append(x: torch.Tensor, cache: dict, *, weight: torch.Tensor | None = None, eps: float = 1e-6,
@@ -676,59 +739,121 @@ def dsa_latent_append(x: torch.Tensor, cache: dict, *, weight: torch.Tensor | No
     """Append x [B,n,576] bf16 to the paged FP8 cache: RMS norm of the 512 latent values (weight
     [512] fp32; None: taken as they are), rotation of the 64 others (cos / sin [max_pos, 32]; None:
     not rotated), e4m3 with one scale per row.  positions: int64 [B,n] (-1: padding), or pos0 + i."""
-    dev = x.device
-    assert x.is_cuda and x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[2] == 576 and x.stride(2) == 1
-    B, n = x.shape[:2]
-    lc, _ = latent_cache_struct(cache, B)
-    assert cache["codes"].device == dev
-    c, s, rows, angles = _tables(cos, sin, dev)
-    assert c is None or angles == 32, "cos and sin: 32 angles for the 64 rope values"
-    a = LatentAppendArgs(B, n, x.data_ptr(), *_token_strides(x), _addr(weight, dev, torch.float32, "weight", 512),
-                         eps, c, s, interleaved, rows, _addr(positions, dev, torch.int64, "positions", B * n), pos0)
-    if n:
-        ws = _flag_word(dev)
-        _launch(dev, load_library().dsa_latent_append, _c.byref(a), _c.byref(lc), ws.data_ptr(), WS_MIN)
-    return cache
+    return _append_rows(latent_cache_struct, "dsa_latent_append", x, cache, weight, eps, cos, sin, interleaved, pos0, positions)
 
 
-def dsa_latent_read(cache: dict, idx: torch.Tensor | None = None, *, n: int | None = None, pos0: int = 0,
-                    out: torch.Tensor | None = None) -> torch.Tensor:
-    """Rows of the paged FP8 cache as bf16 [B,n,576]: positions idx [B,n] int32 (-1: zeros), or
-    pos0 .. pos0 + n - 1 of every sequence."""
-    dev = cache["codes"].device
-    lc, B = latent_cache_struct(cache)
+def dsa_latent4_append(x: torch.Tensor, cache: dict, *, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                       cos: torch.Tensor | None = None, sin: torch.Tensor | None = None, interleaved: bool = False,
+                       pos0: int = 0, positions: torch.Tensor | None = None) -> dict:
+    """dsa_latent_append into a 4-bit cache: e2m1 codes under a power of two for 32 values and a scale per row."""
+    return _append_rows(latent4_cache_struct, "dsa_latent4_append", x, cache, weight, eps, cos, sin, interleaved, pos0, positions)
+
+
+def _read_args(struct, cache, idx, n):
+    """(C struct, sequences, rows of each, address of idx) of a read."""
+    lc, B = struct(cache)
     assert (idx is None) != (n is None), "either idx or n"
-    ip = None
-    if idx is not None:
-        assert idx.dim() == 2 and idx.shape[0] <= B and (cache.get("block_table") is None or idx.shape[0] == B)
-        B, n = idx.shape
-        ip = _addr(idx, dev, torch.int32, "idx")
+    if idx is None:
+        return lc, B, n, None
+    assert idx.dim() == 2 and idx.shape[0] <= B and (cache.get("block_table") is None or idx.shape[0] == B)
+    return lc, idx.shape[0], idx.shape[1], _addr(idx, cache["codes"].device, torch.int32, "idx")
+
+
+def _read_rows(struct, call, cache, idx, n, pos0, out):
+    dev = cache["codes"].device
+    lc, B, n, ip = _read_args(struct, cache, idx, n)
     if out is None:
         out = torch.empty((B, n, 576), dtype=torch.bfloat16, device=dev)
     assert out.shape == (B, n, 576)
     op = _addr(out, dev, torch.bfloat16, "out")
     if n:
         ws = _flag_word(dev)
-        _launch(dev, load_library().dsa_latent_read, _c.byref(lc), B, n, ip, pos0, op, ws.data_ptr(), WS_MIN)
+        _launch(dev, getattr(load_library(), call), _c.byref(lc), B, n, ip, pos0, op, ws.data_ptr(), WS_MIN)
     return out
+
+
+def dsa_latent_read(cache: dict, idx: torch.Tensor | None = None, *, n: int | None = None, pos0: int = 0,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows of the paged FP8 cache as bf16 [B,n,576]: positions idx [B,n] int32 (-1: zeros), or
+    pos0 .. pos0 + n - 1 of every sequence."""
+    return _read_rows(latent_cache_struct, "dsa_latent_read", cache, idx, n, pos0, out)
+
+
+def dsa_latent4_read(cache: dict, idx: torch.Tensor | None = None, *, n: int | None = None, pos0: int = 0,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """dsa_latent_read of a 4-bit cache."""
+    return _read_rows(latent4_cache_struct, "dsa_latent4_read", cache, idx, n, pos0, out)
+
+
+def dsa_latent4_unpack(cache: dict, idx: torch.Tensor | None = None, *, n: int | None = None, pos0: int = 0) -> dict:
+    """The rows that dsa_latent4_read reads as a contiguous FP8 cache of as many sequences: codes [B,n,512]
+    float8_e4m3fn, scales [B,n], rope [B,n,64], without a block table; no value changes."""
+    dev = cache["codes"].device
+    lc, B, n, ip = _read_args(latent4_cache_struct, cache, idx, n)
+    out = dict(codes=torch.empty((B, n, 512), dtype=torch.float8_e4m3fn, device=dev),
+               scales=torch.empty((B, n), dtype=torch.float32, device=dev),
+               rope=torch.empty((B, n, 64), dtype=torch.bfloat16, device=dev), block_table=None)
+    if n:
+        ws = _flag_word(dev)
+        _launch(dev, load_library().dsa_latent4_unpack, _c.byref(lc), B, n, ip, pos0, out["codes"].data_ptr(),
+                out["scales"].data_ptr(), out["rope"].data_ptr(), ws.data_ptr(), WS_MIN)
+    return out
+
+
+def _latent_attn_args(args, cache_struct, at, idx_T):
+    """The C struct `args` of an attention operand dict over the kind of cache that `cache_struct` takes."""
+    q, cache = at["q"], at["cache"]
+    B, T, H, d = q.shape
+    assert q.is_cuda and q.dtype == torch.bfloat16 and d == 576 and q.stride(3) == 1
+    assert H == 1 or q.stride(2) == 576, "the heads of one query must be contiguous"
+    lc, _ = cache_struct(cache, B)
+    assert cache["codes"].device == q.device
+    S = at.get("S")
+    if S is None:
+        S = min((lc.table_ld if lc.block_table else 1) * lc.page_size, 2 ** 31 - 1)
+    assert 0 < S < 2 ** 31, "S: between 1 and 2^31 - 1 positions"
+    return args(B, T, int(S), H, at["scale"], q.data_ptr(), *_token_strides(q), lc, idx_T, None)
 
 
 def latent_attn_struct(at: dict, idx: torch.Tensor) -> LatentAttnArgs:
     """The C struct of a latent attention operand dict: q [B,T,H,576] bf16 (strided along its batch
     and token axes), cache, scale and S (the positions idx may name; None: all a sequence holds)."""
-    q, cache = at["q"], at["cache"]
-    B, T, H, d = q.shape
-    dev = q.device
-    assert q.is_cuda and q.dtype == torch.bfloat16 and d == 576 and q.stride(3) == 1
-    assert H == 1 or q.stride(2) == 576, "the heads of one query must be contiguous"
-    lc, _ = latent_cache_struct(cache, B)
-    assert cache["codes"].device == dev
+    _check_idx(at, idx)
+    return _latent_attn_args(LatentAttnArgs, latent_cache_struct, at, idx.shape[1])
+
+
+def latent4_attn_struct(at: dict, idx: torch.Tensor) -> Latent4AttnArgs:
+    """latent_attn_struct of a 4-bit cache."""
+    _check_idx(at, idx)
+    return _latent_attn_args(Latent4AttnArgs, latent4_cache_struct, at, idx.shape[1])
+
+
+def _check_idx(at, idx):
+    B, T = at["q"].shape[:2]
     assert idx.dim() == 3 and idx.shape[0] == B and idx.shape[1] in (1, T), "idx: [B, T or 1, k]"
-    S = at.get("S")
-    if S is None:
-        S = min((lc.table_ld if lc.block_table else 1) * lc.page_size, 2 ** 31 - 1)
-    assert 0 < S < 2 ** 31, "S: between 1 and 2^31 - 1 positions"
-    return LatentAttnArgs(B, T, int(S), H, at["scale"], q.data_ptr(), *_token_strides(q), lc, idx.shape[1], None)
+
+
+def _attn_outputs(a, dev, out, lse):
+    """(out, its address, lse, its address) of an attention call, allocated where asked for."""
+    if out is None:
+        out = torch.empty((a.B, a.T, a.H, 512), dtype=torch.bfloat16, device=dev)
+    assert out.shape == (a.B, a.T, a.H, 512)
+    if lse is True:
+        lse = torch.empty((a.B, a.T, a.H), dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    return out, _addr(out, dev, torch.bfloat16, "out"), lse, _addr(lse, dev, torch.float32, "lse", a.B * a.T * a.H)
+
+
+def _attn_rows(a, call, at, idx, out, lse, ws):
+    dev = at["q"].device
+    ip = _addr(idx, dev, torch.int32, "idx")
+    out, op, lse, lp = _attn_outputs(a, dev, out, lse)
+    if ws is None:
+        ws = _flag_word(dev)
+    assert ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous()
+    _launch(dev, getattr(load_library(), call), _c.byref(a), ip, idx.shape[2], op, lp, ws.data_ptr(), ws.numel())
+    return out, lse
 
 
 def dsa_latent_attn(at: dict, idx: torch.Tensor, out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = True,
@@ -736,25 +861,55 @@ def dsa_latent_attn(at: dict, idx: torch.Tensor, out: torch.Tensor | None = None
     """Sparse attention over the rows idx [B,T,k] (or [B,1,k], shared by a sequence's T queries) of
     a paged FP8 latent cache: (out [B,T,H,512] bf16, lse [B,T,H] fp32 or None).  `ws`: a workspace
     whose flag word to use (uint8, zero-filled once) instead of the device's."""
-    lib = load_library()
-    a = latent_attn_struct(at, idx)
-    dev = at["q"].device
-    ip = _addr(idx, dev, torch.int32, "idx")
-    k = idx.shape[2]
-    if out is None:
-        out = torch.empty((a.B, a.T, a.H, 512), dtype=torch.bfloat16, device=dev)
-    assert out.shape == (a.B, a.T, a.H, 512)
-    op = _addr(out, dev, torch.bfloat16, "out")
-    if lse is True:
-        lse = torch.empty((a.B, a.T, a.H), dtype=torch.float32, device=dev)
-    elif lse is False:
-        lse = None
-    lp = _addr(lse, dev, torch.float32, "lse", a.B * a.T * a.H)
+    return _attn_rows(latent_attn_struct(at, idx), "dsa_latent_attn", at, idx, out, lse, ws)
+
+
+def dsa_latent4_attn(at: dict, idx: torch.Tensor, out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = True,
+                     ws: torch.Tensor | None = None):
+    """dsa_latent_attn over a 4-bit cache."""
+    return _attn_rows(latent4_attn_struct(at, idx), "dsa_latent4_attn", at, idx, out, lse, ws)
+
+
+def latent_dense_workspace_size(B: int, T: int, S: int, H: int) -> int:
+    """Workspace bytes of a dense attention call on the current device."""
+    return int(load_library().dsa_latent_attn_dense_workspace_size(B, T, S, H))
+
+
+def _attn_dense(a, call, at, lens, causal, out, lse, ws):
+    lib, dev = load_library(), at["q"].device
+    lp = _addr(lens, dev, torch.int32, "lens", a.B)
+    assert lp is not None, "lens: the rows that each sequence holds, int32 [B]"
+    out, op, lse, lse_p = _attn_outputs(a, dev, out, lse)
     if ws is None:
-        ws = _flag_word(dev)
+        # scratch of this call alone (a captured graph keeps its own); the device's flag word
+        a.flags = _flag_word(dev).data_ptr()
+        if dev.index == torch.cuda.current_device():
+            need = lib.dsa_latent_attn_dense_workspace_size(a.B, a.T, a.S, a.H)
+        else:
+            with torch.cuda.device(dev):
+                need = lib.dsa_latent_attn_dense_workspace_size(a.B, a.T, a.S, a.H)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
     assert ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous()
-    _launch(dev, lib.dsa_latent_attn, _c.byref(a), ip, k, op, lp, ws.data_ptr(), ws.numel())
+    _launch(dev, getattr(lib, call), _c.byref(a), lp, bool(causal), op, lse_p, ws.data_ptr(), ws.numel())
     return out, lse
+
+
+def dsa_latent_attn_dense(at: dict, lens: torch.Tensor, *, causal: bool = True, out: torch.Tensor | None = None,
+                          lse: torch.Tensor | bool | None = True, ws: torch.Tensor | None = None):
+    """Attention over every row that a query sees of a paged FP8 latent cache: (out [B,T,H,512] bf16, lse
+    [B,T,H] fp32 or None).  lens: int32 [B], the rows that each sequence holds.  causal: the T queries are its last T
+    rows, each seeing itself and what precedes it; else all see all.  at: as for dsa_latent_attn (S: no sequence
+    holds more).  `ws`: a workspace of latent_dense_workspace_size bytes (uint8, zero-filled once) to use, with its flag
+    word, instead of scratch of this call's own and the device's flag word."""
+    return _attn_dense(_latent_attn_args(LatentAttnArgs, latent_cache_struct, at, 1), "dsa_latent_attn_dense", at, lens,
+                       causal, out, lse, ws)
+
+
+def dsa_latent4_attn_dense(at: dict, lens: torch.Tensor, *, causal: bool = True, out: torch.Tensor | None = None,
+                           lse: torch.Tensor | bool | None = True, ws: torch.Tensor | None = None):
+    """dsa_latent_attn_dense over a 4-bit cache."""
+    return _attn_dense(_latent_attn_args(Latent4AttnArgs, latent4_cache_struct, at, 1), "dsa_latent4_attn_dense", at, lens,
+                       causal, out, lse, ws)
 
 
 def set_wait_limit(cycles: int) -> None:
@@ -826,7 +981,9 @@ __all__ = [
     "topk_overlap_matrix", "indexshare_schedule_score", "indexshare_schedule_search",
     "dsa_quantize_e4m3_append", "indexshare_group_forward_varlen", "Varlen",
     "dsa_norm_rope", "dsa_norm_rope_e4m3", "dsa_latent_append", "dsa_latent_read", "dsa_latent_attn",
-    "NormRopeArgs", "LatentCache", "LatentAppendArgs", "LatentAttnArgs",
+    "dsa_latent_attn_dense", "dsa_latent4_append", "dsa_latent4_read", "dsa_latent4_unpack", "dsa_latent4_attn",
+    "dsa_latent4_attn_dense", "latent_dense_workspace_size",
+    "NormRopeArgs", "LatentCache", "LatentAppendArgs", "LatentAttnArgs", "Latent4Cache", "Latent4AttnArgs",
     "read_device_flags", "workspace", "workspace_size", "topk_workspace_size", "attn_workspace_size",
     "set_wait_limit", "load_library", "DsaError",
     "IndexerArgs", "AttnArgs", "TopkSrc", "Layer",

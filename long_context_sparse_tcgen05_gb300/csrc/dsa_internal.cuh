@@ -259,9 +259,10 @@ int norm_rope_units(int d);  // padded 8-value units of one head
 cudaError_t launch_norm_rope(const NormRopeLaunch& p, cudaStream_t st);
 
 // Paged FP8 latent cache (dsa_latent_cache), checked and with its capacity per sequence.
-constexpr int kLatentDim = 512, kLatentRope = 64;
+constexpr int kLatentDim = 512, kLatentRope = 64, kLatentGroups = kLatentDim / 32;  // groups: of the 4-bit cache
 struct LatentCacheView {
   uint8_t* codes;
+  uint8_t* groups;  // of the 4-bit cache, whose codes are e2m1, two a byte; NULL: e4m3
   float* scales;
   uint16_t* rope;
   const int32_t* table;
@@ -292,6 +293,9 @@ struct LatentReadLaunch {
   int64_t pos0;
   LatentCacheView cache;
   uint16_t* out;
+  uint8_t* out_codes;  // of a row unpacked to FP8: codes, scale, rope values (then `out` is NULL)
+  float* out_scales;
+  uint16_t* out_rope;
   uint32_t* flags;
 };
 cudaError_t launch_latent_read(const LatentReadLaunch& p, cudaStream_t st);
@@ -312,9 +316,19 @@ struct LatentAttnLaunch {
   // group), and the CTAs of a cluster hold a row's parts
   int groups, splits;
   long long wait;
+  // of a call over all rows: rows that each sequence holds, whether a token sees only what lies before the
+  // ones after it, tokens of a tile, tiles of a sequence and head group, the runs and the room of parts
+  const int32_t* lens;
+  int causal, tile_t, tiles_t;
+  int4* shares;
+  float* parts;
 };
 constexpr int kMaxLatentSplits = 8;
 constexpr int kLatentAttnRegs = 80;  // a thread's registers, which the kernel's warpgroups share out
-cudaError_t launch_latent_attn(LatentAttnLaunch p, cudaStream_t st);
+cudaError_t launch_latent_attn(const LatentAttnLaunch& p, cudaStream_t st);
+cudaError_t launch_latent4_attn(const LatentAttnLaunch& p, cudaStream_t st);
+// Over all rows, of either cache (`groups` says which), and the bytes of scratch it needs (16-byte aligned).
+cudaError_t launch_latent_dense(LatentAttnLaunch p, void* scratch, cudaStream_t st);
+size_t latent_dense_scratch(LatentAttnLaunch p);
 
 }  // namespace dsa

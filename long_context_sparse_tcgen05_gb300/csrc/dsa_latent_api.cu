@@ -105,20 +105,33 @@ dsa_status cache_view(const dsa_latent_cache* c, int B, dsa::LatentCacheView& v)
     return fail(DSA_ERR_INVALID_ARG, c->block_table ? "table_ld must be >= 1" : "without a block table n_pages must cover the sequences");
   if (!aligned(c->codes, 16) || !aligned(c->rope, 16) || !aligned(c->scales, 4) || !aligned(c->block_table, 4))
     return fail(DSA_ERR_MISALIGNED, "cache codes and rope need 16-byte alignment, scales and block_table 4-byte");
-  v.codes = c->codes; v.scales = c->scales; v.rope = static_cast<uint16_t*>(c->rope);
+  v.codes = c->codes; v.groups = nullptr; v.scales = c->scales; v.rope = static_cast<uint16_t*>(c->rope);
   v.table = c->block_table; v.table_ld = c->table_ld; v.page_size = c->page_size; v.n_pages = c->n_pages;
   v.cap = c->block_table ? (int64_t)c->table_ld * c->page_size : c->page_size;
   if (v.cap > INT_MAX) v.cap = INT_MAX;
   return DSA_OK;
 }
 
-dsa_status latent_attn_launch(const dsa_latent_attn_args* a, int32_t k, dsa::LatentAttnLaunch& L) {
+// The 4-bit cache's view, by the same checks.
+dsa_status cache_view(const dsa_latent4_cache* c, int B, dsa::LatentCacheView& v) {
+  if (!c) return fail(DSA_ERR_INVALID_ARG, "the cache is NULL");
+  const dsa_latent_cache as{c->n_pages, c->page_size, c->table_ld, c->codes, c->scales, c->rope, c->block_table};
+  const dsa_status s = cache_view(&as, B, v);
+  if (s != DSA_OK) return s;
+  if (!c->groups) return fail(DSA_ERR_INVALID_ARG, "cache groups must be non-NULL");
+  v.groups = c->groups;
+  return DSA_OK;
+}
+
+// Attention args of either cache; k: entries of an index row, 0 without index rows.
+template <class Args>
+dsa_status latent_attn_launch(const Args* a, int32_t k, bool dense, dsa::LatentAttnLaunch& L) {
   if (!a) return fail(DSA_ERR_INVALID_ARG, "attention args are NULL");
   if (a->B < 1 || a->T < 1 || a->S < 1) return fail(DSA_ERR_INVALID_ARG, "B, T and S must be positive");
   if (a->H < 1 || a->H > 128) return fail(DSA_ERR_UNSUPPORTED, "H = %d outside [1, 128]", a->H);
-  if (k < 1 || k > 65536) return fail(DSA_ERR_UNSUPPORTED, "k = %d outside [1, 65536]", k);
+  if (!dense && (k < 1 || k > 65536)) return fail(DSA_ERR_UNSUPPORTED, "k = %d outside [1, 65536]", k);
   if ((int64_t)a->B * a->T > (1 << 24)) return fail(DSA_ERR_UNSUPPORTED, "B * T = %lld queries; at most 2^24", (long long)a->B * a->T);
-  if (a->idx_T != 1 && a->idx_T != a->T) return fail(DSA_ERR_INVALID_ARG, "idx_T = %d is neither 1 nor T = %d", a->idx_T, a->T);
+  if (!dense && a->idx_T != 1 && a->idx_T != a->T) return fail(DSA_ERR_INVALID_ARG, "idx_T = %d is neither 1 nor T = %d", a->idx_T, a->T);
   if (!(a->scale > 0.f) || a->scale > 3.4e38f) return fail(DSA_ERR_INVALID_ARG, "scale must be positive and finite");
   if (!a->q) return fail(DSA_ERR_INVALID_ARG, "q is NULL");
   if (a->q_stride_b < 0 || a->q_stride_t < 0) return fail(DSA_ERR_INVALID_ARG, "strides must be >= 0 (0: dense)");
@@ -137,6 +150,96 @@ dsa_status latent_attn_launch(const dsa_latent_attn_args* a, int32_t k, dsa::Lat
   L.idx_st = a->idx_T == 1 ? 0 : k;
   L.idx_sb = (int64_t)a->idx_T * k;
   return DSA_OK;
+}
+
+template <class Cache>
+dsa_status append_rows(const dsa_latent_append_args* a, const Cache* cache, void* ws, size_t ws_bytes, void* stream) {
+  if (!a) return fail(DSA_ERR_INVALID_ARG, "append args are NULL");
+  if (a->B < 1 || a->n < 0) return fail(DSA_ERR_INVALID_ARG, "B >= 1 and n >= 0 are required");
+  if (dsa_status c = check_count((int64_t)a->B * a->n, 1)) return c;
+  if (!a->x) return fail(DSA_ERR_INVALID_ARG, "x is NULL");
+  if (!a->cos != !a->sin) return fail(DSA_ERR_INVALID_ARG, "cos and sin go together");
+  if (a->cos && a->max_pos < 1) return fail(DSA_ERR_INVALID_ARG, "max_pos must be >= 1");
+  if (a->weight && !(a->eps >= 0.f)) return fail(DSA_ERR_INVALID_ARG, "eps must be >= 0");
+  if (a->x_stride_b < 0 || a->x_stride_t < 0) return fail(DSA_ERR_INVALID_ARG, "strides must be >= 0 (0: dense)");
+  if (a->x_stride_t && a->x_stride_t < 576) return fail(DSA_ERR_INVALID_ARG, "x_stride_t is smaller than 576");
+  if (!aligned(a->x, 16) || a->x_stride_b % 8 || a->x_stride_t % 8)
+    return fail(DSA_ERR_MISALIGNED, "x must be 16-byte aligned, its strides multiples of 8 elements");
+  if (!aligned(a->weight, 16) || !aligned(a->cos, 8) || !aligned(a->sin, 8) || !aligned(a->positions, 8))
+    return fail(DSA_ERR_MISALIGNED, "weight needs 16-byte alignment, cos, sin and positions 8-byte");
+  dsa::LatentAppendLaunch P{};
+  dsa_status s = cache_view(cache, a->B, P.cache);
+  if (s != DSA_OK) return s;
+  const int64_t rows = a->cos && a->max_pos < P.cache.cap ? a->max_pos : P.cache.cap;
+  if (!a->positions && (s = check_range(a->pos0, a->n, rows, "the table or the cache")) != DSA_OK) return s;
+  if ((s = check_ws(ws, ws_bytes)) != DSA_OK) return s;
+  P.B = a->B; P.n = a->n;
+  P.x = static_cast<const uint16_t*>(a->x);
+  P.x_st = a->x_stride_t ? a->x_stride_t : 576;
+  P.x_sb = a->x_stride_b ? a->x_stride_b : a->n * P.x_st;
+  P.weight = a->weight; P.eps = a->eps; P.cos = a->cos; P.sin = a->sin;
+  P.interleaved = a->interleaved != 0; P.max_pos = a->max_pos;
+  P.positions = a->positions; P.pos0 = a->pos0;
+  P.flags = ws_flags(ws);
+  return done(dsa::launch_latent_append(P, static_cast<cudaStream_t>(stream)), "append launch");
+}
+
+// Reads rows to P's outputs; their addresses once more, to be checked: two on 16 bytes, one on 4.
+template <class Cache>
+dsa_status read_rows(const Cache* cache, int32_t B, int32_t n, const int32_t* idx, int64_t pos0, dsa::LatentReadLaunch P,
+                const void* wide, const void* wide2, const void* scales, void* ws, size_t ws_bytes, void* stream) {
+  if (B < 1 || n < 0) return fail(DSA_ERR_INVALID_ARG, "B >= 1 and n >= 0 are required");
+  dsa_status s = check_count((int64_t)B * n, 1);
+  if (s != DSA_OK || (s = cache_view(cache, B, P.cache)) != DSA_OK) return s;
+  if (!wide || !wide2 || !scales) return fail(DSA_ERR_INVALID_ARG, "outputs must be non-NULL");
+  if (!aligned(wide, 16) || !aligned(wide2, 16) || !aligned(scales, 4) || !aligned(idx, 4))
+    return fail(DSA_ERR_MISALIGNED, "rows out must be 16-byte aligned, scales and idx 4-byte");
+  if (!idx && (s = check_range(pos0, n, P.cache.cap, "the cache")) != DSA_OK) return s;
+  if ((s = check_ws(ws, ws_bytes)) != DSA_OK) return s;
+  P.B = B; P.n = n; P.idx = idx; P.pos0 = pos0;
+  P.flags = ws_flags(ws);
+  return done(dsa::launch_latent_read(P, static_cast<cudaStream_t>(stream)), "read launch");
+}
+
+// The status of an attention launch.
+dsa_status attended(cudaError_t e) {
+  if (e == cudaErrorInvalidKernelImage)  // (returned by the launcher's own look at the kernels, too)
+    return fail(DSA_ERR_CUDA, "attention launch: the kernel is not built for this device, or not with the %d registers a "
+                "thread that its warpgroups share out (build it with the package's own build step)", dsa::kLatentAttnRegs);
+  return done(e, "attention launch");
+}
+
+template <class Args>
+dsa_status attend(const Args* a, const int32_t* idx, int32_t k, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  dsa::LatentAttnLaunch L{};
+  dsa_status s = latent_attn_launch(a, k, false, L);
+  if (s != DSA_OK) return s;
+  if (!idx || !out) return fail(DSA_ERR_INVALID_ARG, "idx and out must be non-NULL");
+  if (!aligned(out, 16) || !aligned(idx, 4) || !aligned(lse, 4) || !aligned(a->flags, 4))
+    return fail(DSA_ERR_MISALIGNED, "out must be 16-byte aligned, idx, lse and flags 4-byte");
+  if ((s = check_ws(ws, ws_bytes)) != DSA_OK) return s;
+  L.idx = idx; L.out = static_cast<uint16_t*>(out); L.lse = lse;
+  L.flags = a->flags ? a->flags : ws_flags(ws);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return attended(L.cache.groups ? dsa::launch_latent4_attn(L, st) : dsa::launch_latent_attn(L, st));
+}
+
+template <class Args>
+dsa_status attend_dense(const Args* a, const int32_t* lens, int32_t causal, void* out, float* lse, void* ws, size_t ws_bytes,
+                        void* stream) {
+  dsa::LatentAttnLaunch L{};
+  dsa_status s = latent_attn_launch(a, 0, true, L);
+  if (s != DSA_OK) return s;
+  if (!lens || !out) return fail(DSA_ERR_INVALID_ARG, "lens and out must be non-NULL");
+  if (!aligned(out, 16) || !aligned(lens, 4) || !aligned(lse, 4) || !aligned(a->flags, 4))
+    return fail(DSA_ERR_MISALIGNED, "out must be 16-byte aligned, lens, lse and flags 4-byte");
+  if ((s = check_ws(ws, ws_bytes)) != DSA_OK) return s;
+  const size_t need = dsa::kWsScratch + dsa::latent_dense_scratch(L);
+  if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  L.lens = lens; L.causal = causal != 0;
+  L.out = static_cast<uint16_t*>(out); L.lse = lse;
+  L.flags = a->flags ? a->flags : ws_flags(ws);
+  return attended(dsa::launch_latent_dense(L, static_cast<uint8_t*>(ws) + dsa::kWsScratch, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -195,70 +298,57 @@ dsa_status dsa_norm_rope_e4m3(const dsa_norm_rope_args* a, uint8_t* codes, float
 
 dsa_status dsa_latent_append(const dsa_latent_append_args* a, const dsa_latent_cache* cache, void* ws, size_t ws_bytes,
                              void* stream) {
-  if (!a) return fail(DSA_ERR_INVALID_ARG, "append args are NULL");
-  if (a->B < 1 || a->n < 0) return fail(DSA_ERR_INVALID_ARG, "B >= 1 and n >= 0 are required");
-  if (dsa_status c = check_count((int64_t)a->B * a->n, 1)) return c;
-  if (!a->x) return fail(DSA_ERR_INVALID_ARG, "x is NULL");
-  if (!a->cos != !a->sin) return fail(DSA_ERR_INVALID_ARG, "cos and sin go together");
-  if (a->cos && a->max_pos < 1) return fail(DSA_ERR_INVALID_ARG, "max_pos must be >= 1");
-  if (a->weight && !(a->eps >= 0.f)) return fail(DSA_ERR_INVALID_ARG, "eps must be >= 0");
-  if (a->x_stride_b < 0 || a->x_stride_t < 0) return fail(DSA_ERR_INVALID_ARG, "strides must be >= 0 (0: dense)");
-  if (a->x_stride_t && a->x_stride_t < 576) return fail(DSA_ERR_INVALID_ARG, "x_stride_t is smaller than 576");
-  if (!aligned(a->x, 16) || a->x_stride_b % 8 || a->x_stride_t % 8)
-    return fail(DSA_ERR_MISALIGNED, "x must be 16-byte aligned, its strides multiples of 8 elements");
-  if (!aligned(a->weight, 16) || !aligned(a->cos, 8) || !aligned(a->sin, 8) || !aligned(a->positions, 8))
-    return fail(DSA_ERR_MISALIGNED, "weight needs 16-byte alignment, cos, sin and positions 8-byte");
-  dsa::LatentAppendLaunch P{};
-  dsa_status s = cache_view(cache, a->B, P.cache);
-  if (s != DSA_OK) return s;
-  const int64_t rows = a->cos && a->max_pos < P.cache.cap ? a->max_pos : P.cache.cap;
-  if (!a->positions && (s = check_range(a->pos0, a->n, rows, "the table or the cache")) != DSA_OK) return s;
-  if ((s = check_ws(ws, ws_bytes)) != DSA_OK) return s;
-  P.B = a->B; P.n = a->n;
-  P.x = static_cast<const uint16_t*>(a->x);
-  P.x_st = a->x_stride_t ? a->x_stride_t : 576;
-  P.x_sb = a->x_stride_b ? a->x_stride_b : a->n * P.x_st;
-  P.weight = a->weight; P.eps = a->eps; P.cos = a->cos; P.sin = a->sin;
-  P.interleaved = a->interleaved != 0; P.max_pos = a->max_pos;
-  P.positions = a->positions; P.pos0 = a->pos0;
-  P.flags = ws_flags(ws);
-  return done(dsa::launch_latent_append(P, static_cast<cudaStream_t>(stream)), "append launch");
+  return append_rows(a, cache, ws, ws_bytes, stream);
+}
+dsa_status dsa_latent4_append(const dsa_latent_append_args* a, const dsa_latent4_cache* cache, void* ws, size_t ws_bytes,
+                              void* stream) {
+  return append_rows(a, cache, ws, ws_bytes, stream);
 }
 
 dsa_status dsa_latent_read(const dsa_latent_cache* cache, int32_t B, int32_t n, const int32_t* idx, int64_t pos0, void* out,
                            void* ws, size_t ws_bytes, void* stream) {
-  if (B < 1 || n < 0) return fail(DSA_ERR_INVALID_ARG, "B >= 1 and n >= 0 are required");
   dsa::LatentReadLaunch P{};
-  dsa_status s = check_count((int64_t)B * n, 1);
-  if (s != DSA_OK || (s = cache_view(cache, B, P.cache)) != DSA_OK) return s;
-  if (!out) return fail(DSA_ERR_INVALID_ARG, "out is NULL");
-  if (!aligned(out, 16) || !aligned(idx, 4)) return fail(DSA_ERR_MISALIGNED, "out must be 16-byte aligned, idx 4-byte");
-  if (!idx && (s = check_range(pos0, n, P.cache.cap, "the cache")) != DSA_OK) return s;
-  if ((s = check_ws(ws, ws_bytes)) != DSA_OK) return s;
-  P.B = B; P.n = n; P.idx = idx; P.pos0 = pos0;
   P.out = static_cast<uint16_t*>(out);
-  P.flags = ws_flags(ws);
-  return done(dsa::launch_latent_read(P, static_cast<cudaStream_t>(stream)), "read launch");
+  return read_rows(cache, B, n, idx, pos0, P, out, out, out, ws, ws_bytes, stream);
+}
+dsa_status dsa_latent4_read(const dsa_latent4_cache* cache, int32_t B, int32_t n, const int32_t* idx, int64_t pos0, void* out,
+                            void* ws, size_t ws_bytes, void* stream) {
+  dsa::LatentReadLaunch P{};
+  P.out = static_cast<uint16_t*>(out);
+  return read_rows(cache, B, n, idx, pos0, P, out, out, out, ws, ws_bytes, stream);
+}
+dsa_status dsa_latent4_unpack(const dsa_latent4_cache* cache, int32_t B, int32_t n, const int32_t* idx, int64_t pos0,
+                              uint8_t* codes, float* scales, void* rope, void* ws, size_t ws_bytes, void* stream) {
+  dsa::LatentReadLaunch P{};
+  P.out_codes = codes;
+  P.out_scales = scales;
+  P.out_rope = static_cast<uint16_t*>(rope);
+  return read_rows(cache, B, n, idx, pos0, P, codes, rope, scales, ws, ws_bytes, stream);
 }
 
 size_t dsa_latent_attn_workspace_size(const dsa_latent_attn_args*, int32_t) { return DSA_WS_MIN; }
+size_t dsa_latent_attn_dense_workspace_size(int32_t B, int32_t T, int32_t S, int32_t H) {
+  if (B < 1 || T < 1 || S < 1 || H < 1 || H > 128) return DSA_WS_MIN;  // (the call refuses these)
+  dsa::LatentAttnLaunch L{};
+  L.B = B; L.T = T; L.S = S; L.H = H;
+  return dsa::kWsScratch + dsa::latent_dense_scratch(L);
+}
 
 dsa_status dsa_latent_attn(const dsa_latent_attn_args* a, const int32_t* idx, int32_t k, void* out, float* lse, void* ws,
                            size_t ws_bytes, void* stream) {
-  dsa::LatentAttnLaunch L{};
-  dsa_status s = latent_attn_launch(a, k, L);
-  if (s != DSA_OK) return s;
-  if (!idx || !out) return fail(DSA_ERR_INVALID_ARG, "idx and out must be non-NULL");
-  if (!aligned(out, 16) || !aligned(idx, 4) || !aligned(lse, 4) || !aligned(a->flags, 4))
-    return fail(DSA_ERR_MISALIGNED, "out must be 16-byte aligned, idx, lse and flags 4-byte");
-  if ((s = check_ws(ws, ws_bytes)) != DSA_OK) return s;
-  L.idx = idx; L.out = static_cast<uint16_t*>(out); L.lse = lse;
-  L.flags = a->flags ? a->flags : ws_flags(ws);
-  const cudaError_t e = dsa::launch_latent_attn(L, static_cast<cudaStream_t>(stream));
-  if (e == cudaErrorInvalidKernelImage)  // (returned by the launcher's own look at the kernels, too)
-    return fail(DSA_ERR_CUDA, "attention launch: the kernel is not built for this device, or not with the %d registers a "
-                "thread that its warpgroups share out (build it with the package's own build step)", dsa::kLatentAttnRegs);
-  return done(e, "attention launch");
+  return attend(a, idx, k, out, lse, ws, ws_bytes, stream);
+}
+dsa_status dsa_latent4_attn(const dsa_latent4_attn_args* a, const int32_t* idx, int32_t k, void* out, float* lse, void* ws,
+                            size_t ws_bytes, void* stream) {
+  return attend(a, idx, k, out, lse, ws, ws_bytes, stream);
+}
+dsa_status dsa_latent_attn_dense(const dsa_latent_attn_args* a, const int32_t* lens, int32_t causal, void* out, float* lse,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  return attend_dense(a, lens, causal, out, lse, ws, ws_bytes, stream);
+}
+dsa_status dsa_latent4_attn_dense(const dsa_latent4_attn_args* a, const int32_t* lens, int32_t causal, void* out, float* lse,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  return attend_dense(a, lens, causal, out, lse, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,6 @@
+// Sparse attention over selected rows of the paged 4-bit latent cache.
+#include "latent_attn.cuh"
+
+namespace dsa {
+cudaError_t launch_latent4_attn(const LatentAttnLaunch& p, cudaStream_t st) { return launch_rows<true>(p, st); }
+}  // namespace dsa

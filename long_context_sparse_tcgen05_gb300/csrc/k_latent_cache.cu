@@ -18,13 +18,34 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kMinScale = 0x1p-60f;  // rope / scale stays finite in bf16 for any sane rope value
 
+constexpr float kTopFour = 384.f;  // 6 * 2^6: the largest e2m1 value under the largest group factor
+// The byte of a group whose largest magnitude over the row's scale is m: b - 127 = e, the least of -5 .. 6 with
+// 6 * 2^e = 1.5 * 2^(e + 2) >= m.  (A fraction above a half carries into the exponent.)
+__device__ __forceinline__ uint32_t group_of(float m) {
+  const int e = (int)((__float_as_uint(m) + 0x3fffffu) >> 23) - 127 - 2;
+  return (uint32_t)(min(max(e, -5), 6) + 127);
+}
+// Eight quotients under group byte g as e2m1 codes (nearest, ties to even, at most 6), four bits each.
+template <class Q>
+__device__ __forceinline__ uint32_t codes8(const Q& q, const f32x2* y, uint32_t g) {
+  const float f = __uint_as_float((254u - g) << 23);  // 2^-e
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 z = mul_2(q(y[i]), pair(f, f));
+    w |= pack_e2m1(lo_of(z), hi_of(z)) << (8 * i);
+  }
+  return w;
+}
+
 // Everything a token needs is on its way while the one before it is worked on: its 1,152 bytes in
 // the warp's part of shared memory, its angles and block table entry in registers (its position one
 // token earlier still).  Loaded when its turn came, a token took a warp three dependent loads.
 // kTurn: with rotation tables.  (Without them the rope values stay as they are: an angle of zero, 1 and 0,
 // would spread an infinity or NaN over its pair.  Chosen inside the kernel, a call of 131,072 rows took 59.5,
 // not 57.2 us.)
-template <bool kTurn>
+// kFour: into the 4-bit cache.
+template <bool kTurn, bool kFour>
 __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p) {
   constexpr int kRow = kLatentDim + kLatentRope;
   __shared__ alignas(16) uint16_t rows[2][kThreads / 32][kRow];
@@ -112,16 +133,43 @@ __global__ void __launch_bounds__(kThreads) k_latent_append(LatentAppendLaunch p
       }
     }
     float amax = 0.f;  // (a NaN stays)
+    float top[2];      // of a group of 32 values, which four lanes hold: groups lane / 4 and 8 + lane / 4
+    if constexpr (kFour) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = max3_abs(amax, lo_of(y[e]), hi_of(y[e]));
+      for (int u = 0; u < 2; ++u) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = max3_abs(m, lo_of(y[4 * u + e]), hi_of(y[4 * u + e]));
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        top[u] = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      }
+      amax = max_nan(top[0], top[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = max3_abs(amax, lo_of(y[e]), hi_of(y[e]));
+    }
     // (the bits of a magnitude, NaN on top, order as integers)
     amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-    const float q = amax / 448.f;
-    const float scale = q < kMinScale ? kMinScale : q;  // (a NaN stays)
+    const float q = amax / (kFour ? kTopFour : 448.f);
+    float scale = q < kMinScale ? kMinScale : q;  // (a NaN stays)
+    if (kFour && !(amax < INFINITY)) scale = NAN;  // (e2m1 has no infinity and no NaN to give a row)
     with_quotient(scale, [&](auto div) {
-      uint8_t* codes = p.cache.codes + row * kLatentDim;
-      *reinterpret_cast<uint2*>(codes + lane * 8) = make_uint2(codes4(div, y[0], y[1]), codes4(div, y[2], y[3]));
-      *reinterpret_cast<uint2*>(codes + 256 + lane * 8) = make_uint2(codes4(div, y[4], y[5]), codes4(div, y[6], y[7]));
+      if constexpr (kFour) {
+        const f32x2 t = div(pair(top[0], top[1]));
+        const uint32_t g0 = group_of(lo_of(t)), g1 = group_of(hi_of(t));
+        uint32_t* codes = reinterpret_cast<uint32_t*>(p.cache.codes + row * (kLatentDim / 2));
+        codes[lane] = codes8(div, y, g0);
+        codes[32 + lane] = codes8(div, y + 4, g1);
+        if ((lane & 3) == 0) {
+          uint8_t* groups = p.cache.groups + row * kLatentGroups + (lane >> 2);
+          groups[0] = (uint8_t)g0;
+          groups[8] = (uint8_t)g1;
+        }
+      } else {
+        uint8_t* codes = p.cache.codes + row * kLatentDim;
+        *reinterpret_cast<uint2*>(codes + lane * 8) = make_uint2(codes4(div, y[0], y[1]), codes4(div, y[2], y[3]));
+        *reinterpret_cast<uint2*>(codes + 256 + lane * 8) = make_uint2(codes4(div, y[4], y[5]), codes4(div, y[6], y[7]));
+      }
       // (the scale is the latent values': it does not bound these)
       const f32x2 r = any_quotient(div, kTurn ? pair(a * cs - c * sn, c * cs + a * sn) : pair(a, c), scale);
       const uint32_t rr = pack_bf16(lo_of(r), hi_of(r));
@@ -143,6 +191,17 @@ __device__ __forceinline__ uint4 dequant8(uint2 c, float s) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = e4m3x2_to_float2((uint16_t)((i < 2 ? c.x : c.y) >> ((i & 1) * 16)));
+    o[i] = pack_bf16(f.x * s, f.y * s);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight e2m1 codes times s (the group's power of two in it), as bf16.
+__device__ __forceinline__ uint4 dequant8(uint32_t c, float s) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = e2m1x2_to_float2(c >> (8 * i));
     o[i] = pack_bf16(f.x * s, f.y * s);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
@@ -176,6 +235,48 @@ __global__ void __launch_bounds__(kThreads) k_latent_read(LatentReadLaunch p) {
   }
 }
 
+// Rows of the 4-bit cache: as bf16, or (kUnpack) in the FP8 cache's form, under the same scale.
+template <bool kUnpack>
+__global__ void __launch_bounds__(kThreads) k_latent4_read(LatentReadLaunch p) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t rows = (uint32_t)p.B * p.n;  // (below 2^31: checked by the caller)
+  const uint32_t step = gridDim.x * (kThreads / 32);
+  for (uint32_t r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += step) {
+    const int b = (int)(r / (uint32_t)p.n), i = (int)(r - (uint32_t)b * (uint32_t)p.n);
+    const int64_t pos = p.idx ? (int64_t)__ldg(p.idx + r) : p.pos0 + i;
+    const int64_t row = pos >= 0 ? latent_row(p.cache, b, pos) : -1;
+    if (row < 0 && pos != -1 && lane == 0) atomicOr(p.flags, DSA_FLAG_BAD_INDEX);
+    // (a row that is none: zeros)
+    uint32_t c0 = 0, c1 = 0, g0 = 127, g1 = 127;
+    uint4 rp = make_uint4(0, 0, 0, 0);
+    float s = 1.f;
+    if (row >= 0) {
+      const uint32_t* codes = reinterpret_cast<const uint32_t*>(p.cache.codes + row * (kLatentDim / 2));
+      const uint8_t* groups = p.cache.groups + row * kLatentGroups + (lane >> 2);
+      c0 = __ldg(codes + lane);
+      c1 = __ldg(codes + 32 + lane);
+      g0 = __ldg(groups);
+      g1 = __ldg(groups + 8);
+      if (lane < 8) rp = __ldg(reinterpret_cast<const uint4*>(p.cache.rope + row * kLatentRope) + lane);
+      s = __ldg(p.cache.scales + row);
+    }
+    if constexpr (kUnpack) {
+      uint2* out = reinterpret_cast<uint2*>(p.out_codes + (int64_t)r * kLatentDim);
+      out[lane] = ExpandFour(g0)(c0);
+      out[32 + lane] = ExpandFour(g1)(c1);
+      if (lane < 8) reinterpret_cast<uint4*>(p.out_rope + (int64_t)r * kLatentRope)[lane] = rp;
+      if (lane == 0) p.out_scales[r] = s;
+    } else {
+      uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)r * (kLatentDim + kLatentRope));
+      out[lane] = dequant8(c0, s * __uint_as_float(g0 << 23));
+      out[32 + lane] = dequant8(c1, s * __uint_as_float(g1 << 23));
+      if (lane < 8)
+        out[64 + lane] = make_uint4(pack_bf16(bf_lo(rp.x) * s, bf_hi(rp.x) * s), pack_bf16(bf_lo(rp.y) * s, bf_hi(rp.y) * s),
+                                    pack_bf16(bf_lo(rp.z) * s, bf_hi(rp.z) * s), pack_bf16(bf_lo(rp.w) * s, bf_hi(rp.w) * s));
+    }
+  }
+}
+
 int grid_of(int64_t rows) {
   return (int)std::min<int64_t>((rows + kThreads / 32 - 1) / (kThreads / 32), (int64_t)device_sm_count() * 8);
 }
@@ -186,8 +287,10 @@ cudaError_t launch_latent_append(const LatentAppendLaunch& p, cudaStream_t st) {
   const int64_t rows = (int64_t)p.B * p.n;
   if (rows == 0) return cudaSuccess;
   TraceScope trace(kTraceCache, st);
-  if (p.cos) k_latent_append<true><<<grid_of(rows), kThreads, 0, st>>>(p);
-  else k_latent_append<false><<<grid_of(rows), kThreads, 0, st>>>(p);
+  const bool four = p.cache.groups != nullptr;
+  auto kernel = p.cos ? (four ? k_latent_append<true, true> : k_latent_append<true, false>)
+                      : (four ? k_latent_append<false, true> : k_latent_append<false, false>);
+  kernel<<<grid_of(rows), kThreads, 0, st>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -196,7 +299,8 @@ cudaError_t launch_latent_read(const LatentReadLaunch& p, cudaStream_t st) {
   const int64_t rows = (int64_t)p.B * p.n;
   if (rows == 0) return cudaSuccess;
   TraceScope trace(kTraceCache, st);
-  k_latent_read<<<grid_of(rows), kThreads, 0, st>>>(p);
+  auto kernel = !p.cache.groups ? k_latent_read : p.out_codes ? k_latent4_read<true> : k_latent4_read<false>;
+  kernel<<<grid_of(rows), kThreads, 0, st>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -1,4 +1,4 @@
-// Addressing and decoding of the paged FP8 latent cache on the device.
+// Addressing and decoding of the paged latent cache, FP8 or 4-bit, on the device.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -39,5 +39,37 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"(c));
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
+
+// ---- the 4-bit cache: e2m1 codes (sign, two bits of exponent, one of fraction: 0, 0.5, 1, 1.5, 2, 3, 4, 6) under a
+// group's byte b = e + 127, -5 <= e <= 6.  Every code times 2^e is an e4m3 value: of the magnitudes above 0.5 to 6 the
+// e4m3 codes are c - 8, c, c + 4, c + 8, c + 12, c + 16, c + 20, with c = 8 (e + 7) the code of 2^e itself (their
+// exponents go by steps of 8, their halves by 4; c - 8 >= 8, so all of them are normal).
+
+// Two e2m1 codes (low four bits first) as floats, and two floats as codes (the nearest, ties to even, at most 6).
+__device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t c) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n}\n" : "=r"(h) : "r"(c));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+__device__ __forceinline__ uint32_t pack_e2m1(float lo, float hi) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n}\n" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Eight e2m1 codes (low four bits first) to the e4m3 codes of what they stand for: the eight magnitudes are a table in
+// two registers that a byte permutation looks up, four codes at a time.
+struct ExpandFour {
+  uint32_t lo, hi;  // magnitudes 0-3 and 4-7
+  __device__ __forceinline__ explicit ExpandFour(uint32_t group) {
+    const uint32_t c = (group - 120u) * 0x08080808u;  // (bytes other than 122-133 give some codes)
+    lo = (c & 0xffffff00u) + 0x03fff800u;             // [0, c - 8, c, c + 4]
+    hi = c + 0x14100c08u;                             // [c + 8, c + 12, c + 16, c + 20]
+  }
+  __device__ __forceinline__ uint2 operator()(uint32_t w) const {
+    const uint32_t m = w & 0x77777777u, t = w << 4;  // magnitudes; the even codes' signs at their bytes' tops
+    return make_uint2(__byte_perm(lo, hi, m) | (__byte_perm(t, w, 0x5140) & 0x80808080u),
+                      __byte_perm(lo, hi, m >> 16) | (__byte_perm(t, w, 0x7362) & 0x80808080u));
+  }
+};
 
 }  // namespace dsa
