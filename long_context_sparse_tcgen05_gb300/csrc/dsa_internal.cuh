@@ -324,7 +324,7 @@ struct LatentAttnLaunch {
   float* parts;
 };
 constexpr int kMaxLatentSplits = 8;
-constexpr int kLatentAttnRegs = 80;  // a thread's registers, which the kernel's warpgroups share out
+constexpr int kLatentAttnRegs = 80, kLatent4AttnRegs = 72;  // a thread's registers, which the kernel's warpgroups share out
 cudaError_t launch_latent_attn(const LatentAttnLaunch& p, cudaStream_t st);
 cudaError_t launch_latent4_attn(const LatentAttnLaunch& p, cudaStream_t st);
 // Over all rows, of either cache (`groups` says which), and the bytes of scratch it needs (16-byte aligned).

@@ -131,11 +131,11 @@ cudaError_t launch(LatentAttnLaunch p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
     for (int poll = 0; poll < 2; ++poll)
-      if ((e = prepare_kernel(dense_kernel<kFour>(poll))) != cudaSuccess) return e;
+      if ((e = prepare_kernel<kFour>(dense_kernel<kFour>(poll))) != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
   cudaLaunchAttribute attr{};
-  const cudaLaunchConfig_t cfg = launch_config(runs, 1, st, &attr);
+  const cudaLaunchConfig_t cfg = launch_config<kFour>(runs, 1, st, &attr);
   if ((e = cudaLaunchKernelEx(&cfg, dense_kernel<kFour>(p.wait < kDefaultWaitCycles), p)) != cudaSuccess) return e;
   count_launches(1);
   if (runs > 1) {

@@ -83,12 +83,22 @@ constexpr uint32_t kPBytes = kHg * 128;      // P: per head 64 hi bytes, then 64
 constexpr uint32_t kQCodes = 128 * kLatentDim, kQBytes = kQCodes + 128 * kLatentRope * 2;
 constexpr int kGatherWarps = 4, kSWarp = 4, kPvWarp = 5, kIxWarp0 = 6, kSmWarp0 = 8, kSmWarps = 8, kOWarp0 = 16, kQWarp0 = 20;
 constexpr int kRing = 6;                     // blocks the index warps may be ahead
-constexpr int kThreads = 24 * 32;
-// Registers by warpgroup (warps 0-3, 4-7, ..), moved at the start from the kernel's own kRegs each;
-// the softmax warps spilled in their block loop at kRegs.
-constexpr int kRegs = kLatentAttnRegs, kRegsGather = 56, kRegsGather4 = 64, kRegsIssue = 64, kRegsSm = 104, kRegsEpi = 72;
-static_assert(kRegsGather <= kRegsGather4 && kRegsGather4 + kRegsIssue + 2 * kRegsSm + 2 * kRegsEpi <= 6 * kRegs,
-              "registers the block is launched with");
+constexpr int kWarps = 24, kMoreGather0 = kWarps;
+// The 4-bit kernels have four gather warps more, behind the others: theirs expand the codes.
+template <bool kFour>
+constexpr int kThreads = (kWarps + (kFour ? kGatherWarps : 0)) * 32;
+// Registers by warpgroup (warps 0-3, 4-7, ..), moved at the start from the kernel's own each; the softmax warps
+// spilled in their block loop at that.
+template <bool kFour>
+struct Regs {
+  static constexpr int kLaunch = kLatentAttnRegs, kGather = 56, kIssue = 64, kSm = 104, kEpi = 72;
+  static_assert(kGather + kIssue + 2 * kSm + 2 * kEpi <= 6 * kLaunch, "registers the block is launched with");
+};
+template <>
+struct Regs<true> {
+  static constexpr int kLaunch = kLatent4AttnRegs, kGather = 56, kIssue = 56, kSm = 104, kEpi = 64;
+  static_assert(2 * kGather + kIssue + 2 * kSm + 2 * kEpi <= 7 * kLaunch, "registers the block is launched with");
+};
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColSfA = 416, kColSfB = 424, kColS = 448;
 constexpr int64_t kPartFloats = kHg * kLatentDim + kHg;  // of a part in memory: O by head, then lse
@@ -98,7 +108,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // p_j / s_j <= 2^8 / 2^-60 (the append's least scale), times 2^(E - E0): 2^(10 + 6 + 8 + 60 + 40) = 2^124,
 // within fp32 (with 60 it passed 2^128).
 constexpr float kMove = 40.f;
-constexpr int kInfoReaders = kGatherWarps + 2 + kSmWarps + 4 + 4;
+constexpr int kInfoReaders = kGatherWarps + 2 + kSmWarps + 4 + 4;  // (4-bit: kGatherWarps more)
 constexpr int kEpiThreads = 256;             // O and query warps store an item's O together
 constexpr uint32_t kOPitch = 2 * kLatentDim + 16;  // a staged O row: 8 heads' 16-byte pieces in 32 banks
 static_assert(kHg * kOPitch <= kQBytes, "O is staged in the queries' room");
@@ -399,6 +409,7 @@ __device__ __forceinline__ int dense_blocks(int sees) { return max(1, (sees + kN
 // equal runs, one a CTA, so sequences of any lengths keep the SMs evenly busy.  A run starts and ends inside tiles:
 // those are parts, which k_latent_join puts together.  Every CTA counts all tiles (a few instructions each, over 768
 // threads; a tile's own work is thousands of cycles).  false: nothing to do.
+template <int kThreads>
 __device__ __forceinline__ bool find_share(const LatentAttnLaunch& p, DenseShare& s, int64_t* room) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tiles = p.B * p.tiles_t * p.groups, per = (tiles + kThreads - 1) / kThreads;
@@ -458,7 +469,7 @@ __device__ __forceinline__ bool find_share(const LatentAttnLaunch& p, DenseShare
 // own: the loops of a chunk run at the pace of their instruction fetches, 1.09 against 0.99 ms with the
 // joining code beside them.)
 template <bool kPoll, Form kForm, bool kFour>
-__global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p) {
+__global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLaunch p) {
   constexpr bool kParts = kForm == kRowParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -472,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   int first = blockIdx.x, items = p.B * p.T * p.groups * p.splits;
   const int G = kForm == kAll ? 1 : (int)gridDim.x;
   if constexpr (kForm == kAll) {
-    if (!find_share(p, sm->share, reinterpret_cast<int64_t*>(kv_s))) return;
+    if (!find_share<kThreads<kFour>>(p, sm->share, reinterpret_cast<int64_t*>(kv_s))) return;
     first = sm->share.first;
     items = sm->share.last + 1;
   }
@@ -489,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     mbar_init(&bar.o_full, 1);
     mbar_init(&bar.o_empty, 8);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bar.kv_full[i], kFour ? kGatherWarps : kGatherWarps * 32);
+      mbar_init(&bar.kv_full[i], kFour ? 2 * kGatherWarps : kGatherWarps * 32);
       for (int c = 0; c < 3; ++c) mbar_init(&bar.kv_empty[i][c], 1);
     }
     for (int i = 0; i < kRing; ++i) {
@@ -506,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       mbar_init(&bar.l_full[i], kSmWarps);
       mbar_init(&bar.l_empty[i], 8);
       mbar_init(&bar.info_full[i], 1);
-      mbar_init(&bar.info_empty[i], kInfoReaders);
+      mbar_init(&bar.info_empty[i], kInfoReaders + (kFour ? kGatherWarps : 0));
       mbar_init(&bar.drain[i], 1);
     }
     sm->abort = 0;
@@ -791,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
   };
   // The first item's queries: sixteen warps that have nothing else to do yet convert four heads each,
   // eight of them store the rows (a single decode step waits for nothing longer).
-  if (warp >= kSmWarp0) {
+  if (warp >= kSmWarp0 && warp < kWarps) {
     convert(first, warp - kSmWarp0, 16);
     named_sync(3, 512);
     if (warp >= kOWarp0) {
@@ -800,8 +811,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
   }
 
-  if (warp < kGatherWarps) {
-    reg_dec<kFour ? kRegsGather4 : kRegsGather>();
+  if (warp < kGatherWarps || (kFour && warp >= kMoreGather0)) {
+    reg_dec<Regs<kFour>::kGather>();
     // ================= gather =================
     int it = 0;
     uint32_t g = 0;  // blocks so far
@@ -814,51 +825,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
       if constexpr (kFour) {
-        // A lane takes 16 bytes of codes (a group of 32 values) of rows 2 p + lane / 16 of its warp's 16.  They wait
-        // in registers: a block's loads are made while the one before it is converted, before a stage is free.
-        const int c = lane & 15, half = lane >> 4;
-        uint4 raw[8];
-        uint32_t grp[8];
+        // A warp has eight rows of a block, a lane 16 bytes of codes (a group of 32 values) of each of four of them.  They
+        // wait in registers: a block's loads are made while the one before it is expanded, before a stage is free.
+        // Eight lanes have four groups of two neighbouring rows, so that their stores meet all banks.
+        const int r0 = 8 * (warp < kGatherWarps ? warp : warp - kMoreGather0 + kGatherWarps) + ((lane >> 2) & 1);
+        const int c = (lane & 3) + 4 * (lane >> 3);
+        uint4 raw[4];
+        uint32_t grp[4];
         auto load = [&](int pass, int ri) {
-          const int row = sm->row[ri][warp * 16 + 2 * pass + half];
-          const bool live = row >= 0;  // (a skipped row is zeros)
-          raw[pass] = live ? __ldg(reinterpret_cast<const uint4*>(p.cache.codes + (int64_t)row * (kLatentDim / 2)) + c)
-                           : make_uint4(0, 0, 0, 0);
-          grp[pass] = live ? __ldg(p.cache.groups + (int64_t)row * kLatentGroups + c) : 127u;
+          // (of a skipped row the first row's: a load under a condition was waited for at once, a latency a pass)
+          const uint32_t row = (uint32_t)max(sm->row[ri][r0 + 2 * pass], 0);
+          raw[pass] = __ldg(reinterpret_cast<const uint4*>(p.cache.codes + (uint64_t)row * (kLatentDim / 2)) + c);
+          grp[pass] = __ldg(p.cache.groups + (uint64_t)row * kLatentGroups + c);
         };
         if (nb) {
           const int ri = (int)(g % kRing);
           if (!(ok = wait(&bar.ix_row[ri], (g / kRing) & 1))) break;
 #pragma unroll
-          for (int pass = 0; pass < 8; ++pass) load(pass, ri);
+          for (int pass = 0; pass < 4; ++pass) load(pass, ri);
         }
         for (int j = 0; j < nb; ++j, ++g) {
           const int st = (int)(g % kStages), ri = (int)(g % kRing), rn = (int)((g + 1) % kRing);
-          uint8_t* stage = kv_s + st * kStage;
-          if (!(ok = wait(&bar.kv_empty[st][2], ((g / kStages) & 1) ^ 1))) break;
+          const uint32_t stage = smem_addr(kv_s + st * kStage);
+          const uint32_t free = ((g / kStages) & 1) ^ 1;
+          if (!(ok = wait(&bar.kv_empty[st][2], free))) break;
 #pragma unroll
-          for (int pass = 0; pass < 4; ++pass) {  // the rope atom, as it is
-            const int r = warp * 16 + pass * 4 + (lane >> 3), cc = lane & 7;
-            const int64_t row = sm->row[ri][r];
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(stage + 4 * kAtom + r * 128 + ((cc ^ (r & 7)) << 4))),
-                         "l"(rope + (row < 0 ? 0 : row) * (2 * kLatentRope) + cc * 16), "r"(row < 0 ? 0 : 16)
+          for (int pass = 0; pass < 2; ++pass) {  // the rope atom, as it is
+            const int r = (r0 & ~7) + pass * 4 + (lane >> 3), cc = lane & 7;
+            const int row = sm->row[ri][r];
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(stage + 4 * kAtom + r * 128 + ((cc ^ (r & 7)) << 4)),
+                         "l"(rope + (uint64_t)(uint32_t)max(row, 0) * (2 * kLatentRope) + cc * 16), "r"(row < 0 ? 0 : 16)
                          : "memory");
           }
           const bool more = j + 1 < nb;
-          if (!(ok = (!more || wait(&bar.ix_row[rn], ((g + 1) / kRing) & 1)) && wait(&bar.kv_empty[st][0], ((g / kStages) & 1) ^ 1) &&
-                     wait(&bar.kv_empty[st][1], ((g / kStages) & 1) ^ 1)))
+          if (!(ok = (!more || wait(&bar.ix_row[rn], ((g + 1) / kRing) & 1)) && wait(&bar.kv_empty[st][0], free) &&
+                     wait(&bar.kv_empty[st][1], free)))
             break;
+          const uint32_t at = stage + (c >> 2) * kAtom + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 1)) << 4);
 #pragma unroll
-          for (int pass = 0; pass < 8; ++pass) {
-            const int r = warp * 16 + 2 * pass + half;
-            const ExpandFour x(grp[pass]);
+          for (int pass = 0; pass < 4; ++pass) {
+            const ExpandFour x(grp[pass], sm->row[ri][r0 + 2 * pass] >= 0);  // (a skipped row is zeros)
             const uint2 v0 = x(raw[pass].x), v1 = x(raw[pass].y), v2 = x(raw[pass].z), v3 = x(raw[pass].w);
-            // (atoms of 128 values; four lanes on it store their second words first, so that eight lanes meet all banks)
-            const bool swap = c & 4;
-            const uint32_t at = smem_addr(stage + (c >> 2) * kAtom + r * 128), w = 2 * (c & 3) + swap;
-            const uint4 lo = make_uint4(v0.x, v0.y, v1.x, v1.y), hi = make_uint4(v2.x, v2.y, v3.x, v3.y);
-            st_shared16(at + ((w ^ (r & 7)) << 4), swap ? hi : lo);
-            st_shared16(at + ((w ^ 1 ^ (r & 7)) << 4), swap ? lo : hi);
+            const uint32_t to = (at + 256 * pass) ^ (32 * pass);  // (row & 7 = 2 pass + its low bit)
+            st_shared16(to, make_uint4(v0.x, v0.y, v1.x, v1.y));
+            st_shared16(to ^ 16, make_uint4(v2.x, v2.y, v3.x, v3.y));
             if (more) load(pass, rn);
           }
           asm volatile("cp.async.wait_all;\n" ::: "memory");
@@ -904,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     asm volatile("cp.async.wait_all;\n" ::: "memory");
     finish(false);
   } else if (warp < kSmWarp0) {
-    reg_dec<kRegsIssue>();
+    reg_dec<Regs<kFour>::kIssue>();
     if (warp == kSWarp) {
       // ================= score product =================
       const uint32_t id8 = idesc_mn(0, 0, 128, kNB), id16 = idesc_mn(1, 1, 128, kNB);
@@ -1131,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
     finish(false);
   } else if (warp < kOWarp0) {
-    reg_inc<kRegsSm>();
+    reg_inc<Regs<kFour>::kSm>();
     // ================= softmax =================
     const int hgp = 2 * (warp & 3) + ((warp - kSmWarp0) >> 2);  // this warp's 8 heads
     const int hl = hgp * 8 + (lane >> 2), m = lane & 3;         // this thread's head; keys 8j + 2m + {0, 1}
@@ -1257,7 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
     }
     finish(false);
   } else {
-    reg_dec<kRegsEpi>();
+    if constexpr (Regs<kFour>::kEpi < Regs<kFour>::kLaunch) reg_dec<Regs<kFour>::kEpi>();
     if (warp < kQWarp0) {
       // ================= O^T: block scales, half of the epilogue =================
       const int t = threadIdx.x - kOWarp0 * 32;
@@ -1378,10 +1388,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent_attn(LatentAttnLaunch p)
 static_assert(kColQR == kColQ + 128, "the converted query row is stored in one run of columns");
 
 // A launch whose CTAs work in clusters of n on a row each.
+template <bool kFour>
 cudaLaunchConfig_t launch_config(int ctas, int n, cudaStream_t st, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)ctas);
-  c.blockDim = dim3(kThreads);
+  c.blockDim = dim3(kThreads<kFour>);
   c.dynamicSmemBytes = kSmem;
   c.stream = st;
   attr->id = cudaLaunchAttributeClusterDimension;
@@ -1393,11 +1404,12 @@ cudaLaunchConfig_t launch_config(int ctas, int n, cudaStream_t st, cudaLaunchAtt
 }
 
 // Shared memory for a kernel, and that a block is launched with the registers that its warpgroups' moves count on.
+template <bool kFour>
 cudaError_t prepare_kernel(void (*kern)(LatentAttnLaunch)) {
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != kRegs) return cudaErrorInvalidKernelImage;
+  if (fa.numRegs != Regs<kFour>::kLaunch) return cudaErrorInvalidKernelImage;
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
 }
 
@@ -1439,10 +1451,10 @@ cudaError_t prepare_kernels(ClusterRoom& room) {
     return cudaSuccess;
   }
   for (int k = 0; k < 4; ++k)
-    if ((e = prepare_kernel(kernel_of<kFour>(k & 1, k & 2))) != cudaSuccess) return e;
+    if ((e = prepare_kernel<kFour>(kernel_of<kFour>(k & 1, k & 2))) != cudaSuccess) return e;
   for (int n = 2; n <= kMaxLatentSplits; ++n) {
     cudaLaunchAttribute attr{};
-    const cudaLaunchConfig_t c = launch_config(n, n, nullptr, &attr);
+    const cudaLaunchConfig_t c = launch_config<kFour>(n, n, nullptr, &attr);
     if ((e = cudaOccupancyMaxActiveClusters(&room.clusters[n], kernel_of<kFour>(false, true), &c)) != cudaSuccess) return e;
   }
   int unknown = 0;
@@ -1470,7 +1482,7 @@ cudaError_t launch_rows(LatentAttnLaunch p, cudaStream_t st) {
   const int64_t items = rows * p.splits;
   const int sms = device_sm_count();
   cudaLaunchAttribute attr{};
-  const cudaLaunchConfig_t cfg = launch_config((int)(p.splits > 1 || items < sms ? items : sms), p.splits, st, &attr);
+  const cudaLaunchConfig_t cfg = launch_config<kFour>((int)(p.splits > 1 || items < sms ? items : sms), p.splits, st, &attr);
   if ((e = cudaLaunchKernelEx(&cfg, kernel_of<kFour>(poll, p.splits > 1), p)) != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
