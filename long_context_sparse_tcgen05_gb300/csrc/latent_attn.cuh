@@ -826,52 +826,58 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
       if constexpr (kFour) {
         // A warp has eight rows of a block, a lane 16 bytes of codes (a group of 32 values) of each of four of them.  They
-        // wait in registers: a block's loads are made while the one before it is expanded, before a stage is free.
+        // wait in registers: a block's loads are made while the one before it is expanded, before a stage is free;
+        // so are the copies of its rope values.  Of a skipped row the first row's codes are taken (whatever they are,
+        // they stand for finite values, which its weights of 0 make nothing of) and zeros for rope values: loads under a
+        // condition were waited for at once, a latency each.
         // Eight lanes have four groups of two neighbouring rows, so that their stores meet all banks.
-        const int r0 = 8 * (warp < kGatherWarps ? warp : warp - kMoreGather0 + kGatherWarps) + ((lane >> 2) & 1);
-        const int c = (lane & 3) + 4 * (lane >> 3);
+        const int w0 = 8 * (warp < kGatherWarps ? warp : warp - kMoreGather0 + kGatherWarps);
+        const int r0 = w0 + ((lane >> 2) & 1), c = (lane & 3) + 4 * (lane >> 3);
         uint4 raw[4];
         uint32_t grp[4];
-        auto load = [&](int pass, int ri) {
-          // (of a skipped row the first row's: a load under a condition was waited for at once, a latency a pass)
-          const uint32_t row = (uint32_t)max(sm->row[ri][r0 + 2 * pass], 0);
+        auto load = [&](int pass, const int32_t* rows) {
+          const uint32_t row = (uint32_t)max(rows[r0 + 2 * pass], 0);
           raw[pass] = __ldg(reinterpret_cast<const uint4*>(p.cache.codes + (uint64_t)row * (kLatentDim / 2)) + c);
           grp[pass] = __ldg(p.cache.groups + (uint64_t)row * kLatentGroups + c);
         };
-        if (nb) {
-          const int ri = (int)(g % kRing);
-          if (!(ok = wait(&bar.ix_row[ri], (g / kRing) & 1))) break;
+        auto copy_rope = [&](uint32_t st, const int32_t* rows) {
 #pragma unroll
-          for (int pass = 0; pass < 4; ++pass) load(pass, ri);
-        }
-        for (int j = 0; j < nb; ++j, ++g) {
-          const int st = (int)(g % kStages), ri = (int)(g % kRing), rn = (int)((g + 1) % kRing);
-          const uint32_t stage = smem_addr(kv_s + st * kStage);
-          const uint32_t free = ((g / kStages) & 1) ^ 1;
-          if (!(ok = wait(&bar.kv_empty[st][2], free))) break;
-#pragma unroll
-          for (int pass = 0; pass < 2; ++pass) {  // the rope atom, as it is
-            const int r = (r0 & ~7) + pass * 4 + (lane >> 3), cc = lane & 7;
-            const int row = sm->row[ri][r];
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(stage + 4 * kAtom + r * 128 + ((cc ^ (r & 7)) << 4)),
+          for (int pass = 0; pass < 2; ++pass) {
+            const int r = w0 + pass * 4 + (lane >> 3), cc = lane & 7, row = rows[r];
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(kv_s) + st * kStage + 4 * kAtom + r * 128 + ((cc ^ (r & 7)) << 4)),
                          "l"(rope + (uint64_t)(uint32_t)max(row, 0) * (2 * kLatentRope) + cc * 16), "r"(row < 0 ? 0 : 16)
                          : "memory");
           }
+        };
+        if (nb) {
+          const uint32_t ri = g % kRing, st = g % kStages;
+          if (!(ok = wait(&bar.ix_row[ri], (g / kRing) & 1) && wait(&bar.kv_empty[st][2], ((g / kStages) & 1) ^ 1))) break;
+          copy_rope(st, sm->row[ri]);
+          copies_commit();
+#pragma unroll
+          for (int pass = 0; pass < 4; ++pass) load(pass, sm->row[ri]);
+        }
+        for (int j = 0; j < nb; ++j, ++g) {
+          const uint32_t st = g % kStages, sn = (g + 1) % kStages, rn = (g + 1) % kRing;
+          // The whole stage (its value products end last), the next block's rows, the next stage's rope atom.
+          uint64_t* const bs[3] = {&bar.kv_empty[st][1], &bar.ix_row[rn], &bar.kv_empty[sn][2]};
+          const uint32_t ph[3] = {((g / kStages) & 1) ^ 1, ((g + 1) / kRing) & 1, (((g + 1) / kStages) & 1) ^ 1};
           const bool more = j + 1 < nb;
-          if (!(ok = (!more || wait(&bar.ix_row[rn], ((g + 1) / kRing) & 1)) && wait(&bar.kv_empty[st][0], free) &&
-                     wait(&bar.kv_empty[st][1], free)))
-            break;
-          const uint32_t at = stage + (c >> 2) * kAtom + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 1)) << 4);
+          if (kPoll || !more || !__all_sync(0xffffffffu, try_wait3(bs[0], ph[0], bs[1], ph[1], bs[2], ph[2])))
+            if (!(ok = wait(bs[0], ph[0]) && (!more || (wait(bs[1], ph[1]) && wait(bs[2], ph[2]))))) break;
+          if (more) copy_rope(sn, sm->row[rn]);
+          copies_commit();
+          const uint32_t at = smem_addr(kv_s) + st * kStage + (c >> 2) * kAtom + r0 * 128 + (((2 * (c & 3)) ^ (r0 & 1)) << 4);
 #pragma unroll
           for (int pass = 0; pass < 4; ++pass) {
-            const ExpandFour x(grp[pass], sm->row[ri][r0 + 2 * pass] >= 0);  // (a skipped row is zeros)
+            const ExpandFour x(grp[pass]);
             const uint2 v0 = x(raw[pass].x), v1 = x(raw[pass].y), v2 = x(raw[pass].z), v3 = x(raw[pass].w);
             const uint32_t to = (at + 256 * pass) ^ (32 * pass);  // (row & 7 = 2 pass + its low bit)
             st_shared16(to, make_uint4(v0.x, v0.y, v1.x, v1.y));
             st_shared16(to ^ 16, make_uint4(v2.x, v2.y, v3.x, v3.y));
-            if (more) load(pass, rn);
+            if (more) load(pass, sm->row[rn]);
           }
-          asm volatile("cp.async.wait_all;\n" ::: "memory");
+          copies_wait<1>();  // this block's rope values
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.kv_full[st]);
         }

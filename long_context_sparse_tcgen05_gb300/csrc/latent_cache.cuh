@@ -60,10 +60,11 @@ __device__ __forceinline__ uint32_t pack_e2m1(float lo, float hi) {
 // two registers that a byte permutation looks up, four codes at a time.
 struct ExpandFour {
   uint32_t lo, hi;  // magnitudes 0-3 and 4-7
-  __device__ __forceinline__ explicit ExpandFour(uint32_t group, bool live = true) {  // !live: zeros of either sign
-    const uint32_t c = (group - 120u) * 0x08080808u;                // (bytes other than 122-133 give some codes)
-    lo = live ? (c & 0xffffff00u) + 0x03fff800u : 0u;               // [0, c - 8, c, c + 4]
-    hi = live ? c + 0x14100c08u : 0u;                               // [c + 8, c + 12, c + 16, c + 20]
+  __device__ __forceinline__ explicit ExpandFour(uint32_t group) {
+    // (four bits of the byte count: any byte gives finite values)
+    const uint32_t c = ((group - 122u) & 15u) * 0x08080808u + 0x10101010u;
+    lo = (c & 0xffffff00u) + 0x03fff800u;  // [0, c - 8, c, c + 4]
+    hi = c + 0x14100c08u;                  // [c + 8, c + 12, c + 16, c + 20]
   }
   __device__ __forceinline__ uint2 operator()(uint32_t w) const {
     const uint32_t m = w & 0x77777777u, t = w << 4;  // magnitudes; the even codes' signs at their bytes' tops
