@@ -9,16 +9,18 @@ namespace {
 constexpr int kJoinThreads = 256;
 constexpr int kMaxRuns = 1024;  // CTAs of a call
 
-// Puts the parts of split tiles together: O = sum_s w_s O_s, w_s = e^(lse_s - lse), in a fixed order.  Block (x, y)
-// takes the x-th split tile and the y-th `heads` heads of it (kQuarter: the y-th quarter of one head's dims): threads of a
-// row take four dims each, the rows of threads share the parts.
-template <bool kQuarter>
-__global__ void __launch_bounds__(kJoinThreads) k_latent_join(LatentAttnLaunch p, int ctas, int heads) {
-  constexpr int kCols = kQuarter ? kLatentDim / 16 : kLatentDim / 4, kGroups = kJoinThreads / kCols;
-  __shared__ float wgt[kMaxRuns];
-  __shared__ float4 sums[kGroups][kCols];
+// A split tile that block x of a join has to put together: the x-th of them.
+struct SplitTile {
+  int tile, run, parts, first_slot;
+  // Part s is of run `run - 1 + s`; the first one's is its last tile, the others' their first.
+  __device__ __forceinline__ const float* part(const LatentAttnLaunch& p, int s) const {
+    return p.parts + (int64_t)(s == 0 ? first_slot : 2 * (run - 1 + s)) * kPartFloats;
+  }
+};
+// Found by all threads of a block (parts = 0: there is none).
+__device__ __forceinline__ SplitTile find_split(const LatentAttnLaunch& p, int ctas) {
   __shared__ int2 starts[kMaxRuns];  // of each run: its first tile (-1: none) and block in it
-  __shared__ int found_run, found_parts;
+  __shared__ SplitTile found;
   const int t = threadIdx.x, lane = t & 31;
   for (int c = t; c < ctas; c += kJoinThreads) {
     const int4 s = p.shares[c];
@@ -47,62 +49,109 @@ __global__ void __launch_bounds__(kJoinThreads) k_latent_join(LatentAttnLaunch p
       more = k == 32;
     }
     if (t == 0) {
-      found_run = run;
-      found_parts = n;
+      found.run = run;
+      found.parts = run > 0 ? n : 0;
+      found.tile = run > 0 ? starts[run].x : 0;
+      found.first_slot = run > 0 ? 2 * (run - 1) + (starts[run - 1].x != starts[run].x) : 0;
     }
   }
   __syncthreads();
-  const int run = found_run, parts = found_parts;
-  if (run < 0) return;
-  const int tile = starts[run].x;
-  const Item I = item_of<kAll>(p, tile);
-  // Part s is of run `run - 1 + s`; the first one's is its last tile, the others' their first.
-  const int first_slot = 2 * (run - 1) + (starts[run - 1].x != tile);
-  auto part = [&](int s) -> const float* { return p.parts + (int64_t)(s == 0 ? first_slot : 2 * (run - 1 + s)) * kPartFloats; };
+  return found;
+}
+
+// Puts the parts of split tiles together: O = sum_s w_s O_s, w_s = e^(lse_s - lse), in the order of the parts.  Block
+// (x, y) takes the x-th split tile and the y-th `heads` heads of it, a warp a quarter of a head's dims.
+__global__ void __launch_bounds__(kJoinThreads) k_latent_join(LatentAttnLaunch p, int ctas, int heads) {
+  const SplitTile f = find_split(p, ctas);
+  if (f.parts == 0) return;
+  const Item I = item_of<kAll>(p, f.tile);
   const int64_t out0 = (int64_t)I.row * p.H + I.h0;
-  const int group = t / kCols, col = t % kCols, col0 = kQuarter ? blockIdx.y % 4 * kCols : 0;
-  const int h0 = kQuarter ? blockIdx.y / 4 : blockIdx.y * heads;
-  for (int h = h0; h < min(h0 + (kQuarter ? 1 : heads), I.heads); ++h) {
-    if (t < 32) {
-      float mx = -INFINITY, sum = 0.f;
-      for (int s = lane; s < parts; s += 32) {
-        const float v = part(s)[kHg * kLatentDim + h];
-        wgt[s] = v;
-        mx = fmaxf(mx, v);
-      }
+  const int lane = threadIdx.x & 31, end = min((int)(blockIdx.y + 1) * heads, I.heads) * 4;
+  for (int u = blockIdx.y * heads * 4 + (threadIdx.x >> 5); u < end; u += kJoinThreads / 32) {
+    const int h = u >> 2, quarter = u & 3;
+    float mx = -INFINITY, sum = 0.f;
+    for (int s = lane; s < f.parts; s += 32) mx = fmaxf(mx, f.part(p, s)[kHg * kLatentDim + h]);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      for (int s = lane; s < parts; s += 32) sum += wgt[s] = wgt[s] == -INFINITY ? 0.f : expf(wgt[s] - mx);  // (a NaN stays)
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      for (int s = lane; s < parts; s += 32) wgt[s] = sum == 0.f ? 0.f : wgt[s] / sum;
-      if (t == 0 && p.lse && col0 == 0) p.lse[out0 + h] = sum == 0.f ? -INFINITY : mx + logf(sum);
-    }
-    __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int s = group; s < parts; s += kGroups) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(part(s) + h * kLatentDim) + col0 + col);
-      const float w = wgt[s];
-      acc.x += w * x.x;
-      acc.y += w * x.y;
-      acc.z += w * x.z;
-      acc.w += w * x.w;
-    }
-    sums[group][col] = acc;
-    __syncthreads();
-    if (!group) {
-      for (int i = 1; i < min(kGroups, parts); ++i) {
-        const float4 x = sums[i][col];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
+    for (int s0 = 0; s0 < f.parts; s0 += 32) {
+      float w = 0.f;
+      if (s0 + lane < f.parts) {
+        const float v = f.part(p, s0 + lane)[kHg * kLatentDim + h];
+        w = v == -INFINITY ? 0.f : expf(v - mx);  // (a NaN stays)
       }
-      reinterpret_cast<uint2*>(p.out + (out0 + h) * kLatentDim)[col0 + col] = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+      sum += w;
+#pragma unroll 8
+      for (int s = s0; s < min(s0 + 32, f.parts); ++s) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(f.part(p, s) + h * kLatentDim + quarter * (kLatentDim / 4)) + lane);
+        const float ws = __shfl_sync(0xffffffffu, w, s - s0);
+        acc.x += ws * x.x;
+        acc.y += ws * x.y;
+        acc.z += ws * x.z;
+        acc.w += ws * x.w;
+      }
     }
-    __syncthreads();  // (wgt and sums are free)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float r = sum == 0.f ? 0.f : 1.f / sum;
+    reinterpret_cast<uint2*>(p.out + (out0 + h) * kLatentDim + quarter * (kLatentDim / 4))[lane] =
+        make_uint2(pack_bf16(acc.x * r, acc.y * r), pack_bf16(acc.z * r, acc.w * r));
+    if (p.lse && quarter == 0 && lane == 0) p.lse[out0 + h] = sum == 0.f ? -INFINITY : mx + logf(sum);
   }
+}
+
+// The same of few tiles, which may have a part on every SM: block (x, y) takes a quarter of one head's dims, each of its
+// warps every eighth part.  (131,072 rows of one sequence, 152 parts: 8 us.)
+__global__ void __launch_bounds__(kJoinThreads) k_latent_join_long(LatentAttnLaunch p, int ctas) {
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ float lse[kMaxRuns];
+  __shared__ float4 sums[kWarps][32];
+  __shared__ float sum_s;
+  const SplitTile f = find_split(p, ctas);
+  if (f.parts == 0) return;
+  const Item I = item_of<kAll>(p, f.tile);
+  const int h = blockIdx.y >> 2, quarter = blockIdx.y & 3, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (h >= I.heads) return;
+  for (int s = t; s < f.parts; s += kJoinThreads) lse[s] = f.part(p, s)[kHg * kLatentDim + h];
+  __syncthreads();
+  float mx = -INFINITY;
+  for (int s = lane; s < f.parts; s += 32) mx = fmaxf(mx, lse[s]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  auto weight = [&](int s) { return lse[s] == -INFINITY ? 0.f : expf(lse[s] - mx); };  // (a NaN stays)
+  if (warp == 0) {
+    float sum = 0.f;
+    for (int s = lane; s < f.parts; s += 32) sum += weight(s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sum_s = sum;
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = warp; s < f.parts; s += kWarps) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(f.part(p, s) + h * kLatentDim + quarter * (kLatentDim / 4)) + lane);
+    const float w = weight(s);
+    acc.x += w * x.x;
+    acc.y += w * x.y;
+    acc.z += w * x.z;
+    acc.w += w * x.w;
+  }
+  sums[warp][lane] = acc;
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int i = 1; i < kWarps; ++i) {
+    const float4 x = sums[i][lane];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+  }
+  const int64_t row = (int64_t)I.row * p.H + I.h0 + h;
+  const float r = sum_s == 0.f ? 0.f : 1.f / sum_s;
+  reinterpret_cast<uint2*>(p.out + row * kLatentDim + quarter * (kLatentDim / 4))[lane] =
+      make_uint2(pack_bf16(acc.x * r, acc.y * r), pack_bf16(acc.z * r, acc.w * r));
+  if (p.lse && quarter == 0 && lane == 0) p.lse[row] = sum_s == 0.f ? -INFINITY : mx + logf(sum_s);
 }
 
 template <bool kFour>
@@ -145,11 +194,11 @@ cudaError_t launch(LatentAttnLaunch p, cudaStream_t st) {
   if (runs > 1) {
     const int split = std::min(runs - 1, p.B * p.tiles_t * p.groups);  // split tiles, at most
     const int most = std::min(kHg, p.H * p.tile_t);
-    if (split <= 8) {  // few tiles of many parts: more blocks a tile
-      k_latent_join<true><<<dim3(split, 4 * most), kJoinThreads, 0, st>>>(p, runs, 1);
+    if (split <= 8) {
+      k_latent_join_long<<<dim3(split, 4 * most), kJoinThreads, 0, st>>>(p, runs);
     } else {
       const int heads = split <= 64 ? 2 : 8;
-      k_latent_join<false><<<dim3(split, (most + heads - 1) / heads), kJoinThreads, 0, st>>>(p, runs, heads);
+      k_latent_join<<<dim3(split, (most + heads - 1) / heads), kJoinThreads, 0, st>>>(p, runs, heads);
     }
     count_launches(1);
   }

@@ -61,6 +61,7 @@
 
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "dsa_internal.cuh"
 #include "fp8_rows.cuh"
@@ -407,63 +408,75 @@ __device__ __forceinline__ int dense_blocks(int sees) { return max(1, (sees + kN
 
 // This CTA's share of a call over all rows.  The blocks of all tiles, one tile after another, are divided into
 // equal runs, one a CTA, so sequences of any lengths keep the SMs evenly busy.  A run starts and ends inside tiles:
-// those are parts, which k_latent_join puts together.  Every CTA counts all tiles (a few instructions each, over 768
-// threads; a tile's own work is thousands of cycles).  false: nothing to do.
+// those are parts, which k_latent_join puts together.  Every CTA counts all tiles (a few instructions each, over its
+// threads; a tile's own work is thousands of cycles): each thread its tiles' blocks, then, all threads having
+// met, find() places the run's ends.
 template <int kThreads>
-__device__ __forceinline__ bool find_share(const LatentAttnLaunch& p, DenseShare& s, int64_t* room) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tiles = p.B * p.tiles_t * p.groups, per = (tiles + kThreads - 1) / kThreads;
-  const int lo = min((int)threadIdx.x * per, tiles), hi = min(lo + per, tiles);
-  auto walk = [&](auto&& f) {  // f(tile, blocks) -> go on
-    for (int i = lo; i < hi; ++i) {
-      const Item I = item_of<kAll>(p, i);
-      if (!f(i, dense_blocks(dense_sees(p, I.last, __ldg(p.lens + I.b))))) return;
-    }
-  };
-  int64_t sum = 0;
-  walk([&](int, int n) { return sum += n, true; });
-  int64_t upto = sum;
+struct ShareCount {
+  const LatentAttnLaunch& p;
+  int64_t sum, upto;  // blocks of this thread's tiles; of its warp's threads up to it
+  int lo, hi;
+  __device__ __forceinline__ int blocks(int tile) const {
+    const Item I = item_of<kAll>(p, tile);
+    return dense_blocks(dense_sees(p, I.last, __ldg(p.lens + I.b)));
+  }
+  __device__ __forceinline__ ShareCount(const LatentAttnLaunch& p, int64_t* room) : p(p) {
+    const int tiles = p.B * p.tiles_t * p.groups, per = (tiles + kThreads - 1) / kThreads;
+    lo = min((int)threadIdx.x * per, tiles);
+    hi = min(lo + per, tiles);
+    sum = 0;
+    for (int i = lo; i < hi; ++i) sum += blocks(i);
+    upto = sum;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) room[threadIdx.x >> 5] = upto;
   }
-  if (lane == 31) room[warp] = upto;
-  __syncthreads();
-  int64_t total = 0, before = upto - sum;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += room[w];
-    total += room[w];
-  }
-  const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinRun)), c = blockIdx.x;
-  const int64_t from = total * c / ctas, to = total * (c + 1) / ctas;  // this run: blocks [from, to)
-  if (c >= ctas) {
-    if (threadIdx.x == 0) p.shares[c] = make_int4(-1, 0, -1, 0);
-    return false;
-  }
-  if (from >= before && from < before + sum) {
-    int64_t at = before;
-    walk([&](int i, int n) {
-      if (from >= at + n) return at += n, true;
-      s.first = i;
-      s.first_j0 = (int)(from - at);
+  // false: nothing to do.  (All threads meet in it.)
+  __device__ __forceinline__ bool find(DenseShare& s, const int64_t* room) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t upto_warp = lane < kThreads / 32 ? room[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto_warp, o);
+      if (lane >= o) upto_warp += v;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, upto_warp, 31);
+    const int64_t above = __shfl_sync(0xffffffffu, upto_warp, warp > 0 ? warp - 1 : 0);
+    const int64_t before = (warp > 0 ? above : 0) + upto - sum;
+    // run c: blocks [from, to) (one division, in 32 bits where they suffice)
+    const int c = blockIdx.x, ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinRun));
+    if (c >= ctas) {
+      if (threadIdx.x == 0) p.shares[c] = make_int4(-1, 0, -1, 0);
       return false;
-    });
+    }
+    const int64_t each = total >> 32 ? total / ctas : (int64_t)((uint32_t)total / (uint32_t)ctas);
+    const int rest = (int)(total - each * ctas);
+    const int64_t from = each * c + min(c, rest), to = each * (c + 1) + min(c + 1, rest);
+    if (from < before + sum && to > before) {  // the run has blocks of this thread's tiles
+      int64_t at = before;
+      for (int i = lo; i < hi && at < to; ++i) {
+        const int n = blocks(i);
+        if (from >= at && from < at + n) {
+          s.first = i;
+          s.first_j0 = (int)(from - at);
+        }
+        if (to > at && to <= at + n) {
+          s.last = i;
+          s.last_end = (int)(to - at);
+          s.last_whole = s.last_end == n;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) p.shares[c] = make_int4(s.first, s.first_j0, s.last, s.last_whole);
+    return true;
   }
-  if (to > before && to <= before + sum) {
-    int64_t at = before;
-    walk([&](int i, int n) {
-      if (to > at + n) return at += n, true;
-      s.last = i;
-      s.last_end = (int)(to - at);
-      s.last_whole = s.last_end == n;
-      return false;
-    });
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) p.shares[c] = make_int4(s.first, s.first_j0, s.last, s.last_whole);
-  return true;
-}
+};
 
 // kPoll: a wait limit below the default.  kParts: an item is a part of a row, one a CTA.  (A kernel of its
 // own: the loops of a chunk run at the pace of their instruction fetches, 1.09 against 0.99 ms with the
@@ -482,11 +495,6 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   int first = blockIdx.x, items = p.B * p.T * p.groups * p.splits;
   const int G = kForm == kAll ? 1 : (int)gridDim.x;
-  if constexpr (kForm == kAll) {
-    if (!find_share<kThreads<kFour>>(p, sm->share, reinterpret_cast<int64_t*>(kv_s))) return;
-    first = sm->share.first;
-    items = sm->share.last + 1;
-  }
   // a wait that every lane of a warp makes, with one answer for the warp
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity, abort_flag, p.wait));
@@ -527,10 +535,24 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     tmem_alloc(&sm->tmem, kTmemCols);
     tmem_relinquish();
   }
+  int64_t* const room = reinterpret_cast<int64_t*>(kv_s);  // (no stage is in use yet)
+  using Count = std::conditional_t<kForm == kAll, ShareCount<kThreads<kFour>>, int>;
+  const Count count = [&] {
+    if constexpr (kForm == kAll) return Count(p, room);
+    else return 0;
+  }();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm->tmem, 0);
+  if constexpr (kForm == kAll) {
+    if (!count.find(sm->share, room)) {
+      if (warp == kSWarp) tmem_dealloc(tmem, kTmemCols);
+      return;
+    }
+    first = sm->share.first;
+    items = sm->share.last + 1;
+  }
 
   // Every n-th head of an item's queries, from w on, to hi and lo rows in shared memory (so few heads are
   // spread over the warps too; zeros where there is none).  Two heads at a time, 16 latent values and 2
