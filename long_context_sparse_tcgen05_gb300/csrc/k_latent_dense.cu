@@ -81,14 +81,21 @@ __global__ void __launch_bounds__(kJoinThreads) k_latent_join(LatentAttnLaunch p
         w = v == -INFINITY ? 0.f : expf(v - mx);  // (a NaN stays)
       }
       sum += w;
-#pragma unroll 8
-      for (int s = s0; s < min(s0 + 32, f.parts); ++s) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(f.part(p, s) + h * kLatentDim + quarter * (kLatentDim / 4)) + lane);
-        const float ws = __shfl_sync(0xffffffffu, w, s - s0);
-        acc.x += ws * x.x;
-        acc.y += ws * x.y;
-        acc.z += ws * x.z;
-        acc.w += ws * x.w;
+      for (int s = s0; s < min(s0 + 32, f.parts); s += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // (four on their way together; the last part again where there is none)
+          x[i] = __ldg(reinterpret_cast<const float4*>(f.part(p, min(s + i, f.parts - 1)) + h * kLatentDim + quarter * (kLatentDim / 4)) + lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float ws = __shfl_sync(0xffffffffu, w, s - s0 + i);  // (0 past the last part)
+          if (s + i < f.parts) {
+            acc.x += ws * x[i].x;
+            acc.y += ws * x[i].y;
+            acc.z += ws * x[i].z;
+            acc.w += ws * x[i].w;
+          }
+        }
       }
     }
 #pragma unroll

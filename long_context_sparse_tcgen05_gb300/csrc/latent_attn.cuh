@@ -97,7 +97,7 @@ struct Regs {
 };
 template <>
 struct Regs<true> {
-  static constexpr int kLaunch = kLatent4AttnRegs, kGather = 56, kIssue = 56, kSm = 104, kEpi = 64;
+  static constexpr int kLaunch = kLatent4AttnRegs, kGather = 64, kIssue = 56, kSm = 96, kEpi = 64;
   static_assert(2 * kGather + kIssue + 2 * kSm + 2 * kEpi <= 7 * kLaunch, "registers the block is launched with");
 };
 constexpr uint32_t kTmemCols = 512;
@@ -857,10 +857,12 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         const int r0 = w0 + ((lane >> 2) & 1), c = (lane & 3) + 4 * (lane >> 3);
         uint4 raw[4];
         uint32_t grp[4];
+        const uint8_t* const codes_c = codes + 16 * c;
+        const uint8_t* const groups_c = p.cache.groups + c;
         auto load = [&](int pass, const int32_t* rows) {
           const uint32_t row = (uint32_t)max(rows[r0 + 2 * pass], 0);
-          raw[pass] = __ldg(reinterpret_cast<const uint4*>(p.cache.codes + (uint64_t)row * (kLatentDim / 2)) + c);
-          grp[pass] = __ldg(p.cache.groups + (uint64_t)row * kLatentGroups + c);
+          raw[pass] = __ldg(reinterpret_cast<const uint4*>(codes_c + (uint64_t)row * (kLatentDim / 2)));
+          grp[pass] = __ldg(groups_c + (uint64_t)row * kLatentGroups);
         };
         auto copy_rope = [&](uint32_t st, const int32_t* rows) {
 #pragma unroll
