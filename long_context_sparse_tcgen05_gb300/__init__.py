@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -131,6 +132,8 @@ _lib = None
 def load_library(path: str = LIB_PATH):
     """Load libdsa.so (built by ``build.build()``).  Raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -302,7 +305,7 @@ def _flag_word(dev) -> torch.Tensor:
 
 def _launch(dev, fn, *args) -> None:
     """fn(*args, stream) on `dev`'s current stream, with `dev` current."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
         if status:
             _check(status)
@@ -603,7 +606,7 @@ def _addr(t, dev, dtype, what: str, n: int | None = None):
     """Device address of an optional dense operand, checked against `dev`, dtype and size."""
     if t is None:
         return None
-    assert t.dtype == dtype and t.is_contiguous() and t.device == dev, f"{what}: a dense {dtype} tensor on {dev} is expected"
+    assert t.dtype is dtype and t.is_contiguous() and t.device == dev, f"{what}: a dense {dtype} tensor on {dev} is expected"
     assert n is None or t.numel() == n, f"{what}: {n} values are expected"
     return t.data_ptr()
 
@@ -687,46 +690,65 @@ def dsa_norm_rope_e4m3(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tenso
     return codes, scales
 
 
-def _cache_parts(cache, B):
-    """(pages, page size, table entries a sequence, addresses of scales, rope and table, sequences) of a cache dict."""
+# Native images of the cache and attention structs: packed in one step, where a ctypes structure takes a microsecond or
+# two to fill field by field.
+_CACHE, _CACHE4 = struct.Struct("@iiiPPPP"), struct.Struct("@iiiPPPPP")
+_APPEND = struct.Struct("@iiPqqPfPPiiPq")
+_ATTN_HEAD, _ATTN_TAIL = struct.Struct("@iiiifPqq"), struct.Struct("@iP")
+
+
+def _latent_cache(cache, B):
+    """(image of a dsa_latent_cache, sequences, rows a sequence holds) of a latent cache dict."""
     codes, scales, rope, table = cache["codes"], cache["scales"], cache["rope"], cache.get("block_table")
     dev = codes.device
     pages, page = scales.shape
-    assert codes.is_cuda and codes.is_contiguous() and codes.shape[:2] == scales.shape and rope.shape == (pages, page, 64)
-    seqs = pages if table is None else table.shape[0]
+    assert codes.is_cuda and codes.dtype in (torch.float8_e4m3fn, torch.uint8) and codes.is_contiguous()
+    assert codes.shape == (pages, page, 512) and rope.shape == (pages, page, 64)
+    seqs, ld = (pages, 0) if table is None else table.shape
     assert B is None or (B <= seqs if table is None else B == seqs), "the cache's sequences and the call's differ"
-    return (pages, page, 0 if table is None else table.shape[1], _addr(scales, dev, torch.float32, "scales"),
-            _addr(rope, dev, torch.bfloat16, "rope"), _addr(table, dev, torch.int32, "block_table"), seqs)
+    return _CACHE.pack(pages, page, ld, codes.data_ptr(), _addr(scales, dev, torch.float32, "scales") or 0,
+                       _addr(rope, dev, torch.bfloat16, "rope") or 0, _addr(table, dev, torch.int32, "block_table") or 0), seqs, (ld or 1) * page
+
+
+def _latent4_cache(cache, B):
+    """_latent_cache of a 4-bit one."""
+    codes, groups, scales, rope, table = cache["codes"], cache["groups"], cache["scales"], cache["rope"], cache.get("block_table")
+    dev = codes.device
+    pages, page = scales.shape
+    assert codes.is_cuda and codes.dtype is torch.uint8 and codes.is_contiguous(), "codes: uint8, two codes a byte"
+    assert codes.shape == (pages, page, 256) and groups.shape == (pages, page, 16) and rope.shape == (pages, page, 64)
+    seqs, ld = (pages, 0) if table is None else table.shape
+    assert B is None or (B <= seqs if table is None else B == seqs), "the cache's sequences and the call's differ"
+    return _CACHE4.pack(pages, page, ld, codes.data_ptr(), _addr(groups, dev, torch.uint8, "groups"),
+                        _addr(scales, dev, torch.float32, "scales") or 0, _addr(rope, dev, torch.bfloat16, "rope") or 0,
+                        _addr(table, dev, torch.int32, "block_table") or 0), seqs, (ld or 1) * page
 
 
 def latent_cache_struct(cache: dict, B: int | None = None):
     """(C struct, sequences) of a latent cache dict."""
-    codes = cache["codes"]
-    assert codes.dtype in (torch.float8_e4m3fn, torch.uint8) and codes.shape[2] == 512, "codes: [pages, page, 512] e4m3"
-    pages, page, ld, scales, rope, table, seqs = _cache_parts(cache, B)
-    return LatentCache(pages, page, ld, codes.data_ptr(), scales, rope, table), seqs
+    image, seqs, _ = _latent_cache(cache, B)
+    return LatentCache.from_buffer_copy(image), seqs
 
 
 def latent4_cache_struct(cache: dict, B: int | None = None):
     """(C struct, sequences) of a 4-bit latent cache dict."""
-    codes, groups = cache["codes"], cache["groups"]
-    assert codes.dtype == torch.uint8 and codes.shape[2] == 256, "codes: [pages, page, 256] uint8, two codes a byte"
-    pages, page, ld, scales, rope, table, seqs = _cache_parts(cache, B)
-    assert groups.shape == (pages, page, 16)
-    return Latent4Cache(pages, page, ld, codes.data_ptr(), _addr(groups, codes.device, torch.uint8, "groups"), scales, rope,
-                        table), seqs
+    image, seqs, _ = _latent4_cache(cache, B)
+    return Latent4Cache.from_buffer_copy(image), seqs
 
 
-def _append_rows(struct, call, x, cache, weight, eps, cos, sin, interleaved, pos0, positions):
+def _append_rows(cache_struct, call, x, cache, weight, eps, cos, sin, interleaved, pos0, positions):
     dev = x.device
-    assert x.is_cuda and x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[2] == 576 and x.stride(2) == 1
-    B, n = x.shape[:2]
-    lc, _ = struct(cache, B)
+    assert x.is_cuda and x.dtype is torch.bfloat16 and x.dim() == 3
+    B, n, width = x.shape
+    assert width == 576 and x.stride(2) == 1
+    lc, _ = cache_struct(cache, B)
     assert cache["codes"].device == dev
     c, s, rows, angles = _tables(cos, sin, dev)
     assert c is None or angles == 32, "cos and sin: 32 angles for the 64 rope values"
-    a = LatentAppendArgs(B, n, x.data_ptr(), *_token_strides(x), _addr(weight, dev, torch.float32, "weight", 512),
-                         eps, c, s, interleaved, rows, _addr(positions, dev, torch.int64, "positions", B * n), pos0)
+    a = LatentAppendArgs.from_buffer_copy(_APPEND.pack(
+        B, n, x.data_ptr(), *_token_strides(x), _addr(weight, dev, torch.float32, "weight", 512) or 0, 0.0, c or 0, s or 0,
+        bool(interleaved), rows, _addr(positions, dev, torch.int64, "positions", B * n) or 0, 0))
+    a.eps, a.pos0 = eps, pos0
     if n:
         ws = _flag_word(dev)
         _launch(dev, getattr(load_library(), call), _c.byref(a), _c.byref(lc), ws.data_ptr(), WS_MIN)
@@ -749,23 +771,27 @@ def dsa_latent4_append(x: torch.Tensor, cache: dict, *, weight: torch.Tensor | N
     return _append_rows(latent4_cache_struct, "dsa_latent4_append", x, cache, weight, eps, cos, sin, interleaved, pos0, positions)
 
 
-def _read_args(struct, cache, idx, n):
+def _read_args(cache_struct, cache, idx, n):
     """(C struct, sequences, rows of each, address of idx) of a read."""
-    lc, B = struct(cache)
+    lc, B = cache_struct(cache)
     assert (idx is None) != (n is None), "either idx or n"
     if idx is None:
         return lc, B, n, None
-    assert idx.dim() == 2 and idx.shape[0] <= B and (cache.get("block_table") is None or idx.shape[0] == B)
-    return lc, idx.shape[0], idx.shape[1], _addr(idx, cache["codes"].device, torch.int32, "idx")
+    assert idx.dim() == 2
+    b, n = idx.shape
+    assert b <= B and (b == B or cache.get("block_table") is None)
+    return lc, b, n, _addr(idx, cache["codes"].device, torch.int32, "idx")
 
 
-def _read_rows(struct, call, cache, idx, n, pos0, out):
+def _read_rows(cache_struct, call, cache, idx, n, pos0, out):
     dev = cache["codes"].device
-    lc, B, n, ip = _read_args(struct, cache, idx, n)
+    lc, B, n, ip = _read_args(cache_struct, cache, idx, n)
     if out is None:
         out = torch.empty((B, n, 576), dtype=torch.bfloat16, device=dev)
-    assert out.shape == (B, n, 576)
-    op = _addr(out, dev, torch.bfloat16, "out")
+        op = out.data_ptr()
+    else:
+        assert out.shape == (B, n, 576)
+        op = _addr(out, dev, torch.bfloat16, "out")
     if n:
         ws = _flag_word(dev)
         _launch(dev, getattr(load_library(), call), _c.byref(lc), B, n, ip, pos0, op, ws.data_ptr(), WS_MIN)
@@ -800,59 +826,69 @@ def dsa_latent4_unpack(cache: dict, idx: torch.Tensor | None = None, *, n: int |
     return out
 
 
-def _latent_attn_args(args, cache_struct, at, idx_T):
-    """The C struct `args` of an attention operand dict over the kind of cache that `cache_struct` takes."""
+def _latent_attn_args(args, image_of, at, idx_T):
+    """The C struct `args` of an attention operand dict over the kind of cache that `image_of` takes."""
     q, cache = at["q"], at["cache"]
     B, T, H, d = q.shape
-    assert q.is_cuda and q.dtype == torch.bfloat16 and d == 576 and q.stride(3) == 1
+    assert q.is_cuda and q.dtype is torch.bfloat16 and d == 576 and q.stride(3) == 1
     assert H == 1 or q.stride(2) == 576, "the heads of one query must be contiguous"
-    lc, _ = cache_struct(cache, B)
+    image, _, rows = image_of(cache, B)
     assert cache["codes"].device == q.device
     S = at.get("S")
     if S is None:
-        S = min((lc.table_ld if lc.block_table else 1) * lc.page_size, 2 ** 31 - 1)
+        S = min(rows, 2 ** 31 - 1)
     assert 0 < S < 2 ** 31, "S: between 1 and 2^31 - 1 positions"
-    return args(B, T, int(S), H, at["scale"], q.data_ptr(), *_token_strides(q), lc, idx_T, None)
+    a = args.from_buffer_copy(_ATTN_HEAD.pack(B, T, int(S), H, 0.0, q.data_ptr(), *_token_strides(q)) + image + _ATTN_TAIL.pack(idx_T, 0))
+    a.scale = at["scale"]
+    return a
 
 
 def latent_attn_struct(at: dict, idx: torch.Tensor) -> LatentAttnArgs:
     """The C struct of a latent attention operand dict: q [B,T,H,576] bf16 (strided along its batch
     and token axes), cache, scale and S (the positions idx may name; None: all a sequence holds)."""
-    _check_idx(at, idx)
-    return _latent_attn_args(LatentAttnArgs, latent_cache_struct, at, idx.shape[1])
+    return _latent_attn_args(LatentAttnArgs, _latent_cache, at, _idx_rows(at, idx))
 
 
 def latent4_attn_struct(at: dict, idx: torch.Tensor) -> Latent4AttnArgs:
     """latent_attn_struct of a 4-bit cache."""
-    _check_idx(at, idx)
-    return _latent_attn_args(Latent4AttnArgs, latent4_cache_struct, at, idx.shape[1])
+    return _latent_attn_args(Latent4AttnArgs, _latent4_cache, at, _idx_rows(at, idx))
 
 
-def _check_idx(at, idx):
-    B, T = at["q"].shape[:2]
-    assert idx.dim() == 3 and idx.shape[0] == B and idx.shape[1] in (1, T), "idx: [B, T or 1, k]"
+def _idx_rows(at, idx):
+    B, T, _, _ = at["q"].shape
+    assert idx.dim() == 3, "idx: [B, T or 1, k]"
+    b, t, _ = idx.shape
+    assert b == B and (t == T or t == 1), "idx: [B, T or 1, k]"
+    return t
 
 
 def _attn_outputs(a, dev, out, lse):
     """(out, its address, lse, its address) of an attention call, allocated where asked for."""
     if out is None:
         out = torch.empty((a.B, a.T, a.H, 512), dtype=torch.bfloat16, device=dev)
-    assert out.shape == (a.B, a.T, a.H, 512)
+        op = out.data_ptr()
+    else:
+        assert out.shape == (a.B, a.T, a.H, 512)
+        op = _addr(out, dev, torch.bfloat16, "out")
     if lse is True:
         lse = torch.empty((a.B, a.T, a.H), dtype=torch.float32, device=dev)
-    elif lse is False:
+        return out, op, lse, lse.data_ptr()
+    if lse is False:
         lse = None
-    return out, _addr(out, dev, torch.bfloat16, "out"), lse, _addr(lse, dev, torch.float32, "lse", a.B * a.T * a.H)
+    return out, op, lse, _addr(lse, dev, torch.float32, "lse", a.B * a.T * a.H)
+
+
+def _own_workspace(ws, dev):
+    assert ws.device == dev and ws.dtype is torch.uint8 and ws.is_contiguous()
+    return ws.data_ptr(), ws.numel()
 
 
 def _attn_rows(a, call, at, idx, out, lse, ws):
     dev = at["q"].device
     ip = _addr(idx, dev, torch.int32, "idx")
     out, op, lse, lp = _attn_outputs(a, dev, out, lse)
-    if ws is None:
-        ws = _flag_word(dev)
-    assert ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous()
-    _launch(dev, getattr(load_library(), call), _c.byref(a), ip, idx.shape[2], op, lp, ws.data_ptr(), ws.numel())
+    wp, n = (_flag_word(dev).data_ptr(), WS_MIN) if ws is None else _own_workspace(ws, dev)
+    _launch(dev, getattr(load_library(), call), _c.byref(a), ip, idx.shape[2], op, lp, wp, n)
     return out, lse
 
 
@@ -883,14 +919,16 @@ def _attn_dense(a, call, at, lens, causal, out, lse, ws):
     if ws is None:
         # scratch of this call alone (a captured graph keeps its own); the device's flag word
         a.flags = _flag_word(dev).data_ptr()
-        if dev.index == torch.cuda.current_device():
+        if dev.index == torch._C._cuda_getDevice():
             need = lib.dsa_latent_attn_dense_workspace_size(a.B, a.T, a.S, a.H)
         else:
             with torch.cuda.device(dev):
                 need = lib.dsa_latent_attn_dense_workspace_size(a.B, a.T, a.S, a.H)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    assert ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous()
-    _launch(dev, getattr(lib, call), _c.byref(a), lp, bool(causal), op, lse_p, ws.data_ptr(), ws.numel())
+        wp, n = ws.data_ptr(), need
+    else:
+        wp, n = _own_workspace(ws, dev)
+    _launch(dev, getattr(lib, call), _c.byref(a), lp, bool(causal), op, lse_p, wp, n)
     return out, lse
 
 
@@ -901,14 +939,14 @@ def dsa_latent_attn_dense(at: dict, lens: torch.Tensor, *, causal: bool = True, 
     rows, each seeing itself and what precedes it; else all see all.  at: as for dsa_latent_attn (S: no sequence
     holds more).  `ws`: a workspace of latent_dense_workspace_size bytes (uint8, zero-filled once) to use, with its flag
     word, instead of scratch of this call's own and the device's flag word."""
-    return _attn_dense(_latent_attn_args(LatentAttnArgs, latent_cache_struct, at, 1), "dsa_latent_attn_dense", at, lens,
+    return _attn_dense(_latent_attn_args(LatentAttnArgs, _latent_cache, at, 1), "dsa_latent_attn_dense", at, lens,
                        causal, out, lse, ws)
 
 
 def dsa_latent4_attn_dense(at: dict, lens: torch.Tensor, *, causal: bool = True, out: torch.Tensor | None = None,
                            lse: torch.Tensor | bool | None = True, ws: torch.Tensor | None = None):
     """dsa_latent_attn_dense over a 4-bit cache."""
-    return _attn_dense(_latent_attn_args(Latent4AttnArgs, latent4_cache_struct, at, 1), "dsa_latent4_attn_dense", at, lens,
+    return _attn_dense(_latent_attn_args(Latent4AttnArgs, _latent4_cache, at, 1), "dsa_latent4_attn_dense", at, lens,
                        causal, out, lse, ws)
 
 
