@@ -69,6 +69,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_latent_join(LatentAttnLaunch p
   const int lane = threadIdx.x & 31, end = min((int)(blockIdx.y + 1) * heads, I.heads) * 4;
   for (int u = blockIdx.y * heads * 4 + (threadIdx.x >> 5); u < end; u += kJoinThreads / 32) {
     const int h = u >> 2, quarter = u & 3;
+    auto piece = [&](int s) { return reinterpret_cast<const float4*>(f.part(p, s) + h * kLatentDim + quarter * (kLatentDim / 4)) + lane; };
+    // eight parts on their way together, the first eight before their weights
+    constexpr int kAtOnce = 8;
+    float4 x[kAtOnce];
+    auto load = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (s + i < f.parts) x[i] = __ldg(piece(s + i));
+    };
+    load(0);
     float mx = -INFINITY, sum = 0.f;
     for (int s = lane; s < f.parts; s += 32) mx = fmaxf(mx, f.part(p, s)[kHg * kLatentDim + h]);
 #pragma unroll
@@ -81,14 +91,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_latent_join(LatentAttnLaunch p
         w = v == -INFINITY ? 0.f : expf(v - mx);  // (a NaN stays)
       }
       sum += w;
-      for (int s = s0; s < min(s0 + 32, f.parts); s += 4) {
-        float4 x[4];
+      for (int s = s0; s < min(s0 + 32, f.parts); s += kAtOnce) {
+        if (s > 0) load(s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // (four on their way together; the last part again where there is none)
-          x[i] = __ldg(reinterpret_cast<const float4*>(f.part(p, min(s + i, f.parts - 1)) + h * kLatentDim + quarter * (kLatentDim / 4)) + lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float ws = __shfl_sync(0xffffffffu, w, s - s0 + i);  // (0 past the last part)
+        for (int i = 0; i < kAtOnce; ++i) {
+          const float ws = __shfl_sync(0xffffffffu, w, s - s0 + i);
           if (s + i < f.parts) {
             acc.x += ws * x[i].x;
             acc.y += ws * x[i].y;
@@ -119,6 +126,17 @@ __global__ void __launch_bounds__(kJoinThreads) k_latent_join_long(LatentAttnLau
   const Item I = item_of<kAll>(p, f.tile);
   const int h = blockIdx.y >> 2, quarter = blockIdx.y & 3, t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (h >= I.heads) return;
+  // A warp's parts on their way together, all of them where there are up to 160 parts, before their weights.
+  constexpr int kAtOnce = 20;
+  float4 x[kAtOnce];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int s = s0 + i * kWarps;
+      if (s < f.parts) x[i] = __ldg(reinterpret_cast<const float4*>(f.part(p, s) + h * kLatentDim + quarter * (kLatentDim / 4)) + lane);
+    }
+  };
+  load(warp);
   for (int s = t; s < f.parts; s += kJoinThreads) lse[s] = f.part(p, s)[kHg * kLatentDim + h];
   __syncthreads();
   float mx = -INFINITY;
@@ -134,14 +152,19 @@ __global__ void __launch_bounds__(kJoinThreads) k_latent_join_long(LatentAttnLau
     if (lane == 0) sum_s = sum;
   }
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int s = warp; s < f.parts; s += kWarps) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(f.part(p, s) + h * kLatentDim + quarter * (kLatentDim / 4)) + lane);
-    const float w = weight(s);
-    acc.x += w * x.x;
-    acc.y += w * x.y;
-    acc.z += w * x.z;
-    acc.w += w * x.w;
+  for (int s0 = warp; s0 < f.parts; s0 += kAtOnce * kWarps) {
+    if (s0 != warp) load(s0);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int s = s0 + i * kWarps;
+      if (s < f.parts) {
+        const float w = weight(s);
+        acc.x += w * x[i].x;
+        acc.y += w * x[i].y;
+        acc.z += w * x[i].z;
+        acc.w += w * x[i].w;
+      }
+    }
   }
   sums[warp][lane] = acc;
   __syncthreads();
@@ -201,7 +224,7 @@ cudaError_t launch(LatentAttnLaunch p, cudaStream_t st) {
   if (runs > 1) {
     const int split = std::min(runs - 1, p.B * p.tiles_t * p.groups);  // split tiles, at most
     const int most = std::min(kHg, p.H * p.tile_t);
-    if (split <= 8) {
+    if (split <= 3) {
       k_latent_join_long<<<dim3(split, 4 * most), kJoinThreads, 0, st>>>(p, runs);
     } else {
       const int heads = split <= 64 ? 2 : 8;

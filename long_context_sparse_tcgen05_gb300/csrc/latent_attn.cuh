@@ -103,7 +103,7 @@ struct Regs<true> {
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColSfA = 416, kColSfB = 424, kColS = 448;
 constexpr int64_t kPartFloats = kHg * kLatentDim + kHg;  // of a part in memory: O by head, then lse
-constexpr int kMinRun = 4;                   // blocks of a CTA's run, where there are few
+constexpr int kMinRun = 2;                   // blocks of a CTA's run, where there are few
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // E0 moves when a block's E passes it by this.  A row sum holds up to 1,024 blocks of 64 weights
 // p_j / s_j <= 2^8 / 2^-60 (the append's least scale), times 2^(E - E0): 2^(10 + 6 + 8 + 60 + 40) = 2^124,
