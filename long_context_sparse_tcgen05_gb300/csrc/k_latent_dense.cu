@@ -7,7 +7,6 @@ namespace dsa {
 namespace {
 
 constexpr int kJoinThreads = 256;
-constexpr int kMaxRuns = 1024;  // CTAs of a call
 
 // A split tile that block x of a join has to put together: the x-th of them.
 struct SplitTile {
@@ -197,7 +196,7 @@ void tile(LatentAttnLaunch& p) {
 }
 // CTAs of a call: one per SM, fewer where S says that there are not blocks enough for them.
 int runs_of(const LatentAttnLaunch& p) {
-  const int64_t blocks = (int64_t)p.B * p.tiles_t * p.groups * ((p.S + kNB - 1) / kNB);
+  const int64_t blocks = (int64_t)p.B * p.tiles_t * p.groups * ((p.S - 1) / kNB + 1);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(device_sm_count(), kMaxRuns), blocks / kMinRun));
 }
 

@@ -104,6 +104,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColSfA = 416, kColSfB = 424, kColS = 448;
 constexpr int64_t kPartFloats = kHg * kLatentDim + kHg;  // of a part in memory: O by head, then lse
 constexpr int kMinRun = 2;                   // blocks of a CTA's run, where there are few
+constexpr int kSlack = 20;                   // see ShareCount
+constexpr int kMaxRuns = 1024;               // CTAs of a call over all rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // E0 moves when a block's E passes it by this.  A row sum holds up to 1,024 blocks of 64 weights
 // p_j / s_j <= 2^8 / 2^-60 (the append's least scale), times 2^(E - E0): 2^(10 + 6 + 8 + 60 + 40) = 2^124,
@@ -404,28 +406,42 @@ __device__ __forceinline__ int dense_sees(const LatentAttnLaunch& p, int t, int 
   len = max(0, min(len, p.S));
   return p.causal ? max(0, len - (p.T - 1 - t)) : len;
 }
-__device__ __forceinline__ int dense_blocks(int sees) { return max(1, (sees + kNB - 1) / kNB); }
+__device__ __forceinline__ int dense_blocks(int sees) { return sees < 1 ? 1 : (sees - 1) / kNB + 1; }
 
-// This CTA's share of a call over all rows.  The blocks of all tiles, one tile after another, are divided into
-// equal runs, one a CTA, so sequences of any lengths keep the SMs evenly busy.  A run starts and ends inside tiles:
-// those are parts, which k_latent_join puts together.  Every CTA counts all tiles (a few instructions each, over its
-// threads; a tile's own work is thousands of cycles): each thread its tiles' blocks, then, all threads having
-// met, find() places the run's ends.
+// This CTA's share of a call over all rows: a run of blocks of one tile or of several, one after another.  Runs that
+// end inside tiles leave parts, which k_latent_join puts together.
+//   Few tiles: each is cut into equal parts of at most L blocks, a part a CTA, if some L up to four above the mean gives no
+// more parts than there are CTAs: each segment of a run costs about four blocks beside its blocks (queries, O).
+//   Otherwise the blocks of all tiles, one tile after another, are divided into equal runs, so sequences of any lengths
+// keep the SMs evenly busy.
+// Every CTA counts all tiles (a few instructions each, over its threads; a tile's own work is thousands of cycles): each
+// thread its tiles' blocks, then, all threads having met, find() places the run's ends.
+struct ShareRoom {
+  int64_t warp_sum[32];
+  int parts[kSlack + 1];  // that the tiles make at each L
+  int blocks[kMaxRuns];   // of each tile, where there are few
+};
 template <int kThreads>
 struct ShareCount {
   const LatentAttnLaunch& p;
   int64_t sum, upto;  // blocks of this thread's tiles; of its warp's threads up to it
-  int lo, hi;
+  int tiles, lo, hi;
   __device__ __forceinline__ int blocks(int tile) const {
     const Item I = item_of<kAll>(p, tile);
     return dense_blocks(dense_sees(p, I.last, __ldg(p.lens + I.b)));
   }
-  __device__ __forceinline__ ShareCount(const LatentAttnLaunch& p, int64_t* room) : p(p) {
-    const int tiles = p.B * p.tiles_t * p.groups, per = (tiles + kThreads - 1) / kThreads;
+  __device__ __forceinline__ bool few() const { return tiles <= (int)gridDim.x; }  // (at most kMaxRuns)
+  __device__ __forceinline__ ShareCount(const LatentAttnLaunch& p, ShareRoom& room) : p(p) {
+    tiles = p.B * p.tiles_t * p.groups;
+    const int per = (tiles + kThreads - 1) / kThreads;
     lo = min((int)threadIdx.x * per, tiles);
     hi = min(lo + per, tiles);
     sum = 0;
-    for (int i = lo; i < hi; ++i) sum += blocks(i);
+    for (int i = lo; i < hi; ++i) {
+      const int n = blocks(i);
+      if (few()) room.blocks[i] = n;
+      sum += n;
+    }
     upto = sum;
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -433,12 +449,12 @@ struct ShareCount {
       const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
-    if (lane == 31) room[threadIdx.x >> 5] = upto;
+    if (lane == 31) room.warp_sum[threadIdx.x >> 5] = upto;
   }
   // false: nothing to do.  (All threads meet in it.)
-  __device__ __forceinline__ bool find(DenseShare& s, const int64_t* room) const {
+  __device__ __forceinline__ bool find(DenseShare& s, ShareRoom& room) const {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t upto_warp = lane < kThreads / 32 ? room[lane] : 0;
+    int64_t upto_warp = lane < kThreads / 32 ? room.warp_sum[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int64_t v = __shfl_up_sync(0xffffffffu, upto_warp, o);
@@ -447,8 +463,55 @@ struct ShareCount {
     const int64_t total = __shfl_sync(0xffffffffu, upto_warp, 31);
     const int64_t above = __shfl_sync(0xffffffffu, upto_warp, warp > 0 ? warp - 1 : 0);
     const int64_t before = (warp > 0 ? above : 0) + upto - sum;
+    const int c = blockIdx.x;
+    if (few() && total >> 32 == 0) {
+      const int L0 = max(kMinRun, (int)(((uint32_t)total + gridDim.x - 1) / gridDim.x));
+      if (warp <= kSlack) {
+        int n = 0;
+        for (int i = lane; i < tiles; i += 32) n += (room.blocks[i] + L0 + warp - 1) / (L0 + warp);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) room.parts[warp] = n;
+      }
+      __syncthreads();
+      int L = 0;
+#pragma unroll
+      for (int i = kSlack; i >= 0; --i)
+        if (room.parts[i] <= (int)gridDim.x) L = L0 + i;
+      if (L > 0) {
+        if (warp == 0) {
+          int at = 0, tile = -1, n = 0, part = 0, k = 1;
+          for (int i0 = 0; i0 < tiles && tile < 0; i0 += 32) {
+            const int mine = i0 + lane < tiles ? room.blocks[i0 + lane] : 0, parts = (mine + L - 1) / L;
+            int upto = parts;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+              const int v = __shfl_up_sync(0xffffffffu, upto, o);
+              if (lane >= o) upto += v;
+            }
+            const uint32_t bal = __ballot_sync(0xffffffffu, at + upto > c);
+            if (bal) {
+              const int w = __ffs(bal) - 1;
+              tile = i0 + w;
+              n = __shfl_sync(0xffffffffu, mine, w);
+              k = __shfl_sync(0xffffffffu, parts, w);
+              part = c - (at + __shfl_sync(0xffffffffu, upto, w) - k);
+            }
+            at += __shfl_sync(0xffffffffu, upto, 31);
+          }
+          if (lane == 0) {
+            s.first = s.last = tile;
+            s.first_j0 = (int)((int64_t)n * part / k);
+            s.last_end = (int)((int64_t)n * (part + 1) / k);
+            s.last_whole = part == k - 1;
+            p.shares[c] = make_int4(tile, s.first_j0, tile, s.last_whole);
+          }
+        }
+        __syncthreads();
+        return s.first >= 0;
+      }
+    }
     // run c: blocks [from, to) (one division, in 32 bits where they suffice)
-    const int c = blockIdx.x, ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinRun));
+    const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinRun));
     if (c >= ctas) {
       if (threadIdx.x == 0) p.shares[c] = make_int4(-1, 0, -1, 0);
       return false;
@@ -535,7 +598,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     tmem_alloc(&sm->tmem, kTmemCols);
     tmem_relinquish();
   }
-  int64_t* const room = reinterpret_cast<int64_t*>(kv_s);  // (no stage is in use yet)
+  ShareRoom& room = *reinterpret_cast<ShareRoom*>(kv_s);  // (no stage is in use yet)
   using Count = std::conditional_t<kForm == kAll, ShareCount<kThreads<kFour>>, int>;
   const Count count = [&] {
     if constexpr (kForm == kAll) return Count(p, room);
