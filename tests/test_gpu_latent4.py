@@ -598,3 +598,126 @@ def test_serving_chain_over_the_4_bit_cache():
     low = lat.abs().amax(-1, keepdim=True) * 2.0 ** -6 / 384 * 0.5
     assert bool(((y - lat).abs() <= top / 3 + BF16_STEP * lat.abs() + low).all())
     assert dsa.read_device_flags(DEV) == 0
+
+
+def test_cache_past_32_bit_offsets():
+    """Rows whose codes, and rope values, lie past 4 GiB: written, read, unpacked and attended."""
+    rows = (1 << 24) + 40000
+    if torch.cuda.mem_get_info(DEV)[0] < rows * 420:
+        pytest.skip("not enough memory")
+    cache = dict(codes=torch.zeros((1, rows, 256), dtype=torch.uint8, device=DEV), groups=torch.full((1, rows, 16), 127, dtype=torch.uint8, device=DEV),
+                 scales=torch.ones((1, rows), device=DEV), rope=torch.zeros((1, rows, 64), dtype=torch.bfloat16, device=DEV), block_table=None)
+    n = 300
+    x = torch.randn((1, n, 576), generator=_gen(1), device=DEV).bfloat16()
+    small = _cache(1, n, 0)
+    dsa.dsa_latent4_append(x, cache, pos0=rows - n)
+    dsa.dsa_latent4_append(x, small, pos0=0)
+    far = torch.arange(rows - n, rows, device=DEV).int().reshape(1, n)
+    near = torch.arange(n, device=DEV).int().reshape(1, n)
+    assert torch.equal(dsa.dsa_latent4_read(cache, far), dsa.dsa_latent4_read(small, near))
+    u, v = dsa.dsa_latent4_unpack(cache, far), dsa.dsa_latent4_unpack(small, near)
+    assert torch.equal(u["codes"].view(torch.uint8), v["codes"].view(torch.uint8)) and torch.equal(u["scales"], v["scales"])
+    q = _q(1, 1, 64)
+    got = dsa.dsa_latent4_attn(dict(q=q, cache=cache, scale=1 / 24), far[None].contiguous())
+    assert _same(got, dsa.dsa_latent4_attn(dict(q=q, cache=small, scale=1 / 24), near[None].contiguous()))
+    # all rows: the zeros before them weigh in, too
+    lens = torch.tensor([rows], dtype=torch.int32, device=DEV)
+    o, l = dsa.dsa_latent4_attn_dense(dict(q=q, cache=cache, scale=1 / 24), lens)
+    rows64 = _rows64(small, torch.zeros(n, dtype=torch.long, device=DEV), near[0].long())
+    v, s = rows64[:, :512], small["scales"].reshape(-1).double()
+    sc = (q[0, 0].double() @ rows64.T) / 24
+    lse = torch.logsumexp(torch.cat((sc, torch.full((64, 1), math.log(rows - n), device=DEV, dtype=torch.float64)), 1), 1)
+    assert bool(((l[0, 0].double() - lse).abs() <= 2.0 ** -14 * (1 + lse.abs())).all())
+    p = torch.exp(sc - lse[:, None])
+    ref = p @ v
+    # as in _check_dense: the largest scaled weight is that of a row of zeros (scale 1), or one of the others'
+    top = torch.maximum(torch.exp(-lse), (p * s).amax(-1))[:, None]
+    tol = BF16_STEP * (ref.abs() + p @ v.abs()) + 2.0 ** -14 * top * (v / s[:, None]).abs().sum(0)
+    assert bool(((o[0, 0].double() - ref).abs() <= tol).all())
+    del cache
+    torch.cuda.empty_cache()
+    assert dsa.read_device_flags(DEV) == 0
+
+
+def test_trace_names_the_kernels():
+    cache = _cache(1, 700, 16)
+    x = torch.randn((1, 4, 576), generator=_gen(1), device=DEV).bfloat16()
+    at = dict(q=_q(1, 1, 8), cache=cache, scale=0.05)
+    dsa.trace_enable(64)
+    try:
+        dsa.dsa_latent4_append(x, cache)
+        dsa.dsa_latent4_read(cache, n=4)
+        dsa.dsa_latent4_unpack(cache, n=4)
+        dsa.dsa_latent4_attn(at, _idx(1, 1, 700, 64))
+        before = dsa.launch_count()
+        dsa.dsa_latent4_attn_dense(at, torch.tensor([700], dtype=torch.int32, device=DEV))
+        assert dsa.launch_count() == before + 2  # (attention, and the join of its parts)
+        kinds = [r[0] for r in dsa.trace_read()]
+    finally:
+        dsa.trace_disable()
+    assert kinds == ["cache"] * 3 + ["attention"] * 2
+
+
+def test_captured_decode_steps_advance_in_place():
+    """A decode step in a graph, of an append and dense attention: positions and lengths advance between replays."""
+    B, cap = 3, 500
+    cos, sin = _angles(cap)
+    x = torch.randn((B, 1, 576), generator=_gen(1), device=DEV).bfloat16()
+    q = _q(B, 1, 64)
+    pos = torch.full((B, 1), 200, device=DEV, dtype=torch.int64)
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+    a, b = _cache(B, cap, 16), _cache(B, cap, 16)
+
+    def work(c):
+        lens.copy_(pos[:, 0] + 1)
+        dsa.dsa_latent4_append(x, c, cos=cos, sin=sin, positions=pos)
+        return dsa.dsa_latent4_attn_dense(dict(q=q, cache=c, scale=0.05), lens) + (dsa.dsa_latent4_read(c, pos.int()),)
+
+    work(b)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = work(a)
+    for t in range(5):
+        pos.fill_(200 + 60 * t)
+        x.normal_(generator=_gen(t))
+        g.replay()
+        assert _same(y, work(b))
+    assert dsa.read_device_flags(DEV) == 0
+
+
+@pytest.mark.parametrize("B,T,H", [(152, 1, 64), (153, 1, 64), (76, 1, 128), (77, 1, 100), (30, 20, 16), (200, 3, 20)])
+def test_dense_attention_of_about_as_many_tiles_as_sms(B, T, H):
+    """Cut into equal parts, or divided into equal runs: short and long sequences, empty ones among them."""
+    S = 900
+    cache = _cache(B, S, 64, seed=B)
+    g = torch.Generator()
+    g.manual_seed(B)
+    for top in (40, 900):
+        lens = torch.randint(0, top + 1, (B,), generator=g).tolist()
+        _check_dense(dict(q=_q(B, T, H), cache=cache, scale=1 / 24, S=S), lens, some={(b, t) for b in range(0, B, 7) for t in (0, T - 1)})
+    assert dsa.read_device_flags(DEV) == 0
+
+
+def test_operands_of_other_kinds_are_refused():
+    four, eight = _cache(2, 64, 16), _cache(2, 64, 16, four=False)
+    q, lens = _q(2, 1, 64), torch.tensor([5, 6], dtype=torch.int32, device=DEV)
+    idx = _idx(2, 1, 64, 32)
+    x = torch.zeros((2, 1, 576), device=DEV, dtype=torch.bfloat16)
+    at4, at8 = dict(q=q, cache=four, scale=0.05), dict(q=q, cache=eight, scale=0.05)
+    for call in (lambda: dsa.dsa_latent_attn(at4, idx), lambda: dsa.dsa_latent_append(x, four), lambda: dsa.dsa_latent_read(four, n=3),
+                 lambda: dsa.dsa_latent_attn_dense(at4, lens), lambda: dsa.dsa_latent4_attn_dense(at4, lens.long()),
+                 lambda: dsa.dsa_latent4_attn_dense(at4, lens[:1]), lambda: dsa.dsa_latent4_attn_dense(at4, lens.cpu()),
+                 lambda: dsa.dsa_latent4_attn_dense(at4, None), lambda: dsa.dsa_latent4_attn_dense(dict(at4, S=0), lens),
+                 lambda: dsa.dsa_latent4_attn(at4, idx.long()), lambda: dsa.dsa_latent4_attn(dict(at4, q=q.expand(2, 3, 64, 576)), idx),
+                 lambda: dsa.dsa_latent4_attn(dict(at4, cache=dict(four, groups=four["groups"][:1])), idx),
+                 lambda: dsa.dsa_latent4_attn(dict(at4, cache=dict(four, rope=four["rope"].float())), idx),
+                 lambda: dsa.dsa_latent4_append(x.float(), four), lambda: dsa.dsa_latent4_read(four), lambda: dsa.dsa_latent4_unpack(four, idx, n=3)):
+        with pytest.raises(AssertionError):
+            call()
+    for call in (lambda: dsa.dsa_latent4_attn(at8, idx), lambda: dsa.dsa_latent4_append(x, eight), lambda: dsa.dsa_latent4_read(eight, n=3)):
+        with pytest.raises(KeyError):  # (no groups)
+            call()
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_latent4_attn_dense(dict(at4, S=65), lens)
+    assert dsa.read_device_flags(DEV) == 0

@@ -239,3 +239,110 @@ def test_read_device_flags_reads_the_named_device_on_its_own_stream(monkeypatch,
     monkeypatch.setattr(torch.cuda, "current_stream", stream_of)
     assert dsa.read_device_flags(device) == 5 << index
     assert sorted(reads) == [(words[index, kind], 1000 + index, index) for kind in (0, 1)]
+
+
+# --- the 4-bit cache and attention over all rows ---------------------------------------------------
+
+def _cache4(**kw):
+    return _edit(dsa.Latent4Cache(n_pages=10, page_size=16, table_ld=4, codes=FAKE, groups=FAKE, scales=FAKE, rope=FAKE, block_table=FAKE), kw)
+
+
+def _attn4(**kw):
+    return _edit(dsa.Latent4AttnArgs(B=2, T=3, S=60, H=64, scale=0.04, q=FAKE, cache=_cache4(), idx_T=3), kw)
+
+
+def _dense(lib, a, lens=FAKE, causal=1, out=FAKE, lse=FAKE, ws=FAKE, n=1 << 30):
+    call = lib.dsa_latent4_attn_dense if isinstance(a, dsa.Latent4AttnArgs) else lib.dsa_latent_attn_dense
+    return call(ctypes.byref(a), lens, causal, out, lse, ws, n, None)
+
+
+def test_struct_layouts_of_the_4_bit_cache_match_header(tmp_path):
+    lines, want = [], []
+    for name, cls in (("dsa_latent4_cache", dsa.Latent4Cache), ("dsa_latent4_attn_args", dsa.Latent4AttnArgs)):
+        lines.append(f'printf("%zu ", sizeof({name}));')
+        want.append(ctypes.sizeof(cls))
+        for field, _ in cls._fields_:
+            lines.append(f'printf("%zu ", offsetof({name}, {field}));')
+            want.append(getattr(cls, field).offset)
+    src = tmp_path / "sz.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "dsa.h"\nint main(void){' + "".join(lines) + "return 0;}\n")
+    exe = tmp_path / "sz"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    assert [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()] == want
+
+
+def test_packed_images_are_the_structs():
+    """The binding packs whole structs: every field where ctypes has it."""
+    image = dsa._CACHE4.pack(1, 2, 3, 4, 5, 6, 7, 8)
+    c = dsa.Latent4Cache.from_buffer_copy(image)
+    assert [getattr(c, f) for f, _ in c._fields_] == [1, 2, 3, 4, 5, 6, 7, 8]
+    a = dsa.Latent4AttnArgs.from_buffer_copy(dsa._ATTN_HEAD.pack(11, 12, 13, 14, 0.5, 15, 16, 17) + image + dsa._ATTN_TAIL.pack(18, 19))
+    assert (a.B, a.T, a.S, a.H, a.scale, a.q, a.q_stride_b, a.q_stride_t, a.cache.block_table, a.idx_T, a.flags) == (11, 12, 13, 14, 0.5, 15, 16, 17, 8, 18, 19)
+    image = dsa._CACHE.pack(1, 2, 3, 4, 5, 6, 7)
+    a = dsa.LatentAttnArgs.from_buffer_copy(dsa._ATTN_HEAD.pack(11, 12, 13, 14, 0.5, 15, 16, 17) + image + dsa._ATTN_TAIL.pack(18, 19))
+    assert (a.H, a.cache.n_pages, a.cache.block_table, a.idx_T, a.flags) == (14, 1, 7, 18, 19)
+    p = dsa.LatentAppendArgs.from_buffer_copy(dsa._APPEND.pack(1, 2, 3, 4, 5, 6, 0.25, 7, 8, 9, 10, 11, 12))
+    assert [getattr(p, f) for f, _ in p._fields_] == [1, 2, 3, 4, 5, 6, 0.25, 7, 8, 9, 10, 11, 12]
+
+
+@pytest.mark.parametrize("edits,status", CACHE_BAD + [(dict(groups=None), INVALID)])
+def test_4_bit_cache_refusals(lib, edits, status):
+    c = _cache4(**edits)
+    before = lib.dsa_launch_count()
+    assert lib.dsa_latent4_append(ctypes.byref(_append()), ctypes.byref(c), FAKE, 256, None) == status
+    assert lib.dsa_latent4_read(ctypes.byref(c), 2, 3, FAKE, 0, FAKE, FAKE, 256, None) == status
+    assert lib.dsa_latent4_unpack(ctypes.byref(c), 2, 3, FAKE, 0, FAKE, FAKE, FAKE, FAKE, 256, None) == status
+    a = _attn4(cache=c)
+    assert lib.dsa_latent4_attn(ctypes.byref(a), FAKE, 16, FAKE, FAKE, FAKE, 256, None) == status
+    assert _dense(lib, a) == status
+    assert lib.dsa_launch_count() == before
+
+
+def test_4_bit_call_refusals(lib):
+    c = ctypes.byref(_cache4())
+    before = lib.dsa_launch_count()
+    assert lib.dsa_latent4_append(ctypes.byref(_append(x_stride_t=568)), c, FAKE, 256, None) == INVALID
+    assert lib.dsa_latent4_append(ctypes.byref(_append(positions=None, pos0=62)), c, FAKE, 256, None) == INVALID
+    assert lib.dsa_latent4_append(ctypes.byref(_append()), None, FAKE, 256, None) == INVALID
+    assert lib.dsa_latent4_append(None, c, FAKE, 256, None) == INVALID
+    assert lib.dsa_latent4_append(ctypes.byref(_append()), c, FAKE, 255, None) == WORKSPACE
+    assert lib.dsa_latent4_append(ctypes.byref(_append(n=0)), c, FAKE, 256, None) == OK
+    unpack = lambda B=2, n=3, idx=FAKE, pos0=0, codes=FAKE, scales=FAKE, rope=FAKE, ws=FAKE: lib.dsa_latent4_unpack(c, B, n, idx, pos0, codes, scales, rope, ws, 256, None)  # noqa: E731
+    assert unpack(codes=None) == INVALID and unpack(scales=None) == INVALID and unpack(rope=None) == INVALID
+    assert unpack(codes=FAKE + 8) == MISALIGNED and unpack(rope=FAKE + 8) == MISALIGNED and unpack(scales=FAKE + 2) == MISALIGNED
+    assert unpack(idx=FAKE + 2) == MISALIGNED and unpack(idx=None, pos0=62) == INVALID and unpack(idx=None, pos0=-1) == INVALID
+    assert unpack(B=0) == INVALID and unpack(n=-1) == INVALID and unpack(ws=None) == WORKSPACE and unpack(n=0) == OK
+    assert lib.dsa_latent4_read(c, 2, 3, FAKE, 0, None, FAKE, 256, None) == INVALID
+    assert lib.dsa_latent4_read(c, 2, 0, FAKE, 0, FAKE, FAKE, 256, None) == OK
+    a = _attn4()
+    call = lambda a=a, idx=FAKE, k=16, out=FAKE: lib.dsa_latent4_attn(a and ctypes.byref(a), idx, k, out, FAKE, FAKE, 256, None)  # noqa: E731
+    assert call(a=None) == INVALID and call(idx=None) == INVALID and call(out=None) == INVALID and call(k=0) == UNSUPPORTED
+    assert call(a=_attn4(idx_T=2)) == INVALID and call(a=_attn4(H=129)) == UNSUPPORTED and call(a=_attn4(S=65)) == INVALID
+    assert lib.dsa_launch_count() == before
+
+
+@pytest.mark.parametrize("edits,status", [
+    (dict(B=0), INVALID), (dict(T=0), INVALID), (dict(S=0), INVALID), (dict(S=65), INVALID), (dict(H=0), UNSUPPORTED),
+    (dict(H=129), UNSUPPORTED), (dict(B=1 << 13, T=1 << 13), UNSUPPORTED), (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(q=None), INVALID), (dict(q=FAKE + 8), MISALIGNED), (dict(q_stride_t=64 * 576 - 8), INVALID), (dict(q_stride_b=-8), INVALID),
+    (dict(q_stride_b=3 * 64 * 576 + 4), MISALIGNED), (dict(flags=FAKE + 2), MISALIGNED),
+])
+def test_dense_attention_refusals(lib, edits, status):
+    before = lib.dsa_launch_count()
+    assert _dense(lib, _attn4(**edits)) == status
+    assert _dense(lib, _attn(**edits)) == status
+    assert lib.dsa_last_error() and lib.dsa_launch_count() == before
+
+
+def test_dense_attention_call_refusals_and_workspace(lib):
+    before = lib.dsa_launch_count()
+    for a in (_attn4(), _attn(), _attn4(idx_T=0)):  # (idx_T is not read)
+        assert _dense(lib, a, lens=None) == INVALID and _dense(lib, a, out=None) == INVALID
+        assert _dense(lib, a, lens=FAKE + 2) == MISALIGNED and _dense(lib, a, out=FAKE + 8) == MISALIGNED and _dense(lib, a, lse=FAKE + 2) == MISALIGNED
+        assert _dense(lib, a, ws=None) == WORKSPACE and _dense(lib, a, ws=FAKE + 8) == MISALIGNED
+        need = lib.dsa_latent_attn_dense_workspace_size(2, 3, 60, 64)
+        assert _dense(lib, a, n=need - 1) == WORKSPACE and need > 256
+    size = lib.dsa_latent_attn_dense_workspace_size
+    assert size(0, 1, 1, 1) == size(1, 1, 1, 129) == 256  # calls that are refused
+    assert size(1, 1, 2 ** 31 - 1, 64) >= size(1, 1, 64, 64) > 256
+    assert lib.dsa_launch_count() == before
