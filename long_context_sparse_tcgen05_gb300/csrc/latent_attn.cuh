@@ -1124,7 +1124,11 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         const int j0 = (int)((int64_t)I.split * nbr / p.splits);
         return {ids, I.b, j0, (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0, 0};
       };
-      Blocks cur = blocks_of(first), next{};
+      // (Of a part the row is taken to be full while its end is looked for: its ids are then there a latency earlier, 29.5 ->
+      // 28.3 us a 32-sequence decode step out of L2.  In the kernel that walks many rows the code cost 3%.)
+      Blocks cur{}, next{};
+      int id_0[2], id_2[2], id[2];
+      bool guessed = false;
       // Below, block j >= cur.nb is the next item's block j - cur.nb.
       auto load_ids = [&](int j, int (&id)[2]) {
         const bool here = j < cur.nb;
@@ -1164,7 +1168,21 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       // costs one latency, not all; and so across items.  (One latency after the other took 2,400 cycles
       // a block in a decode step, and 9,000 at the start of every row.)  Only where the item had three
       // blocks or more for this warp; the first blocks of the others' successors wait.
-      int id[2], page[2], off[2], row[2];
+      if constexpr (!kParts) {
+        cur = blocks_of(first);
+      } else {
+        const int first_j = warp - kIxWarp0;  // of this warp
+        const Item I = item_of<kForm>(p, first);
+        const int most = (p.kk + kNB - 1) / kNB, j0 = (int)((int64_t)I.split * most / p.splits);
+        cur = {p.idx + I.b * p.idx_sb + I.t * p.idx_st, I.b, j0, (int)((int64_t)(I.split + 1) * most / p.splits) - j0, 0};
+        load_ids(first_j, id_0);
+        load_ids(first_j + 2, id_2);
+        load_ids(first_j + 4, id);
+        const Blocks found = blocks_of(first);
+        guessed = found.j0 == cur.j0 && found.nb == cur.nb;
+        cur = found;
+      }
+      int page[2], off[2], row[2];
       float scale[2];
       int it = 0;
       uint32_t g = 0;
@@ -1185,15 +1203,17 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         }
         int j = (int)((g ^ (uint32_t)(warp - kIxWarp0)) & 1u);  // this warp's blocks: g + j even or odd
         if (!ahead && j < cur.nb) {
-          int id_0[2], id_2[2];
-          load_ids(j, id_0);
-          load_ids(j + 2, id_2);
-          load_ids(j + 4, id);
+          if (!kParts || !guessed) {
+            load_ids(j, id_0);
+            load_ids(j + 2, id_2);
+            load_ids(j + 4, id);
+          }
           load_pages(j, id_0, page, off);
           resolve(page, off, row);
           load_scales(row, scale);
           load_pages(j + 2, id_2, page, off);
         }
+        guessed = false;
         int known = item + G < items ? 0 : 3;  // the last loads that saw the blocks of this or the next item
         bool seen = known != 0;                // the next item's blocks are known
         next.nb = 0;
