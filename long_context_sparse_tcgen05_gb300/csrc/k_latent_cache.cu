@@ -267,13 +267,13 @@ __global__ void __launch_bounds__(kThreads, 3) k_latent4_append(LatentAppendLaun
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t b[4];
+        float2 z[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const f32x2 z = mul_2(div(y[4 * i + j]), pair(f, f));
-          b[j] = pack_e2m1(lo_of(z), hi_of(z));
+          const f32x2 v = mul_2(div(y[4 * i + j]), pair(f, f));
+          z[j] = make_float2(lo_of(v), hi_of(v));
         }
-        o[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        o[i] = pack_e2m1(z);
       }
       reinterpret_cast<uint4*>(p.cache.codes + row * (kLatentDim / 2))[l] = make_uint4(o[0], o[1], o[2], o[3]);
       p.cache.groups[row * kLatentGroups + l] = (uint8_t)g;
@@ -305,10 +305,11 @@ __device__ __forceinline__ uint4 dequant8(uint2 c, float s) {
 
 // Eight e2m1 codes times s (the group's power of two in it), as bf16.
 __device__ __forceinline__ uint4 dequant8(uint32_t c, float s) {
-  uint32_t o[4];
+  uint32_t o[4], h[4];
+  unpack_e2m1(c, h);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = e2m1x2_to_float2(c >> (8 * i));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
     o[i] = pack_bf16(f.x * s, f.y * s);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);

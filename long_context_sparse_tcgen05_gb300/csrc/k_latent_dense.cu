@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_latent_join(LatentAttnLaunch p
   for (int u = blockIdx.y * heads * 4 + (threadIdx.x >> 5); u < end; u += kJoinThreads / 32) {
     const int h = u >> 2, quarter = u & 3;
     auto piece = [&](int s) { return reinterpret_cast<const float4*>(f.part(p, s) + h * kLatentDim + quarter * (kLatentDim / 4)) + lane; };
-    // eight parts on their way together, the first eight before their weights
-    constexpr int kAtOnce = 8;
+    // four parts on their way together, the first four before their weights
+    constexpr int kAtOnce = 4;
     float4 x[kAtOnce];
     auto load = [&](int s) {
 #pragma unroll
@@ -226,7 +226,7 @@ cudaError_t launch(LatentAttnLaunch p, cudaStream_t st) {
     if (split <= 3) {
       k_latent_join_long<<<dim3(split, 4 * most), kJoinThreads, 0, st>>>(p, runs);
     } else {
-      const int heads = split <= 64 ? 2 : 8;
+      const int heads = split <= 64 ? 4 : 8;
       k_latent_join<<<dim3(split, (most + heads - 1) / heads), kJoinThreads, 0, st>>>(p, runs, heads);
     }
     count_launches(1);

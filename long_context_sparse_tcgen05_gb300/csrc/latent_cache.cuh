@@ -45,16 +45,21 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
 // e4m3 codes are c - 8, c, c + 4, c + 8, c + 12, c + 16, c + 20, with c = 8 (e + 7) the code of 2^e itself (their
 // exponents go by steps of 8, their halves by 4; c - 8 >= 8, so all of them are normal).
 
-// Two e2m1 codes (low four bits first) as floats, and two floats as codes (the nearest, ties to even, at most 6).
-__device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t c) {
-  uint32_t h;
-  asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n}\n" : "=r"(h) : "r"(c));
-  return __half22float2(*reinterpret_cast<__half2*>(&h));
+// Eight e2m1 codes (low four bits first) as pairs of f16.
+__device__ __forceinline__ void unpack_e2m1(uint32_t codes, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
 }
-__device__ __forceinline__ uint32_t pack_e2m1(float lo, float hi) {
-  uint32_t d;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n}\n" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
+// Four pairs of floats as eight codes (the nearest, ties to even, at most 6).
+__device__ __forceinline__ uint32_t pack_e2m1(const float2 (&z)[4]) {
+  uint32_t codes;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(codes)
+      : "f"(z[0].x), "f"(z[0].y), "f"(z[1].x), "f"(z[1].y), "f"(z[2].x), "f"(z[2].y), "f"(z[3].x), "f"(z[3].y));
+  return codes;
 }
 // Eight e2m1 codes (low four bits first) to the e4m3 codes of what they stand for: the eight magnitudes are a table in
 // two registers that a byte permutation looks up, four codes at a time.
