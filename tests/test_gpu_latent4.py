@@ -721,3 +721,16 @@ def test_operands_of_other_kinds_are_refused():
     with pytest.raises(dsa.DsaError):
         dsa.dsa_latent4_attn_dense(dict(at4, S=65), lens)
     assert dsa.read_device_flags(DEV) == 0
+
+
+@pytest.mark.parametrize("B,T,H,top", [(1, 1500, 64, 1500), (3, 400, 64, 500), (2, 2000, 12, 2000), (400, 1, 64, 700), (1, 900, 128, 3000)])
+def test_dense_attention_of_prompts_from_their_start(B, T, H, top):
+    """Tiles of one block and of many in one call, more tiles than SMs: runs that end in any of them."""
+    cache = _cache(B, top, 64, seed=T)
+    g = torch.Generator()
+    g.manual_seed(T)
+    lens = [top] + torch.randint(0, top + 1, (B - 1,), generator=g).tolist()
+    some = {(b, t) for b in range(0, B, max(1, B // 4)) for t in {0, 1, 63, 64, 65, T // 2, T - 2, T - 1} if 0 <= t < T}
+    got = _check_dense(dict(q=_q(B, T, H), cache=cache, scale=1 / 24, S=top), lens, some=some)
+    # every token of a sequence that holds as many rows as there are tokens sees itself: no empty row there
+    assert bool(torch.isfinite(got[1][0]).all()) and dsa.read_device_flags(DEV) == 0
