@@ -585,7 +585,8 @@ uint64_t dsa_launch_count(void);
  * dsa_trace_read(kinds, ms, max_records, dropped): waits for the recorded launches to finish
  *   (host synchronisation on their events), writes up to max_records entries in launch order
  *   -- kinds[i] is DSA_TRACE_INDEXER, _TOPK, _ATTENTION, _OVERLAP or _CACHE (the
- *   norm, latent append and latent read kernels), ms[i] the device time in
+ *   norm, latent append, read and unpack kernels; a dense latent attention call is one record
+ *   for its two kernels), ms[i] the device time in
  *   milliseconds (-1 if unavailable) -- returns the number written, stores in *dropped (may
  *   be NULL) the launches the pool could not record, and clears the records.  Host arrays
  *   are owned by the caller; kinds or ms may be NULL.

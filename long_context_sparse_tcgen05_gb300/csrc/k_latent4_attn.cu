@@ -1,4 +1,5 @@
-// Sparse attention over selected rows of the paged 4-bit latent cache.
+// Sparse attention over selected rows of the paged 4-bit latent cache: the kernel of latent_attn.cuh with gather warps
+// that expand the codes.  404 bytes a row instead of 644.  Measured: see there.
 #include "latent_attn.cuh"
 
 namespace dsa {

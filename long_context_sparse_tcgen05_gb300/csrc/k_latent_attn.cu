@@ -1,4 +1,4 @@
-// Sparse attention over selected rows of the paged FP8 latent cache.
+// Sparse attention over selected rows of the paged FP8 latent cache: the kernel of latent_attn.cuh.
 #include "latent_attn.cuh"
 
 namespace dsa {

@@ -1,11 +1,13 @@
-// The paged FP8 latent cache: appending rows (norm, rotation, quantisation and the write through
-// the block table in one pass) and reading rows back.  A warp takes a token: 16 latent values per
+// The paged latent cache, FP8 or 4-bit: appending rows (norm, rotation, quantisation and the write through
+// the block table in one pass) and reading rows back.  FP8:  a warp takes a token: 16 latent values per
 // lane (two 16-byte loads) and one rotated pair, so the sum of squares and the largest magnitude
 // are warp shuffles.  HBM-bound: 1,152 bytes in and 644 out per appended token (the other way
 // round to read), plus a 256-byte table row.  Measured: 131,072 tokens appended in 55.6 us (4.9 TB/s;
 // 75% of the issue slots, 370 instructions a token, 27 of them quotients) and read back in 41.2 us
 // (5.7 TB/s); 32 x 2,048 selected rows read in 22.6 us (5.2 TB/s); one token each of 32 sequences appended
 // in 3.5 us.
+// 4-bit (404 bytes a row): 131,072 tokens appended in 47 us (5.0 TB/s, 69% of the issue slots, 295 instructions a token), read
+// back in 34.6 us (5.9 TB/s), unpacked to FP8 rows in 24.6 us (5.6 TB/s); 32 x 2,048 selected rows read in 17.5 us (5.9 TB/s).
 #include <algorithm>
 
 #include "dsa_internal.cuh"
@@ -146,7 +148,8 @@ __device__ __forceinline__ uint32_t group_of(float m) {
 
 // Into the 4-bit cache, two tokens a warp: a lane has the 32 values of one group of one of them, so a group's largest
 // value is the lane's own, a row's sums and maximum take four shuffles, and what a token costs beside its values is paid
-// once for two.  (A warp a token, as in the FP8 kernel: 62 us for 131,072 rows; this one XX.)  As there, everything a token
+// once for two.  (A warp a token, as in the FP8 kernel: 62 us for 131,072 rows; this one 47.  Rows copied two or three turns
+// ahead instead of one: no faster.)  As there, everything a token
 // needs is on its way while the one before it is worked on.  The 16-byte pieces of a row lie in shared memory so that
 // eight lanes, each reading from its own 64 bytes, meet all banks; so do the weights.
 template <bool kTurn>
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kThreads) k_latent_read(LatentReadLaunch p) {
 
 // Rows of the 4-bit cache: as bf16, or (kUnpack) in the FP8 cache's form, under the same scale.  A half-warp takes a row,
 // lane l its values 8 l + 128 k .. + 7 (k < 4), so that every store is of whole runs and what a row costs beside its
-// values is paid once for two (a warp a row, 187 instructions each: 30.8 us to unpack 131,072 rows; this one XX).  The
+// values is paid once for two (a warp a row, 187 instructions each: 30.8 us to unpack 131,072 rows; this one, 121, 24.6).  The
 // next row's page and the position after that are on their way meanwhile.
 template <bool kUnpack>
 __global__ void __launch_bounds__(kThreads, 8) k_latent4_read(LatentReadLaunch p) {

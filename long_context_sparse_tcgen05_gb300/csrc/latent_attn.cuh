@@ -1,7 +1,7 @@
-// Sparse attention over selected rows of the paged FP8 latent cache, on tcgen05 tensor cores that
-// read the e4m3 codes as they are stored.
+// Attention over rows of the paged latent cache, FP8 or 4-bit, on tcgen05 tensor cores that read e4m3
+// codes: over selected rows (index rows), or over every row that a query sees.
 //
-// A cache row j stands for s_j [c_j | r_j]: 512 e4m3 codes and 64 bf16 rope values under one fp32
+// An FP8 cache row j stands for s_j [c_j | r_j]: 512 e4m3 codes and 64 bf16 rope values under one fp32
 // scale.  For a head with query q, in base-2 units (a = softmax scale * log2 e):
 //   x_j = a s_j (q_c . c_j + q_r . r_j),   O = sum_j 2^x_j s_j c_j / sum_j 2^x_j.
 // Both products take the codes as FP8 operands, so no row is dequantised; the other operand is
@@ -22,12 +22,20 @@
 // FP8 products accumulate exactly enough in fp32 (sums of 2,048 products of mixed size came out
 // equal to the 64-bit sum).
 //
+// A row of the 4-bit cache has 512 e2m1 codes, a power of two for 32 of them, and the same scale and rope
+// values: each code times its power of two is an e4m3 value (see latent_cache.cuh), so the gather warps expand
+// the codes on their way into shared memory and all that follows is the same, bit for bit.  The tensor cores
+// could read e2m1 codes with a power of two for 32 values of a dot product, which serves the scores; in the value
+// product a row's powers vary along the other axis, so they have to be in the operand.
+//
 // Persistent CTAs, one per SM, walk items (query, group of 64 heads, part of the row's blocks of 64
 // keys).  24 warps:
 //   6-7    take the blocks in turn, up to six ahead: resolve positions through the block table and
 //          read the rows' scales
 //   0-3    copy the rows (16-byte cp.async) into three stages of 40 KB, five 128-byte-swizzled atoms
-//          each, as soon as the products have released them
+//          each, as soon as the products have released them.  4-bit: with 24-27, eight warps, from registers; a
+//          block needs 2,150 warp instructions more, half of them byte permutations and logic that run at half
+//          rate, and four warps took 4.0 ms for what eight do in 1.2
 //   4      S (hi and lo rows, 128 x 64) = Q K^T: A is Q in tensor memory, so the product reads only
 //          the codes from shared memory; 16 FP8 steps and 4 bf16 steps for the rope part
 //   5      O^T (512 x 64) += V^T P^T: four chunks of 128 dims, 2 key steps, hi and lo
@@ -45,10 +53,14 @@
 // operands at 128 bytes a cycle).
 // With few items of long index rows each is split into up to 8 parts of about 128 keys or more, one to each
 // CTA of a cluster, and the parts are joined over the cluster's shared memory.
+// Over all rows, an item is a tile of 64 heads of one or (few heads) several tokens, and a CTA walks a run of
+// blocks over tiles: see ShareCount and k_latent_dense.cu.
 // Waits are bounded (DSA_FLAG_TIMEOUT).
 //
-// Measured (64 heads, k = 2,048): 4,096 queries over 131,072 rows 0.99 ms, 1,170 TFLOP/s, the tensor pipe
-// 51% busy; 32 single tokens over 200,000 rows 28.8 us; one over 20,000 rows 18.7 us.  What bounds it: a
+// Measured (64 heads, k = 2,048, FP8 / 4-bit): 4,096 queries over 131,072 rows 0.98 / 1.20 ms, 1,195 / 973 TFLOP/s, the
+// tensor pipe 51 / 43% busy; 32 single tokens over 200,000 rows 27.3 / 28.3 us; one over 20,000 rows 18.3 / 19.2 us.
+// What bounds the 4-bit form: the gather warps' instructions (a block 2,400 cycles; without half of the products it
+// takes 3% less) and, where rows are at random, 2,000 cycles to their codes.  What bounds the FP8 form: a
 // block's products need 1,360 cycles of the tensor pipe, a block takes 2,000: a softmax warp's waits
 // (200), loads (170), scores and maxima (680), exponentials and stores (740) follow one another, and
 // tensor memory (512 columns in use) has no room for a second score buffer to overlap them with.  A
