@@ -122,8 +122,8 @@ constexpr int kMaxRuns = 1024;               // CTAs of a call over all rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // E0 moves when a block's E passes it by this.  A row sum holds up to 1,024 blocks of 64 weights
 // p_j / s_j <= 2^8 / 2^-60 (the append's least scale), times 2^(E - E0): 2^(10 + 6 + 8 + 60 + 40) = 2^124,
-// within fp32 (with 60 it passed 2^128).
-constexpr float kMove = 40.f;
+// within fp32 (with 60 it passed 2^128).  Over all rows there may be 2^25 blocks: 2^(25 + 6 + 8 + 60 + 24) = 2^123.
+constexpr float kMove = 40.f, kMoveAll = 24.f;
 constexpr int kInfoReaders = kGatherWarps + 2 + kSmWarps + 4 + 4;  // (4-bit: kGatherWarps more)
 constexpr int kEpiThreads = 256;             // O and query warps store an item's O together
 constexpr uint32_t kOPitch = 2 * kLatentDim + 16;  // a staged O row: 8 heads' 16-byte pieces in 32 banks
@@ -1155,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       auto load_ids = [&](int j, int (&id)[2]) {
         const bool here = j < cur.nb;
         const int32_t* ids = here ? cur.ids : next.ids;
-        const int jb = here ? j : j - cur.nb, e0 = ((here ? cur.j0 : next.j0) + jb) * kNB + lane;
+        const int jb = here ? j : j - cur.nb, e0 = (int)((uint32_t)((here ? cur.j0 : next.j0) + jb) * kNB) + lane;
         const bool in = jb < (here ? cur.nb : next.nb);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -1302,7 +1302,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
       if (nb == 0) continue;
-      float E0 = -INFINITY, l = 0.f;
+      float E0 = -INFINITY, l = 0.f, lost = 0.f;
       int any_valid = 0;
       for (int j = 0; j < nb; ++j, ++g) {
         const int ri = (int)(g % kRing), pb = (int)(g & 1);
@@ -1345,7 +1345,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 1));
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 2));
         const float E = ceilf(ymax) - 8.f;  // -inf: no weight in this block
-        const bool move = E > E0 + kMove;   // (E0 starts at -inf)
+        const bool move = E > E0 + (kForm == kAll ? kMoveAll : kMove);  // (E0 starts at -inf)
         const float alpha = move ? ex2(E0 - E) : 1.f;
         const int any = __any_sync(0xffffffffu, move);
         E0 = move ? E : E0;
@@ -1375,7 +1375,15 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
           asm volatile("st.shared.b16 [%0], %1;\n" ::"r"((at ^ ((4 + (jj >> 1)) << 4)) + (jj & 1) * 8), "h"(lo) : "memory");
         }
         const float sum = lo_of(sum2) + hi_of(sum2);
-        l = fmaf(sum, E == -INFINITY ? 0.f : ex2(E - E0), l * alpha);
+        const float f = E == -INFINITY ? 0.f : ex2(E - E0);
+        if constexpr (kForm == kAll) {
+          // of up to 2^25 blocks: with what the last sum lost (Kahan 1965), or 4 million equal weights are off by 2^-8
+          const float term = fmaf(sum, f, -lost * alpha), last = l * alpha;
+          l = last + term;
+          lost = (l - last) - term;
+        } else {
+          l = fmaf(sum, f, l * alpha);
+        }
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&bar.p_full[pb]);

@@ -734,3 +734,22 @@ def test_dense_attention_of_prompts_from_their_start(B, T, H, top):
     got = _check_dense(dict(q=_q(B, T, H), cache=cache, scale=1 / 24, S=top), lens, some=some)
     # every token of a sequence that holds as many rows as there are tokens sees itself: no empty row there
     assert bool(torch.isfinite(got[1][0]).all()) and dsa.read_device_flags(DEV) == 0
+
+
+def test_dense_attention_sums_of_millions_of_rows_of_the_least_scale_stay_finite():
+    """2^22 rows of zeros (their scale is the append's least, 2^-60) behind a block whose weights are 2^39 below theirs, in
+    one CTA each: a row sum of weights over scales is 2^(22 + 68) under a reference that may not stay 2^39 below."""
+    n, T = 1 << 22, 160
+    cache = dict(codes=torch.zeros((1, n, 256), dtype=torch.uint8, device=DEV), groups=torch.full((1, n, 16), 122, dtype=torch.uint8, device=DEV),
+                 scales=torch.full((1, n), 2.0 ** -60, device=DEV), rope=torch.zeros((1, n, 64), dtype=torch.bfloat16, device=DEV), block_table=None)
+    cache["scales"][0, :64] = 1.0
+    cache["rope"][0, :64, 0] = -1.0
+    q = torch.zeros((1, T, 64, 576), dtype=torch.bfloat16, device=DEV)
+    q[..., 512] = 99 * math.log(2)  # y = -99 in base 2, the zeros' -60
+    o, l = dsa.dsa_latent4_attn_dense(dict(q=q, cache=cache, scale=1.0), torch.tensor([n], dtype=torch.int32, device=DEV), causal=False)
+    assert not bool(o.any()) and dsa.read_device_flags(DEV) == 0
+    want = math.log(n - 64)  # (the first block adds e^-68)
+    # (the sums over blocks keep what they lose: as in _check_dense)
+    assert bool(((l.double() - want).abs() <= 2.0 ** -14 * (1 + want)).all())
+    del cache
+    torch.cuda.empty_cache()
