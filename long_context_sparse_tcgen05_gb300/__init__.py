@@ -697,42 +697,52 @@ _APPEND = struct.Struct("@iiPqqPfPPiiPq")
 _ATTN_HEAD, _ATTN_TAIL = struct.Struct("@iiiifPqq"), struct.Struct("@iP")
 
 
+def _table(table, d, pages, B):
+    """(address, entries of a sequence, sequences) of a block table on device number d."""
+    if table is None:
+        assert B is None or B <= pages, "the cache's sequences and the call's differ"
+        return 0, 0, pages
+    seqs, ld = table.shape
+    assert B is None or B == seqs, "the cache's sequences and the call's differ"
+    assert table.dtype is torch.int32 and table.is_contiguous() and table.get_device() == d, "block_table: dense int32 on the cache's device"
+    return table.data_ptr(), ld, seqs
+
+
 def _latent_cache(cache, B):
-    """(image of a dsa_latent_cache, sequences, rows a sequence holds) of a latent cache dict."""
-    codes, scales, rope, table = cache["codes"], cache["scales"], cache["rope"], cache.get("block_table")
-    dev = codes.device
+    """(image of a dsa_latent_cache, sequences, rows a sequence holds, device number) of a latent cache dict."""
+    codes, scales, rope = cache["codes"], cache["scales"], cache["rope"]
     pages, page = scales.shape
-    assert codes.is_cuda and codes.dtype in (torch.float8_e4m3fn, torch.uint8) and codes.is_contiguous()
+    d = codes.get_device()
+    assert d >= 0 and d == scales.get_device() == rope.get_device(), "a cache lies on one CUDA device"
+    assert codes.dtype in (torch.float8_e4m3fn, torch.uint8) and scales.dtype is torch.float32 and rope.dtype is torch.bfloat16
     assert codes.shape == (pages, page, 512) and rope.shape == (pages, page, 64)
-    seqs, ld = (pages, 0) if table is None else table.shape
-    assert B is None or (B <= seqs if table is None else B == seqs), "the cache's sequences and the call's differ"
-    return _CACHE.pack(pages, page, ld, codes.data_ptr(), _addr(scales, dev, torch.float32, "scales") or 0,
-                       _addr(rope, dev, torch.bfloat16, "rope") or 0, _addr(table, dev, torch.int32, "block_table") or 0), seqs, (ld or 1) * page
+    assert codes.is_contiguous() and scales.is_contiguous() and rope.is_contiguous(), "codes, scales and rope: dense"
+    table, ld, seqs = _table(cache.get("block_table"), d, pages, B)
+    return _CACHE.pack(pages, page, ld, codes.data_ptr(), scales.data_ptr(), rope.data_ptr(), table), seqs, (ld or 1) * page, d
 
 
 def _latent4_cache(cache, B):
     """_latent_cache of a 4-bit one."""
-    codes, groups, scales, rope, table = cache["codes"], cache["groups"], cache["scales"], cache["rope"], cache.get("block_table")
-    dev = codes.device
+    codes, groups, scales, rope = cache["codes"], cache["groups"], cache["scales"], cache["rope"]
     pages, page = scales.shape
-    assert codes.is_cuda and codes.dtype is torch.uint8 and codes.is_contiguous(), "codes: uint8, two codes a byte"
+    d = codes.get_device()
+    assert d >= 0 and d == groups.get_device() == scales.get_device() == rope.get_device(), "a cache lies on one CUDA device"
+    assert codes.dtype is torch.uint8 and groups.dtype is torch.uint8 and scales.dtype is torch.float32 and rope.dtype is torch.bfloat16
     assert codes.shape == (pages, page, 256) and groups.shape == (pages, page, 16) and rope.shape == (pages, page, 64)
-    seqs, ld = (pages, 0) if table is None else table.shape
-    assert B is None or (B <= seqs if table is None else B == seqs), "the cache's sequences and the call's differ"
-    return _CACHE4.pack(pages, page, ld, codes.data_ptr(), _addr(groups, dev, torch.uint8, "groups"),
-                        _addr(scales, dev, torch.float32, "scales") or 0, _addr(rope, dev, torch.bfloat16, "rope") or 0,
-                        _addr(table, dev, torch.int32, "block_table") or 0), seqs, (ld or 1) * page
+    assert codes.is_contiguous() and groups.is_contiguous() and scales.is_contiguous() and rope.is_contiguous(), "codes, groups, scales and rope: dense"
+    table, ld, seqs = _table(cache.get("block_table"), d, pages, B)
+    return _CACHE4.pack(pages, page, ld, codes.data_ptr(), groups.data_ptr(), scales.data_ptr(), rope.data_ptr(), table), seqs, (ld or 1) * page, d
 
 
 def latent_cache_struct(cache: dict, B: int | None = None):
     """(C struct, sequences) of a latent cache dict."""
-    image, seqs, _ = _latent_cache(cache, B)
+    image, seqs, _, _ = _latent_cache(cache, B)
     return LatentCache.from_buffer_copy(image), seqs
 
 
 def latent4_cache_struct(cache: dict, B: int | None = None):
     """(C struct, sequences) of a 4-bit latent cache dict."""
-    image, seqs, _ = _latent4_cache(cache, B)
+    image, seqs, _, _ = _latent4_cache(cache, B)
     return Latent4Cache.from_buffer_copy(image), seqs
 
 
@@ -828,17 +838,20 @@ def dsa_latent4_unpack(cache: dict, idx: torch.Tensor | None = None, *, n: int |
 
 def _latent_attn_args(args, image_of, at, idx_T):
     """The C struct `args` of an attention operand dict over the kind of cache that `image_of` takes."""
-    q, cache = at["q"], at["cache"]
-    B, T, H, d = q.shape
-    assert q.is_cuda and q.dtype is torch.bfloat16 and d == 576 and q.stride(3) == 1
-    assert H == 1 or q.stride(2) == 576, "the heads of one query must be contiguous"
-    image, _, rows = image_of(cache, B)
-    assert cache["codes"].device == q.device
+    q = at["q"]
+    B, T, H, width = q.shape
+    sb, st, sh, sd = q.stride()
+    assert q.dtype is torch.bfloat16 and width == 576 and sd == 1, "q: [B, T, H, 576] bf16"
+    assert H == 1 or sh == 576, "the heads of one query must be contiguous"
+    assert (sb or B < 2) and (st or T < 2), _BROADCAST
+    image, _, rows, d = image_of(at["cache"], B)
+    assert q.get_device() == d, "q and the cache lie on one CUDA device"
     S = at.get("S")
     if S is None:
         S = min(rows, 2 ** 31 - 1)
     assert 0 < S < 2 ** 31, "S: between 1 and 2^31 - 1 positions"
-    a = args.from_buffer_copy(_ATTN_HEAD.pack(B, T, int(S), H, 0.0, q.data_ptr(), *_token_strides(q)) + image + _ATTN_TAIL.pack(idx_T, 0))
+    a = args.from_buffer_copy(_ATTN_HEAD.pack(B, T, int(S), H, 0.0, q.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0) + image +
+                              _ATTN_TAIL.pack(idx_T, 0))
     a.scale = at["scale"]
     return a
 
