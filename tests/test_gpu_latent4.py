@@ -334,6 +334,25 @@ def test_sparse_attention_nan_rows_strided_queries_and_shared_index_rows():
     assert _same([o[0], l[0]], [want[0][0], want[1][0]]) and bool(o[1].isnan().all())
 
 
+@pytest.mark.parametrize("B,T,H,k", [(1, 200, 1, 70), (2, 400, 5, 33), (1, 300, 16, 2048), (3, 130, 40, 64), (2, 100, 64, 100), (1, 90, 128, 65),
+                                     (1, 153, 63, 1), (1, 77, 65, 300), (1, 5000, 3, 20)])
+def test_sparse_attention_of_many_tokens_of_one_index_row(B, T, H, k):
+    """Tokens of one index row share tiles where their queries lie side by side; the bits are those of an index row each."""
+    S = 2100
+    cache, q, idx = _cache(B, S, 64, seed=k), _q(B, T, H), _idx(B, 1, S, k, seed=H)
+    q[0, T // 2] *= 40.0  # (a token whose maximum moves where its neighbours' do not)
+    q[0, T // 3, 0, 3] = math.nan
+    each = idx.expand(B, T, k).contiguous()
+    apart = torch.empty((B, T, H + 1, 576), device=DEV, dtype=torch.bfloat16)[:, :, :H]
+    apart.copy_(q)
+    for call, c in ((dsa.dsa_latent4_attn, cache), (dsa.dsa_latent_attn, dsa.dsa_latent4_unpack(cache, n=S))):
+        at = dict(q=q, cache=c, scale=0.05, S=S)
+        want = call(at, each)
+        assert _same(call(at, idx), want) and _same(call(dict(at, q=apart), idx), want)
+        assert bool(want[0][0, T // 3, 0].isnan().all()) and not bool(want[0][0, 0].isnan().any())
+        assert not bool(call(at, torch.full_like(idx, -1))[0].any()) and dsa.read_device_flags(DEV) == 0
+
+
 # --- attention over every row --------------------------------------------------------------------
 
 def _call(cache):
