@@ -727,17 +727,16 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     }
   };
 
-  // An item's queries into L2, while the item before it is worked on: converting them waits for their loads, which shows where
-  // the items are short.  6 x 300 tokens of 64 heads, k 50 / 250: 130 -> 114, 160 -> 150 us, FP8 129 -> 108, 147 -> 131; dense,
-  // 1,216 tokens over 64 rows: 102 -> 93.  Not behind an item of more than four blocks (dense, 1,024 rows: 210 -> 214), nor for
-  // rows of up to 16 heads, which are loaded at once (one head: 79 -> 82).
+  // A row's queries into L2, while the item before it is worked on: converting them waits for their loads, which shows where
+  // the items are short.  6 x 300 tokens of 64 heads, k 50 / 250: 130 -> 114, 160 -> 150 us, FP8 129 -> 108, 147 -> 131.  Not
+  // behind an item of more than four blocks (nothing to win), nor for rows of up to 16 heads, which are loaded at once (one
+  // head: 79 -> 82).  Nor over all rows: tiles of one block gain (1,216 tokens over 64 rows: 102 -> 93), but a prompt of 4,096
+  // tokens loses (FP8 1,167 -> 1,184) and 1,024 tokens of 128 heads over 8,192 rows, too (1,962 -> 1,977).
   constexpr int kFetchBlocks = 4, kFetchHeads = 16;
   auto fetch = [&](int item) {
     const Item I = item_of<kForm>(p, item);
-    const int tokens = kForm == kAll ? I.last + 1 - I.t : 1, heads = p.groups > 1 ? I.heads : p.H;
     const uint16_t* q = p.q + I.b * p.q_sb + I.t * p.q_st + (int64_t)I.h0 * kD;
-    for (int t = lane; t < tokens; t += 32)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q + t * p.q_st), "r"(heads * kD * 2) : "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(I.heads * kD * 2) : "memory");
   };
 
   // An item's O, once its sums and its last value product are there: dim chunks 0 and 2 by the O warps,
@@ -1503,8 +1502,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
           nb = ok ? sm->nb[it & 1] : 0;
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
-          if (kForm != kRowParts && qw == 0 && nb <= kFetchBlocks && item + G < items && (kForm == kAll || p.H > kFetchHeads))
-            fetch(item + G);
+          if (kForm == kRows && qw == 0 && nb <= kFetchBlocks && item + G < items && p.H > kFetchHeads) fetch(item + G);
           if (ok && nb) ok = wait(&bar.q_empty, (oc & 1) ^ 1);
           if (named_sync_or(2, 128, !ok)) {  // all rows are there; the four warps go on or leave together
             ok = false;
