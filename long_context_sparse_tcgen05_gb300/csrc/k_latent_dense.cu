@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_latent_join_long(LatentAttnLau
 }
 
 template <bool kFour>
-auto dense_kernel(bool poll) {
+auto dense_kernel(bool poll, bool tiles) {
+  if constexpr (!kFour)
+    if (tiles) return poll ? k_latent_attn<true, kAllTiles, kFour> : k_latent_attn<false, kAllTiles, kFour>;
   return poll ? k_latent_attn<true, kAll, kFour> : k_latent_attn<false, kAll, kFour>;
 }
 
@@ -225,13 +227,14 @@ cudaError_t launch(LatentAttnLaunch p, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-    for (int poll = 0; poll < 2; ++poll)
-      if ((e = prepare_kernel<kFour>(dense_kernel<kFour>(poll))) != cudaSuccess) return e;
+    for (int k = 0; k < 4; ++k)
+      if ((e = prepare_kernel<kFour>(dense_kernel<kFour>(k & 1, k & 2))) != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
   cudaLaunchAttribute attr{};
   const cudaLaunchConfig_t cfg = launch_config<kFour>(runs, 1, st, &attr);
-  if ((e = cudaLaunchKernelEx(&cfg, dense_kernel<kFour>(p.wait < kDefaultWaitCycles), p)) != cudaSuccess) return e;
+  const bool tiles = p.causal && p.tile_t > 1;
+  if ((e = cudaLaunchKernelEx(&cfg, dense_kernel<kFour>(p.wait < kDefaultWaitCycles, tiles), p)) != cudaSuccess) return e;
   count_launches(1);
   if (runs > 1) {
     const int split = std::min(runs - 1, p.B * p.tiles_t * p.groups);  // split tiles, at most

@@ -132,8 +132,10 @@ static_assert(kHg * kLatentDim * sizeof(float) <= kStages * kStage + 2 * kPBytes
 static_assert(kHg * kMaxLatentSplits * sizeof(float) <= kQBytes, "the parts' weights in the queries' room");
 
 // What a kernel walks.  kRows: whole index rows; kRowParts: parts of index rows, one a CTA, joined over a
-// cluster; kAll: all rows that the queries see, divided into equal runs of blocks.
-enum Form { kRows, kRowParts, kAll };
+// cluster; kAll: all rows that the queries see, divided into equal runs of blocks; kAllTiles: the same of FP8 rows some of
+// which not every token of a tile sees.  (In a kernel of its own: what it does about NaN codes costs calls without such tiles
+// 6%, a prompt of 4,096 tokens of 64 heads 1,147 -> 1,218 us, and its own calls 4%, of 16 heads 323 -> 336.)
+enum Form { kRows, kRowParts, kAll, kAllTiles };
 
 struct Bars {
   uint64_t q_full, q_empty, qs_full[2];
@@ -343,6 +345,18 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
+// Zeros in the place of NaN among the sixteen e4m3 codes at `at` in shared memory.
+__device__ __forceinline__ void drop_nan_codes(uint32_t at) {
+  uint32_t w[4], any = 0;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t hit = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // (0x7f alone carries into its top bit)
+    any |= hit;
+    w[i] &= ~((hit >> 7) * 0xffu);
+  }
+  if (any) st_shared16(at, make_uint4(w[0], w[1], w[2], w[3]));
+}
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -391,7 +405,7 @@ struct Item {
 template <Form kForm>
 __device__ __forceinline__ Item item_of(const LatentAttnLaunch& p, int item) {
   Item r;
-  if constexpr (kForm == kAll) {
+  if constexpr (kForm >= kAll) {
     const int u = item / p.groups;
     r.h0 = (item - u * p.groups) * kHg;
     r.b = u / p.tiles_t;
@@ -568,7 +582,7 @@ struct ShareCount {
 // joining code beside them.)
 template <bool kPoll, Form kForm, bool kFour>
 __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLaunch p) {
-  constexpr bool kParts = kForm == kRowParts;
+  constexpr bool kParts = kForm == kRowParts, kDense = kForm >= kAll;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kv_s = base;
@@ -579,7 +593,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
   volatile int* abort_flag = &sm->abort;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   int first = blockIdx.x, items = p.B * p.T * p.groups * p.splits;
-  const int G = kForm == kAll ? 1 : (int)gridDim.x;
+  const int G = kDense ? 1 : (int)gridDim.x;
   // a wait that every lane of a warp makes, with one answer for the warp
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity, abort_flag, p.wait));
@@ -621,16 +635,16 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     tmem_relinquish();
   }
   ShareRoom& room = *reinterpret_cast<ShareRoom*>(kv_s);  // (no stage is in use yet)
-  using Count = std::conditional_t<kForm == kAll, ShareCount<kThreads<kFour>>, int>;
+  using Count = std::conditional_t<kDense, ShareCount<kThreads<kFour>>, int>;
   const Count count = [&] {
-    if constexpr (kForm == kAll) return Count(p, room);
+    if constexpr (kDense) return Count(p, room);
     else return 0;
   }();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm->tmem, 0);
-  if constexpr (kForm == kAll) {
+  if constexpr (kDense) {
     if (!count.find(sm->share, room)) {
       if (warp == kSWarp) tmem_dealloc(tmem, kTmemCols);
       return;
@@ -648,7 +662,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     const Item I = item_of<kForm>(p, item);
     const uint16_t* q0 = p.q + I.b * p.q_sb + I.t * p.q_st + (int64_t)I.h0 * kD;
     auto head_at = [&](int h) -> const uint16_t* {
-      if (kForm != kAll || p.tile_t == 1) return q0 + (int64_t)h * kD;
+      if (!kDense || p.tile_t == 1) return q0 + (int64_t)h * kD;
       const int t = h / p.H;
       return q0 + t * p.q_st + (int64_t)(h - t * p.H) * kD;
     };
@@ -659,7 +673,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const bool live = h + k * n < I.heads;
-        const uint4* q = reinterpret_cast<const uint4*>(head_at(kForm == kAll && !live ? 0 : h + k * n));
+        const uint4* q = reinterpret_cast<const uint4*>(head_at(kDense && !live ? 0 : h + k * n));
         nx[k][0] = live ? __ldg(q + lane) : make_uint4(0, 0, 0, 0);
         nx[k][1] = live ? __ldg(q + 32 + lane) : make_uint4(0, 0, 0, 0);
         nr[k] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + kLatentDim / 8) + lane) : 0u;
@@ -761,7 +775,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     tc_fence_after();
     // (a head without weights, sum 0, gives zeros whatever its products left)
     const bool none = __any_sync(0xffffffffu, ls[lane] == 0.f || ls[32 + lane] == 0.f);
-    const int slot = kForm == kAll ? sm->share.slot(item) : -1;
+    const int slot = kDense ? sm->share.slot(item) : -1;
     if (kParts || slot >= 0) {  // fp32 rows over the stages, which the last products have read, or to memory; 32 dims of a head a store
       float* rows = kParts ? reinterpret_cast<float*>(kv_s) : p.parts + (int64_t)slot * kPartFloats;
 #pragma unroll 1
@@ -1134,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       };
       auto blocks_of = [&](int item) -> Blocks {
         const Item I = item_of<kForm>(p, item);
-        if constexpr (kForm == kAll) {
+        if constexpr (kDense) {
           const int sees = dense_sees(p, I.last, __ldg(p.lens + I.b)), j0 = item == first ? sm->share.first_j0 : 0;
           return {nullptr, I.b, j0, (item == sm->share.last ? sm->share.last_end : dense_blocks(sees)) - j0, sees};
         }
@@ -1171,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         const bool in = jb < (here ? cur.nb : next.nb);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if constexpr (kForm == kAll) id[u] = in && e0 + u * 32 < (here ? cur.sees : next.sees) ? e0 + u * 32 : -1;
+          if constexpr (kDense) id[u] = in && e0 + u * 32 < (here ? cur.sees : next.sees) ? e0 + u * 32 : -1;
           else id[u] = in && e0 + u * 32 < p.kk ? __ldg(ids + e0 + u * 32) : -1;
         }
       };
@@ -1226,7 +1240,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
           if (!(ok = wait(&bar.info_empty[it & 1], ((it >> 1) & 1) ^ 1))) break;
           if (lane == 0) {
             sm->nb[it & 1] = cur.nb;
-            if constexpr (kForm == kAll) {
+            if constexpr (kDense) {
               sm->j0[it & 1] = cur.j0;
               sm->sees[it & 1] = cur.sees;
               const int len = __ldg(p.lens + cur.b);
@@ -1266,7 +1280,10 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
             float* sc = reinterpret_cast<float*>(&sm->sc[ri][r >> 1]) + (r & 1);
             sc[0] = row[u] >= 0 ? scale[u] : 0.f;
             sc[2] = row[u] >= 0 ? log2f(scale[u]) : -INFINITY;
-            sm->isc[ri][r] = row[u] >= 0 ? 1.f / scale[u] : 0.f;
+            const float inv = row[u] >= 0 ? 1.f / scale[u] : 0.f;
+            // (never a NaN: it leaves the zero weights of a tile's tokens that do not see the row at zero, and those that do
+            // have a NaN weight by its scale alone)
+            sm->isc[ri][r] = kDense ? fminf(inv, 0x1p60f) : inv;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.ix_full[ri]);
@@ -1302,7 +1319,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       // Of a tile of several tokens: the keys of the item's first block on that this thread's head sees (its last
       // token's are all there are).
       int left = INT_MAX;
-      if constexpr (kForm == kAll) {
+      if constexpr (kDense) {
         const Item I = item_of<kForm>(p, item);
         if (p.causal && p.tile_t > 1) left = sm->sees[it & 1] - (I.last - I.t - min(hl / p.H, I.last - I.t)) - sm->j0[it & 1] * kNB;
       }
@@ -1340,9 +1357,9 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
           const f32x2 t = fma_2(pair(__uint_as_float(r[4 * jj + 2]), __uint_as_float(r[4 * jj + 3])), pair(0.0625f, 0.0625f),
                                 pair(__uint_as_float(r[4 * jj]), __uint_as_float(r[4 * jj + 1])));
           y[jj] = fma_2(t, mul_2(pair(cq, cq), pair(s.x, s.y)), pair(s.z, s.w));
-          if constexpr (kForm != kAll) ymax = max3(ymax, lo_of(y[jj]), hi_of(y[jj]));
+          if constexpr (!kDense) ymax = max3(ymax, lo_of(y[jj]), hi_of(y[jj]));
         }
-        if constexpr (kForm == kAll) {
+        if constexpr (kDense) {
           if (__any_sync(0xffffffffu, left < kNB)) {
 #pragma unroll
             for (int jj = 0; jj < 8; ++jj) {
@@ -1357,7 +1374,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 1));
         ymax = fmaxf(ymax, __shfl_xor_sync(0xffffffffu, ymax, 2));
         const float E = ceilf(ymax) - 8.f;  // -inf: no weight in this block
-        const bool move = E > E0 + (kForm == kAll ? kMoveAll : kMove);  // (E0 starts at -inf)
+        const bool move = E > E0 + (kDense ? kMoveAll : kMove);  // (E0 starts at -inf)
         const float alpha = move ? ex2(E0 - E) : 1.f;
         const int any = __any_sync(0xffffffffu, move);
         E0 = move ? E : E0;
@@ -1388,7 +1405,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         }
         const float sum = lo_of(sum2) + hi_of(sum2);
         const float f = E == -INFINITY ? 0.f : ex2(E - E0);
-        if constexpr (kForm == kAll) {
+        if constexpr (kDense) {
           // of up to 2^25 blocks: with what the last sum lost (Kahan 1965), or 4 million equal weights are off by 2^-8
           const float term = fmaf(sum, f, -lost * alpha), last = l * alpha;
           l = last + term;
@@ -1411,7 +1428,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         sm->lsum[oc & 1][hl] = l == 0.f ? 0.f : 1.f / l;
         const Item I = item_of<kForm>(p, item);
         const float v = l == 0.f ? -INFINITY : (E0 + log2f(l)) * kLn2;
-        const int slot = kForm == kAll ? sm->share.slot(item) : -1;
+        const int slot = kDense ? sm->share.slot(item) : -1;
         if (kParts) sm->part_lse[hl] = v;
         else if (slot >= 0) p.parts[(int64_t)slot * kPartFloats + kHg * kLatentDim + hl] = v;
         else if (p.lse && hl < I.heads) p.lse[(int64_t)I.row * p.H + I.h0 + hl] = v;
@@ -1437,6 +1454,15 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       for (int item = first; ok && item < items; item += G, ++it) {
         if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
         const int nb = sm->nb[it & 1];
+        // (FP8 rows) Keys of the item from `hidden` on, up to `hidden_end`, are not seen by every token of the tile.
+        int hidden = INT_MAX, hidden_end = 0;
+        if constexpr (kForm == kAllTiles && !kFour) {
+          if (p.causal && p.tile_t > 1) {
+            const Item I = item_of<kForm>(p, item);
+            hidden_end = sm->sees[it & 1] - sm->j0[it & 1] * kNB;
+            hidden = max(0, hidden_end - (I.last - I.t));
+          }
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
         if (nb == 0) {  // nothing selected: O = 0, LSE = -inf
@@ -1475,6 +1501,15 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
                 tmem_st_x8(tmem + lane_base + kColO + c * kHg + 8 * w, v[c]);
               }
             }
+          }
+          if (kForm == kAllTiles && !kFour && j * kNB + kNB - 1 >= hidden) {
+            // Weights of rows that a token does not see are zero, which times a NaN code would still reach its values.  The
+            // scores have been taken of those codes, so that tokens which see them have NaN weights: zeros in their place.
+            if (!(ok = wait(&bar.kv_full[g % kStages], (g / kStages) & 1))) break;
+#pragma unroll 1
+            for (int r = max(0, hidden - j * kNB) + (warp & 3); r < min(kNB, hidden_end - j * kNB); r += 4)
+              drop_nan_codes(smem_addr(kv_s) + g % kStages * kStage + (lane >> 3) * kAtom + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            async_fence();
           }
           // the block's scales (the products that read this buffer's last ones are done: the softmax
           // waited for them before it wrote these)

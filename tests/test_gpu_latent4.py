@@ -772,3 +772,39 @@ def test_dense_attention_sums_of_millions_of_rows_of_the_least_scale_stay_finite
     assert bool(((l.double() - want).abs() <= 2.0 ** -14 * (1 + want)).all())
     del cache
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("B,T,H,S", [(1, 70, 1, 300), (2, 40, 16, 300), (1, 33, 21, 129), (2, 7, 32, 5000), (1, 9, 33, 200), (1, 600, 16, 600), (1, 5, 64, 300)])
+@pytest.mark.parametrize("back", [1, 4, 66])
+def test_dense_attention_what_is_not_finite_reaches_only_the_tokens_that_see_it(B, T, H, S, back, four):
+    """A row that is not finite, `back` positions before a sequence's end: tokens before it keep their bits, whether
+    their heads share a tile with tokens that see it or not."""
+    at_row = S - back
+    cache = _cache(B, S, 48, four, seed=S)
+    at = dict(q=_q(B, T, H), cache=cache, scale=0.05, S=S)
+    lens = torch.full((B,), S, dtype=torch.int32, device=DEV)
+    want = _call(cache)(at, lens)
+    first = max(0, T - back)  # the first token of sequence 0 that sees the row
+    assert dsa.read_device_flags(DEV) == 0 and bool(torch.isfinite(want[0]).all())
+    r = int(_flat(cache, torch.zeros(1, dtype=torch.long, device=DEV), torch.tensor([at_row], device=DEV)))
+    append = dsa.dsa_latent4_append if four else dsa.dsa_latent_append
+    for kind in ("nan", "inf", "scale", "rope nan", "rope inf") + (() if four else ("code", "code inside")):
+        c = {k: v.clone() for k, v in cache.items()}
+        if kind in ("nan", "inf"):
+            x = torch.randn((B, 1, 576), generator=_gen(back), device=DEV).bfloat16()
+            x[0, 0, 300] = math.nan if kind == "nan" else -math.inf
+            append(x, c, positions=torch.tensor([[at_row]] + [[-1]] * (B - 1), device=DEV))
+            assert not math.isfinite(float(c["scales"].view(-1)[r]))
+        elif kind == "scale":
+            c["scales"].view(-1)[r] = math.nan
+        elif kind.startswith("rope"):
+            c["rope"].view(-1, 64)[r, 5] = math.nan if kind == "rope nan" else math.inf
+        else:  # an e4m3 NaN under a finite scale
+            c["codes"].view(torch.uint8).view(-1, 512)[r, 0 if kind == "code" else 499] = 0xFF if kind == "code" else 0x7F
+        o, l = _call(cache)(dict(at, cache=c), lens)
+        assert _same([o[0, :first], l[0, :first]], [want[0][0, :first], want[1][0, :first]]), kind
+        assert _same([o[1:], l[1:]], [want[0][1:], want[1][1:]]), kind
+        if kind != "rope inf":  # (which may be a score of minus infinity)
+            assert bool(o[0, first:].isnan().all()) and bool(l[0, first:].isnan().all()), kind
+    assert dsa.read_device_flags(DEV) == 0
