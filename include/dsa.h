@@ -476,7 +476,7 @@ size_t dsa_latent_attn_workspace_size(const dsa_latent_attn_args* a, int32_t k);
  *           [0, lens[b] - T + 1 + t): itself and what precedes it; 0: every query sees [0, lens[b])
  * A query that sees nothing gets out = 0, lse = -inf; positions without a valid page are skipped and raise
  * DSA_FLAG_BAD_INDEX.  The args' idx_T is not read.  Precision as dsa_latent_attn (the 64 neighbours: positions
- * 64 i .. 64 i + 63).  The rows of all queries are divided evenly over the SMs, whatever the lengths, and
+ * 64 i .. 64 i + 63); sums over more than 2^18 rows are made of sums over 2^18 at a time.  The rows of all queries are divided evenly over the SMs, whatever the lengths, and
  * partial results are joined in a fixed order: results do not vary from run to run on one kind of device.
  * ws: dsa_latent_attn_dense_workspace_size bytes (of the current device): the flag word, and scratch that calls
  * which may overlap must not share. */

@@ -196,11 +196,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_latent_join_long(LatentAttnLau
   if (p.lse && quarter == 0 && lane == 0) p.lse[row] = sum_s == 0.f ? -INFINITY : mx + logf(sum_s);
 }
 
-template <bool kFour>
-auto dense_kernel(bool poll, bool tiles) {
+template <bool kPoll, bool kFour>
+auto dense_kernel(Form form) {
+  if (form == kAllLong) return k_latent_attn<kPoll, kAllLong, kFour>;
   if constexpr (!kFour)
-    if (tiles) return poll ? k_latent_attn<true, kAllTiles, kFour> : k_latent_attn<false, kAllTiles, kFour>;
-  return poll ? k_latent_attn<true, kAll, kFour> : k_latent_attn<false, kAll, kFour>;
+    if (form == kAllTiles) return k_latent_attn<kPoll, kAllTiles, kFour>;
+  return k_latent_attn<kPoll, kAll, kFour>;
+}
+template <bool kFour>
+auto dense_kernel(bool poll, Form form) {
+  return poll ? dense_kernel<true, kFour>(form) : dense_kernel<false, kFour>(form);
 }
 
 // How a call's queries lie on tiles of 64 heads: of one token a group of 64, or, of few heads, several tokens.
@@ -215,6 +220,12 @@ int runs_of(const LatentAttnLaunch& p) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(device_sm_count(), kMaxRuns), blocks / kMinRun));
 }
 
+// Blocks of one tile that a CTA may walk, at most: of few tiles their equal parts, else all that a run holds (see ShareCount).
+int64_t most_blocks(const LatentAttnLaunch& p, int runs) {
+  const int64_t tiles = (int64_t)p.B * p.tiles_t * p.groups, blocks = (p.S - 1) / kNB + 1;
+  return std::min(blocks, tiles * (blocks + kMostCost) / runs + 2 * (kMostCost + kMinRun));
+}
+
 template <bool kFour>
 cudaError_t launch(LatentAttnLaunch p, cudaStream_t st) {
   TraceScope trace(kTraceAttention, st);
@@ -227,14 +238,15 @@ cudaError_t launch(LatentAttnLaunch p, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-    for (int k = 0; k < 4; ++k)
-      if ((e = prepare_kernel<kFour>(dense_kernel<kFour>(k & 1, k & 2))) != cudaSuccess) return e;
+    for (int poll = 0; poll < 2; ++poll)
+      for (Form form : {kAll, kAllTiles, kAllLong})
+        if ((e = prepare_kernel<kFour>(dense_kernel<kFour>(poll, form))) != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
   cudaLaunchAttribute attr{};
   const cudaLaunchConfig_t cfg = launch_config<kFour>(runs, 1, st, &attr);
-  const bool tiles = p.causal && p.tile_t > 1;
-  if ((e = cudaLaunchKernelEx(&cfg, dense_kernel<kFour>(p.wait < kDefaultWaitCycles, tiles), p)) != cudaSuccess) return e;
+  const Form form = most_blocks(p, runs) > kMaxBlocks ? kAllLong : p.causal && p.tile_t > 1 ? kAllTiles : kAll;
+  if ((e = cudaLaunchKernelEx(&cfg, dense_kernel<kFour>(p.wait < kDefaultWaitCycles, form), p)) != cudaSuccess) return e;
   count_launches(1);
   if (runs > 1) {
     const int split = std::min(runs - 1, p.B * p.tiles_t * p.groups);  // split tiles, at most

@@ -20,7 +20,7 @@
 //     products: in ten of a row's 32 blocks, a third of a decode step).  Only when E passes
 //     E0 + 40 is O rescaled and E0 moved.  Row sums take p_j / s_j, times 2^(E - E0), in fp32.
 // FP8 products accumulate exactly enough in fp32 (sums of 2,048 products of mixed size came out
-// equal to the 64-bit sum).
+// equal to the 64-bit sum; those of millions do not, see kMaxBlocks).
 //
 // A row of the 4-bit cache has 512 e2m1 codes, a power of two for 32 of them, and the same scale and rope
 // values: each code times its power of two is an e4m3 value (see latent_cache.cuh), so the gather warps expand
@@ -116,9 +116,19 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColQR = 384, kColSfA = 416, kColSfB = 424, kColS = 448;
 constexpr int64_t kPartFloats = kHg * kLatentDim + kHg;  // of a part in memory: O by head, then lse
 constexpr int kMinRun = 2;                   // blocks of a CTA's run, where there are few
-constexpr int kTileCost = 10;                // of a tile beside its blocks, in blocks: see ShareCount
+constexpr int kTileCost = 10, kMostCost = kTileCost + 3;  // of a tile beside its blocks, in blocks: see ShareCount
 constexpr int kSlack = 20;                   // see ShareCount
 constexpr int kMaxRuns = 1024;               // CTAs of a call over all rows
+// Of a call over all rows, blocks that go into one O in tensor memory.  A CTA walks a longer tile in several items and adds
+// their O's in memory, in fp32: each of a block's four additions may lose a last place (2^-23), and they lose in one direction.
+// FP8 rows of one sign in one O came out short by (beside bf16's rounding, 2e-3 norm-wise) 2^18 rows 2e-4, 2^20 1.6e-3, 2^22
+// 1.1e-2, equal ones by up to 1.8e-2.  2^18 rows, 2^14 additions, stay within 2^-9.  And a wait, which may last an item, stays
+// far below its limit however long the rows are.
+constexpr int kMaxBlocks = 4096;
+// What is told of an item: its blocks and, of kAllLong, whether its tile goes on in the CTA's next item, or began in an
+// earlier one.
+constexpr int kBlocksMask = 0xffff, kGoesOn = 1 << 16, kBegan = 1 << 17;
+static_assert(kMaxBlocks <= kBlocksMask);
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // E0 moves when a block's E passes it by this.  A row sum holds up to 1,024 blocks of 64 weights
 // p_j / s_j <= 2^8 / 2^-60 (the append's least scale), times 2^(E - E0): 2^(10 + 6 + 8 + 60 + 40) = 2^124,
@@ -134,8 +144,9 @@ static_assert(kHg * kMaxLatentSplits * sizeof(float) <= kQBytes, "the parts' wei
 // What a kernel walks.  kRows: whole index rows; kRowParts: parts of index rows, one a CTA, joined over a
 // cluster; kAll: all rows that the queries see, divided into equal runs of blocks; kAllTiles: the same of FP8 rows some of
 // which not every token of a tile sees.  (In a kernel of its own: what it does about NaN codes costs calls without such tiles
-// 6%, a prompt of 4,096 tokens of 64 heads 1,147 -> 1,218 us, and its own calls 4%, of 16 heads 323 -> 336.)
-enum Form { kRows, kRowParts, kAll, kAllTiles };
+// 6%, a prompt of 4,096 tokens of 64 heads 1,147 -> 1,218 us, and its own calls 4%, of 16 heads 323 -> 336.)  kAllLong: any of
+// these calls of which a CTA may have more than kMaxBlocks of one tile (3 to 6% slower a block, so a kernel of its own, too).
+enum Form { kRows, kRowParts, kAll, kAllTiles, kAllLong };
 
 struct Bars {
   uint64_t q_full, q_empty, qs_full[2];
@@ -167,18 +178,19 @@ struct Small {
   int valid[kRing];                      // some row of the block counts
   alignas(16) float alpha[2][kHg];       // by block parity: factor of O where `need` is set
   uint32_t sf[2][kHg];                   // by block parity: a block's scale, as exponent + 127 in each byte
-  alignas(16) float lsum[2][kHg];        // reciprocal row sums, by item parity
+  alignas(16) float lsum[2][kHg];        // reciprocal row sums, by item parity (of a tile that goes on: 1, or 0 without weights)
   float part_lse[kHg];                   // of a part of a row
   float qs[2][kHg], qnext[kHg];          // 2^-k of the item's heads, and of the converted next one's
   alignas(8) uint8_t need[2][8];         // by block parity and group of 8 heads: O must be rescaled
   Bars bar;
   uint32_t tmem;
   int abort;
-  int nb[2];                             // blocks of the item, by item parity
+  int nb[2];                             // blocks of the item (and flags), by item parity
   // of a call over all rows: the item's first block and the positions that its last token sees, by item
   // parity; this CTA's share of the tiles
   int j0[2], sees[2];
   DenseShare share;
+  float carry[2][kHg];                   // of a tile that began before, by item parity: factor of the O's so far
 };
 constexpr size_t kSmem = 1024 + kStages * kStage + 2 * kPBytes + kQBytes + sizeof(Small);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -456,7 +468,7 @@ struct ShareCount {
   const LatentAttnLaunch& p;
   int64_t sum, upto;  // cost of this thread's tiles; of its warp's threads up to it
   // A tile's own cost beside its n blocks.
-  __device__ __forceinline__ static int own(int n) { return max(kTileCost, kTileCost + 3 - n / 4); }
+  __device__ __forceinline__ static int own(int n) { return max(kTileCost, kMostCost - n / 4); }
   int tiles, lo, hi;
   __device__ __forceinline__ int blocks(int tile) const {
     const Item I = item_of<kAll>(p, tile);
@@ -582,7 +594,7 @@ struct ShareCount {
 // joining code beside them.)
 template <bool kPoll, Form kForm, bool kFour>
 __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLaunch p) {
-  constexpr bool kParts = kForm == kRowParts, kDense = kForm >= kAll;
+  constexpr bool kParts = kForm == kRowParts, kDense = kForm >= kAll, kLong = kForm == kAllLong;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kv_s = base;
@@ -594,6 +606,9 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   int first = blockIdx.x, items = p.B * p.T * p.groups * p.splits;
   const int G = kDense ? 1 : (int)gridDim.x;
+  // of what is told of an item: its blocks, and how far on the next item is
+  auto blocks_told = [](int told) { return kLong ? told & kBlocksMask : told; };
+  auto step = [&](int told) { return kLong && (told & kGoesOn) ? 0 : G; };
   // a wait that every lane of a warp makes, with one answer for the warp
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, bar_wait<kPoll>(b, parity, abort_flag, p.wait));
@@ -761,7 +776,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
   auto meet_last = [&](bool ok) {
     if (!met_failure) named_sync_or(1, kEpiThreads, !ok);
   };
-  auto epilogue = [&](int item, int oc) -> bool {
+  auto epilogue = [&](int item, int oc, int told) -> bool {
     const int q4 = warp & 3, cw = warp < kQWarp0 ? 0 : 1;
     const Item I = item_of<kForm>(p, item);
     const float* ls = sm->lsum[oc & 1];
@@ -775,8 +790,32 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     tc_fence_after();
     // (a head without weights, sum 0, gives zeros whatever its products left)
     const bool none = __any_sync(0xffffffffu, ls[lane] == 0.f || ls[32 + lane] == 0.f);
-    const int slot = kDense ? sm->share.slot(item) : -1;
-    if (kParts || slot >= 0) {  // fp32 rows over the stages, which the last products have read, or to memory; 32 dims of a head a store
+    const int part = kDense ? sm->share.slot(item) : -1;
+    // (a tile that the CTA has whole, in several items, passes through the room of its last part, which comes later)
+    const bool several = kLong && (told & (kGoesOn | kBegan)) != 0;
+    const int slot = several && part < 0 ? 2 * (int)blockIdx.x + 1 : part;
+    if (several) {  // (a thread reads what it wrote itself)
+      float* rows = p.parts + (int64_t)slot * kPartFloats;
+#pragma unroll 1
+      for (int i = 0; i < kHg / 4; ++i) {
+        const int c = i & 1, h0 = 8 * (i >> 1);
+        if (h0 >= I.heads) break;
+        const int dim = (2 * c + cw) * 128 + q4 * 32 + lane;
+        uint32_t r[8];
+        tmem_ld_x8(o_addr + 2 * c * kHg + h0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          float* at = rows + (h0 + u) * kLatentDim + dim;
+          const float a = ls[h0 + u];
+          float v = __uint_as_float(r[u]);
+          if (told & kBegan) v = fmaf(*at, sm->carry[oc & 1][h0 + u], v);
+          v = a == 0.f ? 0.f : v * a;
+          if ((told & kGoesOn) || part >= 0) *at = v;
+          else if (h0 + u < I.heads) reinterpret_cast<__nv_bfloat16*>(p.out)[((int64_t)I.row * p.H + I.h0 + h0 + u) * kLatentDim + dim] = __float2bfloat16_rn(v);
+        }
+      }
+    } else if (kParts || slot >= 0) {  // fp32 rows over the stages, which the last products have read, or to memory; 32 dims of a head a store
       float* rows = kParts ? reinterpret_cast<float*>(kv_s) : p.parts + (int64_t)slot * kPartFloats;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
@@ -952,9 +991,10 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     bool ok = true;
     const uint8_t* const codes = p.cache.codes;
     const uint8_t* const rope = reinterpret_cast<const uint8_t*>(p.cache.rope);
-    for (int item = first; ok && item < items; item += G, ++it) {
+    for (int item = first, told = 0; ok && item < items; item += step(told), ++it) {
       if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
-      const int nb = sm->nb[it & 1];
+      told = sm->nb[it & 1];
+      const int nb = blocks_told(told);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
       if constexpr (kFour) {
@@ -1063,9 +1103,10 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       int it = 0, oc = 0;
       uint32_t g = 0;
       bool ok = true;
-      for (int item = first; ok && item < items; item += G, ++it) {
+      for (int item = first, told = 0; ok && item < items; item += step(told), ++it) {
         if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
-        const int nb = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
+        told = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
+        const int nb = blocks_told(told);
         if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
         if (nb == 0) continue;
         if (!(ok = wait(&bar.q_full, oc & 1))) break;
@@ -1103,9 +1144,10 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       int it = 0, oc = 0;
       uint32_t g = 0;
       bool ok = true;
-      for (int item = first; ok && item < items; item += G, ++it) {
+      for (int item = first, told = 0; ok && item < items; item += step(told), ++it) {
         if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
-        const int nb = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
+        told = __shfl_sync(0xffffffffu, sm->nb[it & 1], 0);
+        const int nb = blocks_told(told);
         if (lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
         if (nb == 0) continue;
         if (!(ok = wait(&bar.o_empty, (oc & 1) ^ 1))) break;
@@ -1146,11 +1188,14 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         int b, j0, nb;
         int sees;  // of a call over all rows: the positions that the tile's last token sees
       };
+      // Of a call over all rows, where this CTA's blocks of a tile begin and end.
+      auto tile_begin = [&](int tile) { return tile == first ? sm->share.first_j0 : 0; };
+      auto tile_end = [&](int tile, int sees) { return tile == sm->share.last ? sm->share.last_end : dense_blocks(sees); };
       auto blocks_of = [&](int item) -> Blocks {
         const Item I = item_of<kForm>(p, item);
         if constexpr (kDense) {
-          const int sees = dense_sees(p, I.last, __ldg(p.lens + I.b)), j0 = item == first ? sm->share.first_j0 : 0;
-          return {nullptr, I.b, j0, (item == sm->share.last ? sm->share.last_end : dense_blocks(sees)) - j0, sees};
+          const int sees = dense_sees(p, I.last, __ldg(p.lens + I.b)), j0 = tile_begin(item), nb = tile_end(item, sees) - j0;
+          return {nullptr, I.b, j0, kLong ? min(nb, kMaxBlocks) : nb, sees};
         }
         const int32_t* ids = p.idx + I.b * p.idx_sb + I.t * p.idx_st;
         // blocks of the row = 1 + (last entry other than -1) / 64, searched from the end
@@ -1172,9 +1217,15 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         const int j0 = (int)((int64_t)I.split * nbr / p.splits);
         return {ids, I.b, j0, (int)((int64_t)(I.split + 1) * nbr / p.splits) - j0, 0};
       };
+      Blocks cur{}, next{};
+      // The blocks behind `cur` of a tile that goes on.  (Chosen inside blocks_of, or in a function around both, a prompt of 4,096
+      // FP8 rows took 2% longer.)
+      auto rest_of = [&](int tile) -> Blocks {
+        const int j0 = cur.j0 + cur.nb;
+        return {nullptr, cur.b, j0, min(tile_end(tile, cur.sees) - j0, kMaxBlocks), cur.sees};
+      };
       // (Of a part the row is taken to be full while its end is looked for: its ids are then there a latency earlier, 29.5 ->
       // 28.3 us a 32-sequence decode step out of L2.  In the kernel that walks many rows the code cost 3%.)
-      Blocks cur{}, next{};
       int id_0[2], id_2[2], id[2];
       bool guessed = false;
       // Below, block j >= cur.nb is the next item's block j - cur.nb.
@@ -1235,11 +1286,13 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       int it = 0;
       uint32_t g = 0;
       bool ok = true, ahead = false;  // ahead: id, page, off, row and scale are the item's
-      for (int item = first; ok && item < items; item += G, ++it) {
+      for (int item = first, told = 0; ok && item < items; item += step(told), ++it) {
+        if constexpr (kLong)
+          told = (cur.j0 + cur.nb < tile_end(item, cur.sees) ? kGoesOn : 0) | (cur.j0 > tile_begin(item) ? kBegan : 0);
         if (warp == kIxWarp0) {
           if (!(ok = wait(&bar.info_empty[it & 1], ((it >> 1) & 1) ^ 1))) break;
           if (lane == 0) {
-            sm->nb[it & 1] = cur.nb;
+            sm->nb[it & 1] = cur.nb | told;
             if constexpr (kDense) {
               sm->j0[it & 1] = cur.j0;
               sm->sees[it & 1] = cur.sees;
@@ -1262,7 +1315,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
           load_pages(j + 2, id_2, page, off);
         }
         guessed = false;
-        int known = item + G < items ? 0 : 3;  // the last loads that saw the blocks of this or the next item
+        int known = item + step(told) < items ? 0 : 3;  // the last loads that saw the blocks of this or the next item
         bool seen = known != 0;                // the next item's blocks are known
         next.nb = 0;
         for (; j < cur.nb; j += 2) {
@@ -1293,11 +1346,13 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
           load_ids(j + 6, id);
           known = j + 6 < cur.nb || seen ? known + 1 : 0;
           if (!seen && j + 8 >= cur.nb) {
-            next = blocks_of(item + G);
+            if (kLong && (told & kGoesOn)) next = rest_of(item);
+            else next = blocks_of(item + G);
             seen = true;
           }
         }
-        if (!seen) next = blocks_of(item + G);
+        if (kLong && !seen && (told & kGoesOn)) next = rest_of(item);
+        else if (!seen) next = blocks_of(item + G);
         ahead = known >= 3;
         g += cur.nb;
         cur = next;
@@ -1313,9 +1368,14 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     int it = 0, oc = 0;
     uint32_t g = 0;
     bool ok = true;
-    for (int item = first; ok && item < items; item += G, ++it) {
+    // of this thread's head, of a tile in several items: what the loop over its blocks keeps from one to the next, and the power
+    // of two that O was held under when it was last added to memory
+    [[maybe_unused]] float kept_E0, kept_l, kept_lost, E_added;
+    [[maybe_unused]] int kept_valid;
+    for (int item = first, told = 0; ok && item < items; item += step(told), ++it) {
       if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
-      const int nb = sm->nb[it & 1];
+      told = sm->nb[it & 1];
+      const int nb = blocks_told(told);
       // Of a tile of several tokens: the keys of the item's first block on that this thread's head sees (its last
       // token's are all there are).
       int left = INT_MAX;
@@ -1333,6 +1393,8 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       if (nb == 0) continue;
       float E0 = -INFINITY, l = 0.f, lost = 0.f;
       int any_valid = 0;
+      if constexpr (kLong)
+        if (told & kBegan) E0 = kept_E0, l = kept_l, lost = kept_lost, any_valid = kept_valid;
       for (int j = 0; j < nb; ++j, ++g) {
         const int ri = (int)(g % kRing), pb = (int)(g & 1);
         // the block's scales, the release of P(g - 2) (and with it of its scales), the scores.  (Uniform
@@ -1420,11 +1482,21 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         }
       }
       if (!ok) break;
+      if constexpr (kLong) {
+        if (told & kGoesOn) kept_E0 = E0, kept_l = l, kept_lost = lost, kept_valid = any_valid;
+      }
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if (!any_valid) l = 0.f;
       if (!(ok = wait(&bar.l_empty[oc & 1], ((oc >> 1) & 1) ^ 1))) break;
-      if (m == 0) {
+      if constexpr (kLong) {
+        if (m == 0) {
+          sm->carry[oc & 1][hl] = ex2(E_added - E0);
+          if (told & kGoesOn) sm->lsum[oc & 1][hl] = l == 0.f ? 0.f : 1.f;
+        }
+        E_added = E0;
+      }
+      if (m == 0 && !(kLong && (told & kGoesOn))) {
         sm->lsum[oc & 1][hl] = l == 0.f ? 0.f : 1.f / l;
         const Item I = item_of<kForm>(p, item);
         const float v = l == 0.f ? -INFINITY : (E0 + log2f(l)) * kLn2;
@@ -1451,12 +1523,13 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       int it = 0, oc = 0;
       uint32_t g = 0;
       bool ok = true;
-      for (int item = first; ok && item < items; item += G, ++it) {
+      for (int item = first, told = 0; ok && item < items; item += step(told), ++it) {
         if (!(ok = wait(&bar.info_full[it & 1], (it >> 1) & 1))) break;
-        const int nb = sm->nb[it & 1];
+        told = sm->nb[it & 1];
+        const int nb = blocks_told(told);
         // (FP8 rows) Keys of the item from `hidden` on, up to `hidden_end`, are not seen by every token of the tile.
         int hidden = INT_MAX, hidden_end = 0;
-        if constexpr (kForm == kAllTiles && !kFour) {
+        if constexpr (kForm > kAll && !kFour) {
           if (p.causal && p.tile_t > 1) {
             const Item I = item_of<kForm>(p, item);
             hidden_end = sm->sees[it & 1] - sm->j0[it & 1] * kNB;
@@ -1502,7 +1575,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
               }
             }
           }
-          if (kForm == kAllTiles && !kFour && j * kNB + kNB - 1 >= hidden) {
+          if (kForm > kAll && !kFour && j * kNB + kNB - 1 >= hidden) {
             // Weights of rows that a token does not see are zero, which times a NaN code would still reach its values.  The
             // scores have been taken of those codes, so that tokens which see them have NaN weights: zeros in their place.
             if (!(ok = wait(&bar.kv_full[g % kStages], (g / kStages) & 1))) break;
@@ -1519,7 +1592,7 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.sf_full[g & 1]);
         }
-        if (!ok || !(ok = epilogue(item, oc))) break;
+        if (!ok || !(ok = epilogue(item, oc, told))) break;
         ++oc;
       }
       meet_last(ok);
@@ -1527,14 +1600,15 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
       // ================= queries: hi and lo rows; half of the epilogue =================
       const int qw = warp - kQWarp0;
       int it = 0, oc = 0;
-      int last = -1;  // the item whose O is still to be stored
+      int last = -1, last_told = 0;  // the item whose O is still to be stored
       bool ok = true;
-      for (int item = first; item < items || last >= 0; item += G, ++it) {
-        int nb = 0;
+      for (int item = first, told = 0; item < items || last >= 0; item += step(told), ++it) {
+        int nb = told = 0;
         if (item < items) {
           if (it > 0) convert(item, qw, 4);
           ok = wait(&bar.info_full[it & 1], (it >> 1) & 1);
-          nb = ok ? sm->nb[it & 1] : 0;
+          told = ok ? sm->nb[it & 1] : 0;
+          nb = blocks_told(told);
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(&bar.info_empty[it & 1]);
           if (kForm == kRows && qw == 0 && nb <= kFetchBlocks && item + G < items && p.H > kFetchHeads) fetch(item + G);
@@ -1559,9 +1633,10 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
         }
         // the O warps wait in the last item's epilogue: join them before any wait on a later item
         // than this one, whose publication they hold up
-        if (last >= 0 && !(ok = epilogue(last, oc - 1))) break;
+        if (last >= 0 && !(ok = epilogue(last, oc - 1, last_told))) break;
         if (nb) ++oc;
         last = nb ? item : -1;
+        last_told = told;
       }
       meet_last(ok);
       asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");

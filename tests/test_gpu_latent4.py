@@ -808,3 +808,90 @@ def test_dense_attention_what_is_not_finite_reaches_only_the_tokens_that_see_it(
         if kind != "rope inf":  # (which may be a score of minus infinity)
             assert bool(o[0, first:].isnan().all()) and bool(l[0, first:].isnan().all()), kind
     assert dsa.read_device_flags(DEV) == 0
+
+
+# --- rows that one accumulation does not hold ------------------------------------------------------
+
+def _long_cache(n, four, seed, page=8192):
+    """n positions over one page of rows of one sign: their mean is the result of equal weights."""
+    g = _gen(seed)
+    cache = dict(scales=torch.full((1, page), 255 / 128, device=DEV), rope=torch.zeros((1, page, 64), dtype=torch.bfloat16, device=DEV),
+                 block_table=torch.zeros((1, n // page), dtype=torch.int32, device=DEV))
+    if four:
+        cache["codes"] = torch.randint(1, 8, (1, page, 512), generator=g, device=DEV).to(torch.uint8)
+        cache["codes"] = cache["codes"][..., 0::2] + 16 * cache["codes"][..., 1::2]
+        cache["groups"] = torch.full((1, page, 16), 127, dtype=torch.uint8, device=DEV)
+    else:
+        cache["codes"] = (1 + torch.rand((1, page, 512), generator=g, device=DEV) * 15).to(E4M3)
+    return cache
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("lg", [16, 18, 20, 22])
+@pytest.mark.parametrize("equal", [True, False])
+def test_dense_attention_sums_of_values_over_long_rows(lg, equal, four):
+    """Equal weights over 2^lg rows, more tiles than SMs: a CTA walks whole tiles.  Weights times scales are 255 = 256 - 1, two e4m3
+    terms exactly, so what is off beside bf16's rounding is the sum alone.  Of 2^18 rows at a time it takes 2^14
+    additions (four a block of 64), each of which may lose a last place, 2^-23 of a sum that is at most the last: 2^-9; up to
+    16 of those are added with at most 2^-24 each, and the weights' own sums are fp32, too: 2^-18 covers both."""
+    n, T = 1 << lg, 160
+    cache = _long_cache(n, four, lg)
+    if equal:
+        cache["codes"] = cache["codes"].view(torch.uint8)[:, :1].expand(-1, 8192, -1).contiguous().view(cache["codes"].dtype)
+    rows = _latent64(cache, torch.arange(8192, device=DEV)) * 255 / 128
+    want = rows.mean(0)
+    q = torch.zeros((1, T, 64, 576), dtype=torch.bfloat16, device=DEV)
+    o, l = _call(cache)(dict(q=q, cache=cache, scale=1.0), torch.tensor([n], dtype=torch.int32, device=DEV), causal=False)
+    off = ((o.double() - want).abs() / want).amax()
+    assert float(off) <= BF16_STEP + 2.0 ** (min(lg, 18) - 4 - 23) + FP32_WORK, float(off)
+    assert bool(((l.double() - math.log(n)).abs() <= 2.0 ** -14 * (1 + math.log(n))).all())
+    assert dsa.read_device_flags(DEV) == 0
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("B,T,H,S,lens", [
+    (1, 160, 64, 270000, [270000]),                  # two items a tile, and runs that end in either
+    (1, 700, 8, 560000, [559990]),                   # 64 / 8 tokens a tile, fewer tiles than SMs
+    (1, 640, 16, 262200, [262200]),                  # tiles that end with the second item's first block, or before it
+    (200, 1, 64, 530000, [530000 - 2600 * b for b in range(200)]),
+    (2, 90, 128, 540000, [540000, 262144]),
+    (2, 3, 64, 530000, [530000, 524289]),            # (parts on every SM: one item each)
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_dense_attention_of_tiles_in_several_items(B, T, H, S, lens, causal, four):
+    g = _gen(S)
+    cache = _cache(1, S, 64, four, seed=S, spread=0.5)
+    if B > 1:  # (the sequences' pages are the same ones, in other orders)
+        table = cache["block_table"][0]
+        cache["block_table"] = torch.stack([table[torch.randperm(table.numel(), generator=g, device=DEV)] for _ in range(B)]).contiguous()
+    some = {(b, t) for b in {0, B // 2, B - 1} for t in {0, 1, T // 2, T - 1}}
+    at = dict(q=_q(B, T, H), cache=cache, scale=1 / 24, S=S)
+    got = _check_dense(at, lens, causal, some=some)
+    assert _same(got, _call(cache)(at, torch.tensor(lens, dtype=torch.int32, device=DEV), causal=causal))
+    assert dsa.read_device_flags(DEV) == 0
+
+
+def test_dense_attention_references_that_move_between_items():
+    """Scores that rise, or fall, by more than a reference keeps from one item of a tile to the next; empty items first; a
+    NaN in the second item reaches the heads of the tokens that see it, all others keep their bits."""
+    S, T, H = 800000, 300, 32
+    cache = _cache(1, S, 64, four=False)
+    cache["scales"].fill_(0.01)
+    cache["rope"].zero_()
+    flat, pos = cache["rope"].view(-1, 64), torch.arange(S, device=DEV)
+    at = _flat(cache, torch.zeros_like(pos), pos)
+    q = _q(1, T, H, 0.05)
+    q[..., 512] = 8.0
+    some = {(0, t) for t in (0, 1, 150, T - 2, T - 1)}
+    for step in (131072, 262144, 400000):
+        for sign in (1, -1):
+            flat[at, 0] = ((pos // step) * 100.0 * sign / 0.01).bfloat16()
+            got = _check_dense(dict(q=q, cache=cache, scale=1 / 24), [S], some=some)
+    c = dict(cache, codes=cache["codes"].clone())
+    c["codes"].view(torch.uint8).view(-1, 512)[at[S - 2], 77] = 0x7F
+    o, l = dsa.dsa_latent_attn_dense(dict(q=q, cache=c, scale=1 / 24), torch.tensor([S], dtype=torch.int32, device=DEV))
+    assert _same([o[0, :T - 2], l[0, :T - 2]], [got[0][0, :T - 2], got[1][0, :T - 2]])
+    assert bool(o[0, T - 2:].isnan().all()) and bool(l[0, T - 2:].isnan().all())
+    flat[at, 0] = torch.where(pos < 600000, -math.inf, 0.0).bfloat16()  # nothing but minus infinity in the first items
+    _check_dense(dict(q=q, cache=cache, scale=1 / 24), [S], some=some)
+    assert dsa.read_device_flags(DEV) == 0
