@@ -895,3 +895,20 @@ def test_dense_attention_references_that_move_between_items():
     flat[at, 0] = torch.where(pos < 600000, -math.inf, 0.0).bfloat16()  # nothing but minus infinity in the first items
     _check_dense(dict(q=q, cache=cache, scale=1 / 24), [S], some=some)
     assert dsa.read_device_flags(DEV) == 0
+
+
+def test_dense_attention_waits_do_not_grow_with_the_rows():
+    """2^22 rows, which a CTA walks in 10^8 cycles and more: no wait lasts longer than 4,096 blocks (10^7), so that a limit of 3 * 10^7
+    cycles is not met."""
+    n, T = 1 << 22, 160
+    cache = _long_cache(n, True, 1)
+    at = dict(q=_q(1, T, 64, 0.05), cache=cache, scale=1 / 24)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    want = dsa.dsa_latent4_attn_dense(at, lens)
+    try:
+        dsa.set_wait_limit(30_000_000)
+        got = dsa.dsa_latent4_attn_dense(at, lens)
+        torch.cuda.synchronize()
+    finally:
+        dsa.set_wait_limit(0)
+    assert dsa.read_device_flags(DEV) == 0 and _same(got, want)
