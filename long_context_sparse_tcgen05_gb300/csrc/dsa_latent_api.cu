@@ -201,11 +201,11 @@ dsa_status read_rows(const Cache* cache, int32_t B, int32_t n, const int32_t* id
   return done(dsa::launch_latent_read(P, static_cast<cudaStream_t>(stream)), "read launch");
 }
 
-// The status of an attention launch.
-dsa_status attended(cudaError_t e) {
+// The status of an attention launch over this cache.
+dsa_status attended(cudaError_t e, const dsa::LatentCacheView& cache) {
   if (e == cudaErrorInvalidKernelImage)  // (returned by the launcher's own look at the kernels, too)
     return fail(DSA_ERR_CUDA, "attention launch: the kernel is not built for this device, or not with the %d registers a "
-                "thread that its warpgroups share out (build it with the package's own build step)", dsa::kLatentAttnRegs);
+                "thread that its warpgroups share out (build it with the package's own build step)", cache.groups ? dsa::kLatent4AttnRegs : dsa::kLatentAttnRegs);
   return done(e, "attention launch");
 }
 
@@ -221,7 +221,7 @@ dsa_status attend(const Args* a, const int32_t* idx, int32_t k, void* out, float
   L.idx = idx; L.out = static_cast<uint16_t*>(out); L.lse = lse;
   L.flags = a->flags ? a->flags : ws_flags(ws);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return attended(L.cache.groups ? dsa::launch_latent4_attn(L, st) : dsa::launch_latent_attn(L, st));
+  return attended(L.cache.groups ? dsa::launch_latent4_attn(L, st) : dsa::launch_latent_attn(L, st), L.cache);
 }
 
 template <class Args>
@@ -239,7 +239,7 @@ dsa_status attend_dense(const Args* a, const int32_t* lens, int32_t causal, void
   L.lens = lens; L.causal = causal != 0;
   L.out = static_cast<uint16_t*>(out); L.lse = lse;
   L.flags = a->flags ? a->flags : ws_flags(ws);
-  return attended(dsa::launch_latent_dense(L, static_cast<uint8_t*>(ws) + dsa::kWsScratch, static_cast<cudaStream_t>(stream)));
+  return attended(dsa::launch_latent_dense(L, static_cast<uint8_t*>(ws) + dsa::kWsScratch, static_cast<cudaStream_t>(stream)), L.cache);
 }
 
 }  // namespace

@@ -346,3 +346,40 @@ def test_dense_attention_call_refusals_and_workspace(lib):
     assert size(0, 1, 1, 1) == size(1, 1, 1, 129) == 256  # calls that are refused
     assert size(1, 1, 2 ** 31 - 1, 64) >= size(1, 1, 64, 64) > 256
     assert lib.dsa_launch_count() == before
+
+
+def test_a_refused_kernel_image_is_told_with_its_own_registers(tmp_path):
+    """The entry points over launchers that refuse their kernels: the message names what that cache's kernels are built with."""
+    src = tmp_path / "refused.cu"
+    src.write_text(r'''
+#include "dsa_latent_api.cu"
+namespace dsa {
+dsa_status record_error(dsa_status s, const char* msg) { return printf("%s\n", msg), s; }
+int norm_rope_units(int) { return 0; }
+cudaError_t launch_norm_rope(const NormRopeLaunch&, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_latent_append(const LatentAppendLaunch&, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_latent_read(const LatentReadLaunch&, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_latent_attn(const LatentAttnLaunch&, cudaStream_t) { return cudaErrorInvalidKernelImage; }
+cudaError_t launch_latent4_attn(const LatentAttnLaunch&, cudaStream_t) { return cudaErrorInvalidKernelImage; }
+cudaError_t launch_latent_dense(LatentAttnLaunch, void*, cudaStream_t) { return cudaErrorInvalidKernelImage; }
+size_t latent_dense_scratch(LatentAttnLaunch) { return 0; }
+}  // namespace dsa
+int main() {
+  static_assert(dsa::kLatentAttnRegs != dsa::kLatent4AttnRegs);
+  void* m = reinterpret_cast<void*>(1 << 20);
+  int32_t* i = static_cast<int32_t*>(m);
+  dsa_latent_attn_args a{1, 1, 4, 64, 0.5f, m, 0, 0, {1, 4, 0, static_cast<uint8_t*>(m), static_cast<float*>(m), m, nullptr}, 1, nullptr};
+  dsa_latent4_attn_args b{1, 1, 4, 64, 0.5f, m, 0, 0, {1, 4, 0, static_cast<uint8_t*>(m), static_cast<uint8_t*>(m), static_cast<float*>(m), m, nullptr}, 1, nullptr};
+  dsa_latent_attn(&a, i, 1, m, nullptr, m, 1 << 20, nullptr);
+  dsa_latent_attn_dense(&a, i, 1, m, nullptr, m, 1 << 20, nullptr);
+  dsa_latent4_attn(&b, i, 1, m, nullptr, m, 1 << 20, nullptr);
+  dsa_latent4_attn_dense(&b, i, 1, m, nullptr, m, 1 << 20, nullptr);
+  printf("%d %d\n", dsa::kLatentAttnRegs, dsa::kLatent4AttnRegs);
+}
+''')
+    exe = tmp_path / "refused"
+    subprocess.run([dsa_build.NVCC, *dsa_build.ARCH, *dsa_build.FLAGS, "-cudart", "static", str(src), "-o", str(exe)], check=True)
+    *told, regs = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.splitlines()
+    eight, four = regs.split()
+    assert len(told) == 4
+    assert all(f" {eight} registers" in m for m in told[:2]) and all(f" {four} registers" in m for m in told[2:]), told
