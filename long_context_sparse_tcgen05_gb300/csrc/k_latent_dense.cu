@@ -3,7 +3,7 @@
 //   O = sum_j 2^x_j s_j c_j / sum_j 2^x_j over j < lens - T + 1 + t (causal) or j < lens.
 // The lengths are device values, so every CTA finds its run from them (ShareCount); the host knows only how many runs
 // there may be.  A part of a tile is left in memory as fp32 rows normalised by its own sum and their log sums, two parts a
-// CTA at most, which makes the scratch a constant of the device: 40 MB.  A second kernel weighs and adds them in order.
+// CTA at most: 40 MB of scratch at one CTA an SM, less where S says that there are fewer runs.  A second kernel weighs and adds them in order.
 // A tile of few heads takes several tokens, which share its rows: 16 heads of a token fill a quarter of the 64.
 //
 // Measured (64 heads, 4-bit): one token over 131,072 rows 39 us (36 with the rows in L2: 28 the runs of 13.5 blocks, of which
@@ -251,6 +251,10 @@ cudaError_t launch(LatentAttnLaunch p, cudaStream_t st) {
   if (runs > 1) {
     const int split = std::min(runs - 1, p.B * p.tiles_t * p.groups);  // split tiles, at most
     const int most = std::min(kHg, p.H * p.tile_t);
+    // The join of many parts for up to three tiles, the short one with four heads a block for up to 64, us with the long one /
+    // four / eight heads (single tokens of 64 heads, 131,072 rows unless said): 1 sequence 37 / 64 / 95, 2 60 / 70 / 86, 3 80 / 83 / 96,
+    // 4 99 / 95 / 106, 8 of 65,536 108 / 90 / 95, 16 of 32,768 133 / 92 / 94, 32 of up to 32,768 172 / 95 / 98, 140 of up to 20,000
+    // - / 210 / 208.  (Of 8 heads, 4 sequences: 85 / 93 / 102.)
     if (split <= 3) {
       k_latent_join_long<<<dim3(split, 4 * most), kJoinThreads, 0, st>>>(p, runs);
     } else {

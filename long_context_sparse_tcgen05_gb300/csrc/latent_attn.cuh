@@ -35,7 +35,7 @@
 //   0-3    copy the rows (16-byte cp.async) into three stages of 40 KB, five 128-byte-swizzled atoms
 //          each, as soon as the products have released them.  4-bit: with 24-27, eight warps, from registers; a
 //          block needs 2,150 warp instructions more, half of them byte permutations and logic that run at half
-//          rate, and four warps took 4.0 ms for what eight do in 1.2
+//          rate, and four warps took 3.1 ms for what eight do in 1.2
 //   4      S (hi and lo rows, 128 x 64) = Q K^T: A is Q in tensor memory, so the product reads only
 //          the codes from shared memory; 16 FP8 steps and 4 bf16 steps for the rope part
 //   5      O^T (512 x 64) += V^T P^T: four chunks of 128 dims, 2 key steps, hi and lo
@@ -449,13 +449,18 @@ __device__ __forceinline__ int dense_blocks(int sees) { return sees < 1 ? 1 : (s
 
 // This CTA's share of a call over all rows: a run of blocks of one tile or of several, one after another.  Runs that
 // end inside tiles leave parts, which k_latent_join puts together.
-//   Few tiles: each is cut into equal parts of at most L blocks, a part a CTA, if some L up to four above the mean gives no
-// more parts than there are CTAs: each segment of a run costs about four blocks beside its blocks (queries, O).
+//   Few tiles: each is cut into equal parts of at most L blocks, a part a CTA, if some L up to kSlack above the mean gives no
+// more parts than there are CTAs, since a run over a tile's end has a second segment, which costs more than its blocks
+// (queries, O).  Up to 20 above, against up to 4 (8 and 12 alike), us: two chunks of 301 tokens of 16 heads over 4,099 and
+// 2,050 rows 91 / 98 (FP8 87 / 92; parts of 65 blocks at a mean of 47, so only 20 admits them); but 32 sequences of 1,024 to
+// 32,768 rows 95 / 92, 60 of up to 20,000 rows 110 / 101, and within 1 for eight shapes of shorter rows.  (The slack is a
+// number of blocks whatever the mean: one row of 4,000 among 99 of up to 64 34.6 / 33.7.)
 //   Otherwise all tiles, one after another, are divided into runs of equal cost, so sequences of any lengths keep the SMs
-// evenly busy.  A tile costs its blocks (1.15 us each) and about ten more: measured alone, 6 us beside its blocks where it is
-// long, 11 us where it has one, a chain of latencies.  A run that ends among those ends with the tile before.  A prompt of
-// 4,096 tokens, 64 heads: by blocks alone 3.7 ms (the first CTA had 330 short tiles), with 6 more a tile 1.45, 10 more 1.34,
-// 14 more 1.36.
+// evenly busy.  A tile costs its blocks (1.15 us each) and own() more: ten, and up to three more where it has fewer than
+// twelve.  (Measured alone, 6 us beside its blocks where it is long, 11 us where it has one, a chain of latencies; ten
+// blocks are 11.)  A run that ends among those ends with the tile before.  A prompt of 4,096 tokens, 64 heads: by blocks alone
+// 3.7 ms (the first CTA had 330 short tiles), with 5 more a tile 1.86 (FP8 1.69), 10 more 1.37 (1.15), own() 1.35 (1.15), 13
+// more 1.34 (1.19).  Tiles of up to eight blocks would rather have ten: 1,216 tokens over 512 rows 126 us, with own() 140.
 // Every CTA counts all tiles (a few instructions each, over its threads; a tile's own work is thousands of cycles): each
 // thread its tiles' blocks, then, all threads having met, find() places the run's ends.
 struct ShareRoom {
