@@ -476,8 +476,10 @@ size_t dsa_latent_attn_workspace_size(const dsa_latent_attn_args* a, int32_t k);
  *           [0, lens[b] - T + 1 + t): itself and what precedes it; 0: every query sees [0, lens[b])
  * A query that sees nothing gets out = 0, lse = -inf; positions without a valid page are skipped and raise
  * DSA_FLAG_BAD_INDEX.  The args' idx_T is not read.  Precision as dsa_latent_attn (the 64 neighbours: positions
- * 64 i .. 64 i + 63); sums over more than 2^18 rows are made of sums over 2^18 at a time.  The rows of all queries are divided evenly over the SMs, whatever the lengths, and
- * partial results are joined in a fixed order: results do not vary from run to run on one kind of device.
+ * 64 i .. 64 i + 63); sums over more than 2^18 rows are made of sums over 2^18 at a time.  The rows of all queries are
+ * divided evenly over the SMs, whatever the lengths, and partial results are joined in a fixed order: results do not vary
+ * from run to run on one kind of device.  (Where S leaves it open whether a CTA has that many rows of a query, two kernels
+ * are launched, one of which finds in 5 us that the lengths are not for it: let S say what the sequences may hold.)
  * ws: dsa_latent_attn_dense_workspace_size bytes (of the current device): the flag word, and scratch that calls
  * which may overlap must not share. */
 dsa_status dsa_latent_attn_dense(const dsa_latent_attn_args* a, const int32_t* lens, int32_t causal, void* out, float* lse,
@@ -586,7 +588,7 @@ uint64_t dsa_launch_count(void);
  *   (host synchronisation on their events), writes up to max_records entries in launch order
  *   -- kinds[i] is DSA_TRACE_INDEXER, _TOPK, _ATTENTION, _OVERLAP or _CACHE (the
  *   norm, latent append, read and unpack kernels; a dense latent attention call is one record
- *   for its two kernels), ms[i] the device time in
+ *   for its two or three kernels), ms[i] the device time in
  *   milliseconds (-1 if unavailable) -- returns the number written, stores in *dropped (may
  *   be NULL) the launches the pool could not record, and clears the records.  Host arrays
  *   are owned by the caller; kinds or ms may be NULL.

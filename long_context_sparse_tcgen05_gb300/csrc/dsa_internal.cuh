@@ -320,6 +320,7 @@ struct LatentAttnLaunch {
   // ones after it, tokens of a tile, tiles of a sequence and head group, the runs and the room of parts
   const int32_t* lens;
   int causal, tile_t, tiles_t;
+  int by_length;  // two kernels are launched, for tiles of any length and for shorter ones; the lengths say whose work it is
   int4* shares;
   float* parts;
 };

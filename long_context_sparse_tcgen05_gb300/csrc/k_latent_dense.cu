@@ -245,9 +245,14 @@ cudaError_t launch(LatentAttnLaunch p, cudaStream_t st) {
   }
   cudaLaunchAttribute attr{};
   const cudaLaunchConfig_t cfg = launch_config<kFour>(runs, 1, st, &attr);
-  const Form form = most_blocks(p, runs) > kMaxBlocks ? kAllLong : p.causal && p.tile_t > 1 ? kAllTiles : kAll;
-  if ((e = cudaLaunchKernelEx(&cfg, dense_kernel<kFour>(p.wait < kDefaultWaitCycles, form), p)) != cudaSuccess) return e;
+  const bool poll = p.wait < kDefaultWaitCycles;
+  p.by_length = most_blocks(p, runs) > kMaxBlocks;
+  if ((e = cudaLaunchKernelEx(&cfg, dense_kernel<kFour>(poll, p.causal && p.tile_t > 1 ? kAllTiles : kAll), p)) != cudaSuccess) return e;
   count_launches(1);
+  if (p.by_length) {
+    if ((e = cudaLaunchKernelEx(&cfg, dense_kernel<kFour>(poll, kAllLong), p)) != cudaSuccess) return e;
+    count_launches(1);
+  }
   if (runs > 1) {
     const int split = std::min(runs - 1, p.B * p.tiles_t * p.groups);  // split tiles, at most
     const int most = std::min(kHg, p.H * p.tile_t);

@@ -145,7 +145,8 @@ static_assert(kHg * kMaxLatentSplits * sizeof(float) <= kQBytes, "the parts' wei
 // cluster; kAll: all rows that the queries see, divided into equal runs of blocks; kAllTiles: the same of FP8 rows some of
 // which not every token of a tile sees.  (In a kernel of its own: what it does about NaN codes costs calls without such tiles
 // 6%, a prompt of 4,096 tokens of 64 heads 1,147 -> 1,218 us, and its own calls 4%, of 16 heads 323 -> 336.)  kAllLong: any of
-// these calls of which a CTA may have more than kMaxBlocks of one tile (3 to 6% slower a block, so a kernel of its own, too).
+// these calls of which a CTA may have more than kMaxBlocks of one tile (3 to 6% slower a block, so a kernel of its own, too:
+// where S leaves it open whether any tile is that long, both are launched, and one of them finds that the work is not its own).
 enum Form { kRows, kRowParts, kAll, kAllTiles, kAllLong };
 
 struct Bars {
@@ -475,6 +476,7 @@ struct ShareCount {
   // A tile's own cost beside its n blocks.
   __device__ __forceinline__ static int own(int n) { return max(kTileCost, kMostCost - n / 4); }
   int tiles, lo, hi;
+  bool longer;  // one of this thread's tiles has more than kMaxBlocks
   __device__ __forceinline__ int blocks(int tile) const {
     const Item I = item_of<kAll>(p, tile);
     return dense_blocks(dense_sees(p, I.last, __ldg(p.lens + I.b)));
@@ -486,8 +488,10 @@ struct ShareCount {
     lo = min((int)threadIdx.x * per, tiles);
     hi = min(lo + per, tiles);
     sum = 0;
+    longer = false;
     for (int i = lo; i < hi; ++i) {
       const int n = blocks(i);
+      longer |= n > kMaxBlocks;
       if (few()) room.blocks[i] = n;
       sum += n + own(n);
     }
@@ -661,11 +665,13 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
     else return 0;
   }();
   tc_fence_before();
-  __syncthreads();
+  bool other = false;  // the work is the other kernel's
+  if constexpr (kDense) other = (__syncthreads_or(count.longer) != 0) != kLong && p.by_length;
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm->tmem, 0);
   if constexpr (kDense) {
-    if (!count.find(sm->share, room)) {
+    if (other || !count.find(sm->share, room)) {
       if (warp == kSWarp) tmem_dealloc(tmem, kTmemCols);
       return;
     }

@@ -912,3 +912,28 @@ def test_dense_attention_waits_do_not_grow_with_the_rows():
     finally:
         dsa.set_wait_limit(0)
     assert dsa.read_device_flags(DEV) == 0 and _same(got, want)
+
+
+@pytest.mark.parametrize("four,H", [(True, 64), (False, 64), (False, 16)])
+def test_dense_attention_lengths_choose_the_kernel(four, H):
+    """Room for rows that one accumulation does not hold, whether they are there or not: short sequences give the bits of
+    a call that knows they are, and a captured call follows its lengths past 2^18 rows and back."""
+    cap, T = 400000, 161 * max(1, 64 // H)
+    small = _cache(1, 5000, 64, four, seed=3)
+    big = dict(small, block_table=small["block_table"][0].repeat(-(-cap // 64) // small["block_table"].shape[1] + 1)[None, :-(-cap // 64)].contiguous())
+    q = _q(1, T, H)
+    n = torch.tensor([4900], dtype=torch.int32, device=DEV)
+    want = _call(small)(dict(q=q, cache=small, scale=1 / 24, S=5000), n)
+    at = dict(q=q, cache=big, scale=1 / 24, S=cap)
+    before = dsa.launch_count()
+    assert _same(_call(big)(at, n), want)
+    assert dsa.launch_count() == before + 3  # (a kernel of which the lengths say that it has nothing to do, too)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _call(big)(at, n)
+    some = {(0, 0), (0, T // 2), (0, T - 1)}
+    for rows in (4900, 262144, 262145, cap, 0, 4900):
+        n.fill_(rows)
+        graph.replay()
+        assert _same(got, _check_dense(at, [rows], some=some))
+    assert _same(got, want) and dsa.read_device_flags(DEV) == 0
