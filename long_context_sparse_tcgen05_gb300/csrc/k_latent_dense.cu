@@ -9,7 +9,7 @@
 // Measured (64 heads, 4-bit): one token over 131,072 rows 39 us (36 with the rows in L2: 28 the runs of 13.5 blocks, of which
 // 7.5 to the first score product and 2 to leave the part, and 8 the join of 152 parts); 32 tokens over 1,024 to 32,768
 // rows 95 us; 1,024 tokens over 32,768 rows 3.92 ms, 1,172 TFLOP/s; 4,096 tokens of a prompt 1.34 to 1.40 ms (FP8 1.15 to 1.20); two chunks of
-// 301 tokens of 16 heads over 4,099 and 2,050 rows (FP8) 87 us.  Bounded like the sparse kernels (a block 2,200 cycles).
+// 301 tokens of 16 heads over 4,099 and 2,050 rows (FP8) 88 to 91 us; 608 tokens over 524,288 rows 38.6 ms (FP8 36.5).  Bounded like the sparse kernels (a block 2,200 cycles).
 // Tried: the join launched early (griddepcontrol): 35.4 us either way; told early by the attention kernel: 40; blocks
 // walked from a start of each CTA's own, against many CTAs asking for the same rows at once: 2% slower.
 #include <algorithm>

@@ -53,8 +53,8 @@
 // operands at 128 bytes a cycle).
 // With few items of long index rows each is split into up to 8 parts of about 128 keys or more, one to each
 // CTA of a cluster, and the parts are joined over the cluster's shared memory.
-// Over all rows, an item is a tile of 64 heads of one or (few heads) several tokens, and a CTA walks a run of
-// blocks over tiles: see ShareCount and k_latent_dense.cu.
+// Over all rows, an item is a tile of 64 heads of one or (few heads) several tokens, or 2^18 rows of a longer one, and a
+// CTA walks a run of blocks over tiles: see ShareCount, kMaxBlocks and k_latent_dense.cu.
 // Waits are bounded (DSA_FLAG_TIMEOUT).
 //
 // Measured (64 heads, k = 2,048, FP8 / 4-bit): 4,096 queries over 131,072 rows 0.98 / 1.20 ms, 1,195 / 973 TFLOP/s, the
@@ -144,7 +144,7 @@ static_assert(kHg * kMaxLatentSplits * sizeof(float) <= kQBytes, "the parts' wei
 // What a kernel walks.  kRows: whole index rows; kRowParts: parts of index rows, one a CTA, joined over a
 // cluster; kAll: all rows that the queries see, divided into equal runs of blocks; kAllTiles: the same of FP8 rows some of
 // which not every token of a tile sees.  (In a kernel of its own: what it does about NaN codes costs calls without such tiles
-// 6%, a prompt of 4,096 tokens of 64 heads 1,147 -> 1,218 us, and its own calls 4%, of 16 heads 323 -> 336.)  kAllLong: any of
+// 6%, a prompt of 4,096 tokens of 64 heads 1,147 -> 1,218 us, and its own calls 2 to 4%, of 16 heads 323 -> 329 to 336.)  kAllLong: any of
 // these calls of which a CTA may have more than kMaxBlocks of one tile (3 to 6% slower a block, so a kernel of its own, too:
 // where S leaves it open whether any tile is that long, both are launched, and one of them finds that the work is not its own).
 enum Form { kRows, kRowParts, kAll, kAllTiles, kAllLong };
