@@ -1345,9 +1345,9 @@ __global__ void __launch_bounds__(kThreads<kFour>, 1) k_latent_attn(LatentAttnLa
             sc[0] = row[u] >= 0 ? scale[u] : 0.f;
             sc[2] = row[u] >= 0 ? log2f(scale[u]) : -INFINITY;
             const float inv = row[u] >= 0 ? 1.f / scale[u] : 0.f;
-            // (never a NaN: it leaves the zero weights of a tile's tokens that do not see the row at zero, and those that do
-            // have a NaN weight by its scale alone)
-            sm->isc[ri][r] = kDense ? fminf(inv, 0x1p60f) : inv;
+            // (always finite, the largest float instead of a NaN: it leaves the zero weights of a tile's tokens that do not see
+            // the row at zero, and those that do have a NaN weight by its scale alone)
+            sm->isc[ri][r] = kDense ? fminf(inv, 0x1.fffffep127f) : inv;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.ix_full[ri]);
